@@ -148,6 +148,42 @@ typedef struct se_h2o_state {
     int32_t recent;           /* newest positions never evicted (1 <= recent <= budget) */
 } se_h2o_state;
 
+/* Pages of a paged cache as their owner hands them out ([jetabc] fixed-size pages
+ * and a table from tokens to pages): a stack of free physical pages beside the
+ * block table.  Sequence b holds the physical pages block_table[b][0, n_pages[b]).
+ *   free_pages  int32 [num_pages]: free pages, the first *n_free entries; the top
+ *               of the stack is free_pages[*n_free - 1]; entries at and past
+ *               *n_free mean nothing
+ *   n_free      int32 [1]
+ *   n_pages     int32 [batch]: pages each sequence holds
+ *   block_table int32 [batch][max_pages_per_seq], ctx_len int32 [batch]: those of
+ *               the se_paged_kv that uses the pages (one pool serves every layer) */
+typedef struct se_page_pool {
+    int32_t* free_pages;
+    int32_t* n_free;
+    int32_t* n_pages;
+    int32_t* block_table;
+    int32_t* ctx_len;
+    int32_t num_pages;
+    int32_t max_pages_per_seq;
+} se_page_pool;
+
+/* A step's new tokens, packed: the rows of all sequences one after another, each
+ * sequence's in ascending, consecutive positions.
+ *   start int32 [batch + 1]: first row of each sequence; rows at and past
+ *         start[batch] belong to none
+ *   seq   int32 [max_tokens]: sequence of each row, -1 past the last sequence
+ *   pos   int32 [max_tokens]: logical position of each row (-1: no page was left)
+ *   slot  int32 [max_tokens]: physical page * 16 + pos % 16 (-1: no page was left);
+ *         head h of the token is cache row (page * num_kv_heads + h) * 16 + pos % 16 */
+typedef struct se_chunk {
+    int32_t* start;
+    int32_t* seq;
+    int32_t* pos;
+    int32_t* slot;
+    int32_t max_tokens;
+} se_chunk;
+
 /* Decode options (optional; NULL means all defaults). */
 typedef struct se_decode_opts {
     int32_t out_dtype;        /* 0 = bf16 output (default), 1 = fp32 output */
@@ -174,6 +210,20 @@ typedef struct se_quest_step_opts {
                                  append included, are invalid */
 } se_quest_step_opts;
 
+/* Options of se_chunk_attn (optional; NULL means all defaults). */
+typedef struct se_chunk_attn_opts {
+    int32_t out_dtype;        /* 0 = bf16 output (default), 1 = fp32 output */
+    int32_t window;           /* 0: every key up to the query's position; else only
+                                 the last `window` of them (the query's own
+                                 position included) and the first `sink` */
+    int32_t sink;             /* first positions seen whatever the window */
+    int64_t q_stride;         /* elements from one token's q to the next (0:
+                                 num_q_heads * head_dim), a multiple of 8 */
+    void* ev_kernel_begin;    /* NULL or a cudaEvent_t recorded right before / */
+    void* ev_kernel_end;      /* right after the attention kernel (timing only;
+                                 captured as external event-record nodes) */
+} se_chunk_attn_opts;
+
 /* ---- library ------------------------------------------------------------ */
 const char* se_status_str(int status);      /* static string, never NULL */
 int se_version(void);                       /* ABI version, currently 1 */
@@ -196,6 +246,9 @@ size_t se_quest_step_workspace(int batch, int num_kv_heads, int num_q_heads, int
                                int max_pages_per_seq, int max_splits);
 size_t se_snapkv_workspace(int batch, int num_kv_heads, int num_q_heads, int window, int max_ctx);
 size_t se_h2o_workspace(int batch, int num_kv_heads, int num_q_heads, int head_dim, int seg_cap);
+size_t se_page_pool_workspace(int batch);   /* se_chunk_plan and se_pages_release */
+size_t se_chunk_attn_workspace(int batch, int max_tokens, int num_kv_heads, int num_q_heads,
+                               int head_dim);
 
 /* ---- page summaries ----------------------------------------------------- */
 /* Rebuilds meta for every valid (page, head) of the first `batch` sequences:
@@ -214,6 +267,82 @@ int se_page_meta_build(const se_paged_kv* kv, int batch,
  * selection reuse; see se_sparse_decode).  Workspace: se_small_workspace(). */
 int se_kv_append(const se_paged_kv* kv, const void* k_new, const void* v_new, int batch,
                  void* ws, size_t ws_bytes, se_stream_t stream);
+
+/* ---- prompts in chunks: pages, rows and attention of many new tokens ------------
+ * Three calls take a batch of requests with any numbers of new tokens (whole
+ * prompts, chunks of them, single tokens, drafted tokens to check) through a paged
+ * cache: se_chunk_plan gives the tokens pages and rows, se_kv_append_chunk writes
+ * them (once per layer), se_chunk_attn attends (once per layer).  The cache is
+ * then as se_kv_append would have left it, page summaries included, and decodes
+ * with any method here.  se_pages_release takes a finished sequence's pages back.
+ *
+ * se_chunk_plan: new_len int32 [batch] new tokens per sequence; they follow the
+ * ctx_len[b] tokens held.  Sequence b needs
+ *   need[b] = max(0, ceil((ctx_len[b] + new_len[b]) / 16) - n_pages[b]) pages
+ * and is served when it needs none, or when need[0] + ... + need[b] <= *n_free (so
+ * no request overtakes one before it).  Its i-th new page is the one i +
+ * need[0] + ... + need[b-1] below the top of the stack; the block table receives it and
+ * n_pages and *n_free count it.  chunk is filled: start (the running sum of
+ * new_len, at most max_tokens), seq, pos = ctx_len[b] + i, slot; rows past the last
+ * sequence get seq = pos = slot = -1.  A sequence that is not served, or whose
+ * rows pass max_tokens, or whose tokens pass max_pages_per_seq pages: it takes no
+ * page, its rows get pos = slot = -1, SE_DEV_CAPACITY (the latter two count as
+ * need[b] = 0 for those behind).  A negative length, or n_pages[b] fewer than
+ * ctx_len[b] needs (or more than max_pages_per_seq): SE_DEV_BAD_LENGTH, need[b] = 0
+ * and no rows (new_len < 0) or rows with pos = slot = -1.  A page outside [0, num_pages) met on the stack or in the block
+ * table: SE_DEV_BAD_INDEX, the slots on it are -1.  ctx_len is not changed (the append commits it),
+ * so a plan that is made again before the append finds its pages held and takes
+ * no others.  Limits: 0 <= max_tokens <= 2^24.
+ * Workspace: se_page_pool_workspace(batch), zero-filled before its first use: it
+ * holds an arrival counter, which every call leaves at zero. */
+int se_chunk_plan(const se_page_pool* pool, const int32_t* new_len, int batch,
+                  const se_chunk* chunk, void* ws, size_t ws_bytes, se_stream_t stream);
+
+/* Puts the pages of every sequence with done[b] != 0 (int32 [batch]) back on the
+ * stack and sets its n_pages and ctx_len to 0.  The pages go back last page
+ * first (the first released sequence's first page ends on top), so a plan that
+ * takes as many takes them in the order of their sequences.  A stack that would pass num_pages entries (a page released
+ * twice): SE_DEV_CAPACITY, nothing is released.  n_pages outside
+ * [0, max_pages_per_seq]: SE_DEV_BAD_LENGTH, clamped.
+ * Workspace: as se_chunk_plan. */
+int se_pages_release(const se_page_pool* pool, const int32_t* done, int batch, void* ws,
+                     size_t ws_bytes, se_stream_t stream);
+
+/* Append of a chunk: for every row t of the chunk with slot[t] >= 0 and every KV head,
+ * k_new/v_new (bf16 [max_tokens][num_kv_heads][head_dim], tokens row_stride elements
+ * apart; 0: num_kv_heads * head_dim; a multiple of 8) go to the cache row of slot[t]
+ * and the key is folded into the summary of its page (a page whose first token
+ * is among the rows is set anew); ctx_len[seq[t]] becomes pos[t] + 1 of the
+ * sequence's last row.  The same result as se_kv_append token by token.  kv->meta
+ * may be NULL (no summaries are kept).  A slot outside the pages, or a seq or pos outside
+ * the block table: SE_DEV_BAD_INDEX, row dropped.  Workspace: se_small_workspace(). */
+int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_new,
+                       int64_t row_stride, const se_chunk* chunk, int batch, void* ws,
+                       size_t ws_bytes, se_stream_t stream);
+
+/* Attention of a chunk of new tokens over a paged cache that holds them already
+ * (after se_kv_append_chunk).  For sequence b, row t in [start[b], start[b+1]),
+ * p = pos[start[b]] + t - start[b], query head g of KV head h:
+ *   s[j] = scale * q[t,hG+g] . k[j]   over the keys j <= p, j < ctx_len[b] with
+ *          window = 0, or j > p - window, or j < sink
+ *   out[t,hG+g] = sum_j softmax_j(s) v[j];   lse[t,hG+g] = log sum_j exp(s[j])
+ * A row that sees no key (pos = -1 among them) gives out = 0, lse = -inf; rows of
+ * out and lse at and past start[batch] are left as they were.
+ * q bf16 [max_tokens][num_q_heads][head_dim] (opts->q_stride); out bf16 or fp32
+ * [max_tokens][num_q_heads][head_dim]; lse fp32 [max_tokens][num_q_heads] or NULL.
+ * kv->meta is not used and may be NULL.  The results do not depend on timing (the pieces of a
+ * split row are joined in a fixed order).  A block-table entry outside the pages sets SE_DEV_BAD_INDEX and its
+ * keys count as absent; ctx_len outside [0, 16 * max_pages_per_seq], or a row
+ * position at or past ctx_len[b]: SE_DEV_BAD_LENGTH, clamped.  start outside [0, max_tokens] or
+ * descending: SE_DEV_BAD_LENGTH, clamped (a descending sequence has no rows).
+ * Held keys and values are finite; what lies past ctx_len in a page may be anything.
+ * scale finite; window, sink >= 0; 0 <= max_tokens <= 2^24.
+ * Workspace: se_chunk_attn_workspace(...), zero-filled before its first use:
+ * it holds arrival counters at a fixed offset, which every call leaves at zero, so one
+ * workspace serves calls of any shape whose size it covers. */
+int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, int batch,
+                  int num_q_heads, float scale, const se_chunk_attn_opts* opts, void* out,
+                  float* lse, void* ws, size_t ws_bytes, se_stream_t stream);
 
 /* ---- (a) Quest page selection ([tokendh] Quest picks pages by the query) ----
  * For unit u = (b, h) with query heads g of KV head h and n = ceil(ctx_len[b]/16):

@@ -48,6 +48,24 @@ class H2OStateC(ctypes.Structure):
     _fields_ = [("kv", VarlenKVC), ("budget", ctypes.c_int32), ("recent", ctypes.c_int32)]
 
 
+class PagePoolC(ctypes.Structure):
+    _fields_ = [("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("n_pages", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("ctx_len", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("max_pages_per_seq", ctypes.c_int32)]
+
+
+class ChunkC(ctypes.Structure):
+    _fields_ = [("start", ctypes.c_void_p), ("seq", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("slot", ctypes.c_void_p), ("max_tokens", ctypes.c_int32)]
+
+
+class ChunkAttnOptsC(ctypes.Structure):
+    _fields_ = [("out_dtype", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("sink", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("ev_kernel_begin", ctypes.c_void_p), ("ev_kernel_end", ctypes.c_void_p)]
+
+
 class DecodeOptsC(ctypes.Structure):
     _fields_ = [("out_dtype", ctypes.c_int32), ("max_splits", ctypes.c_int32),
                 ("logits_out", ctypes.c_void_p), ("logits_stride", ctypes.c_int32),
@@ -79,6 +97,12 @@ SIGNATURES = {
     "se_quest_step_workspace": (_SZ, [_I, _I, _I, _I, _I, _I]),
     "se_snapkv_workspace": (_SZ, [_I, _I, _I, _I, _I]),
     "se_h2o_workspace": (_SZ, [_I, _I, _I, _I, _I]),
+    "se_page_pool_workspace": (_SZ, [_I]),
+    "se_chunk_attn_workspace": (_SZ, [_I, _I, _I, _I, _I]),
+    "se_chunk_plan": (_I, [_VP, _VP, _I, _VP, _VP, _SZ, _VP]),
+    "se_pages_release": (_I, [_VP, _VP, _I, _VP, _SZ, _VP]),
+    "se_kv_append_chunk": (_I, [_VP, _VP, _VP, _I64, _VP, _I, _VP, _SZ, _VP]),
+    "se_chunk_attn": (_I, [_VP, _VP, _VP, _I, _I, _F, _VP, _VP, _VP, _VP, _SZ, _VP]),
     "se_page_meta_build": (_I, [_VP, _I, _VP, _SZ, _VP]),
     "se_kv_append": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
     "se_quest_select": (_I, [_VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
@@ -235,6 +259,49 @@ class H2OState:
         return H2OStateC(self.kv.c, self.budget, self.recent)
 
 
+@dataclasses.dataclass
+class PagePool:
+    free_pages: torch.Tensor   # int32 [num_pages], the first n_free entries are free
+    n_free: torch.Tensor       # int32 [1]
+    n_pages: torch.Tensor      # int32 [B]
+    block_table: torch.Tensor  # int32 [B][max_pages], the PagedKV's
+    ctx_len: torch.Tensor      # int32 [B], the PagedKV's
+
+    @property
+    def c(self) -> PagePoolC:
+        return PagePoolC(_p(self.free_pages), _p(self.n_free), _p(self.n_pages),
+                         _p(self.block_table), _p(self.ctx_len), self.free_pages.numel(),
+                         self.block_table.shape[1])
+
+    @staticmethod
+    def empty(batch: int, num_pages: int, max_pages_per_seq: int, device="cuda") -> "PagePool":
+        """Every page free (page 0 handed out first), no sequence holds any."""
+        return PagePool(
+            torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+            torch.full((1,), num_pages, dtype=torch.int32, device=device),
+            torch.zeros(batch, dtype=torch.int32, device=device),
+            torch.full((batch, max_pages_per_seq), -1, dtype=torch.int32, device=device),
+            torch.zeros(batch, dtype=torch.int32, device=device))
+
+
+@dataclasses.dataclass
+class Chunk:
+    start: torch.Tensor        # int32 [B + 1]
+    seq: torch.Tensor          # int32 [max_tokens]
+    pos: torch.Tensor          # int32 [max_tokens]
+    slot: torch.Tensor         # int32 [max_tokens]
+
+    @property
+    def c(self) -> ChunkC:
+        return ChunkC(_p(self.start), _p(self.seq), _p(self.pos), _p(self.slot), self.seq.numel())
+
+    @staticmethod
+    def empty(batch: int, max_tokens: int, device="cuda") -> "Chunk":
+        rows = torch.full((3, max_tokens), -1, dtype=torch.int32, device=device)
+        return Chunk(torch.zeros(batch + 1, dtype=torch.int32, device=device), rows[0], rows[1],
+                     rows[2])
+
+
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """A zeroed device workspace (status word cleared)."""
     return torch.zeros(max(256, int(nbytes)), dtype=torch.uint8, device=device)
@@ -298,6 +365,63 @@ def se_kv_append(kv: PagedKV, k_new, v_new, batch: int, ws, stream=None):
     c = kv.c
     _check(load().se_kv_append(ctypes.byref(c), _p(k_new), _p(v_new), batch, _p(ws), ws.numel(),
                                _stream(stream)), "se_kv_append")
+
+
+def se_page_pool_workspace(batch: int) -> int:
+    return load().se_page_pool_workspace(batch)
+
+
+def se_chunk_attn_workspace(batch, max_tokens, num_kv_heads, num_q_heads, head_dim) -> int:
+    return load().se_chunk_attn_workspace(batch, max_tokens, num_kv_heads, num_q_heads, head_dim)
+
+
+def se_chunk_plan(pool: PagePool, new_len, batch: int, chunk: Chunk, ws, stream=None):
+    """Pages, positions and cache rows of each sequence's new tokens."""
+    c, cc = pool.c, chunk.c
+    _check(load().se_chunk_plan(ctypes.byref(c), _p(new_len), batch, ctypes.byref(cc), _p(ws),
+                                ws.numel(), _stream(stream)), "se_chunk_plan")
+
+
+def se_pages_release(pool: PagePool, done, batch: int, ws, stream=None):
+    """Pages of the sequences with done[b] != 0 back onto the free stack."""
+    c = pool.c
+    _check(load().se_pages_release(ctypes.byref(c), _p(done), batch, _p(ws), ws.numel(),
+                                   _stream(stream)), "se_pages_release")
+
+
+def _token_stride(x, what: str) -> int:
+    """Elements between tokens of a [tokens][heads][head_dim] tensor, which may be a
+    slice of wider rows (a packed q/k/v projection)."""
+    if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+        raise SparseEngineError(f"{what}: [tokens][heads][head_dim] with contiguous heads needed, "
+                                f"got shape {tuple(x.shape)} strides {x.stride()}")
+    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+
+
+def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, stream=None):
+    """Append the chunk's rows; k_new and v_new [max_tokens][Hkv][D] may be slices
+    of wider rows."""
+    c, cc = kv.c, chunk.c
+    stride = _token_stride(k_new, "se_kv_append_chunk k_new")
+    if stride != _token_stride(v_new, "se_kv_append_chunk v_new"):
+        raise SparseEngineError("se_kv_append_chunk: k_new and v_new strides differ")
+    _check(load().se_kv_append_chunk(ctypes.byref(c), _p(k_new), _p(v_new), stride,
+                                     ctypes.byref(cc), batch, _p(ws), ws.numel(),
+                                     _stream(stream)), "se_kv_append_chunk")
+
+
+def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, scale: float, out,
+                  lse, ws, out_dtype: int = 0, window: int = 0, sink: int = 0, ev_begin=None,
+                  ev_end=None, stream=None):
+    """Causal attention of the chunk's tokens over the paged cache; q
+    [max_tokens][Hq][D] may be a slice of wider rows."""
+    c, cc = kv.c, chunk.c
+    opts = ChunkAttnOptsC(out_dtype, window, sink, _token_stride(q, "se_chunk_attn q"),
+                          ev_begin.cuda_event if ev_begin is not None else None,
+                          ev_end.cuda_event if ev_end is not None else None)
+    _check(load().se_chunk_attn(ctypes.byref(c), _p(q), ctypes.byref(cc), batch, num_q_heads,
+                                scale, ctypes.byref(opts), _p(out), _p(lse), _p(ws), ws.numel(),
+                                _stream(stream)), "se_chunk_attn")
 
 
 def se_quest_select(kv: PagedKV, q, batch: int, num_q_heads: int, budget_tokens, sel_pages,

@@ -4,6 +4,7 @@
 // enqueues its kernels on the caller's stream.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -92,6 +93,25 @@ int check_varlen(const se_varlen_kv* kv) {
     return SE_OK;
 }
 
+int check_pool(const se_page_pool* p) {
+    if (!p || !p->free_pages || !p->n_free || !p->n_pages || !p->block_table || !p->ctx_len)
+        return SE_ERR_INVALID_ARG;
+    if (p->num_pages <= 0 || p->max_pages_per_seq <= 0) return SE_ERR_INVALID_ARG;
+    // slots and positions are int32
+    if (p->num_pages > INT32_MAX / SE_PAGE_SIZE || p->max_pages_per_seq > INT32_MAX / SE_PAGE_SIZE)
+        return SE_ERR_UNSUPPORTED;
+    return SE_OK;
+}
+
+constexpr int kMaxChunkTokens = 1 << 24;
+
+int check_chunk(const se_chunk* c) {
+    if (!c || !c->start || c->max_tokens < 0) return SE_ERR_INVALID_ARG;
+    if (c->max_tokens > 0 && (!c->seq || !c->pos || !c->slot)) return SE_ERR_INVALID_ARG;
+    if (c->max_tokens > kMaxChunkTokens) return SE_ERR_UNSUPPORTED;
+    return SE_OK;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SE_OK : SE_ERR_CUDA; }
 
 }  // namespace
@@ -153,6 +173,98 @@ int se_kv_append(const se_paged_kv* kv, const void* k_new, const void* v_new, in
     if ((rc = check_ws(ws, ws_bytes, se_small_workspace()))) return rc;
     return cuda_status(launch_kv_append(*kv, k_new, v_new, batch, static_cast<int*>(ws),
                                         static_cast<cudaStream_t>(stream)));
+}
+
+size_t se_page_pool_workspace(int batch) { return batch < 0 ? 0 : page_pool_ws_bytes(); }
+
+int se_chunk_plan(const se_page_pool* pool, const int32_t* new_len, int batch,
+                  const se_chunk* chunk, void* ws, size_t ws_bytes, se_stream_t stream) {
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if ((rc = check_chunk(chunk))) return rc;
+    if (batch < 0 || (batch > 0 && !new_len)) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_page_pool_workspace(batch)))) return rc;
+    return cuda_status(launch_chunk_plan(*pool, new_len, batch, *chunk, static_cast<int*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int se_pages_release(const se_page_pool* pool, const int32_t* done, int batch, void* ws,
+                     size_t ws_bytes, se_stream_t stream) {
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if (batch < 0 || (batch > 0 && !done)) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_page_pool_workspace(batch)))) return rc;
+    if (batch == 0) return SE_OK;
+    return cuda_status(launch_pages_release(*pool, done, batch, static_cast<int*>(ws),
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_new,
+                       int64_t row_stride, const se_chunk* chunk, int batch, void* ws,
+                       size_t ws_bytes, se_stream_t stream) {
+    int rc = check_paged(kv, false);
+    if (rc) return rc;
+    if ((rc = check_chunk(chunk))) return rc;
+    if (batch < 0) return SE_ERR_INVALID_ARG;
+    if (batch > 0 && chunk->max_tokens > 0 && (!k_new || !v_new)) return SE_ERR_INVALID_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16)) return SE_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)kv->num_kv_heads * kv->head_dim;
+    if (row_stride == 0) row_stride = row;
+    if (row_stride < row || row_stride % 8) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_small_workspace()))) return rc;
+    if (batch == 0) return SE_OK;
+    return cuda_status(launch_kv_append_chunk(*kv, k_new, v_new, row_stride, *chunk, batch,
+                                              static_cast<int*>(ws),
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+size_t se_chunk_attn_workspace(int batch, int max_tokens, int num_kv_heads, int num_q_heads,
+                               int head_dim) {
+    if (batch < 0 || max_tokens < 0 || max_tokens > kMaxChunkTokens || num_kv_heads <= 0 ||
+        num_q_heads <= 0 || num_q_heads % num_kv_heads || !head_dim_ok(head_dim) ||
+        !group_ok(num_q_heads / num_kv_heads))
+        return 0;
+    return chunk_attn_ws_bytes(batch, max_tokens, num_kv_heads, num_q_heads, head_dim);
+}
+
+int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, int batch,
+                  int num_q_heads, float scale, const se_chunk_attn_opts* opts, void* out,
+                  float* lse, void* ws, size_t ws_bytes, se_stream_t stream) {
+    int rc = check_paged(kv, false);
+    if (rc) return rc;
+    if ((rc = check_chunk(chunk))) return rc;
+    if (batch < 0 || num_q_heads <= 0) return SE_ERR_INVALID_ARG;
+    if (num_q_heads % kv->num_kv_heads || !group_ok(num_q_heads / kv->num_kv_heads))
+        return SE_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return SE_ERR_INVALID_ARG;
+    se_chunk_attn_opts o = {0, 0, 0, 0, nullptr, nullptr};
+    if (opts) o = *opts;
+    const int64_t row = (int64_t)num_q_heads * kv->head_dim;
+    if (o.q_stride == 0) o.q_stride = row;
+    if (o.out_dtype != 0 && o.out_dtype != 1) return SE_ERR_INVALID_ARG;
+    if (o.window < 0 || o.sink < 0) return SE_ERR_INVALID_ARG;
+    if (o.q_stride < row || o.q_stride % 8) return SE_ERR_INVALID_ARG;
+    if (kv->max_pages_per_seq > INT32_MAX / SE_PAGE_SIZE) return SE_ERR_UNSUPPORTED;
+    if (batch == 0 || chunk->max_tokens == 0) return SE_OK;
+    if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes,
+                       se_chunk_attn_workspace(batch, chunk->max_tokens, kv->num_kv_heads,
+                                               num_q_heads, kv->head_dim))))
+        return rc;
+    ChunkAttnArgs a;
+    a.q = q;
+    a.q_stride = o.q_stride;
+    a.Hq = num_q_heads;
+    a.scale = scale;
+    a.window = o.window;
+    a.sink = o.sink;
+    a.out_dtype = o.out_dtype;
+    a.out = out;
+    a.lse = lse;
+    return cuda_status(launch_chunk_attn(*kv, *chunk, batch, a, ws,
+                                         static_cast<cudaEvent_t>(o.ev_kernel_begin),
+                                         static_cast<cudaEvent_t>(o.ev_kernel_end),
+                                         static_cast<cudaStream_t>(stream)));
 }
 
 int se_quest_select(const se_paged_kv* kv, const void* q, int batch, int num_q_heads,

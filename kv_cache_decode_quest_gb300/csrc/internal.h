@@ -51,6 +51,32 @@ cudaError_t launch_view_sink_recent(const se_paged_kv& kv, int batch, int sink_p
 cudaError_t launch_view_from_segments(const se_varlen_kv& kv, int batch, const se_view& view,
                                       int* status, cudaStream_t s);
 
+// ---- pages.cu ----
+size_t page_pool_ws_bytes();
+cudaError_t launch_chunk_plan(const se_page_pool& pool, const int32_t* new_len, int batch,
+                              const se_chunk& ck, int* ws, cudaStream_t s);
+cudaError_t launch_pages_release(const se_page_pool& pool, const int32_t* done, int batch, int* ws,
+                                 cudaStream_t s);
+cudaError_t launch_kv_append_chunk(const se_paged_kv& kv, const void* k_new, const void* v_new,
+                                   int64_t row_stride, const se_chunk& ck, int batch, int* status,
+                                   cudaStream_t s);
+
+// ---- chunk_attn.cu ----
+struct ChunkAttnArgs {
+    const void* q;
+    int64_t q_stride;        // elements between tokens
+    int Hq;
+    float scale;
+    int window, sink;
+    int out_dtype;
+    void* out;
+    float* lse;
+};
+size_t chunk_attn_ws_bytes(int batch, int max_tokens, int H, int Hq, int D);
+cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int batch,
+                              const ChunkAttnArgs& a, void* ws, cudaEvent_t ev_begin,
+                              cudaEvent_t ev_end, cudaStream_t s);
+
 // ---- quest.cu ----
 size_t quest_ws_bytes(int units, int max_pages);
 // k_new / v_new non-null: the decode-step append of the new token is fused in

@@ -1,0 +1,460 @@
+// Paging of chunks of new tokens: which pages and rows they get
+// (se_chunk_plan), pages taken back (se_pages_release), and the append of the
+// rows with their page summaries (se_kv_append_chunk).  Pages of 16 tokens
+// with a token->page table follow the paged KV layout of "长程 agent 把显存撑爆以后",
+// section "四、为什么进不了 vLLM 一类的引擎".
+#include <algorithm>
+
+#include "append.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace se {
+namespace {
+
+// Workspace: the status word, then at byte 256 the arrival counter of the
+// kernel's blocks (zero between calls).
+constexpr int kCounterWord = 64;
+
+// Exclusive block-wide sums of two 64-bit values per thread (lengths come from
+// the device and may be anything: 64 bits hold the sum of any 1024 of them).
+// `tmp` holds 2 * 33 values.  All threads call it; *ta, *tb receive the totals.
+__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long* tmp,
+                                            long long* ta, long long* tb) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    long long x = a, y = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, x, o);
+        const long long v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) {
+            x += u;
+            y += v;
+        }
+    }
+    if (lane == 31) {
+        tmp[warp] = x;
+        tmp[33 + warp] = y;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        long long p = lane < nw ? tmp[lane] : 0, q = lane < nw ? tmp[33 + lane] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long u = __shfl_up_sync(0xffffffffu, p, o);
+            const long long v = __shfl_up_sync(0xffffffffu, q, o);
+            if (lane >= o) {
+                p += u;
+                q += v;
+            }
+        }
+        if (lane < nw) {
+            tmp[lane] = p;
+            tmp[33 + lane] = q;
+        }
+    }
+    __syncthreads();
+    *ta = tmp[nw - 1];
+    *tb = tmp[33 + nw - 1];
+    a = x - a + (warp > 0 ? tmp[warp - 1] : 0);
+    b = y - b + (warp > 0 ? tmp[33 + warp - 1] : 0);
+    __syncthreads();
+}
+
+// True in every thread of the last block of the grid to get here; what the
+// other blocks read before is then read, and their writes are visible.
+__device__ __forceinline__ bool last_block(int* counter) {
+    __shared__ int s_last;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    __threadfence();
+    return s_last != 0;
+}
+
+struct SeqPlan {
+    int ctx, held, n;       // tokens and pages held, new tokens (rows in the packed arrays)
+    int need;               // pages it takes when it is served (counted for those behind it)
+    int flags;              // SE_DEV_* bits
+    bool ok;                // lengths consistent
+};
+
+__device__ __forceinline__ SeqPlan seq_plan(const se_page_pool& p, const int32_t* new_len, int b) {
+    SeqPlan s;
+    s.ctx = p.ctx_len[b];
+    s.held = p.n_pages[b];
+    const int n = new_len[b];
+    s.n = max(n, 0);
+    s.flags = 0;
+    s.need = 0;
+    const long long cap = static_cast<long long>(p.max_pages_per_seq) * kPage;
+    s.ok = n >= 0 && s.ctx >= 0 && s.ctx <= cap && s.held >= (s.ctx + kPage - 1) / kPage &&
+           s.held <= p.max_pages_per_seq;
+    if (!s.ok) {
+        s.flags = SE_DEV_BAD_LENGTH;
+    } else if (static_cast<long long>(s.ctx) + s.n > cap) {
+        s.ok = false;
+        s.flags = SE_DEV_CAPACITY;
+    } else {
+        s.need = max(0, static_cast<int>((static_cast<long long>(s.ctx) + s.n + kPage - 1) / kPage) - s.held);
+    }
+    return s;
+}
+
+// One launch for the whole plan.  Every block scans all sequences (a few
+// words each, from L2) and writes its own range of the packed rows: a row's
+// page comes straight from the free stack or from the part of the block table that
+// was there before, so no block waits for another.  What the scan read
+// (n_pages, n_free) is updated by the last block to finish, which scans again.
+// Latency bound: the bytes (12 per row, 4 per new page, 12 per sequence) take
+// less time than the launch up to some hundred thousand rows.
+__global__ void __launch_bounds__(1024)
+    chunk_plan_kernel(se_page_pool pool, const int32_t* new_len, int batch, se_chunk ck,
+                      int rows_per_block, int* ws) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ int smem[];
+    const int nt = blockDim.x;
+    int* s_start = smem;            // [nt + 1] first row of each sequence of the pass
+    int* s_ctx = s_start + nt + 1;
+    int* s_held = s_ctx + nt;
+    int* s_top = s_held + nt;       // stack index of the sequence's first new page; -1: not served
+    __shared__ long long tmp[66];
+    int* status = ws;
+    const long long max_rows = ck.max_tokens;
+    const int r0 = min(blockIdx.x * rows_per_block, ck.max_tokens);
+    const int r1 = min(r0 + rows_per_block, ck.max_tokens);
+    int n_free = *pool.n_free;
+    int bad_flags = 0;
+    if (n_free < 0 || n_free > pool.num_pages) {
+        bad_flags |= SE_DEV_BAD_LENGTH;
+        n_free = n_free < 0 ? 0 : pool.num_pages;
+    }
+    long long row_base = 0, need_base = 0;
+    for (int b0 = 0; b0 < batch; b0 += nt) {
+        const int b = b0 + threadIdx.x;
+        SeqPlan s = {};
+        if (b < batch) s = seq_plan(pool, new_len, b);
+        long long row = s.n, need = s.need, rows = 0, needs = 0;
+        block_scan2(row, need, tmp, &rows, &needs);
+        row += row_base;
+        // a sequence whose rows pass max_tokens takes no page, and those behind
+        // it neither (their rows pass it too); their needs stay out of the count,
+        // which only they would have read
+        bool ok = s.ok;
+        if (ok && row + s.n > max_rows) {
+            ok = false;
+            s.flags |= SE_DEV_CAPACITY;
+        }
+        need += need_base;
+        if (ok && s.need > 0 && need + s.need > n_free) {
+            ok = false;
+            s.flags |= SE_DEV_CAPACITY;
+        }
+        s_start[threadIdx.x] = static_cast<int>(min(row, max_rows));
+        s_ctx[threadIdx.x] = s.ctx;
+        s_held[threadIdx.x] = s.held;
+        s_top[threadIdx.x] = ok ? static_cast<int>(max(0ll, n_free - 1 - need)) : -1;
+        const int c_end = static_cast<int>(min(row_base + rows, max_rows));
+        if (threadIdx.x == 0) s_start[nt] = c_end;
+        if (blockIdx.x == 0 && b < batch) {
+            if (b == 0) ck.start[0] = 0;
+            ck.start[b + 1] = static_cast<int>(min(row + s.n, max_rows));
+            bad_flags |= s.flags;
+        }
+        __syncthreads();
+        const int lo = max(r0, static_cast<int>(min(row_base, max_rows)));
+        const int hi = min(r1, c_end);
+        for (int t = lo + threadIdx.x; t < hi; t += nt) {
+            // the last sequence of the pass that starts at or before row t
+            int i = 0;
+            for (int step = nt >> 1; step > 0; step >>= 1)
+                if (s_start[i + step] <= t) i += step;
+            const int q = b0 + i;
+            int pos = -1, slot = -1;
+            if (s_top[i] >= 0) {
+                pos = s_ctx[i] + (t - s_start[i]);
+                const int pg = pos / kPage;
+                int32_t* entry = pool.block_table + (int64_t)q * pool.max_pages_per_seq + pg;
+                const int fresh = pg - s_held[i];
+                int phys = fresh < 0 ? *entry : pool.free_pages[s_top[i] - fresh];
+                if (phys < 0 || phys >= pool.num_pages) {
+                    bad_flags |= SE_DEV_BAD_INDEX;
+                    phys = -1;
+                }
+                if (fresh >= 0 && (pos % kPage == 0)) *entry = phys;
+                if (phys >= 0) slot = phys * kPage + pos % kPage;
+            }
+            ck.seq[t] = q;
+            ck.pos[t] = pos;
+            ck.slot[t] = slot;
+        }
+        row_base += rows;
+        need_base += needs;
+        __syncthreads();
+    }
+    const int live = static_cast<int>(min(row_base, max_rows));
+    if (blockIdx.x == 0 && batch == 0 && threadIdx.x == 0) ck.start[0] = 0;
+    for (int t = max(r0, live) + threadIdx.x; t < r1; t += nt) {
+        ck.seq[t] = -1;
+        ck.pos[t] = -1;
+        ck.slot[t] = -1;
+    }
+    if (bad_flags) flag(status, bad_flags);
+    if (!last_block(ws + kCounterWord)) return;
+    // commit: the same scan, now storing what each served sequence holds
+    long long taken = 0;
+    row_base = need_base = 0;
+    for (int b0 = 0; b0 < batch; b0 += nt) {
+        const int b = b0 + threadIdx.x;
+        SeqPlan s = {};
+        if (b < batch) s = seq_plan(pool, new_len, b);
+        long long row = s.n, need = s.need, rows = 0, needs = 0;
+        block_scan2(row, need, tmp, &rows, &needs);
+        const bool ok = s.ok && row_base + row + s.n <= max_rows && s.need > 0 &&
+                        need_base + need + s.need <= n_free;
+        if (ok) pool.n_pages[b] = s.held + s.need;
+        long long got = ok ? s.need : 0, none = 0, gots = 0, nones = 0;
+        block_scan2(got, none, tmp, &gots, &nones);
+        taken += gots;
+        row_base += rows;
+        need_base += needs;
+    }
+    if (threadIdx.x == 0) {
+        *pool.n_free = n_free - static_cast<int>(taken);
+        ws[kCounterWord] = 0;
+    }
+}
+
+// Pages of the flagged sequences back onto the stack: i-th released page (in
+// sequence order) to the i-th place below the new top.  Every block scans all
+// sequences and copies its share of the pages; the last block to finish
+// clears the lengths and moves the top.
+__global__ void __launch_bounds__(1024)
+    pages_release_kernel(se_page_pool pool, const int32_t* done, int batch, int* ws) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ int smem[];
+    const int nt = blockDim.x;
+    long long* s_first = reinterpret_cast<long long*>(smem);    // [nt + 1]
+    __shared__ long long tmp[66];
+    int* status = ws;
+    int bad_flags = 0;
+    int n_free = *pool.n_free;
+    if (n_free < 0 || n_free > pool.num_pages) {
+        bad_flags |= SE_DEV_BAD_LENGTH;
+        n_free = n_free < 0 ? 0 : pool.num_pages;
+    }
+    auto held_of = [&](int b) -> long long {
+        if (b >= batch || done[b] == 0) return 0;
+        const int n = pool.n_pages[b];
+        if (n < 0 || n > pool.max_pages_per_seq) {
+            bad_flags |= SE_DEV_BAD_LENGTH;
+            return n < 0 ? 0 : pool.max_pages_per_seq;
+        }
+        return n;
+    };
+    long long total = 0;
+    for (int b0 = 0; b0 < batch; b0 += nt) {
+        long long held = held_of(b0 + threadIdx.x), none = 0, sum = 0, nones = 0;
+        block_scan2(held, none, tmp, &sum, &nones);
+        total += sum;
+    }
+    const bool fits = n_free + total <= pool.num_pages;
+    if (!fits) bad_flags |= SE_DEV_CAPACITY;
+    long long base = 0;
+    for (int b0 = 0; fits && b0 < batch; b0 += nt) {
+        long long first = held_of(b0 + threadIdx.x), none = 0, sum = 0, nones = 0;
+        block_scan2(first, none, tmp, &sum, &nones);
+        s_first[threadIdx.x] = first;
+        if (threadIdx.x == 0) s_first[nt] = sum;
+        __syncthreads();
+        for (long long i = (long long)blockIdx.x * nt + threadIdx.x; i < sum;
+             i += (long long)gridDim.x * nt) {
+            int k = 0;
+            for (int step = nt >> 1; step > 0; step >>= 1)
+                if (s_first[k + step] <= i) k += step;
+            const int pg = static_cast<int>(i - s_first[k]);
+            pool.free_pages[n_free + total - 1 - (base + i)] =
+                pool.block_table[(int64_t)(b0 + k) * pool.max_pages_per_seq + pg];
+        }
+        base += sum;
+        __syncthreads();
+    }
+    if (bad_flags) flag(status, bad_flags);
+    if (!last_block(ws + kCounterWord)) return;
+    if (fits) {
+        for (int b = threadIdx.x; b < batch; b += nt) {
+            if (done[b] == 0) continue;
+            pool.n_pages[b] = 0;
+            pool.ctx_len[b] = 0;
+        }
+        if (threadIdx.x == 0) *pool.n_free = n_free + static_cast<int>(total);
+    }
+    if (threadIdx.x == 0) ws[kCounterWord] = 0;
+}
+
+// Append of packed rows.  Block i looks at rows [16i, 16i + 16); a run of rows
+// that lie one after another in one page is a piece (at most 16 rows), the work of one
+// warp for one KV head, which owns that page's summary while it works: no
+// atomics and a fixed result.  Each warp finds the pieces that begin in the block
+// from the slots of 32 rows around it (ballots).  A row is D/8 16-byte vectors, so
+// RP rows move side by side; all loads of a piece are in flight before the
+// first store.  HBM bound for long chunks (each byte read once and written once),
+// latency bound for a few rows.
+template <int D>
+__global__ void __launch_bounds__(128)
+    kv_append_chunk_kernel(se_paged_kv kv, const uint4* k_new, const uint4* v_new,
+                           int64_t row_stride, se_chunk ck, int batch, int* status) {
+    constexpr int SEGS = D / 8, RP = 32 / SEGS, IT = kPage / RP;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int H = kv.num_kv_heads;
+    // lane l looks at row 16i - 1 + l
+    const int t = static_cast<int>(blockIdx.x) * kPage - 1 + lane;
+    int slot = -1, pos = -1, seq = -1;
+    if (t >= 0 && t < ck.max_tokens) {
+        slot = ck.slot[t];
+        pos = ck.pos[t];
+        seq = ck.seq[t];
+        if (slot != -1 &&
+            (slot < 0 || slot / kPage >= kv.num_pages || seq < 0 || seq >= batch || pos < 0 ||
+             pos / kPage >= kv.max_pages_per_seq || pos % kPage != slot % kPage)) {
+            if (lane >= 1 && lane <= kPage && warp == 0) flag(status, SE_DEV_BAD_INDEX);
+            slot = -1;
+        }
+    }
+    const bool valid = slot >= 0;
+    const int pslot = __shfl_up_sync(0xffffffffu, slot, 1);
+    const int pseq = __shfl_up_sync(0xffffffffu, seq, 1);
+    const int ppos = __shfl_up_sync(0xffffffffu, pos, 1);
+    const bool cont = valid && lane > 0 && pslot >= 0 && pseq == seq && ppos + 1 == pos &&
+                      pslot + 1 == slot && pos % kPage != 0;
+    const uint32_t cont_m = __ballot_sync(0xffffffffu, cont);
+    const uint32_t lead_m = __ballot_sync(0xffffffffu, valid && !cont) & 0x1fffeu;
+    const int nseq = __shfl_down_sync(0xffffffffu, valid ? seq : -1, 1);
+    if (warp == 0 && blockIdx.y == 0 && valid && lane >= 1 && lane <= kPage && nseq != seq)
+        kv.ctx_len[seq] = pos + 1;
+    const int seg = lane % SEGS, rp = lane / SEGS;
+    uint4* K = static_cast<uint4*>(kv.k);
+    uint4* V = static_cast<uint4*>(kv.v);
+    uint4* M = static_cast<uint4*>(kv.meta);
+    const int units = __popc(lead_m) * H;
+    const int nw = (blockDim.x >> 5) * gridDim.y;
+    for (int u = warp + (blockDim.x >> 5) * blockIdx.y; u < units; u += nw) {
+        const int h = u % H;
+        uint32_t rest = lead_m;
+        for (int i = u / H; i > 0; --i) rest &= rest - 1;
+        const int f = __ffs(rest) - 1;                              // lane of the piece's first row
+        const int len = min(kPage, 1 + __ffs(~(cont_m >> (f + 1))) - 1);
+        const int slot0 = __shfl_sync(0xffffffffu, slot, f);
+        const int pos0 = __shfl_sync(0xffffffffu, pos, f);
+        const int seq0 = __shfl_sync(0xffffffffu, seq, f);
+        const int64_t src = (int64_t)(static_cast<int>(blockIdx.x) * kPage - 1 + f) * row_stride +
+                            h * SEGS + seg;
+        uint4 k[IT], v[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = i * RP + rp;
+            if (r < len) {
+                k[i] = k_new[src + r * row_stride];
+                v[i] = v_new[src + r * row_stride];
+            }
+        }
+        const int64_t m0 =
+            ((((int64_t)seq0 * kv.max_pages_per_seq + pos0 / kPage) * H + h) * 2) * SEGS + seg;
+        const bool fold = pos0 % kPage != 0;
+        uint4 old_mn = make_uint4(0, 0, 0, 0), old_mx = old_mn;
+        if (M != nullptr && fold && rp == 0) {
+            old_mn = M[m0];
+            old_mx = M[m0 + SEGS];
+        }
+        const int64_t dst =
+            (((int64_t)(slot0 / kPage) * H + h) * kPage + slot0 % kPage) * SEGS + seg;
+        Bf8 mn, mx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            mn.x[e] = INFINITY;
+            mx.x[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = i * RP + rp;
+            if (r < len) {
+                K[dst + r * SEGS] = k[i];
+                V[dst + r * SEGS] = v[i];
+                const Bf8 x = unpack8(k[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    mn.x[e] = fminf(mn.x[e], x.x[e]);
+                    mx.x[e] = fmaxf(mx.x[e], x.x[e]);
+                }
+            }
+        }
+        if (M == nullptr) continue;
+#pragma unroll
+        for (int o = SEGS; o < 32; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                mn.x[e] = fminf(mn.x[e], __shfl_xor_sync(0xffffffffu, mn.x[e], o));
+                mx.x[e] = fmaxf(mx.x[e], __shfl_xor_sync(0xffffffffu, mx.x[e], o));
+            }
+        if (rp == 0) {
+            if (fold) {
+                const Bf8 a = unpack8(old_mn), c = unpack8(old_mx);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    mn.x[e] = fminf(a.x[e], mn.x[e]);
+                    mx.x[e] = fmaxf(c.x[e], mx.x[e]);
+                }
+            }
+            M[m0] = pack8(mn);
+            M[m0 + SEGS] = pack8(mx);
+        }
+    }
+}
+
+}  // namespace
+
+size_t page_pool_ws_bytes() { return 512; }
+
+cudaError_t launch_chunk_plan(const se_page_pool& pool, const int32_t* new_len, int batch,
+                              const se_chunk& ck, int* ws, cudaStream_t s) {
+    const int nt = batch > 256 ? 1024 : 256;
+    const int grid = max(1, min(num_sms(), (ck.max_tokens + 4 * nt - 1) / (4 * nt)));
+    const int per = (ck.max_tokens + grid - 1) / grid;
+    return launch_pdl(chunk_plan_kernel, dim3(grid), dim3(nt), (4 * nt + 1) * sizeof(int), s, pool,
+                      new_len, batch, ck, per, ws);
+}
+
+cudaError_t launch_pages_release(const se_page_pool& pool, const int32_t* done, int batch, int* ws,
+                                 cudaStream_t s) {
+    const int nt = batch > 256 ? 1024 : 256;
+    // a block for every 4096 table entries that could be released
+    const int64_t most = std::min<int64_t>((int64_t)batch * pool.max_pages_per_seq, pool.num_pages);
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms(), most / 4096)));
+    return launch_pdl(pages_release_kernel, dim3(grid), dim3(nt), (nt + 1) * sizeof(long long), s,
+                      pool, done, batch, ws);
+}
+
+cudaError_t launch_kv_append_chunk(const se_paged_kv& kv, const void* k_new, const void* v_new,
+                                   int64_t row_stride, const se_chunk& ck, int batch, int* status,
+                                   cudaStream_t s) {
+    const int blocks = (ck.max_tokens + kPage - 1) / kPage;
+    if (blocks == 0) return cudaSuccess;
+    // few rows: more blocks share one group of 16, down to one piece a warp
+    // (16 pieces x the heads, four warps a block)
+    const int share = std::max(1, std::min(4 * num_sms() / blocks, 4 * kv.num_kv_heads));
+    const dim3 grid(blocks, share);
+    const uint4* k = static_cast<const uint4*>(k_new);
+    const uint4* v = static_cast<const uint4*>(v_new);
+    if (kv.head_dim == 128)
+        return launch_pdl(kv_append_chunk_kernel<128>, grid, dim3(128), 0, s, kv, k, v,
+                          row_stride / 8, ck, batch, status);
+    return launch_pdl(kv_append_chunk_kernel<64>, grid, dim3(128), 0, s, kv, k, v, row_stride / 8,
+                      ck, batch, status);
+}
+
+}  // namespace se

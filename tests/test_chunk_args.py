@@ -1,0 +1,129 @@
+"""The chunk operators' argument checks (all on the host, before any CUDA call)."""
+import ctypes
+
+import pytest
+import torch
+
+from kv_cache_decode_quest_gb300 import binding, build
+
+FAKE = 1 << 20                      # never dereferenced: validation fails first
+P = ctypes.c_void_p(FAKE)
+INVALID, UNSUPPORTED, WORKSPACE = -1, -2, -3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+def pool(**kw):
+    c = binding.PagePoolC(FAKE, FAKE, FAKE, FAKE, FAKE, 10, 4)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def chunk(**kw):
+    c = binding.ChunkC(FAKE, FAKE, FAKE, FAKE, 32)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+def paged(**kw):
+    c = binding.PagedKVC(FAKE, FAKE, None, FAKE, FAKE, 10, 4, 4, 128, 16)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return ctypes.byref(c)
+
+
+BAD_POOLS = [dict(free_pages=None), dict(n_free=None), dict(n_pages=None), dict(block_table=None),
+             dict(ctx_len=None), dict(num_pages=0), dict(max_pages_per_seq=0)]
+
+
+def test_plan(lib):
+    def call(p=pool(), new=P, batch=2, c=chunk(), ws=P, nbytes=512):
+        return lib.se_chunk_plan(p, new, batch, c, ws, nbytes, None)
+    for bad in BAD_POOLS:
+        assert call(p=pool(**bad)) == INVALID, bad
+    assert call(p=pool(num_pages=1 << 28)) == UNSUPPORTED
+    assert call(p=pool(max_pages_per_seq=1 << 28)) == UNSUPPORTED
+    assert call(p=None) == INVALID and call(c=None) == INVALID and call(new=None) == INVALID
+    for bad in (dict(start=None), dict(seq=None), dict(pos=None), dict(slot=None),
+                dict(max_tokens=-1)):
+        assert call(c=chunk(**bad)) == INVALID, bad
+    assert call(c=chunk(max_tokens=(1 << 24) + 1)) == UNSUPPORTED
+    assert call(batch=-1) == INVALID
+    assert call(ws=None) == WORKSPACE and call(nbytes=256) == WORKSPACE
+    assert call(ws=ctypes.c_void_p(FAKE + 16)) == WORKSPACE
+    assert lib.se_page_pool_workspace(1) == 512 and lib.se_page_pool_workspace(-1) == 0
+
+
+def test_release(lib):
+    def call(p=pool(), done=P, batch=2, ws=P, nbytes=512):
+        return lib.se_pages_release(p, done, batch, ws, nbytes, None)
+    for bad in BAD_POOLS:
+        assert call(p=pool(**bad)) == INVALID, bad
+    assert call(done=None) == INVALID and call(batch=-1) == INVALID
+    assert call(ws=None) == WORKSPACE and call(nbytes=511) == WORKSPACE
+    assert call(done=None, batch=0) == 0
+
+
+def test_append(lib):
+    def call(kv=paged(), k=P, v=P, stride=0, c=chunk(), batch=2, ws=P, nbytes=256):
+        return lib.se_kv_append_chunk(kv, k, v, stride, c, batch, ws, nbytes, None)
+    assert call(kv=paged(k=None)) == INVALID and call(kv=paged(block_table=None)) == INVALID
+    assert call(kv=paged(head_dim=96)) == UNSUPPORTED and call(kv=paged(page_size=8)) == UNSUPPORTED
+    assert call(k=None) == INVALID and call(v=None) == INVALID
+    assert call(k=ctypes.c_void_p(FAKE + 8)) == INVALID
+    assert call(v=ctypes.c_void_p(FAKE + 8)) == INVALID
+    assert call(stride=511) == INVALID and call(stride=516) == INVALID and call(stride=-512) == INVALID
+    assert call(batch=-1) == INVALID and call(c=chunk(seq=None)) == INVALID
+    assert call(ws=None) == WORKSPACE and call(nbytes=255) == WORKSPACE
+    assert call(k=None, v=None, batch=0) == 0
+    assert call(k=None, v=None, c=chunk(max_tokens=0, seq=None, pos=None, slot=None)) == 0
+
+
+def test_attn(lib):
+    need = lib.se_chunk_attn_workspace(2, 32, 4, 32, 128)
+    assert need >= 256 and need % 256 == 0
+
+    def opts(**kw):
+        o = binding.ChunkAttnOptsC(0, 0, 0, 0, None, None)
+        for k, v in kw.items():
+            setattr(o, k, v)
+        return ctypes.byref(o)
+
+    def call(kv=paged(), q=P, c=chunk(), batch=2, hq=32, scale=0.1, o=None, out=P, ws=P,
+             nbytes=need):
+        return lib.se_chunk_attn(kv, q, c, batch, hq, scale, o, out, None, ws, nbytes, None)
+    assert call(kv=paged(v=None)) == INVALID and call(kv=paged(ctx_len=None)) == INVALID
+    assert call(kv=paged(head_dim=80)) == UNSUPPORTED and call(kv=paged(page_size=32)) == UNSUPPORTED
+    assert call(kv=paged(max_pages_per_seq=1 << 28)) == UNSUPPORTED
+    assert call(hq=12) == UNSUPPORTED and call(hq=30) == UNSUPPORTED and call(hq=0) == INVALID
+    assert call(q=None) == INVALID and call(out=None) == INVALID and call(c=None) == INVALID
+    assert call(q=ctypes.c_void_p(FAKE + 2)) == INVALID
+    assert call(out=ctypes.c_void_p(FAKE + 8)) == INVALID
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        assert call(scale=bad) == INVALID
+    for bad in (dict(out_dtype=2), dict(window=-1), dict(sink=-1), dict(q_stride=4088),
+                dict(q_stride=4100), dict(q_stride=-4096)):
+        assert call(o=opts(**bad)) == INVALID, bad
+    assert call(c=chunk(max_tokens=(1 << 24) + 1)) == UNSUPPORTED
+    assert call(batch=-1) == INVALID
+    assert call(ws=None) == WORKSPACE and call(nbytes=need - 1) == WORKSPACE
+    assert call(q=None, out=None, batch=0) == 0
+    assert call(q=None, out=None, c=chunk(max_tokens=0, seq=None, pos=None, slot=None)) == 0
+    for bad in ((-1, 32, 4, 32, 128), (1, -1, 4, 32, 128), (1, 32, 0, 32, 128), (1, 32, 4, 30, 128),
+                (1, 32, 4, 32, 96), (1, 32, 4, 12, 128), (1, (1 << 24) + 1, 4, 32, 128)):
+        assert lib.se_chunk_attn_workspace(*bad) == 0, bad
+
+
+def test_binding_refuses_layouts_it_cannot_pass(lib):
+    x = torch.zeros(4, 4, 128, dtype=torch.bfloat16)
+    assert binding._token_stride(x, "x") == 512
+    assert binding._token_stride(torch.zeros(4, 12, 128)[:, 4:8], "x") == 1536
+    for bad in (x.transpose(1, 2), x[:, :, ::2], x[:, ::2], x.view(16, 128)):
+        with pytest.raises(binding.SparseEngineError):
+            binding._token_stride(bad, "x")
