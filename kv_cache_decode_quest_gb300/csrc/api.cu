@@ -35,7 +35,8 @@ int num_sms() {
     return v;
 }
 
-bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int head_dim) {
+namespace {
+bool have_encode() {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -44,12 +45,34 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int head_
             q == cudaDriverEntryPointSuccess)
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     });
-    if (!g_encode || rows <= 0) return false;
+    return g_encode != nullptr;
+}
+}  // namespace
+
+bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int head_dim) {
+    if (!have_encode() || rows <= 0) return false;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(rows)};
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(head_dim) * 2};
     const cuuint32_t box[2] = {64, 16};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base),
+                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool encode_heads_map(CUtensorMap* map, const void* base, int tokens, int heads, int64_t stride,
+                      int group, int head_dim) {
+    if (!have_encode() || tokens <= 0) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(heads),
+                                static_cast<cuuint64_t>(tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                                   static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group),
+                               static_cast<cuuint32_t>(128 / group)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
                                 dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -104,6 +127,7 @@ int check_pool(const se_page_pool* p) {
 }
 
 constexpr int kMaxChunkTokens = 1 << 24;
+constexpr int kMaxChunkPages = 1 << 26;      // of a sequence: positions stay below 2^30
 
 int check_chunk(const se_chunk* c) {
     if (!c || !c->start || c->max_tokens < 0) return SE_ERR_INVALID_ARG;
@@ -244,7 +268,8 @@ int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, i
     if (o.out_dtype != 0 && o.out_dtype != 1) return SE_ERR_INVALID_ARG;
     if (o.window < 0 || o.sink < 0) return SE_ERR_INVALID_ARG;
     if (o.q_stride < row || o.q_stride % 8) return SE_ERR_INVALID_ARG;
-    if (kv->max_pages_per_seq > INT32_MAX / SE_PAGE_SIZE) return SE_ERR_UNSUPPORTED;
+    if (kv->max_pages_per_seq > kMaxChunkPages || batch > chunk_attn_max_batch())
+        return SE_ERR_UNSUPPORTED;
     if (batch == 0 || chunk->max_tokens == 0) return SE_OK;
     if (!q || !out || !aligned(q, 16) || !aligned(out, 16)) return SE_ERR_INVALID_ARG;
     if ((rc = check_ws(ws, ws_bytes,

@@ -1,10 +1,34 @@
-// Attention of a chunk of new tokens over a paged cache (se_chunk_attn).
+// Attention of a chunk of new tokens over a paged cache (se_chunk_attn), on the
+// 5th-generation tensor cores.
 //
 // Rows (token, query head of the KV head's group) of one (sequence, KV head)
-// share its keys; 16 rows at a time walk the keys page by page with a running
-// maximum and sum (online softmax, fp32): per page, 16 x 16 scores, then
-// O <- O * exp(m_old - m_new) + P V.
+// share its keys.  A block is up to 256 such rows; it walks its keys in tiles of
+// 128 (8 pages):  S = Q K^T,  m' = max(m, rowmax S),  P = exp2(S' - m'),
+// l <- l exp2(m - m') + rowsum P,  O <- O exp2(m - m') + P V,  out = O / l, with S'
+// the logits scaled by log2 e.  Every running value is fp32; P is rounded to
+// bf16 for the product with V (bf16 output: the result is rounded as coarsely
+// anyway) or split into two bf16 terms (fp32 output: 16 mantissa bits).
+//
+// One resident CTA per SM takes an equal share of all key tiles of all blocks
+// (a share may begin and end inside a block's keys), found from the lengths on the
+// device, so there is no plan kernel and no host knowledge of lengths.  Warp roles:
+//   producer  block-table look-ups, TMA copies of Q, and of K and V pages into a
+//             ring of tiles (128-byte swizzle)
+//   MMA       one thread issues tcgen05.mma: S into tensor memory, P V with P read
+//             from tensor memory (it replaces S in place)
+//   softmax   two groups of four warps, one thread per row
+// A block of more than 128 rows gives each softmax group its own 128 rows and both use
+// each tile; a smaller one (short chunks, single tokens) gives them alternate
+// tiles of the same rows, joined at the end through tensor memory.  While one group
+// computes its exponentials, the tensor cores work for the other.  O stays in
+// tensor memory and is rescaled only when a row's maximum has grown by more than
+// 2^8 (the true maximum is not needed: any reference within 2^8 keeps P and l
+// far from overflow, and the same one divides out).
+// A block cut between CTAs is joined by the last of them to finish, in the
+// order of its keys (the result does not depend on timing).
 #include <algorithm>
+
+#include "cudaTypedefs.h"
 
 #include "common.cuh"
 #include "internal.h"
@@ -12,150 +36,877 @@
 namespace se {
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kBlockRows = 256;                    // rows of a block: two accumulators of 128
+constexpr int kKeys = 128;                         // keys of a tile
+constexpr int kTilePages = kKeys / kPage;
+constexpr int kSoftWarps = 8;
+constexpr int kThreads = (kSoftWarps + 2) * 32;    // + producer + MMA
+constexpr int kItems = 4;                          // work items in flight between the roles
+constexpr int kMaxCtas = 256;
+constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescale = 8.f;                    // log2 of the growth that rescales O
+
+// Workspace: status word, at byte 256 the arrival counters [kMaxCtas][2], then
+// the partial results: two pieces per CTA (the one it takes over and the one it hands
+// on), each [2 groups][128] (reference, sum) and [2][128][D] fp32.
+constexpr size_t kCounterOff = 256;
+constexpr size_t kPartOff = kCounterOff + kMaxCtas * 2 * sizeof(int);
+
+template <int D>
+struct Shape {
+    static constexpr int kHalves = D / 64;                  // 64-column regions
+    static constexpr int kRegion = 128 * 128;               // 128 rows of 128 bytes
+    static constexpr int kTile = kHalves * kRegion;         // 128 rows of Q, K or V
+    static constexpr int kStages = D == 128 ? 5 : 10;
+    static constexpr size_t kCtrl = 3072;
+    static constexpr size_t kSmem = (size_t)(2 + kStages) * kTile + kCtrl;
+};
+
+struct Item {
+    int b, h;
+    int tok0;          // packed row of the block's first token
+    int rows;          // rows of the block (tokens * G)
+    int pos0;          // position of the block's first token
+    int len;           // tokens held
+    int ts, tl;        // tile j is key tile j (j < ts), else j - ts + tl
+    int j0, n;         // this piece: tiles [j0, j0 + n); n = 0: no more work
+    int split;         // the block is cut: this piece is partial
+    int c0, c1;        // CTAs that share the block
+};
 
 struct Params {
     se_paged_kv kv;
     se_chunk ck;
-    int batch;
-    ChunkAttnArgs a;
-    int* status;
+    int batch, G, Hq;
+    int max_blocks;                // blocks numbered at most
+    int window, sink;
+    float scale_log2;              // > 0
+    uint32_t negate;               // instruction descriptor bit for a negative scale
+    int out_f32;
+    void* out;
+    float* lse;
+    uint8_t* ws;
 };
 
-__device__ __forceinline__ int chunk_start(const Params& p, int b, bool& bad) {
-    const int s = p.ck.start[b];
-    if (s < 0 || s > p.ck.max_tokens) bad = true;
-    return min(max(s, 0), p.ck.max_tokens);
+struct Seq {
+    int s0, n, p0, len;            // first packed row, new tokens, first position, tokens held
+};
+
+__device__ __forceinline__ Seq seq_info(const Params& p, int b, int& bad) {
+    int s0 = p.ck.start[b], s1 = p.ck.start[b + 1];
+    int len = p.kv.ctx_len[b];
+    if (s0 < 0 || s0 > p.ck.max_tokens || s1 < s0 || s1 > p.ck.max_tokens) bad |= SE_DEV_BAD_LENGTH;
+    s0 = min(max(s0, 0), p.ck.max_tokens);
+    s1 = min(max(s1, 0), p.ck.max_tokens);
+    const int cap = p.kv.max_pages_per_seq * kPage;
+    if (len < 0 || len > cap) bad |= SE_DEV_BAD_LENGTH;
+    Seq s;
+    s.s0 = s0;
+    s.n = max(0, s1 - s0);
+    s.len = min(max(len, 0), cap);
+    s.p0 = s.n > 0 ? p.ck.pos[s0] : 0;
+    if (s.p0 < 0) {                 // no page was found for the chunk: its rows see nothing
+        s.p0 = 0;
+        s.len = 0;
+    } else {
+        s.p0 = min(s.p0, cap);
+        if (s.n > 0 && s.p0 + s.n > s.len) bad |= SE_DEV_BAD_LENGTH;
+    }
+    return s;
 }
 
-// Row blocks of sequence b are numbered from floor(start[b] * G / 16) + b on:
-// each sequence has at most as many as the next one's first number leaves.
-template <int D>
-__global__ void __launch_bounds__(128) chunk_attn_simple_kernel(const Params p) {
-    constexpr int DT = D / 8;                       // head_dim elements per thread
-    __shared__ float qs[kRows][D + 1], ks[kPage][D + 1], vs[kPage][D], ps[kRows][kPage];
-    const int H = p.kv.num_kv_heads, G = p.a.Hq / H;
-    const int h = blockIdx.y;
-    bool bad = false;
-    int lo = 0, hi = p.batch;                        // last b whose first number is <= blockIdx.x
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        const long long first = (long long)chunk_start(p, mid, bad) * G / kRows + mid;
-        if (first <= (long long)blockIdx.x) lo = mid;
-        else hi = mid;
+// Blocks of sequence b are numbered from floor(start[b] * G / 256) + b on: each
+// sequence has at most as many as the next one's first number leaves, and no
+// scan over the sequences is needed.
+__device__ __forceinline__ int first_block(int s0, int G, int b) { return s0 * G / kBlockRows + b; }
+
+// Key tiles that block blk of a sequence looks at (at least one: a block that sees
+// nothing has one tile, all of it masked).
+struct Tiles {
+    int rows, ts, tl, n;
+};
+__device__ __forceinline__ Tiles block_tiles(const Params& p, const Seq& s, int blk) {
+    Tiles t = {0, 0, 0, 0};
+    const int row0 = blk * kBlockRows;
+    t.rows = min(kBlockRows, s.n * p.G - row0);
+    if (blk < 0 || t.rows <= 0) return t;
+    const int tok = row0 / p.G;
+    const int p_lo = s.p0 + tok;
+    const int keys = min(p_lo + (t.rows + p.G - 1) / p.G, s.len);     // keys below this are seen
+    const int th = (keys + kKeys - 1) / kKeys;
+    if (p.window > 0) {
+        t.tl = min(max(0, p_lo - p.window + 1) / kKeys, th);
+        t.ts = min(p.sink / kKeys + (p.sink % kKeys != 0), t.tl);
     }
-    const int b = lo;
-    const int s0 = chunk_start(p, b, bad), s1 = chunk_start(p, b + 1, bad);
-    if (s1 < s0) bad = true;
-    const long long blk = (long long)blockIdx.x - ((long long)s0 * G / kRows + b);
-    const long long row0 = blk * kRows, rows = (long long)max(0, s1 - s0) * G;
-    const int cap = p.kv.max_pages_per_seq * kPage;
-    int L = p.kv.ctx_len[b];
-    if (L < 0 || L > cap) {
-        bad = true;
-        L = L < 0 ? 0 : cap;
-    }
-    if (bad && threadIdx.x == 0) flag(p.status, SE_DEV_BAD_LENGTH);
-    if (blk < 0 || row0 >= rows) return;
-    const int p0 = p.ck.pos[s0];
-    const int r = threadIdx.x / 8, c = threadIdx.x % 8;
-    const uint16_t* Q = static_cast<const uint16_t*>(p.a.q);
-    for (int i = threadIdx.x; i < kRows * D; i += blockDim.x) {
-        const long long row = min(row0 + i / D, rows - 1);
-        const int64_t t = s0 + row / G;
-        qs[i / D][i % D] = __uint_as_float(
-            (uint32_t)Q[t * p.a.q_stride + (h * G + row % G) * D + i % D] << 16);
-    }
-    const long long my = min(row0 + r, rows - 1);
-    const int pos = p0 < 0 ? -1 : p0 + static_cast<int>(my / G);
-    if (pos >= L && p0 >= 0 && c == 0) flag(p.status, SE_DEV_BAD_LENGTH);
-    float m = -INFINITY, l = 0.f, o[DT];
-#pragma unroll
-    for (int i = 0; i < DT; ++i) o[i] = 0.f;
-    const int last = p0 < 0 ? -1 : p0 + static_cast<int>(min(row0 + kRows - 1, rows - 1) / G);
-    const int keys = min(L, last + 1);
-    const int first_pos = p0 < 0 ? -1 : p0 + static_cast<int>(row0 / G);
-    for (int pg = 0; pg * kPage < keys; ++pg) {
-        // pages that no row of the block sees
-        if (p.a.window && pg * kPage >= p.a.sink && pg * kPage + kPage - 1 <= first_pos - p.a.window)
-            continue;
-        const int phys = p.kv.block_table[(int64_t)b * p.kv.max_pages_per_seq + pg];
-        if (phys < 0 || phys >= p.kv.num_pages) {
-            if (threadIdx.x == 0) flag(p.status, SE_DEV_BAD_INDEX);
-            continue;
+    t.n = max(1, t.ts + th - t.tl);
+    return t;
+}
+
+__device__ __forceinline__ int tile_of(const Item& it, int j) {
+    return j < it.ts ? j : j - it.ts + it.tl;
+}
+
+struct Ctrl {
+    uint64_t full[10], empty[10];
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t ml_full, ml_empty;            // the groups' (reference, sum) of a shared block
+    uint64_t part[2];                      // a group's partial rows are written
+    uint64_t item_full[kItems], item_empty[kItems];
+    uint64_t done;
+    uint32_t tmem;
+    int abort;
+    int last[2];
+    int any_absent;                        // a block-table entry named no page
+    Item items[kItems];
+    float2 ml[2][128];
+};
+
+// Warp-uniform bounded wait.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* c, int* status) {
+    bool ok = mbar_try_wait(bar, parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+        if (!ok) ok = mbar_wait(bar, parity, &c->abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && (threadIdx.x & 31) == 0) {
+            *static_cast<volatile int*>(&c->abort) = 1;
+            flag(status, SE_DEV_TIMEOUT);
         }
-        const int valid = min(kPage, L - pg * kPage);
-        const int64_t base = ((int64_t)phys * H + h) * kPage * D;
-        const uint16_t* K = static_cast<const uint16_t*>(p.kv.k) + base;
-        const uint16_t* V = static_cast<const uint16_t*>(p.kv.v) + base;
+    }
+    return ok;
+}
+
+// Low n bits set (n clamped to [0, 32]).
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_attn_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+                      const __grid_constant__ CUtensorMap tv, const Params p) {
+    using S = Shape<D>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* qs = smem;                                  // [2][kTile]
+    uint8_t* ring = smem + 2 * S::kTile;                 // [kStages][kTile]
+    Ctrl* c = reinterpret_cast<Ctrl*>(ring + S::kStages * S::kTile);
+    static_assert(sizeof(Ctrl) <= S::kCtrl, "control block");
+    static_assert((size_t)kMaxBatch * 20 + 1024 <= S::kSmem - S::kCtrl, "lengths fit beside");
+    int* status = reinterpret_cast<int*>(p.ws);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int H = p.kv.num_kv_heads, G = p.G;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::kStages; ++s) {
+            mbar_init(&c->full[s], 1);
+            mbar_init(&c->empty[s], 1);
+        }
+        mbar_init(&c->q_full, 1);
+        mbar_init(&c->q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->s_full[i], 1);
+            mbar_init(&c->p_full[i], 4);
+            mbar_init(&c->o_done[i], 1);
+            mbar_init(&c->part[i], 4);
+        }
+        mbar_init(&c->ml_full, kSoftWarps);
+        mbar_init(&c->ml_empty, kSoftWarps);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(&c->item_full[i], 1);
+            mbar_init(&c->item_empty[i], kSoftWarps + 1);
+        }
+        mbar_init(&c->done, 1);
+        c->abort = 0;
+        c->any_absent = 0;
+        fence_barrier_init();
+    }
+    if (warp == kSoftWarps + 1) tmem_alloc(&c->tmem, 512);
+    pdl_wait();
+    pdl_trigger();
+
+    // ---- this CTA's share (the lengths are staged where Q and the ring will be) ----
+    long long* sums = reinterpret_cast<long long*>(smem);
+    Seq* seqs = reinterpret_cast<Seq*>(smem + 1024);
+    int* firsts = reinterpret_cast<int*>(smem + 1024 + (size_t)kMaxBatch * sizeof(Seq));
+    __syncthreads();
+    {
+        int bad = 0;
+        for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+            const Seq s = seq_info(p, b, bad);
+            seqs[b] = s;
+            firsts[b] = first_block(s.s0, G, b);
+        }
+        if (bad && blockIdx.x == 0) flag(status, bad);
+    }
+    __syncthreads();
+    auto find_seq = [&](int x) {                     // last sequence whose first number is <= x
+        int lo = 0, hi = p.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (firsts[mid] <= x) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+    // exclusive prefix of `v` over the threads; total in *sum
+    auto scan = [&](int v, long long* sum) -> long long {
+        int x = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
         __syncthreads();
-        for (int i = threadIdx.x; i < kPage * D; i += blockDim.x) {
-            ks[i / D][i % D] = __uint_as_float((uint32_t)K[i] << 16);
-            vs[i / D][i % D] = i / D < valid ? __uint_as_float((uint32_t)V[i] << 16) : 0.f;
-        }
+        if (lane == 31) sums[warp] = x;
         __syncthreads();
-        float s2[2], mx = m;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int j = c + 8 * e, key = pg * kPage + j;
-            float x = 0.f;
-            for (int d = 0; d < D; ++d) x = fmaf(qs[r][d], ks[j][d], x);
-            const bool see = key <= pos && key < L &&
-                             (p.a.window == 0 || key > pos - p.a.window || key < p.a.sink);
-            s2[e] = see ? x * p.a.scale * kLog2e : -INFINITY;
-            mx = fmaxf(mx, s2[e]);
+        long long before = 0, all = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sums[w];
+            all += sums[w];
         }
-#pragma unroll
-        for (int w = 1; w < 8; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        const float corr = exp2f(m - ref);
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float w = exp2f(s2[e] - ref);
-            ps[r][c + 8 * e] = w;
-            sum += w;
-        }
-#pragma unroll
-        for (int w = 1; w < 8; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        l = l * corr + sum;
-        m = mx;
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < DT; ++i) {
-            float x = o[i] * corr;
-            for (int j = 0; j < kPage; ++j) x = fmaf(ps[r][j], vs[j][c + 8 * i], x);
-            o[i] = x;
-        }
-        __syncwarp();
+        *sum = all;
+        return before + x - v;
+    };
+    // units: tiles x heads, in the order (block, head, tile)
+    long long total = 0, mine = 0;
+    int nt = 0, my_b = 0;
+    const int passes = (p.max_blocks + kThreads - 1) / kThreads;
+    for (int i = 0; i < passes; ++i) {
+        const int x = i * kThreads + threadIdx.x;
+        my_b = find_seq(x);
+        nt = x < p.max_blocks ? block_tiles(p, seqs[my_b], x - firsts[my_b]).n : 0;
+        long long sum;
+        mine = scan(nt, &sum);
+        total += sum;
     }
-    if (row0 + r >= rows) return;
-    const int64_t t = s0 + my / G;
-    const int64_t oh = t * p.a.Hq + h * G + my % G;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll
-    for (int i = 0; i < DT; ++i) {
-        if (p.a.out_dtype == 1)
-            static_cast<float*>(p.a.out)[oh * D + c + 8 * i] = o[i] * inv;
-        else
-            static_cast<uint16_t*>(p.a.out)[oh * D + c + 8 * i] = to_bf16_bits(o[i] * inv);
+    // (no share is empty: a block's pieces are those of consecutive CTAs)
+    const long long U = total * H, NC = min((long long)gridDim.x, U);
+    const bool idle = blockIdx.x >= NC;
+    const long long u0 = idle ? 0 : U * blockIdx.x / NC, u1 = idle ? 0 : U * (blockIdx.x + 1) / NC;
+    long long* s_start = sums + 16;                  // first block, its prefix
+    if (u0 < u1) {
+        long long base = 0;
+        for (int i = 0; i < passes; ++i) {
+            const int x = i * kThreads + threadIdx.x;
+            long long sum;
+            if (passes > 1) {
+                my_b = find_seq(x);
+                nt = x < p.max_blocks ? block_tiles(p, seqs[my_b], x - firsts[my_b]).n : 0;
+                mine = scan(nt, &sum);
+            } else {
+                sum = total;
+            }
+            if ((base + mine) * H <= u0 && u0 < (base + mine + nt) * H) {
+                s_start[0] = my_b;
+                s_start[1] = x - firsts[my_b];
+                s_start[2] = base + mine;
+            }
+            base += sum;
+            if (base * H > u0) break;                // uniform
+        }
     }
-    if (p.a.lse && c == 0) p.a.lse[oh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    __syncthreads();
+    int b = 0, blk = 0;
+    long long pre = 0;
+    Seq win = {0, 0, 0, 0};                          // lane i: sequence b_win + i
+    int b_win = 0;
+    if (u0 < u1) {
+        b = static_cast<int>(s_start[0]);
+        blk = static_cast<int>(s_start[1]);
+        pre = s_start[2];
+        b_win = b;
+        if (b + lane < p.batch) win = seqs[b + lane];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c->tmem;
+
+    if (warp == kSoftWarps) {
+        // ------------------------------ producer ------------------------------
+        fence_proxy_async_smem();                    // the staged lengths are read: TMA may write
+        if (lane == 0) {
+            prefetch_tmap(&tq);
+            prefetch_tmap(&tk);
+            prefetch_tmap(&tv);
+        }
+        uint32_t seq = 0;                            // ring positions used
+        int items = 0, loads_q = 0;
+        long long u = u0;
+        int h = 0;
+        bool first = true, go = true;
+        while (go) {
+            // the next block with tiles
+            Seq s = {0, 0, 0, 0};
+            Tiles t = {0, 0, 0, 0};
+            if (u < u1) {
+                while (true) {
+                    if (b >= b_win + 32) {
+                        b_win = b;
+                        int bad = 0;
+                        if (b + lane < p.batch) win = seq_info(p, b + lane, bad);
+                    }
+                    const int src = b - b_win;
+                    s.s0 = __shfl_sync(0xffffffffu, win.s0, src);
+                    s.n = __shfl_sync(0xffffffffu, win.n, src);
+                    s.p0 = __shfl_sync(0xffffffffu, win.p0, src);
+                    s.len = __shfl_sync(0xffffffffu, win.len, src);
+                    t = block_tiles(p, s, blk);
+                    if (t.n > 0 || b + 1 >= p.batch) break;
+                    ++b;
+                    blk = 0;
+                }
+            }
+            Item it;
+            it.b = b;
+            it.n = 0;
+            if (u < u1 && t.n > 0) {
+                if (first) {
+                    h = static_cast<int>((u - pre * H) / t.n);
+                    first = false;
+                }
+                const long long us = (pre * H) + (long long)h * t.n;     // the item's first unit
+                it.h = h;
+                it.tok0 = s.s0 + blk * (kBlockRows / G);
+                it.rows = t.rows;
+                it.pos0 = s.p0 + blk * (kBlockRows / G);
+                it.len = s.len;
+                it.ts = t.ts;
+                it.tl = t.tl;
+                it.j0 = static_cast<int>(u - us);
+                it.n = static_cast<int>(min(u1 - u, (long long)(t.n - it.j0)));
+                it.split = it.n < t.n;
+                it.c0 = static_cast<int>(((us + 1) * NC - 1) / U);
+                it.c1 = static_cast<int>(((us + t.n) * NC - 1) / U);
+            }
+            const int slot = items % kItems;
+            if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
+            if (lane == 0) {
+                c->items[slot] = it;
+                mbar_arrive(&c->item_full[slot]);
+            }
+            ++items;
+            if (it.n == 0) break;
+            // lanes 0..15 issue a tile's boxes: page lane & 7, columns 64 * (lane >> 3)
+            const int32_t* bt = p.kv.block_table + (int64_t)it.b * p.kv.max_pages_per_seq;
+            const int absent_row = p.kv.num_pages * H * kPage;            // past the map: reads zero
+            auto fetch = [&](int j) -> int {         // -1: a page past the end, or past the piece
+                const int pg = tile_of(it, it.j0 + j) * kTilePages + (lane & 7);
+                return (j < it.n && pg * kPage < it.len) ? bt[pg] : -1;
+            };
+            auto row_of = [&](int j, int phys) -> int {
+                const int pg = tile_of(it, it.j0 + j) * kTilePages + (lane & 7);
+                if (pg * kPage >= it.len) return absent_row;
+                if (phys < 0 || phys >= p.kv.num_pages) {
+                    *static_cast<volatile int*>(&c->any_absent) = 1;
+                    __threadfence_block();
+                    flag(status, SE_DEV_BAD_INDEX);
+                    return absent_row;
+                }
+                return (phys * H + it.h) * kPage;
+            };
+            auto load = [&](const CUtensorMap* map, int row) -> bool {
+                const int st = seq % S::kStages;
+                if (!warp_wait(&c->empty[st], ((seq / S::kStages) & 1) ^ 1, c, status)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&c->full[st], S::kTile);
+                __syncwarp();
+                if (lane < 8 * S::kHalves)
+                    tma_load_2d(ring + st * S::kTile + (lane >> 3) * S::kRegion + (lane & 7) * 2048,
+                                map, &c->full[st], (lane >> 3) * 64, row);
+                ++seq;
+                return true;
+            };
+            int nxt1 = fetch(0), nxt2 = fetch(1);
+            int row_k = row_of(0, nxt1), row_v;
+            go = load(&tk, row_k);
+            if (go) {
+                go = warp_wait(&c->q_empty, (loads_q & 1) ^ 1, c, status);
+                if (go && lane == 0) {
+                    const int tiles = it.rows > 128 ? 2 : 1;
+                    mbar_arrive_expect_tx(&c->q_full, tiles * S::kTile);
+                    for (int w = 0; w < tiles; ++w)
+                        for (int hf = 0; hf < S::kHalves; ++hf)
+                            tma_load_3d(qs + w * S::kTile + hf * S::kRegion, &tq, &c->q_full, hf * 64,
+                                        it.h * G, it.tok0 + w * (128 / G));
+                }
+                __syncwarp();
+                if (go) ++loads_q;
+            }
+            for (int j = 0; go && j < it.n; ++j) {   // K of tile j + 1, then V of tile j
+                row_v = row_k;
+                nxt1 = nxt2;
+                nxt2 = fetch(j + 2);
+                if (j + 1 < it.n) {
+                    row_k = row_of(j + 1, nxt1);
+                    go = load(&tk, row_k);
+                }
+                if (go) go = load(&tv, row_v);
+            }
+            // on to the next item: heads within the block, then the next block
+            u += it.n;
+            if (++h == H) {
+                h = 0;
+                pre += t.n;
+                ++blk;
+            }
+        }
+        if (lane == 0) {
+            // every copy has landed before the block exits
+            volatile int never = 0;
+            const uint32_t from = seq > (uint32_t)S::kStages ? seq - S::kStages : 0;
+            for (uint32_t i = from; i < seq; ++i)
+                mbar_wait(&c->full[i % S::kStages], (i / S::kStages) & 1, &never);
+            if (loads_q > 0) mbar_wait(&c->q_full, (loads_q - 1) & 1, &never);
+        }
+        __syncwarp();
+    } else if (warp == kSoftWarps + 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        const uint32_t q_addr = smem_u32(qs), r_addr = smem_u32(ring);
+        const uint32_t idesc_s = umma_idesc_bf16_f32(128, kKeys) | p.negate;
+        const uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | kUmmaBMnMajor;
+        uint32_t base = 0;                           // ring position of the item's first tile
+        uint32_t np[2] = {0, 0};                     // P tiles taken from each group
+        bool go = true;
+        for (int items = 0; go; ++items) {
+            const int slot = items % kItems;
+            if (!warp_wait(&c->item_full[slot], (items / kItems) & 1, c, status)) break;
+            const Item it = c->items[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->item_empty[slot]);
+            if (it.n == 0) break;
+            const int n = it.n;
+            const bool both = it.rows > 128;         // each group has its own rows
+            auto k_pos = [&](int j) -> uint32_t { return base + (j == 0 ? 0 : 2 * j - 1); };
+            auto v_pos = [&](int j) -> uint32_t { return base + min(2 * j + 2, 2 * n - 1); };
+            auto wait_full = [&](uint32_t pos) {
+                return warp_wait(&c->full[pos % S::kStages], (pos / S::kStages) & 1, c, status);
+            };
+            auto release = [&](uint32_t pos) { umma_commit(&c->empty[pos % S::kStages]); };
+            auto scores = [&](int w, uint32_t pos) {  // S_w = Q_w K^T
+                const uint32_t ka = r_addr + (pos % S::kStages) * S::kTile;
+                const uint32_t qa = q_addr + (both ? w * S::kTile : 0);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = (ks >> 2) * S::kRegion + (ks & 3) * 32;
+                    umma_bf16(tmem + w * 128, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off),
+                              idesc_s, ks > 0);
+                }
+                umma_commit(&c->s_full[w]);
+            };
+            auto values = [&](int w, uint32_t pos, bool acc) {   // O_w (+)= P_w V
+                const uint32_t va = r_addr + (pos % S::kStages) * S::kTile;
+#pragma unroll
+                for (int part = 0; part < (F32 ? 2 : 1); ++part)
+#pragma unroll
+                    for (int ks = 0; ks < kKeys / 16; ++ks)
+                        umma_bf16_ts(tmem + 256 + w * D, tmem + w * 128 + part * 64 + ks * 8,
+                                     umma_desc_mn_sw128(va + ks * 2048, S::kRegion), idesc_o,
+                                     acc || part > 0 || ks > 0);
+                umma_commit(&c->o_done[w]);
+            };
+            // rows of the last page past the held tokens may be anything, and 0 * NaN is
+            // not 0: V's are cleared before the product
+            auto clear_tail = [&](int j, uint32_t pos) {
+                const int k0 = tile_of(it, it.j0 + j) * kKeys;
+                const int tail = it.len - k0;        // valid rows of the tile
+                if (tail <= 0 || tail >= kKeys || tail % kPage == 0) return;
+                uint8_t* v = ring + (pos % S::kStages) * S::kTile;
+                const int r_end = (tail / kPage + 1) * kPage;
+                for (int i = lane; i < (r_end - tail) * 8 * S::kHalves; i += 32) {
+                    const int r = tail + i / (8 * S::kHalves), o = i % (8 * S::kHalves);
+                    *reinterpret_cast<uint4*>(v + (o >> 3) * S::kRegion + r * 128 + (o & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+            };
+            go = warp_wait(&c->q_full, items & 1, c, status) && wait_full(k_pos(0));
+            if (!go) break;
+            tc_fence_after();
+            if (lane == 0) {
+                scores(0, k_pos(0));
+                if (both) scores(1, k_pos(0));
+                release(k_pos(0));
+                if (n == 1) umma_commit(&c->q_empty);
+            }
+            if (!both && n > 1) {
+                go = wait_full(k_pos(1));
+                if (!go) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    scores(1, k_pos(1));
+                    release(k_pos(1));
+                    if (n == 2) umma_commit(&c->q_empty);
+                }
+            }
+            for (int j = 0; go && j < n; ++j) {
+                const int ahead = both ? j + 1 : j + 2;              // K tile to score next
+                go = wait_full(v_pos(j));
+                if (!go) break;
+                clear_tail(j, v_pos(j));
+                for (int w = both ? 0 : (j & 1); w < (both ? 2 : (j & 1) + 1); ++w) {
+                    go = warp_wait(&c->p_full[w], np[w] & 1, c, status);
+                    if (!go) break;
+                    ++np[w];
+                    tc_fence_after();
+                    if (lane == 0) values(w, v_pos(j), both ? j > 0 : j > 1);
+                    if (ahead < n) {
+                        if (!both || w == 0) {
+                            go = wait_full(k_pos(ahead));
+                            if (!go) break;
+                            tc_fence_after();
+                        }
+                        if (lane == 0) scores(w, k_pos(ahead));
+                    }
+                }
+                if (!go) break;
+                if (lane == 0) {
+                    release(v_pos(j));
+                    if (ahead < n) {
+                        release(k_pos(ahead));
+                        if (ahead == n - 1) umma_commit(&c->q_empty);
+                    }
+                }
+            }
+            base += 2 * n;
+        }
+        if (lane == 0) {
+            umma_commit(&c->done);                   // every MMA of this CTA has finished
+            volatile int never = 0;
+            mbar_wait(&c->done, 0, &never);
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------ softmax ------------------------------
+        const int w = warp >> 2, q4 = warp & 3;      // group, lane quadrant of tensor memory
+        const int r = q4 * 32 + lane;                // row of the accumulator
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        const uint32_t t_s = lane_base + w * 128;
+        const int lg = __ffs(G) - 1;
+        const float sl2 = p.scale_log2;
+        uint32_t ns = 0;                             // S tiles seen by this group
+        uint32_t no = 0;                             // P tiles handed to the tensor cores
+        uint32_t n_ml = 0, n_part = 0;
+        for (int items = 0;; ++items) {
+            const int slot = items % kItems;
+            if (!warp_wait(&c->item_full[slot], (items / kItems) & 1, c, status)) break;
+            const Item it = c->items[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->item_empty[slot]);
+            if (it.n == 0) break;
+            const bool both = it.rows > 128;
+            const int wrow0 = both ? w * 128 : 0;    // the accumulator's first row in the block
+            const int row = wrow0 + r;
+            const bool warp_live = wrow0 + q4 * 32 < it.rows;
+            // padding rows repeat the last row
+            const int pos = it.pos0 + (min(row, it.rows - 1) >> lg);
+            const int pos_lo = __shfl_sync(0xffffffffu, pos, 0);
+            const int pos_hi = __shfl_sync(0xffffffffu, pos, 31);
+            const int last = min(pos, it.len - 1);   // last key seen
+            const int last_lo = min(pos_lo, it.len - 1);
+            float m = -INFINITY, l = 0.f;            // reference (log2 units) and sum
+            const int mine_n = both ? it.n : (it.n - w + 1) / 2;
+            bool ok = true;
+            for (int i = 0; i < mine_n; ++i) {
+                ok = warp_wait(&c->s_full[w], ns & 1, c, status);
+                if (!ok) break;
+                ++ns;
+                tc_fence_after();
+                if (warp_live) {
+                    const int j = both ? i : 2 * i + w;
+                    const int k0 = tile_of(it, it.j0 + j) * kKeys;
+                    float v[kKeys];
+                    tmem_ld128(t_s, v);
+                    const bool absent =
+                        __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->any_absent) != 0);
+                    const bool whole = k0 + kKeys - 1 <= last_lo && !absent &&
+                                       (p.window == 0 || k0 > pos_hi - p.window ||
+                                        k0 + kKeys <= p.sink);
+                    if (!whole) {
+                        uint32_t pages = 0xffu;      // pages of the tile that are there
+                        if (absent) {
+                            bool there = false;
+                            const int pg = k0 / kPage + (lane & 7);
+                            if (pg * kPage < it.len) {
+                                const int phys =
+                                    p.kv.block_table[(int64_t)it.b * p.kv.max_pages_per_seq + pg];
+                                there = phys >= 0 && phys < p.kv.num_pages;
+                            }
+                            pages = __ballot_sync(0xffffffffu, there) & 0xffu;
+                        }
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int at = k0 + 32 * x;
+                            uint32_t see = low_bits(last - at + 1);
+                            if (p.window > 0)
+                                see &= ~low_bits(pos - p.window + 1 - at) | low_bits(p.sink - at);
+                            see &= ((pages >> (2 * x)) & 1 ? 0xffffu : 0u) |
+                                   ((pages >> (2 * x + 1)) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                v[32 * x + e] = (see >> e) & 1 ? v[32 * x + e] : -INFINITY;
+                        }
+                    }
+                    float mx[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+                    for (int e = 4; e < kKeys; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                    const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
+                    if (__any_sync(0xffffffffu, grow)) {
+                        const float to = grow ? top : m;
+                        const float alpha = to == m ? 1.f : ex2_approx(m - to);
+                        if (i > 0) {
+                            // the previous product is complete before O is touched
+                            ok = warp_wait(&c->o_done[w], (no - 1) & 1, c, status);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (int x = 0; x < D; x += 32) {
+                                float o[32];
+                                tmem_ld32(lane_base + 256 + w * D + x, o);
+                                uint32_t st[32];
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) st[e] = __float_as_uint(o[e] * alpha);
+                                tmem_st16(lane_base + 256 + w * D + x, st);
+                                tmem_st16(lane_base + 256 + w * D + x + 16, st + 16);
+                            }
+                        }
+                        l *= alpha;
+                        m = to;
+                    }
+                    const float neg = m == -INFINITY ? 0.f : -m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float a = ex2_approx(fmaf(v[32 * x + e], sl2, neg));
+                            const float d = ex2_approx(fmaf(v[32 * x + e + 1], sl2, neg));
+                            sum[e & 2] += a;
+                            sum[(e & 2) + 1] += d;
+                            hi[e / 2] = pack_bf16(a, d);
+                            if (F32) lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
+                        }
+                        tmem_st16(t_s + 16 * x, hi);
+                        if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->p_full[w]);
+                ++no;
+            }
+            if (!ok) break;
+            // ---- the item's rows ----
+            // columns of this group's share: all D of its rows, or half of D of the rows
+            // that both groups share
+            const int cols = both ? D : D / 2, col0 = both ? 0 : w * (D / 2);
+            const int n1 = both ? 0 : it.n / 2;      // tiles of group 1 (shared rows)
+            float w0 = 1.f, w1 = 0.f;                // weights of the two accumulators
+            // (each group has at least one tile, but group 1 of one shared tile)
+            if (mine_n > 0 && !warp_wait(&c->o_done[w], (no - 1) & 1, c, status)) break;
+            if (!both) {
+                c->ml[w][r] = make_float2(m, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->ml_full);
+                if (!warp_wait(&c->ml_full, n_ml & 1, c, status)) break;
+                const float2 a = c->ml[0][r], d = n1 > 0 ? c->ml[1][r] : make_float2(-INFINITY, 0.f);
+                m = fmaxf(a.x, d.x);
+                w0 = m == -INFINITY ? 1.f : ex2_approx(a.x - m);
+                w1 = m == -INFINITY ? 0.f : ex2_approx(d.x - m);
+                l = a.y * w0 + d.y * w1;
+            }
+            tc_fence_after();
+            const int trow = min(row, it.rows - 1);
+            const int64_t oh = (int64_t)(it.tok0 + (trow >> lg)) * p.Hq + it.h * G + (trow & (G - 1));
+            const bool live = row < it.rows;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            // partial results: slot of this CTA's piece
+            const size_t part_rows = (size_t)2 * 128;
+            uint8_t* parts = p.ws + kPartOff;
+            const size_t slot_bytes = part_rows * (8 + 4 * D);
+            const int piece = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == it.c0 ? 1 : 0);
+            auto part_ml = [&](int s) {
+                return reinterpret_cast<float2*>(parts + s * slot_bytes) + w * 128;
+            };
+            auto part_o = [&](int s) {
+                return reinterpret_cast<float*>(parts + s * slot_bytes + part_rows * 8) +
+                       (size_t)w * 128 * D;
+            };
+            if (warp_live) {
+                if (it.split) {
+                    part_ml(piece)[r] = make_float2(m, l);
+                } else if (p.lse && live && (both || w == 0)) {
+                    p.lse[oh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                }
+#pragma unroll
+                for (int x0 = 0; x0 < D; x0 += 32) {
+                    if (x0 >= cols) break;
+                    const int x = col0 + x0;
+                    float o[32];
+                    tmem_ld32(lane_base + 256 + (both ? w * D : 0) + x, o);
+                    if (!both && n1 > 0) {
+                        float o1[32];
+                        tmem_ld32(lane_base + 256 + D + x, o1);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o1[e] * w1;
+                    }
+                    if (!live) {
+                        // padding row
+                    } else if (it.split) {
+                        float4* dst = reinterpret_cast<float4*>(part_o(piece) + (size_t)r * cols + x0);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else if (F32) {
+                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + oh * D + x);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv,
+                                                 o[4 * e + 3] * inv);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + oh * D + x);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                                pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                                pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before();
+            if (!both) {
+                // neither group's next product may start before both have read
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->ml_empty);
+                if (!warp_wait(&c->ml_empty, n_ml & 1, c, status)) break;
+                ++n_ml;
+            }
+            if (!it.split) continue;
+            // ---- the last CTA of a cut block joins its pieces ----
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->part[w]);
+            if (!warp_wait(&c->part[w], n_part & 1, c, status)) break;
+            ++n_part;
+            int* counter = reinterpret_cast<int*>(p.ws + kCounterOff) + 2 * it.c0 + w;
+            const int pieces = it.c1 - it.c0 + 1;
+            if (q4 == 0 && lane == 0) {
+                const int before = atomicAdd(counter, 1);
+                const bool is_last = before == pieces - 1;
+                if (is_last) *counter = 0;
+                c->last[w] = is_last;
+                __threadfence();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c->part[w]);
+            if (!warp_wait(&c->part[w], n_part & 1, c, status)) break;
+            ++n_part;
+            if (!c->last[w]) continue;
+            __threadfence();
+            // a warp per row; lanes over the columns
+            const int rows_here = min(128, it.rows - wrow0);
+            for (int rr = q4; rr < rows_here; rr += 4) {
+                float mm = -INFINITY;
+                for (int s = lane; s < pieces; s += 32)
+                    mm = fmaxf(mm, __ldcg(&part_ml(2 * (it.c0 + s) + (s == 0 ? 1 : 0))[rr]).x);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+                const float ref = mm == -INFINITY ? 0.f : mm;
+                float ll = 0.f;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int s = 0; s < pieces; ++s) {
+                    const int sl = 2 * (it.c0 + s) + (s == 0 ? 1 : 0);
+                    const float2 x = __ldcg(&part_ml(sl)[rr]);
+                    const float f = ex2_approx(x.x - ref);
+                    ll += x.y * f;
+                    if (lane * 4 < cols) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(
+                                                    part_o(sl) + (size_t)rr * cols) + lane);
+                        acc.x += y.x * f;
+                        acc.y += y.y * f;
+                        acc.z += y.z * f;
+                        acc.w += y.w * f;
+                    }
+                }
+                const int brow = wrow0 + rr;
+                const int64_t o2 = (int64_t)(it.tok0 + (brow >> lg)) * p.Hq + it.h * G + (brow & (G - 1));
+                const float iv = ll > 0.f ? 1.f / ll : 0.f;
+                if (p.lse && lane == 0 && (both || w == 0))
+                    p.lse[o2] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                if (lane * 4 < cols) {
+                    const int64_t at = o2 * D + col0 + lane * 4;
+                    if (F32)
+                        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+                            make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+                    else
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
+                            make_uint2(pack_bf16(acc.x * iv, acc.y * iv),
+                                       pack_bf16(acc.z * iv, acc.w * iv));
+                }
+            }
+        }
+    }
+    // every role is done (copies landed, MMAs completed, tensor memory read)
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftWarps + 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool F32>
+cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                const Params& p, int grid, cudaStream_t s) {
+    auto kern = chunk_attn_kernel<D, F32>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Shape<D>::kSmem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(grid), dim3(kThreads), Shape<D>::kSmem, s, tq, tk, tv, p);
 }
 
 }  // namespace
 
-size_t chunk_attn_ws_bytes(int, int, int, int, int) { return 256; }
+int chunk_attn_max_batch() { return kMaxBatch; }
+
+size_t chunk_attn_ws_bytes(int, int, int, int, int D) {
+    return kPartOff + (size_t)kMaxCtas * 2 * 256 * (8 + 4 * (size_t)D);
+}
 
 cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int batch,
                               const ChunkAttnArgs& a, void* ws, cudaEvent_t ev_begin,
                               cudaEvent_t ev_end, cudaStream_t s) {
-    Params p{kv, ck, batch, a, static_cast<int*>(ws)};
-    const int G = a.Hq / kv.num_kv_heads;
-    const int64_t blocks = (int64_t)ck.max_tokens * G / kRows + batch;
-    const dim3 grid(static_cast<unsigned>(blocks), kv.num_kv_heads);
+    const int D = kv.head_dim, H = kv.num_kv_heads;
+    Params p;
+    p.kv = kv;
+    p.ck = ck;
+    p.batch = batch;
+    p.G = a.Hq / H;
+    p.Hq = a.Hq;
+    p.max_blocks = static_cast<int>((int64_t)ck.max_tokens * p.G / kBlockRows) + batch;
+    p.window = a.window;
+    p.sink = a.sink;
+    // a negative scale negates the products; a zero one becomes so small that
+    // every logit is zero to fp32 (masked ones stay -inf)
+    p.scale_log2 = std::max(std::abs(a.scale) * kLog2e, 1e-37f);
+    p.negate = a.scale < 0.f ? kUmmaNegateA : 0u;
+    p.out_f32 = a.out_dtype;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.ws = static_cast<uint8_t*>(ws);
+    CUtensorMap tq, tk, tv;
+    if (!encode_rows_map(&tk, kv.k, (int64_t)kv.num_pages * H * kPage, D) ||
+        !encode_rows_map(&tv, kv.v, (int64_t)kv.num_pages * H * kPage, D) ||
+        !encode_heads_map(&tq, a.q, ck.max_tokens, a.Hq, a.q_stride, p.G, D))
+        return cudaErrorInvalidValue;
+    const int grid = std::min(num_sms(), kMaxCtas);
     // inside a stream capture the timing events become event-record nodes
     auto record = [&](cudaEvent_t ev) {
         cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
@@ -167,9 +918,12 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
     };
     cudaError_t e;
     if (ev_begin && (e = record(ev_begin)) != cudaSuccess) return e;
-    if (kv.head_dim == 128) chunk_attn_simple_kernel<128><<<grid, 128, 0, s>>>(p);
-    else chunk_attn_simple_kernel<64><<<grid, 128, 0, s>>>(p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const bool f32 = a.out_dtype == 1;
+    if (D == 128)
+        e = f32 ? run<128, true>(tq, tk, tv, p, grid, s) : run<128, false>(tq, tk, tv, p, grid, s);
+    else
+        e = f32 ? run<64, true>(tq, tk, tv, p, grid, s) : run<64, false>(tq, tk, tv, p, grid, s);
+    if (e != cudaSuccess) return e;
     if (ev_end && (e = record(ev_end)) != cudaSuccess) return e;
     return cudaSuccess;
 }

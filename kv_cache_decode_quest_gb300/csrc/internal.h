@@ -72,6 +72,7 @@ struct ChunkAttnArgs {
     void* out;
     float* lse;
 };
+int chunk_attn_max_batch();
 size_t chunk_attn_ws_bytes(int batch, int max_tokens, int H, int Hq, int D);
 cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int batch,
                               const ChunkAttnArgs& a, void* ws, cudaEvent_t ev_begin,
@@ -156,5 +157,9 @@ cudaError_t launch_h2o_step(const se_h2o_state& st, const void* q, const void* k
 // ---- tensor maps (api.cu) ----
 // 2-D bf16 map over [rows][head_dim] with 16-row x 64-column boxes, 128B swizzle.
 bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int head_dim);
+// 3-D bf16 map over [tokens][heads][head_dim] (tokens `stride` elements apart) with boxes
+// of 64 columns x `group` heads x 128 / group tokens (128 rows), 128B swizzle.
+bool encode_heads_map(CUtensorMap* map, const void* base, int tokens, int heads, int64_t stride,
+                      int group, int head_dim);
 
 }  // namespace se
