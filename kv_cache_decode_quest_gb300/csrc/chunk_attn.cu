@@ -40,7 +40,12 @@ constexpr int kBlockRows = 256;                    // rows of a block: two accum
 constexpr int kKeys = 128;                         // keys of a tile
 constexpr int kTilePages = kKeys / kPage;
 constexpr int kSoftWarps = 8;
-constexpr int kThreads = (kSoftWarps + 2) * 32;    // + producer + MMA
+constexpr int kThreads = (kSoftWarps + 4) * 32;    // + producer, MMA, two idle warps
+// Registers a thread: the launch gives 384 threads 168 each; the four warps that
+// do not compute rows hand theirs to the eight that do (88 * 128 + 208 * 256 =
+// 168 * 384), which hold a row of 128 logits.
+constexpr int kRegsFew = 88, kRegsMany = 208;
+static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * kThreads, "registers of the launch");
 constexpr int kItems = 4;                          // work items in flight between the roles
 constexpr int kMaxCtas = 256;
 constexpr int kMaxBatch = 8192;
@@ -161,7 +166,7 @@ struct Ctrl {
     int last[2];
     int any_absent;                        // a block-table entry named no page
     Item items[kItems];
-    float2 ml[2][128];
+    float2 ml[2][128];                     // of a block that both groups share
 };
 
 // Warp-uniform bounded wait.
@@ -324,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = c->tmem;
 
+    if (warp >= kSoftWarps) {
+    regs_fewer<kRegsFew>();
     if (warp == kSoftWarps) {
         // ------------------------------ producer ------------------------------
         fence_proxy_async_smem();                    // the staged lengths are read: TMA may write
@@ -463,56 +470,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kSoftWarps + 1) {
         // ------------------------------ MMA issuer ------------------------------
-        const uint32_t q_addr = smem_u32(qs), r_addr = smem_u32(ring);
+        // The whole warp runs this with the same values; an elected lane issues.
+        // Descriptor words: the high one is the operand's layout, the low one
+        // its address / 16 (and V's column stride), to which offsets are added.
+        const uint64_t qd = umma_desc_sw128(smem_u32(qs)), kd = umma_desc_sw128(smem_u32(ring));
+        const uint64_t vd = umma_desc_mn_sw128(smem_u32(ring), S::kRegion);
+        const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
+        const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
+        const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
         const uint32_t idesc_s = umma_idesc_bf16_f32(128, kKeys) | p.negate;
         const uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | kUmmaBMnMajor;
-        uint32_t base = 0;                           // ring position of the item's first tile
-        uint32_t np[2] = {0, 0};                     // P tiles taken from each group
-        bool go = true;
-        for (int items = 0; go; ++items) {
+        const uint32_t bar_empty = smem_u32(&c->empty[0]);
+        const uint32_t bar_s = smem_u32(&c->s_full[0]), bar_o = smem_u32(&c->o_done[0]);
+        const uint32_t bar_q = smem_u32(&c->q_empty);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        uint32_t st = 0, ph = 0;                     // ring stage and its phase
+        uint32_t np0 = 0, np1 = 0;                   // phases of P of each group
+        auto wait_stage = [&]() { return warp_wait(&c->full[st], ph, c, status); };
+        auto next_stage = [&]() {
+            if (++st == S::kStages) {
+                st = 0;
+                ph ^= 1;
+            }
+        };
+        auto scores = [&](uint32_t w, uint32_t qt, uint32_t stage) {      // S_w = Q_qt K^T
+            const uint32_t ka = k_lo + stage * (S::kTile / 16), qa = q_lo + qt * (S::kTile / 16);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                constexpr int kHalf = S::kRegion / 16;
+                const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 2;
+                umma_bf16_warp(tm + w * 128, qa + off, q_hi, ka + off, k_hi, idesc_s, ks > 0);
+            }
+            umma_commit_warp(bar_s + w * 8);
+        };
+        auto values = [&](uint32_t w, uint32_t stage, uint32_t acc) {     // O_w (+)= P_w V
+            const uint32_t va = v_lo + stage * (S::kTile / 16);
+#pragma unroll
+            for (int part = 0; part < (F32 ? 2 : 1); ++part)
+#pragma unroll
+                for (int ks = 0; ks < kKeys / 16; ++ks)
+                    umma_bf16_ts_warp(tm + 256 + w * D, tm + w * 128 + part * 64 + ks * 8,
+                                      va + ks * 128, v_hi, idesc_o, part + ks > 0 ? 1u : acc);
+            umma_commit_warp(bar_o + w * 8);
+        };
+        for (int items = 0;; ++items) {
             const int slot = items % kItems;
             if (!warp_wait(&c->item_full[slot], (items / kItems) & 1, c, status)) break;
-            const Item it = c->items[slot];
+            const Item* ip = &c->items[slot];
+            const int n = __shfl_sync(0xffffffffu, ip->n, 0);
+            const bool both = __shfl_sync(0xffffffffu, ip->rows, 0) > 128;   // rows of its own each
+            const int len = ip->len, ts = ip->ts, tl = ip->tl, j0 = ip->j0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&c->item_empty[slot]);
-            if (it.n == 0) break;
-            const int n = it.n;
-            const bool both = it.rows > 128;         // each group has its own rows
-            auto k_pos = [&](int j) -> uint32_t { return base + (j == 0 ? 0 : 2 * j - 1); };
-            auto v_pos = [&](int j) -> uint32_t { return base + min(2 * j + 2, 2 * n - 1); };
-            auto wait_full = [&](uint32_t pos) {
-                return warp_wait(&c->full[pos % S::kStages], (pos / S::kStages) & 1, c, status);
-            };
-            auto release = [&](uint32_t pos) { umma_commit(&c->empty[pos % S::kStages]); };
-            auto scores = [&](int w, uint32_t pos) {  // S_w = Q_w K^T
-                const uint32_t ka = r_addr + (pos % S::kStages) * S::kTile;
-                const uint32_t qa = q_addr + (both ? w * S::kTile : 0);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks) {
-                    const uint32_t off = (ks >> 2) * S::kRegion + (ks & 3) * 32;
-                    umma_bf16(tmem + w * 128, umma_desc_sw128(qa + off), umma_desc_sw128(ka + off),
-                              idesc_s, ks > 0);
-                }
-                umma_commit(&c->s_full[w]);
-            };
-            auto values = [&](int w, uint32_t pos, bool acc) {   // O_w (+)= P_w V
-                const uint32_t va = r_addr + (pos % S::kStages) * S::kTile;
-#pragma unroll
-                for (int part = 0; part < (F32 ? 2 : 1); ++part)
-#pragma unroll
-                    for (int ks = 0; ks < kKeys / 16; ++ks)
-                        umma_bf16_ts(tmem + 256 + w * D, tmem + w * 128 + part * 64 + ks * 8,
-                                     umma_desc_mn_sw128(va + ks * 2048, S::kRegion), idesc_o,
-                                     acc || part > 0 || ks > 0);
-                umma_commit(&c->o_done[w]);
-            };
+            if (n == 0) break;
             // rows of the last page past the held tokens may be anything, and 0 * NaN is
-            // not 0: V's are cleared before the product
-            auto clear_tail = [&](int j, uint32_t pos) {
-                const int k0 = tile_of(it, it.j0 + j) * kKeys;
-                const int tail = it.len - k0;        // valid rows of the tile
-                if (tail <= 0 || tail >= kKeys || tail % kPage == 0) return;
-                uint8_t* v = ring + (pos % S::kStages) * S::kTile;
+            // not 0: V's are cleared before the product.  They are in the piece's tile
+            // `tail_j`, if any (the tiles of a block are in key order).
+            const int tail_k0 = len / kKeys * kKeys;
+            const int tail_t = tail_k0 / kKeys;
+            const int tail_at = tail_t < ts ? tail_t : tail_t - tl + ts;
+            const int tail_j =
+                len % kPage == 0 || (tail_t >= ts && tail_t < tl) ? -1 : tail_at - j0;
+            auto clear_tail = [&](uint32_t stage) {
+                const int tail = len - tail_k0;
+                uint8_t* v = ring + stage * S::kTile;
                 const int r_end = (tail / kPage + 1) * kPage;
                 for (int i = lane; i < (r_end - tail) * 8 * S::kHalves; i += 32) {
                     const int r = tail + i / (8 * S::kHalves), o = i % (8 * S::kHalves);
@@ -522,64 +543,89 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            go = warp_wait(&c->q_full, items & 1, c, status) && wait_full(k_pos(0));
-            if (!go) break;
+            // ring order: K0, then for each tile j: K_{j + 1}, V_j
+            if (!warp_wait(&c->q_full, items & 1, c, status) || !wait_stage()) break;
             tc_fence_after();
-            if (lane == 0) {
-                scores(0, k_pos(0));
-                if (both) scores(1, k_pos(0));
-                release(k_pos(0));
-                if (n == 1) umma_commit(&c->q_empty);
-            }
+            scores(0, 0, st);
+            if (both) scores(1, 1, st);
+            umma_commit_warp(bar_empty + st * 8);
+            next_stage();
             if (!both && n > 1) {
-                go = wait_full(k_pos(1));
-                if (!go) break;
+                if (!wait_stage()) break;
                 tc_fence_after();
-                if (lane == 0) {
-                    scores(1, k_pos(1));
-                    release(k_pos(1));
-                    if (n == 2) umma_commit(&c->q_empty);
-                }
+                scores(1, 0, st);
+                umma_commit_warp(bar_empty + st * 8);
+                next_stage();
             }
-            for (int j = 0; go && j < n; ++j) {
-                const int ahead = both ? j + 1 : j + 2;              // K tile to score next
-                go = wait_full(v_pos(j));
-                if (!go) break;
-                clear_tail(j, v_pos(j));
-                for (int w = both ? 0 : (j & 1); w < (both ? 2 : (j & 1) + 1); ++w) {
-                    go = warp_wait(&c->p_full[w], np[w] & 1, c, status);
+            const int ahead = both ? 1 : 2;          // tiles the scores run ahead
+            if (n <= ahead) umma_commit_warp(bar_q);
+            bool go = true;
+            if (both) {
+                for (int j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    const uint32_t ks = st, kph = ph;
+                    if (more) next_stage();
+                    const uint32_t vs = st;
+                    go = wait_stage();               // V_j (K_{j + 1} was loaded before it)
+                    next_stage();
+                    if (go && more) go = warp_wait(&c->full[ks], kph, c, status);
                     if (!go) break;
-                    ++np[w];
+                    if (j == tail_j) clear_tail(vs);
+                    go = warp_wait(&c->p_full[0], np0 & 1, c, status);
+                    if (!go) break;
+                    ++np0;
                     tc_fence_after();
-                    if (lane == 0) values(w, v_pos(j), both ? j > 0 : j > 1);
-                    if (ahead < n) {
-                        if (!both || w == 0) {
-                            go = wait_full(k_pos(ahead));
-                            if (!go) break;
-                            tc_fence_after();
-                        }
-                        if (lane == 0) scores(w, k_pos(ahead));
+                    values(0, vs, j > 0);
+                    if (more) scores(0, 0, ks);
+                    go = warp_wait(&c->p_full[1], np1 & 1, c, status);
+                    if (!go) break;
+                    ++np1;
+                    tc_fence_after();
+                    values(1, vs, j > 0);
+                    umma_commit_warp(bar_empty + vs * 8);
+                    if (more) {
+                        scores(1, 1, ks);
+                        umma_commit_warp(bar_empty + ks * 8);
+                        if (j + 2 == n) umma_commit_warp(bar_q);
                     }
                 }
-                if (!go) break;
-                if (lane == 0) {
-                    release(v_pos(j));
-                    if (ahead < n) {
-                        release(k_pos(ahead));
-                        if (ahead == n - 1) umma_commit(&c->q_empty);
+            } else {
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t w = j & 1;
+                    const uint32_t vs = st;          // V_j, then K_{j + 2}
+                    go = wait_stage();
+                    if (!go) break;
+                    next_stage();
+                    if (j == tail_j) clear_tail(vs);
+                    go = warp_wait(&c->p_full[w], (w ? np1 : np0) & 1, c, status);
+                    if (!go) break;
+                    if (w) ++np1;
+                    else ++np0;
+                    tc_fence_after();
+                    values(w, vs, j > 1);
+                    umma_commit_warp(bar_empty + vs * 8);
+                    if (j + 2 < n) {
+                        go = wait_stage();
+                        if (!go) break;
+                        tc_fence_after();
+                        scores(w, 0, st);
+                        umma_commit_warp(bar_empty + st * 8);
+                        next_stage();
+                        if (j + 3 == n) umma_commit_warp(bar_q);
                     }
                 }
             }
-            base += 2 * n;
-        }
-        if (lane == 0) {
-            umma_commit(&c->done);                   // every MMA of this CTA has finished
-            volatile int never = 0;
-            mbar_wait(&c->done, 0, &never);
+            if (!go) break;
         }
         __syncwarp();
+        umma_commit_warp(smem_u32(&c->done));        // every MMA of this CTA has finished
+        volatile int never = 0;
+        mbar_wait(&c->done, 0, &never);
+        __syncwarp();
+    }
     } else {
         // ------------------------------ softmax ------------------------------
+        regs_more<kRegsMany>();
         const int w = warp >> 2, q4 = warp & 3;      // group, lane quadrant of tensor memory
         const int r = q4 * 32 + lane;                // row of the accumulator
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
@@ -651,7 +697,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int e = 4; e < kKeys; ++e) mx[e & 3] = fmaxf(mx[e & 3], v[e]);
+                    for (int e = 4; e + 8 <= kKeys; e += 8)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mx[x] = fmaxf(fmaxf(mx[x], v[e + x]), v[e + 4 + x]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[kKeys - 4 + x]);
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
                     if (__any_sync(0xffffffffu, grow)) {
@@ -662,38 +713,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = warp_wait(&c->o_done[w], (no - 1) & 1, c, status);
                             if (!ok) break;
                             tc_fence_after();
+#pragma unroll 1
+                            for (int x = 0; x < D; x += 16) {
+                                uint32_t o[16];
+                                tmem_ld16(lane_base + 256 + w * D + x, o);
 #pragma unroll
-                            for (int x = 0; x < D; x += 32) {
-                                float o[32];
-                                tmem_ld32(lane_base + 256 + w * D + x, o);
-                                uint32_t st[32];
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) st[e] = __float_as_uint(o[e] * alpha);
-                                tmem_st16(lane_base + 256 + w * D + x, st);
-                                tmem_st16(lane_base + 256 + w * D + x + 16, st + 16);
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                                tmem_st16(lane_base + 256 + w * D + x, o);
                             }
                         }
                         l *= alpha;
                         m = to;
                     }
                     const float neg = m == -INFINITY ? 0.f : -m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    const uint64_t neg2 = f32x2(neg, neg), scale2 = f32x2(sl2, sl2);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
                         uint32_t hi[16], lo[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
-                            const float a = ex2_approx(fmaf(v[32 * x + e], sl2, neg));
-                            const float d = ex2_approx(fmaf(v[32 * x + e + 1], sl2, neg));
-                            sum[e & 2] += a;
-                            sum[(e & 2) + 1] += d;
+                            float a, d;
+                            f32x2_split(fma_f32x2(f32x2(v[32 * x + e], v[32 * x + e + 1]), scale2, neg2),
+                                        a, d);
+                            a = ex2_approx(a);
+                            d = ex2_approx(d);
+                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(a, d));
                             hi[e / 2] = pack_bf16(a, d);
                             if (F32) lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
                         }
                         tmem_st16(t_s + 16 * x, hi);
                         if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float s0, s1;
+                    f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
+                    l += s0 + s1;
                     tmem_st_wait();
                 }
                 tc_fence_before();
@@ -812,45 +867,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++n_part;
             if (!c->last[w]) continue;
             __threadfence();
-            // a warp per row; lanes over the columns
             const int rows_here = min(128, it.rows - wrow0);
-            for (int rr = q4; rr < rows_here; rr += 4) {
+            auto slot_of = [&](int s) { return 2 * (it.c0 + s) + (s == 0 ? 1 : 0); };
+            // reference and sum of each row, a thread per row, kept for the group
+            {
                 float mm = -INFINITY;
-                for (int s = lane; s < pieces; s += 32)
-                    mm = fmaxf(mm, __ldcg(&part_ml(2 * (it.c0 + s) + (s == 0 ? 1 : 0))[rr]).x);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+                for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
                 const float ref = mm == -INFINITY ? 0.f : mm;
                 float ll = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int s = 0; s < pieces; ++s) {
-                    const int sl = 2 * (it.c0 + s) + (s == 0 ? 1 : 0);
-                    const float2 x = __ldcg(&part_ml(sl)[rr]);
-                    const float f = ex2_approx(x.x - ref);
-                    ll += x.y * f;
-                    if (lane * 4 < cols) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(
-                                                    part_o(sl) + (size_t)rr * cols) + lane);
-                        acc.x += y.x * f;
-                        acc.y += y.y * f;
-                        acc.z += y.z * f;
-                        acc.w += y.w * f;
+                    const float2 x = __ldcg(&part_ml(slot_of(s))[r]);
+                    ll += x.y * ex2_approx(x.x - ref);
+                }
+                c->ml[w][r] = make_float2(ref, ll > 0.f ? 1.f / ll : 0.f);
+                if (p.lse && live && (both || w == 0))
+                    p.lse[oh] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            }
+            __syncwarp();
+            // the warp's own 32 rows, kJoin at a time (their loads overlap), lanes over columns
+            constexpr int kJoin = 8;
+            const int lanes = cols / 4;              // 16-byte vectors of a row
+            for (int r0 = q4 * 32; r0 < min(q4 * 32 + 32, rows_here); r0 += kJoin) {
+                float4 acc[kJoin];
+#pragma unroll
+                for (int i = 0; i < kJoin; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int s = 0; s < pieces; ++s) {
+                    const float4* src = reinterpret_cast<const float4*>(part_o(slot_of(s)));
+                    const float2* ml = part_ml(slot_of(s));
+                    float4 y[kJoin];
+                    float f[kJoin];
+#pragma unroll
+                    for (int i = 0; i < kJoin; ++i) {
+                        const int rr = min(r0 + i, rows_here - 1);
+                        f[i] = __ldcg(&ml[rr]).x;
+                        y[i] = __ldcg(src + (size_t)rr * lanes + min(lane, lanes - 1));
+                    }
+#pragma unroll
+                    for (int i = 0; i < kJoin; ++i) {
+                        const float k = ex2_approx(f[i] - c->ml[w][min(r0 + i, rows_here - 1)].x);
+                        acc[i].x += y[i].x * k;
+                        acc[i].y += y[i].y * k;
+                        acc[i].z += y[i].z * k;
+                        acc[i].w += y[i].w * k;
                     }
                 }
-                const int brow = wrow0 + rr;
-                const int64_t o2 = (int64_t)(it.tok0 + (brow >> lg)) * p.Hq + it.h * G + (brow & (G - 1));
-                const float iv = ll > 0.f ? 1.f / ll : 0.f;
-                if (p.lse && lane == 0 && (both || w == 0))
-                    p.lse[o2] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-                if (lane * 4 < cols) {
+#pragma unroll
+                for (int i = 0; i < kJoin; ++i) {
+                    if (r0 + i >= rows_here || lane >= lanes) continue;
+                    const int brow = wrow0 + r0 + i;
+                    const int64_t o2 =
+                        (int64_t)(it.tok0 + (brow >> lg)) * p.Hq + it.h * G + (brow & (G - 1));
+                    const float iv = c->ml[w][r0 + i].y;
                     const int64_t at = o2 * D + col0 + lane * 4;
                     if (F32)
-                        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
-                            make_float4(acc.x * iv, acc.y * iv, acc.z * iv, acc.w * iv);
+                        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(
+                            acc[i].x * iv, acc[i].y * iv, acc[i].z * iv, acc[i].w * iv);
                     else
                         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                            make_uint2(pack_bf16(acc.x * iv, acc.y * iv),
-                                       pack_bf16(acc.z * iv, acc.w * iv));
+                            make_uint2(pack_bf16(acc[i].x * iv, acc[i].y * iv),
+                                       pack_bf16(acc[i].z * iv, acc[i].w * iv));
                 }
             }
         }
