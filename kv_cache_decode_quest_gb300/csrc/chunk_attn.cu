@@ -48,6 +48,7 @@ constexpr int kRegsFew = 88, kRegsMany = 208;
 static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * kThreads, "registers of the launch");
 constexpr int kItems = 4;                          // work items in flight between the roles
 constexpr int kMaxCtas = 256;
+constexpr int kBlockCost = 2;                      // a block's fixed work, in tiles
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -149,6 +150,8 @@ __device__ __forceinline__ Tiles block_tiles(const Params& p, const Seq& s, int 
     return t;
 }
 
+__device__ __forceinline__ int block_cost(const Tiles& t) { return t.n > 0 ? t.n + kBlockCost : 0; }
+
 __device__ __forceinline__ int tile_of(const Item& it, int j) {
     return j < it.ts ? j : j - it.ts + it.tl;
 }
@@ -156,7 +159,7 @@ __device__ __forceinline__ int tile_of(const Item& it, int j) {
 struct Ctrl {
     uint64_t full[10], empty[10];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_full[2], o_done[2];
+    uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
     uint64_t ml_full, ml_empty;            // the groups' (reference, sum) of a shared block
     uint64_t part[2];                      // a group's partial rows are written
     uint64_t item_full[kItems], item_empty[kItems];
@@ -181,6 +184,26 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* 
         }
     }
     return ok;
+}
+
+// 4 x 4 transpose of 16-byte units over each group of four lanes: lane i ends with
+// unit i of the rows that lanes 0..3 of the group held.
+__device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
+    auto swap = [&](uint4& a, uint4& b, int bit) {
+        const bool up = lane & bit;
+        const uint4 give = up ? a : b;
+        uint4 got;
+        got.x = __shfl_xor_sync(0xffffffffu, give.x, bit);
+        got.y = __shfl_xor_sync(0xffffffffu, give.y, bit);
+        got.z = __shfl_xor_sync(0xffffffffu, give.z, bit);
+        got.w = __shfl_xor_sync(0xffffffffu, give.w, bit);
+        if (up) a = got;
+        else b = got;
+    };
+    swap(x[0], x[1], 1);
+    swap(x[2], x[3], 1);
+    swap(x[0], x[2], 2);
+    swap(x[1], x[3], 2);
 }
 
 // Low n bits set (n clamped to [0, 32]).
@@ -212,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&c->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->s_full[i], 1);
+            mbar_init(&c->p_half[i], 4);
             mbar_init(&c->p_full[i], 4);
             mbar_init(&c->o_done[i], 1);
             mbar_init(&c->part[i], 4);
@@ -274,14 +298,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         *sum = all;
         return before + x - v;
     };
-    // units: tiles x heads, in the order (block, head, tile)
+    // units: (tiles + the fixed cost) x heads, in the order (block, head, tile); the fixed
+    // cost comes before a block's first tile
     long long total = 0, mine = 0;
     int nt = 0, my_b = 0;
     const int passes = (p.max_blocks + kThreads - 1) / kThreads;
     for (int i = 0; i < passes; ++i) {
         const int x = i * kThreads + threadIdx.x;
         my_b = find_seq(x);
-        nt = x < p.max_blocks ? block_tiles(p, seqs[my_b], x - firsts[my_b]).n : 0;
+        nt = x < p.max_blocks ? block_cost(block_tiles(p, seqs[my_b], x - firsts[my_b])) : 0;
         long long sum;
         mine = scan(nt, &sum);
         total += sum;
@@ -298,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             long long sum;
             if (passes > 1) {
                 my_b = find_seq(x);
-                nt = x < p.max_blocks ? block_tiles(p, seqs[my_b], x - firsts[my_b]).n : 0;
+                nt = x < p.max_blocks ? block_cost(block_tiles(p, seqs[my_b], x - firsts[my_b])) : 0;
                 mine = scan(nt, &sum);
             } else {
                 sum = total;
@@ -366,15 +391,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     blk = 0;
                 }
             }
+            const int cost = block_cost(t);
             Item it;
             it.b = b;
             it.n = 0;
-            if (u < u1 && t.n > 0) {
+            long long next = u1;
+            if (u < u1 && t.n > 0) {             // (n stays 0 if the share ends before a tile)
                 if (first) {
-                    h = static_cast<int>((u - pre * H) / t.n);
+                    h = static_cast<int>((u - pre * H) / cost);
                     first = false;
                 }
-                const long long us = (pre * H) + (long long)h * t.n;     // the item's first unit
+                const long long us = pre * H + (long long)h * cost;      // the item's first unit
+                const long long t0 = us + kBlockCost;                    // its first tile's
+                next = min(u1, us + cost);
                 it.h = h;
                 it.tok0 = s.s0 + blk * (kBlockRows / G);
                 it.rows = t.rows;
@@ -382,11 +411,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it.len = s.len;
                 it.ts = t.ts;
                 it.tl = t.tl;
-                it.j0 = static_cast<int>(u - us);
-                it.n = static_cast<int>(min(u1 - u, (long long)(t.n - it.j0)));
+                it.j0 = static_cast<int>(max(0ll, u - t0));
+                it.n = static_cast<int>(max(0ll, next - t0)) - it.j0;
                 it.split = it.n < t.n;
-                it.c0 = static_cast<int>(((us + 1) * NC - 1) / U);
-                it.c1 = static_cast<int>(((us + t.n) * NC - 1) / U);
+                it.c0 = static_cast<int>(((t0 + 1) * NC - 1) / U);
+                it.c1 = static_cast<int>(((us + cost) * NC - 1) / U);
             }
             const int slot = items % kItems;
             if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
@@ -452,10 +481,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (go) go = load(&tv, row_v);
             }
             // on to the next item: heads within the block, then the next block
-            u += it.n;
+            u = next;
             if (++h == H) {
                 h = 0;
-                pre += t.n;
+                pre += cost;
                 ++blk;
             }
         }
@@ -503,15 +532,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             umma_commit_warp(bar_s + w * 8);
         };
-        auto values = [&](uint32_t w, uint32_t stage, uint32_t acc) {     // O_w (+)= P_w V
+        // O_w (+)= P_w V for the first / second 64 keys of the tile
+        auto values = [&](uint32_t w, uint32_t stage, uint32_t acc, int half) {
             const uint32_t va = v_lo + stage * (S::kTile / 16);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part)
 #pragma unroll
-                for (int ks = 0; ks < kKeys / 16; ++ks)
+                for (int k = 0; k < kKeys / 32; ++k) {
+                    const int ks = half * (kKeys / 32) + k;
                     umma_bf16_ts_warp(tm + 256 + w * D, tm + w * 128 + part * 64 + ks * 8,
-                                      va + ks * 128, v_hi, idesc_o, part + ks > 0 ? 1u : acc);
+                                      va + ks * 128, v_hi, idesc_o,
+                                      half + part + k > 0 ? 1u : acc);
+                }
+        };
+        auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase) -> bool {
+            if (!warp_wait(&c->p_half[w], phase, c, status)) return false;
+            tc_fence_after();
+            values(w, stage, acc, 0);
+            if (!warp_wait(&c->p_full[w], phase, c, status)) return false;
+            tc_fence_after();
+            values(w, stage, acc, 1);
             umma_commit_warp(bar_o + w * 8);
+            return true;
         };
         for (int items = 0;; ++items) {
             const int slot = items % kItems;
@@ -571,17 +613,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (go && more) go = warp_wait(&c->full[ks], kph, c, status);
                     if (!go) break;
                     if (j == tail_j) clear_tail(vs);
-                    go = warp_wait(&c->p_full[0], np0 & 1, c, status);
+                    go = product(0, vs, j > 0, np0 & 1);
                     if (!go) break;
                     ++np0;
-                    tc_fence_after();
-                    values(0, vs, j > 0);
                     if (more) scores(0, 0, ks);
-                    go = warp_wait(&c->p_full[1], np1 & 1, c, status);
+                    go = product(1, vs, j > 0, np1 & 1);
                     if (!go) break;
                     ++np1;
-                    tc_fence_after();
-                    values(1, vs, j > 0);
                     umma_commit_warp(bar_empty + vs * 8);
                     if (more) {
                         scores(1, 1, ks);
@@ -597,12 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!go) break;
                     next_stage();
                     if (j == tail_j) clear_tail(vs);
-                    go = warp_wait(&c->p_full[w], (w ? np1 : np0) & 1, c, status);
+                    go = product(w, vs, j > 1, (w ? np1 : np0) & 1);
                     if (!go) break;
                     if (w) ++np1;
                     else ++np0;
-                    tc_fence_after();
-                    values(w, vs, j > 1);
                     umma_commit_warp(bar_empty + vs * 8);
                     if (j + 2 < n) {
                         go = wait_stage();
@@ -695,6 +731,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v[32 * x + e] = (see >> e) & 1 ? v[32 * x + e] : -INFINITY;
                         }
                     }
+                    // The first half of P is computed with the reference as it was, beside the
+                    // row's maximum (the one needs the exponential unit, the other does not).
+                    // Only where a row has outgrown its reference is it done again; P
+                    // goes to tensor memory, which nobody reads before it is handed over.
+                    const uint64_t scale2 = f32x2(sl2, sl2);
+                    uint64_t sum[2] = {0, 0};
+                    float neg = m == -INFINITY ? 0.f : -m;
+                    auto quarter = [&](int x) {
+                        const uint64_t neg2 = f32x2(neg, neg);
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float a, d;
+                            f32x2_split(fma_f32x2(f32x2(v[32 * x + e], v[32 * x + e + 1]), scale2, neg2),
+                                        a, d);
+                            a = ex2_approx(a);
+                            d = ex2_approx(d);
+                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(a, d));
+                            hi[e / 2] = pack_bf16(a, d);
+                            if (F32) lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
+                        }
+                        tmem_st16(t_s + 16 * x, hi);
+                        if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
+                    };
+                    quarter(0);
+                    quarter(1);
                     float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
                     for (int e = 4; e + 8 <= kKeys; e += 8)
@@ -725,31 +787,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         l *= alpha;
                         m = to;
+                        neg = m == -INFINITY ? 0.f : -m;
+                        sum[0] = sum[1] = 0;
+                        tmem_st_wait();
+                        quarter(0);
+                        quarter(1);
                     }
-                    const float neg = m == -INFINITY ? 0.f : -m;
-                    const uint64_t neg2 = f32x2(neg, neg), scale2 = f32x2(sl2, sl2);
-                    uint64_t sum[2] = {0, 0};
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        uint32_t hi[16], lo[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            float a, d;
-                            f32x2_split(fma_f32x2(f32x2(v[32 * x + e], v[32 * x + e + 1]), scale2, neg2),
-                                        a, d);
-                            a = ex2_approx(a);
-                            d = ex2_approx(d);
-                            sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(a, d));
-                            hi[e / 2] = pack_bf16(a, d);
-                            if (F32) lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
-                        }
-                        tmem_st16(t_s + 16 * x, hi);
-                        if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
-                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c->p_half[w]);
+                    quarter(2);
+                    quarter(3);
                     float s0, s1;
                     f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
                     l += s0 + s1;
                     tmem_st_wait();
+                } else if (lane == 0) {
+                    mbar_arrive(&c->p_half[w]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -778,11 +833,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = a.y * w0 + d.y * w1;
             }
             tc_fence_after();
-            const int trow = min(row, it.rows - 1);
-            const int64_t oh = (int64_t)(it.tok0 + (trow >> lg)) * p.Hq + it.h * G + (trow & (G - 1));
             const bool live = row < it.rows;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            // partial results: slot of this CTA's piece
+            // (token, head) row of `out` that row `x` of the block is
+            auto out_row = [&](int x) {
+                return (int64_t)(it.tok0 + (x >> lg)) * p.Hq + it.h * G + (x & (G - 1));
+            };
+            // 32 columns of the warp's 32 rows to `out`: four lanes write 64 bytes
+            // of one row together (a lane by itself would touch one line per 16 bytes)
+            auto store32 = [&](const float (&o)[32], float k, int x) {
+                constexpr int kParts = F32 ? 2 : 1;
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                    uint4 u[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float* f = o + (F32 ? 16 * part + 4 * e : 8 * e);
+                        if (F32)
+                            u[e] = make_uint4(__float_as_uint(f[0] * k), __float_as_uint(f[1] * k),
+                                              __float_as_uint(f[2] * k), __float_as_uint(f[3] * k));
+                        else
+                            u[e] = make_uint4(pack_bf16(f[0] * k, f[1] * k), pack_bf16(f[2] * k, f[3] * k),
+                                              pack_bf16(f[4] * k, f[5] * k), pack_bf16(f[6] * k, f[7] * k));
+                    }
+                    transpose4(u, lane);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int x_row = wrow0 + q4 * 32 + (lane & ~3) + e;
+                        if (x_row < it.rows)
+                            reinterpret_cast<uint4*>(
+                                static_cast<uint8_t*>(p.out) +
+                                (out_row(x_row) * D + x + (F32 ? 16 * part : 0)) * (F32 ? 4 : 2))[lane & 3] =
+                                u[e];
+                    }
+                }
+            };
+            // partial results of a cut block: [piece][group] (reference, sum) of 128 rows and
+            // 16-byte column units of 128 rows each
             const size_t part_rows = (size_t)2 * 128;
             uint8_t* parts = p.ws + kPartOff;
             const size_t slot_bytes = part_rows * (8 + 4 * D);
@@ -791,14 +878,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return reinterpret_cast<float2*>(parts + s * slot_bytes) + w * 128;
             };
             auto part_o = [&](int s) {
-                return reinterpret_cast<float*>(parts + s * slot_bytes + part_rows * 8) +
-                       (size_t)w * 128 * D;
+                return reinterpret_cast<float4*>(parts + s * slot_bytes + part_rows * 8) +
+                       (size_t)w * 32 * D + r;
             };
             if (warp_live) {
                 if (it.split) {
                     part_ml(piece)[r] = make_float2(m, l);
                 } else if (p.lse && live && (both || w == 0)) {
-                    p.lse[oh] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[out_row(row)] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 }
 #pragma unroll
                 for (int x0 = 0; x0 < D; x0 += 32) {
@@ -812,29 +899,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = o[e] * w0 + o1[e] * w1;
                     }
-                    if (!live) {
-                        // padding row
-                    } else if (it.split) {
-                        float4* dst = reinterpret_cast<float4*>(part_o(piece) + (size_t)r * cols + x0);
+                    if (it.split) {
+                        float4* dst = part_o(piece) + x0 / 4 * 128;
+                        if (live) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    } else if (F32) {
-                        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + oh * D + x);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            dst[e] = make_float4(o[4 * e] * inv, o[4 * e + 1] * inv, o[4 * e + 2] * inv,
-                                                 o[4 * e + 3] * inv);
+                            for (int e = 0; e < 8; ++e)
+                                dst[e * 128] =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                        __syncwarp();
                     } else {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + oh * D + x);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                                pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                                pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                                pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+                        store32(o, inv, x);
                     }
-                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -867,66 +943,46 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++n_part;
             if (!c->last[w]) continue;
             __threadfence();
-            const int rows_here = min(128, it.rows - wrow0);
+            if (!warp_live) continue;
             auto slot_of = [&](int s) { return 2 * (it.c0 + s) + (s == 0 ? 1 : 0); };
-            // reference and sum of each row, a thread per row, kept for the group
-            {
-                float mm = -INFINITY;
-                for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
-                const float ref = mm == -INFINITY ? 0.f : mm;
-                float ll = 0.f;
-                for (int s = 0; s < pieces; ++s) {
-                    const float2 x = __ldcg(&part_ml(slot_of(s))[r]);
-                    ll += x.y * ex2_approx(x.x - ref);
-                }
-                c->ml[w][r] = make_float2(ref, ll > 0.f ? 1.f / ll : 0.f);
-                if (p.lse && live && (both || w == 0))
-                    p.lse[oh] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            float mm = -INFINITY;
+            for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
+            const float ref = mm == -INFINITY ? 0.f : mm;
+            float ll = 0.f;
+            for (int s = 0; s < pieces; ++s) {
+                const float2 x = __ldcg(&part_ml(slot_of(s))[r]);
+                ll += x.y * ex2_approx(x.x - ref);
             }
-            __syncwarp();
-            // the warp's own 32 rows, kJoin at a time (their loads overlap), lanes over columns
-            constexpr int kJoin = 8;
-            const int lanes = cols / 4;              // 16-byte vectors of a row
-            for (int r0 = q4 * 32; r0 < min(q4 * 32 + 32, rows_here); r0 += kJoin) {
-                float4 acc[kJoin];
+            if (p.lse && live && (both || w == 0))
+                p.lse[out_row(row)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+            const float iv = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll 1
+            for (int x0 = 0; x0 < cols; x0 += 32) {
+                float o[32];
 #pragma unroll
-                for (int i = 0; i < kJoin; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 2
                 for (int s = 0; s < pieces; ++s) {
-                    const float4* src = reinterpret_cast<const float4*>(part_o(slot_of(s)));
-                    const float2* ml = part_ml(slot_of(s));
-                    float4 y[kJoin];
-                    float f[kJoin];
+                    const int sl = slot_of(s);
+                    float4 y[8];
+                    if (live) {
 #pragma unroll
-                    for (int i = 0; i < kJoin; ++i) {
-                        const int rr = min(r0 + i, rows_here - 1);
-                        f[i] = __ldcg(&ml[rr]).x;
-                        y[i] = __ldcg(src + (size_t)rr * lanes + min(lane, lanes - 1));
+                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(part_o(sl) + (x0 / 4 + e) * 128);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+                    const float k = ex2_approx(__ldcg(&part_ml(sl)[r]).x - ref);
 #pragma unroll
-                    for (int i = 0; i < kJoin; ++i) {
-                        const float k = ex2_approx(f[i] - c->ml[w][min(r0 + i, rows_here - 1)].x);
-                        acc[i].x += y[i].x * k;
-                        acc[i].y += y[i].y * k;
-                        acc[i].z += y[i].z * k;
-                        acc[i].w += y[i].w * k;
+                    for (int e = 0; e < 8; ++e) {
+                        o[4 * e] += y[e].x * k;
+                        o[4 * e + 1] += y[e].y * k;
+                        o[4 * e + 2] += y[e].z * k;
+                        o[4 * e + 3] += y[e].w * k;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < kJoin; ++i) {
-                    if (r0 + i >= rows_here || lane >= lanes) continue;
-                    const int brow = wrow0 + r0 + i;
-                    const int64_t o2 =
-                        (int64_t)(it.tok0 + (brow >> lg)) * p.Hq + it.h * G + (brow & (G - 1));
-                    const float iv = c->ml[w][r0 + i].y;
-                    const int64_t at = o2 * D + col0 + lane * 4;
-                    if (F32)
-                        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(
-                            acc[i].x * iv, acc[i].y * iv, acc[i].z * iv, acc[i].w * iv);
-                    else
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) =
-                            make_uint2(pack_bf16(acc[i].x * iv, acc[i].y * iv),
-                                       pack_bf16(acc[i].z * iv, acc[i].w * iv));
-                }
+                __syncwarp();
+                store32(o, iv, col0 + x0);
             }
         }
     }
@@ -941,8 +997,8 @@ template <int D, bool F32>
 cudaError_t run(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                 const Params& p, int grid, cudaStream_t s) {
     auto kern = chunk_attn_kernel<D, F32>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Shape<D>::kSmem));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem(kern, Shape<D>::kSmem, done);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(grid), dim3(kThreads), Shape<D>::kSmem, s, tq, tk, tv, p);
 }
