@@ -49,6 +49,7 @@ static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * kThreads, "registers of 
 constexpr int kItems = 4;                          // work items in flight between the roles
 constexpr int kMaxCtas = 256;
 constexpr int kBlockCost = 2;                      // a block's fixed work, in tiles
+constexpr int kMinShare = 4;                       // units a CTA takes at least
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -85,7 +86,7 @@ struct Item {
 struct Params {
     se_paged_kv kv;
     se_chunk ck;
-    int batch, G, Hq;
+    int batch, G, lg, Hq;          // G = 1 << lg query heads per KV head
     int max_blocks;                // blocks numbered at most
     int window, sink;
     float scale_log2;              // > 0
@@ -138,9 +139,8 @@ __device__ __forceinline__ Tiles block_tiles(const Params& p, const Seq& s, int 
     const int row0 = blk * kBlockRows;
     t.rows = min(kBlockRows, s.n * p.G - row0);
     if (blk < 0 || t.rows <= 0) return t;
-    const int tok = row0 / p.G;
-    const int p_lo = s.p0 + tok;
-    const int keys = min(p_lo + (t.rows + p.G - 1) / p.G, s.len);     // keys below this are seen
+    const int p_lo = s.p0 + (row0 >> p.lg);
+    const int keys = min(p_lo + ((t.rows + p.G - 1) >> p.lg), s.len);    // keys below this are seen
     const int th = (keys + kKeys - 1) / kKeys;
     if (p.window > 0) {
         t.tl = min(max(0, p_lo - p.window + 1) / kKeys, th);
@@ -149,6 +149,21 @@ __device__ __forceinline__ Tiles block_tiles(const Params& p, const Seq& s, int 
     t.n = max(1, t.ts + th - t.tl);
     return t;
 }
+
+// Shares of U units over n CTAs: the first `extra` CTAs get one more than the others.
+__device__ __forceinline__ unsigned long long udiv(unsigned long long a, unsigned long long b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+struct Shares {
+    long long each, extra;
+    __device__ __forceinline__ Shares(long long U, long long n)
+        : each(static_cast<long long>(udiv(U, n))), extra(U - each * n) {}
+    __device__ __forceinline__ long long begin(int c) const { return each * c + min((long long)c, extra); }
+    __device__ __forceinline__ int of(long long u) const {       // the CTA whose share holds unit u
+        const long long big = extra * (each + 1);
+        return static_cast<int>(u < big ? udiv(u, each + 1) : extra + udiv(u - big, each));
+    }
+};
 
 __device__ __forceinline__ int block_cost(const Tiles& t) { return t.n > 0 ? t.n + kBlockCost : 0; }
 
@@ -312,9 +327,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         total += sum;
     }
     // (no share is empty: a block's pieces are those of consecutive CTAs)
-    const long long U = total * H, NC = min((long long)gridDim.x, U);
+    const long long U = total * H;
+    const long long NC = min((long long)gridDim.x, (U + kMinShare - 1) / kMinShare);
+    const Shares shares(U, max(1ll, NC));
     const bool idle = blockIdx.x >= NC;
-    const long long u0 = idle ? 0 : U * blockIdx.x / NC, u1 = idle ? 0 : U * (blockIdx.x + 1) / NC;
+    const long long u0 = idle ? 0 : shares.begin(blockIdx.x), u1 = idle ? 0 : shares.begin(blockIdx.x + 1);
     long long* s_start = sums + 16;                  // first block, its prefix
     if (u0 < u1) {
         long long base = 0;
@@ -392,30 +409,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const int cost = block_cost(t);
-            Item it;
+            Item it = {};
             it.b = b;
             it.n = 0;
             long long next = u1;
             if (u < u1 && t.n > 0) {             // (n stays 0 if the share ends before a tile)
                 if (first) {
-                    h = static_cast<int>((u - pre * H) / cost);
+                    h = static_cast<int>(udiv(u - pre * H, cost));
                     first = false;
                 }
                 const long long us = pre * H + (long long)h * cost;      // the item's first unit
                 const long long t0 = us + kBlockCost;                    // its first tile's
                 next = min(u1, us + cost);
                 it.h = h;
-                it.tok0 = s.s0 + blk * (kBlockRows / G);
+                it.tok0 = s.s0 + blk * (kBlockRows >> p.lg);
                 it.rows = t.rows;
-                it.pos0 = s.p0 + blk * (kBlockRows / G);
+                it.pos0 = s.p0 + blk * (kBlockRows >> p.lg);
                 it.len = s.len;
                 it.ts = t.ts;
                 it.tl = t.tl;
                 it.j0 = static_cast<int>(max(0ll, u - t0));
                 it.n = static_cast<int>(max(0ll, next - t0)) - it.j0;
                 it.split = it.n < t.n;
-                it.c0 = static_cast<int>(((t0 + 1) * NC - 1) / U);
-                it.c1 = static_cast<int>(((us + cost) * NC - 1) / U);
+                if (it.split) {
+                    it.c0 = shares.of(t0);
+                    it.c1 = shares.of(us + cost - 1);
+                }
             }
             const int slot = items % kItems;
             if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
@@ -465,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int w = 0; w < tiles; ++w)
                         for (int hf = 0; hf < S::kHalves; ++hf)
                             tma_load_3d(qs + w * S::kTile + hf * S::kRegion, &tq, &c->q_full, hf * 64,
-                                        it.h * G, it.tok0 + w * (128 / G));
+                                        it.h * G, it.tok0 + w * (128 >> p.lg));
                 }
                 __syncwarp();
                 if (go) ++loads_q;
@@ -666,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = q4 * 32 + lane;                // row of the accumulator
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         const uint32_t t_s = lane_base + w * 128;
-        const int lg = __ffs(G) - 1;
+        const int lg = p.lg;
         const float sl2 = p.scale_log2;
         uint32_t ns = 0;                             // S tiles seen by this group
         uint32_t no = 0;                             // P tiles handed to the tensor cores
@@ -733,8 +752,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     // The first half of P is computed with the reference as it was, beside the
                     // row's maximum (the one needs the exponential unit, the other does not).
-                    // Only where a row has outgrown its reference is it done again; P
-                    // goes to tensor memory, which nobody reads before it is handed over.
+                    // Only where a row has outgrown its reference is it done again (and
+                    // for the first tile, which has none, only then); P goes to tensor
+                    // memory, which nobody reads before it is handed over.
                     const uint64_t scale2 = f32x2(sl2, sl2);
                     uint64_t sum[2] = {0, 0};
                     float neg = m == -INFINITY ? 0.f : -m;
@@ -755,8 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(t_s + 16 * x, hi);
                         if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
                     };
-                    quarter(0);
-                    quarter(1);
+                    if (i > 0) {
+                        quarter(0);
+                        quarter(1);
+                    }
                     float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
                     for (int e = 4; e + 8 <= kKeys; e += 8)
@@ -767,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[kKeys - 4 + x]);
                     const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
                     const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
-                    if (__any_sync(0xffffffffu, grow)) {
+                    if (i == 0 || __any_sync(0xffffffffu, grow)) {
                         const float to = grow ? top : m;
                         const float alpha = to == m ? 1.f : ex2_approx(m - to);
                         if (i > 0) {
@@ -945,10 +967,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __threadfence();
             if (!warp_live) continue;
             auto slot_of = [&](int s) { return 2 * (it.c0 + s) + (s == 0 ? 1 : 0); };
-            float mm = -INFINITY;
+            float mm = -INFINITY, ll = 0.f;
+#pragma unroll 8
             for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
             const float ref = mm == -INFINITY ? 0.f : mm;
-            float ll = 0.f;
+#pragma unroll 8
             for (int s = 0; s < pieces; ++s) {
                 const float2 x = __ldcg(&part_ml(slot_of(s))[r]);
                 ll += x.y * ex2_approx(x.x - ref);
@@ -961,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
                 for (int s = 0; s < pieces; ++s) {
                     const int sl = slot_of(s);
                     float4 y[8];
@@ -1020,6 +1043,7 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
     p.ck = ck;
     p.batch = batch;
     p.G = a.Hq / H;
+    for (p.lg = 0; 1 << p.lg < p.G;) ++p.lg;
     p.Hq = a.Hq;
     p.max_blocks = static_cast<int>((int64_t)ck.max_tokens * p.G / kBlockRows) + batch;
     p.window = a.window;

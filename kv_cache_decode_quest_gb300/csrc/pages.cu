@@ -131,6 +131,11 @@ __global__ void __launch_bounds__(1024)
         bad_flags |= SE_DEV_BAD_LENGTH;
         n_free = n_free < 0 ? 0 : pool.num_pages;
     }
+    // in one pass (batch <= nt): what this thread's sequence holds afterwards (-1: as
+    // before), and the pages taken by all
+    int holds = -1;
+    __shared__ int s_taken;
+    if (threadIdx.x == 0) s_taken = 0;
     long long row_base = 0, need_base = 0;
     for (int b0 = 0; b0 < batch; b0 += nt) {
         const int b = b0 + threadIdx.x;
@@ -151,6 +156,11 @@ __global__ void __launch_bounds__(1024)
         if (ok && s.need > 0 && need + s.need > n_free) {
             ok = false;
             s.flags |= SE_DEV_CAPACITY;
+        }
+        // pages go out in sequence order, so the last served sequence's end is the sum
+        if (batch <= nt && ok && s.need > 0) {
+            holds = s.held + s.need;
+            atomicMax(&s_taken, static_cast<int>(need + s.need));
         }
         s_start[threadIdx.x] = static_cast<int>(min(row, max_rows));
         s_ctx[threadIdx.x] = s.ctx;
@@ -202,8 +212,18 @@ __global__ void __launch_bounds__(1024)
         ck.slot[t] = -1;
     }
     if (bad_flags) flag(status, bad_flags);
-    if (!last_block(ws + kCounterWord)) return;
-    // commit: the same scan, now storing what each served sequence holds
+    if (gridDim.x > 1 && !last_block(ws + kCounterWord)) return;
+    if (batch <= nt) {
+        // every block knows what each sequence takes
+        if (holds >= 0) pool.n_pages[threadIdx.x] = holds;
+        if (threadIdx.x == 0) {
+            *pool.n_free = n_free - s_taken;
+            ws[kCounterWord] = 0;
+        }
+        return;
+    }
+    __syncthreads();                             // (one block: its reads of n_pages are done)
+    // the same scan again, now storing what each served sequence holds
     long long taken = 0;
     row_base = need_base = 0;
     for (int b0 = 0; b0 < batch; b0 += nt) {
@@ -255,18 +275,22 @@ __global__ void __launch_bounds__(1024)
         }
         return n;
     };
-    long long total = 0;
+    long long total = 0, mine = 0;                 // mine: in one pass, pages before this sequence's
     for (int b0 = 0; b0 < batch; b0 += nt) {
-        long long held = held_of(b0 + threadIdx.x), none = 0, sum = 0, nones = 0;
-        block_scan2(held, none, tmp, &sum, &nones);
+        long long none = 0, sum = 0, nones = 0;
+        mine = held_of(b0 + threadIdx.x);
+        block_scan2(mine, none, tmp, &sum, &nones);
         total += sum;
     }
     const bool fits = n_free + total <= pool.num_pages;
     if (!fits) bad_flags |= SE_DEV_CAPACITY;
     long long base = 0;
     for (int b0 = 0; fits && b0 < batch; b0 += nt) {
-        long long first = held_of(b0 + threadIdx.x), none = 0, sum = 0, nones = 0;
-        block_scan2(first, none, tmp, &sum, &nones);
+        long long first = mine, none = 0, sum = total, nones = 0;
+        if (batch > nt) {
+            first = held_of(b0 + threadIdx.x);
+            block_scan2(first, none, tmp, &sum, &nones);
+        }
         s_first[threadIdx.x] = first;
         if (threadIdx.x == 0) s_first[nt] = sum;
         __syncthreads();
@@ -283,7 +307,8 @@ __global__ void __launch_bounds__(1024)
         __syncthreads();
     }
     if (bad_flags) flag(status, bad_flags);
-    if (!last_block(ws + kCounterWord)) return;
+    if (gridDim.x > 1 && !last_block(ws + kCounterWord)) return;
+    __syncthreads();                             // (one block: its reads of n_pages are done)
     if (fits) {
         for (int b = threadIdx.x; b < batch; b += nt) {
             if (done[b] == 0) continue;
