@@ -187,18 +187,21 @@ struct Ctrl {
     float2 ml[2][128];                     // of a block that both groups share
 };
 
-// Warp-uniform bounded wait.
+// Warp-uniform bounded wait.  Tries are counted (each is suspended by the hardware for
+// some time of its own choice) rather than a clock read: that keeps the code of the
+// many waits short, and a first pass through this kernel runs at the rate its
+// code arrives.  A suspension hint, or polling without one, made a chunk of 2048 at
+// 32K 5% slower than this form.
+constexpr uint32_t kWaitTries = 1u << 20;
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* c, int* status) {
-    bool ok = mbar_try_wait(bar, parity);
-    if (!__all_sync(0xffffffffu, ok)) {
-        if (!ok) ok = mbar_wait(bar, parity, &c->abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok && (threadIdx.x & 31) == 0) {
-            *static_cast<volatile int*>(&c->abort) = 1;
-            flag(status, SE_DEV_TIMEOUT);
-        }
+#pragma unroll 1
+    for (uint32_t n = 0;; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if (n == kWaitTries || __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->abort))) break;
     }
-    return ok;
+    *static_cast<volatile int*>(&c->abort) = 1;
+    flag(status, SE_DEV_TIMEOUT);
+    return false;
 }
 
 // 4 x 4 transpose of 16-byte units over each group of four lanes: lane i ends with
@@ -533,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bar_q = smem_u32(&c->q_empty);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         uint32_t st = 0, ph = 0;                     // ring stage and its phase
-        uint32_t np0 = 0, np1 = 0;                   // phases of P of each group
+        uint32_t np = 0;                             // bit w: phase of group w's P
         auto wait_stage = [&]() { return warp_wait(&c->full[st], ph, c, status); };
         auto next_stage = [&]() {
             if (++st == S::kStages) {
@@ -544,25 +547,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto scores = [&](uint32_t w, uint32_t qt, uint32_t stage) {      // S_w = Q_qt K^T
             const uint32_t ka = k_lo + stage * (S::kTile / 16), qa = q_lo + qt * (S::kTile / 16);
 #pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks) {
-                constexpr int kHalf = S::kRegion / 16;
-                const uint32_t off = (ks >> 2) * kHalf + (ks & 3) * 2;
-                umma_bf16_warp(tm + w * 128, qa + off, q_hi, ka + off, k_hi, idesc_s, ks > 0);
-            }
+            for (int x = 0; x < S::kHalves; ++x)
+                umma_bf16_warp4(tm + w * 128, qa + x * (S::kRegion / 16), q_hi,
+                                ka + x * (S::kRegion / 16), k_hi, idesc_s, x > 0);
             umma_commit_warp(bar_s + w * 8);
         };
         // O_w (+)= P_w V for the first / second 64 keys of the tile
         auto values = [&](uint32_t w, uint32_t stage, uint32_t acc, int half) {
-            const uint32_t va = v_lo + stage * (S::kTile / 16);
+            const uint32_t va = v_lo + stage * (S::kTile / 16) + half * 512;
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part)
-#pragma unroll
-                for (int k = 0; k < kKeys / 32; ++k) {
-                    const int ks = half * (kKeys / 32) + k;
-                    umma_bf16_ts_warp(tm + 256 + w * D, tm + w * 128 + part * 64 + ks * 8,
-                                      va + ks * 128, v_hi, idesc_o,
-                                      half + part + k > 0 ? 1u : acc);
-                }
+                umma_bf16_ts_warp4(tm + 256 + w * D, tm + w * 128 + part * 64 + half * 32, va, v_hi,
+                                   idesc_o, half + part > 0 ? 1u : acc);
         };
         auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase) -> bool {
             if (!warp_wait(&c->p_half[w], phase, c, status)) return false;
@@ -604,71 +600,51 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            // ring order: K0, then for each tile j: K_{j + 1}, V_j
-            if (!warp_wait(&c->q_full, items & 1, c, status) || !wait_stage()) break;
-            tc_fence_after();
-            scores(0, 0, st);
-            if (both) scores(1, 1, st);
-            umma_commit_warp(bar_empty + st * 8);
-            next_stage();
-            if (!both && n > 1) {
-                if (!wait_stage()) break;
-                tc_fence_after();
-                scores(1, 0, st);
-                umma_commit_warp(bar_empty + st * 8);
-                next_stage();
-            }
-            const int ahead = both ? 1 : 2;          // tiles the scores run ahead
-            if (n <= ahead) umma_commit_warp(bar_q);
+            // The scores run `ahead` tiles before the products: both groups take every
+            // tile, or tile j is group j & 1's.  Ring order: K0, then for each tile j:
+            // K_{j + 1}, V_j (the same order either way).
+            if (!warp_wait(&c->q_full, items & 1, c, status)) break;
+            const int ahead = both ? 1 : 2;
             bool go = true;
-            if (both) {
-                for (int j = 0; j < n; ++j) {
-                    const bool more = j + 1 < n;
-                    const uint32_t ks = st, kph = ph;
-                    if (more) next_stage();
-                    const uint32_t vs = st;
-                    go = wait_stage();               // V_j (K_{j + 1} was loaded before it)
-                    next_stage();
-                    if (go && more) go = warp_wait(&c->full[ks], kph, c, status);
-                    if (!go) break;
-                    if (j == tail_j) clear_tail(vs);
-                    go = product(0, vs, j > 0, np0 & 1);
-                    if (!go) break;
-                    ++np0;
-                    if (more) scores(0, 0, ks);
-                    go = product(1, vs, j > 0, np1 & 1);
-                    if (!go) break;
-                    ++np1;
-                    umma_commit_warp(bar_empty + vs * 8);
-                    if (more) {
-                        scores(1, 1, ks);
-                        umma_commit_warp(bar_empty + ks * 8);
-                        if (j + 2 == n) umma_commit_warp(bar_q);
-                    }
-                }
-            } else {
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t w = j & 1;
-                    const uint32_t vs = st;          // V_j, then K_{j + 2}
+#pragma unroll 1
+            for (int j = -ahead; j < n; ++j) {
+                const bool more = j + ahead < n;
+                uint32_t ks = st, kph = ph;
+                if (both && more) next_stage();
+                const uint32_t vs = st;
+                if (j >= 0) {
                     go = wait_stage();
                     if (!go) break;
                     next_stage();
                     if (j == tail_j) clear_tail(vs);
-                    go = product(w, vs, j > 1, (w ? np1 : np0) & 1);
-                    if (!go) break;
-                    if (w) ++np1;
-                    else ++np0;
-                    umma_commit_warp(bar_empty + vs * 8);
-                    if (j + 2 < n) {
-                        go = wait_stage();
+                }
+                if (!both) {
+                    ks = st;
+                    kph = ph;
+                    if (more) next_stage();
+                }
+                const uint32_t w_begin = both ? 0 : j & 1;
+                const uint32_t w_end = both ? 2 : (j & 1) + 1;
+#pragma unroll 1
+                for (uint32_t w = w_begin; w < w_end; ++w) {
+                    if (j >= 0) {
+                        go = product(w, vs, j >= ahead, (np >> w) & 1);
                         if (!go) break;
-                        tc_fence_after();
-                        scores(w, 0, st);
-                        umma_commit_warp(bar_empty + st * 8);
-                        next_stage();
-                        if (j + 3 == n) umma_commit_warp(bar_q);
+                        np ^= 1u << w;
+                        if (w + 1 == w_end) umma_commit_warp(bar_empty + vs * 8);
+                    }
+                    if (more) {
+                        if (w == w_begin) {
+                            go = warp_wait(&c->full[ks], kph, c, status);
+                            if (!go) break;
+                            tc_fence_after();
+                        }
+                        scores(w, both ? w : 0, ks);
                     }
                 }
+                if (!go) break;
+                if (more) umma_commit_warp(bar_empty + ks * 8);
+                if (j + ahead == n - 1) umma_commit_warp(bar_q);
             }
             if (!go) break;
         }
@@ -775,21 +751,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(t_s + 16 * x, hi);
                         if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
                     };
-                    if (i > 0) {
-                        quarter(0);
-                        quarter(1);
-                    }
-                    float mx[4] = {v[0], v[1], v[2], v[3]};
+                    bool settled = false;
+                    while (true) {                   // (one copy of the code: it is long)
+                        if (settled || i > 0) {
+                            quarter(0);
+                            quarter(1);
+                        }
+                        if (settled) break;
+                        settled = true;
+                        float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                    for (int e = 4; e + 8 <= kKeys; e += 8)
+                        for (int e = 4; e + 8 <= kKeys; e += 8)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            mx[x] = fmaxf(fmaxf(mx[x], v[e + x]), v[e + 4 + x]);
+                            for (int x = 0; x < 4; ++x)
+                                mx[x] = fmaxf(fmaxf(mx[x], v[e + x]), v[e + 4 + x]);
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[kKeys - 4 + x]);
-                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                    const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
-                    if (i == 0 || __any_sync(0xffffffffu, grow)) {
+                        for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[kKeys - 4 + x]);
+                        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+                        const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
+                        if (i > 0 && !__any_sync(0xffffffffu, grow)) break;
                         const float to = grow ? top : m;
                         const float alpha = to == m ? 1.f : ex2_approx(m - to);
                         if (i > 0) {
@@ -812,9 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         neg = m == -INFINITY ? 0.f : -m;
                         sum[0] = sum[1] = 0;
                         tmem_st_wait();
-                        quarter(0);
-                        quarter(1);
                     }
+                    if (!ok) break;
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -909,9 +888,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (p.lse && live && (both || w == 0)) {
                     p.lse[out_row(row)] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 }
-#pragma unroll
-                for (int x0 = 0; x0 < D; x0 += 32) {
-                    if (x0 >= cols) break;
+#pragma unroll 1
+                for (int x0 = 0; x0 < cols; x0 += 32) {
                     const int x = col0 + x0;
                     float o[32];
                     tmem_ld32(lane_base + 256 + (both ? w * D : 0) + x, o);
@@ -968,10 +946,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_live) continue;
             auto slot_of = [&](int s) { return 2 * (it.c0 + s) + (s == 0 ? 1 : 0); };
             float mm = -INFINITY, ll = 0.f;
-#pragma unroll 8
+#pragma unroll 4
             for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
             const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 8
+#pragma unroll 4
             for (int s = 0; s < pieces; ++s) {
                 const float2 x = __ldcg(&part_ml(slot_of(s))[r]);
                 ll += x.y * ex2_approx(x.x - ref);
@@ -984,7 +962,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float o[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
                 for (int s = 0; s < pieces; ++s) {
                     const int sl = slot_of(s);
                     float4 y[8];

@@ -483,31 +483,50 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t smem_addr, uint3
 constexpr uint32_t kUmmaNegateA = 1u << 13;      // instruction descriptor: -A * B
 constexpr uint32_t kUmmaBMnMajor = 1u << 16;     // instruction descriptor: B is MN-major
 // Whole-warp forms: every lane passes the same (warp-uniform) operands, one elected
-// lane issues.  The operands then stay in uniform registers, which the
-// instructions take: a lane-0 branch around the same instructions moves every
-// descriptor there one by one.  The descriptor's high word is constant for
-// an operand, the low word is base + offset / 16.
-__device__ __forceinline__ void umma_bf16_warp(uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi,
-                                               uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
-                                               uint32_t accumulate) {
+// lane issues four instructions (K = 64).  The operands then stay in uniform
+// registers, which the instructions take: a lane-0 branch around the same
+// instructions moves every descriptor there one by one.  A descriptor's high word is
+// constant for an operand, its low word is base + offset / 16.
+// A and B K-major with the 128-byte swizzle: 16 elements of K are 32 bytes.
+__device__ __forceinline__ void umma_bf16_warp4(uint32_t tmem_d, uint32_t a_lo, uint32_t a_hi,
+                                                uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                                uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
         "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t"
+        "add.u32 x, %1, 2;\n\tadd.u32 y, %3, 2;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 4;\n\tadd.u32 y, %3, 4;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t"
+        "add.u32 x, %1, 6;\n\tadd.u32 y, %3, 6;\n\t"
+        "mov.b64 a, {x, %2};\n\tmov.b64 b, {y, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, t;\n\t}"
         ::"r"(tmem_d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
 }
-// A from tensor memory (two K elements per 32-bit column), B from shared memory.
-__device__ __forceinline__ void umma_bf16_ts_warp(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
-                                                  uint32_t b_hi, uint32_t idesc,
-                                                  uint32_t accumulate) {
+// A from tensor memory (two K elements per 32-bit column: 16 of K are 8 columns), B
+// MN-major from shared memory (16 rows of K are 2048 bytes).
+__device__ __forceinline__ void umma_bf16_ts_warp4(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
+                                                   uint32_t b_hi, uint32_t idesc,
+                                                   uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "{\n\t.reg .pred p, q, t;\n\t.reg .b64 b;\n\t.reg .b32 x, y;\n\t"
         "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
         "mov.b64 b, {%2, %3};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t}"
         ::"r"(tmem_d), "r"(tmem_a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
 }
 __device__ __forceinline__ void umma_commit_warp(uint32_t bar) {
