@@ -27,6 +27,7 @@
 // A block cut between CTAs is joined by the last of them to finish, in the
 // order of its keys (the result does not depend on timing).
 #include <algorithm>
+#include <cstddef>
 
 #include "cudaTypedefs.h"
 
@@ -55,11 +56,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;                    // log2 of the growth that rescales O
 
-// Workspace: status word, at byte 256 the arrival counters [kMaxCtas][2], then
+// Workspace: status word, at byte 256 the arrival counters [kMaxCtas][8 warps], then
 // the partial results: two pieces per CTA (the one it takes over and the one it hands
 // on), each [2 groups][128] (reference, sum) and [2][128][D] fp32.
 constexpr size_t kCounterOff = 256;
-constexpr size_t kPartOff = kCounterOff + kMaxCtas * 2 * sizeof(int);
+constexpr size_t kPartOff = kCounterOff + kMaxCtas * 8 * sizeof(int);
 
 template <int D>
 struct Shape {
@@ -80,7 +81,7 @@ struct Item {
     int ts, tl;        // tile j is key tile j (j < ts), else j - ts + tl
     int j0, n;         // this piece: tiles [j0, j0 + n); n = 0: no more work
     int split;         // the block is cut: this piece is partial
-    int c0, c1;        // CTAs that share the block
+    long long t0, t1;  // the block's tiles as units of work
 };
 
 struct Params {
@@ -158,6 +159,7 @@ struct Shares {
     long long each, extra;
     __device__ __forceinline__ Shares(long long U, long long n)
         : each(static_cast<long long>(udiv(U, n))), extra(U - each * n) {}
+    __device__ __forceinline__ Shares(long long each, long long extra, int) : each(each), extra(extra) {}
     __device__ __forceinline__ long long begin(int c) const { return each * c + min((long long)c, extra); }
     __device__ __forceinline__ int of(long long u) const {       // the CTA whose share holds unit u
         const long long big = extra * (each + 1);
@@ -172,20 +174,27 @@ __device__ __forceinline__ int tile_of(const Item& it, int j) {
 }
 
 struct Ctrl {
+    // barriers (initialised by a thread each: see barrier_count)
     uint64_t full[10], empty[10];
     uint64_t q_full, q_empty;
-    uint64_t s_full[2], p_half[2], p_full[2], o_done[2];
-    uint64_t ml_full, ml_empty;            // the groups' (reference, sum) of a shared block
-    uint64_t part[2];                      // a group's partial rows are written
-    uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t done;
+    uint64_t s_full[2], o_done[2];
+    uint64_t item_full[kItems], done;
+    uint64_t p_half[2], p_full[2];         // 4 warps each
+    uint64_t ml_full, ml_empty;            // a shared block's two groups: all softmax warps
+    uint64_t item_empty[kItems];           // all softmax warps and the MMA warp
     uint32_t tmem;
     int abort;
-    int last[2];
     int any_absent;                        // a block-table entry named no page
+    long long share_each, share_extra;
     Item items[kItems];
     float2 ml[2][128];                     // of a block that both groups share
 };
+
+constexpr int kBarriers = 10 + 10 + 2 + 2 + 2 + kItems + 1 + 2 + 2 + 2 + kItems;
+__device__ __forceinline__ uint32_t barrier_count(int i) {
+    constexpr int kOnes = 10 + 10 + 2 + 2 + 2 + kItems + 1;
+    return i < kOnes ? 1 : i < kOnes + 4 ? 4 : i < kOnes + 6 ? kSoftWarps : kSoftWarps + 1;
+}
 
 // Warp-uniform bounded wait.  Tries are counted (each is suspended by the hardware for
 // some time of its own choice) rather than a clock read: that keeps the code of the
@@ -244,40 +253,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int H = p.kv.num_kv_heads, G = p.G;
 
+    static_assert(offsetof(Ctrl, tmem) == kBarriers * 8, "barriers first");
+    if (threadIdx.x < kBarriers) {
+        mbar_init(c->full + threadIdx.x, barrier_count(threadIdx.x));
+        fence_barrier_init();
+    }
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S::kStages; ++s) {
-            mbar_init(&c->full[s], 1);
-            mbar_init(&c->empty[s], 1);
-        }
-        mbar_init(&c->q_full, 1);
-        mbar_init(&c->q_empty, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c->s_full[i], 1);
-            mbar_init(&c->p_half[i], 4);
-            mbar_init(&c->p_full[i], 4);
-            mbar_init(&c->o_done[i], 1);
-            mbar_init(&c->part[i], 4);
-        }
-        mbar_init(&c->ml_full, kSoftWarps);
-        mbar_init(&c->ml_empty, kSoftWarps);
-        for (int i = 0; i < kItems; ++i) {
-            mbar_init(&c->item_full[i], 1);
-            mbar_init(&c->item_empty[i], kSoftWarps + 1);
-        }
-        mbar_init(&c->done, 1);
         c->abort = 0;
         c->any_absent = 0;
-        fence_barrier_init();
     }
     if (warp == kSoftWarps + 1) tmem_alloc(&c->tmem, 512);
     pdl_wait();
     pdl_trigger();
 
     // ---- this CTA's share (the lengths are staged where Q and the ring will be) ----
-    long long* sums = reinterpret_cast<long long*>(smem);
+    int* sums = reinterpret_cast<int*>(smem);
     Seq* seqs = reinterpret_cast<Seq*>(smem + 1024);
     int* firsts = reinterpret_cast<int*>(smem + 1024 + (size_t)kMaxBatch * sizeof(Seq));
-    __syncthreads();
     {
         int bad = 0;
         for (int b = threadIdx.x; b < p.batch; b += kThreads) {
@@ -297,7 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return lo;
     };
-    // exclusive prefix of `v` over the threads; total in *sum
+    // exclusive prefix of `v` over the threads; total in *sum (one barrier: the warps'
+    // sums alternate between two buffers)
+    int flip = 0;
     auto scan = [&](int v, long long* sum) -> long long {
         int x = v;
 #pragma unroll
@@ -305,13 +299,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int y = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += y;
         }
-        __syncthreads();
-        if (lane == 31) sums[warp] = x;
+        int* part = sums + flip * 16;
+        flip ^= 1;
+        if (lane == 31) part[warp] = x;
         __syncthreads();
         long long before = 0, all = 0;
+#pragma unroll
         for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sums[w];
-            all += sums[w];
+            const int y = part[w];
+            before += w < warp ? y : 0;
+            all += y;
         }
         *sum = all;
         return before + x - v;
@@ -335,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Shares shares(U, max(1ll, NC));
     const bool idle = blockIdx.x >= NC;
     const long long u0 = idle ? 0 : shares.begin(blockIdx.x), u1 = idle ? 0 : shares.begin(blockIdx.x + 1);
-    long long* s_start = sums + 16;                  // first block, its prefix
+    long long* s_start = reinterpret_cast<long long*>(smem + 256);   // sequence, block, prefix
     if (u0 < u1) {
         long long base = 0;
         for (int i = 0; i < passes; ++i) {
@@ -357,21 +354,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (base * H > u0) break;                // uniform
         }
     }
+    if (threadIdx.x == 0) {
+        c->share_each = shares.each;
+        c->share_extra = shares.extra;
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
     int b = 0, blk = 0;
     long long pre = 0;
     Seq win = {0, 0, 0, 0};                          // lane i: sequence b_win + i
     int b_win = 0;
-    if (u0 < u1) {
+    if (warp == kSoftWarps && u0 < u1) {
         b = static_cast<int>(s_start[0]);
         blk = static_cast<int>(s_start[1]);
         pre = s_start[2];
         b_win = b;
         if (b + lane < p.batch) win = seqs[b + lane];
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
     const uint32_t tmem = c->tmem;
 
     if (warp >= kSoftWarps) {
@@ -434,19 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it.j0 = static_cast<int>(max(0ll, u - t0));
                 it.n = static_cast<int>(max(0ll, next - t0)) - it.j0;
                 it.split = it.n < t.n;
-                if (it.split) {
-                    it.c0 = shares.of(t0);
-                    it.c1 = shares.of(us + cost - 1);
-                }
+                it.t0 = t0;
+                it.t1 = us + cost;
             }
-            const int slot = items % kItems;
-            if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
-            if (lane == 0) {
-                c->items[slot] = it;
-                mbar_arrive(&c->item_full[slot]);
-            }
-            ++items;
-            if (it.n == 0) break;
             // lanes 0..15 issue a tile's boxes: page lane & 7, columns 64 * (lane >> 3)
             const int32_t* bt = p.kv.block_table + (int64_t)it.b * p.kv.max_pages_per_seq;
             const int absent_row = p.kv.num_pages * H * kPage;            // past the map: reads zero
@@ -477,6 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return true;
             };
             int nxt1 = fetch(0), nxt2 = fetch(1);
+            const int slot = items % kItems;
+            if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
+            if (lane == 0) {
+                c->items[slot] = it;
+                mbar_arrive(&c->item_full[slot]);
+            }
+            ++items;
+            if (it.n == 0) break;
             int row_k = row_of(0, nxt1), row_v;
             go = load(&tk, row_k);
             if (go) {
@@ -665,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = p.scale_log2;
         uint32_t ns = 0;                             // S tiles seen by this group
         uint32_t no = 0;                             // P tiles handed to the tensor cores
-        uint32_t n_ml = 0, n_part = 0;
+        uint32_t n_ml = 0;
         for (int items = 0;; ++items) {
             const int slot = items % kItems;
             if (!warp_wait(&c->item_full[slot], (items / kItems) & 1, c, status)) break;
@@ -874,7 +872,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t part_rows = (size_t)2 * 128;
             uint8_t* parts = p.ws + kPartOff;
             const size_t slot_bytes = part_rows * (8 + 4 * D);
-            const int piece = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == it.c0 ? 1 : 0);
+            int c0 = 0, pieces = 1;                  // CTAs [c0, c0 + pieces) share the block
+            if (it.split) {
+                const Shares sh(c->share_each, c->share_extra, 0);
+                c0 = sh.of(it.t0);
+                pieces = sh.of(it.t1 - 1) - c0 + 1;
+            }
+            const int piece = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0);
             auto part_ml = [&](int s) {
                 return reinterpret_cast<float2*>(parts + s * slot_bytes) + w * 128;
             };
@@ -921,30 +925,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!warp_wait(&c->ml_empty, n_ml & 1, c, status)) break;
                 ++n_ml;
             }
-            if (!it.split) continue;
-            // ---- the last CTA of a cut block joins its pieces ----
-            __threadfence();
+            if (!it.split || !warp_live) continue;
+            // ---- the pieces of a cut block are joined by the last to finish: the warps of a
+            // quadrant of a group, one in each CTA, by themselves ----
+            int is_last = 0;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c->part[w]);
-            if (!warp_wait(&c->part[w], n_part & 1, c, status)) break;
-            ++n_part;
-            int* counter = reinterpret_cast<int*>(p.ws + kCounterOff) + 2 * it.c0 + w;
-            const int pieces = it.c1 - it.c0 + 1;
-            if (q4 == 0 && lane == 0) {
-                const int before = atomicAdd(counter, 1);
-                const bool is_last = before == pieces - 1;
+            if (lane == 0) {
+                int* counter = reinterpret_cast<int*>(p.ws + kCounterOff) + 8 * c0 + warp;
+                __threadfence();
+                is_last = atomicAdd(counter, 1) == pieces - 1;
                 if (is_last) *counter = 0;
-                c->last[w] = is_last;
                 __threadfence();
             }
+            if (!__shfl_sync(0xffffffffu, is_last, 0)) continue;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c->part[w]);
-            if (!warp_wait(&c->part[w], n_part & 1, c, status)) break;
-            ++n_part;
-            if (!c->last[w]) continue;
-            __threadfence();
-            if (!warp_live) continue;
-            auto slot_of = [&](int s) { return 2 * (it.c0 + s) + (s == 0 ? 1 : 0); };
+            auto slot_of = [&](int s) { return 2 * (c0 + s) + (s == 0 ? 1 : 0); };
             float mm = -INFINITY, ll = 0.f;
 #pragma unroll 4
             for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
