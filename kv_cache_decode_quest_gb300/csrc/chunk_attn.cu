@@ -50,17 +50,18 @@ static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * kThreads, "registers of 
 constexpr int kItems = 4;                          // work items in flight between the roles
 constexpr int kMaxCtas = 256;
 constexpr int kBlockCost = 2;                      // a block's fixed work, in tiles
+constexpr int kJoinFlat = 8;                       // pieces joined in one go at most
 constexpr int kMinShare = 4;                       // units a CTA takes at least
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.f;                    // log2 of the growth that rescales O
 
-// Workspace: status word, at byte 256 the arrival counters [kMaxCtas][8 warps], then
+// Workspace: status word, at byte 256 the arrival counters [kMaxCtas][2 levels][8 warps], then
 // the partial results: two pieces per CTA (the one it takes over and the one it hands
 // on), each [2 groups][128] (reference, sum) and [2][128][D] fp32.
 constexpr size_t kCounterOff = 256;
-constexpr size_t kPartOff = kCounterOff + kMaxCtas * 8 * sizeof(int);
+constexpr size_t kPartOff = kCounterOff + kMaxCtas * 16 * sizeof(int);
 
 template <int D>
 struct Shape {
@@ -927,58 +928,88 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!it.split || !warp_live) continue;
             // ---- the pieces of a cut block are joined by the last to finish: the warps of a
-            // quadrant of a group, one in each CTA, by themselves ----
-            int is_last = 0;
-            __syncwarp();
-            if (lane == 0) {
-                int* counter = reinterpret_cast<int*>(p.ws + kCounterOff) + 8 * c0 + warp;
-                __threadfence();
-                is_last = atomicAdd(counter, 1) == pieces - 1;
-                if (is_last) *counter = 0;
-                __threadfence();
-            }
-            if (!__shfl_sync(0xffffffffu, is_last, 0)) continue;
-            __syncwarp();
-            auto slot_of = [&](int s) { return 2 * (c0 + s) + (s == 0 ? 1 : 0); };
-            float mm = -INFINITY, ll = 0.f;
-#pragma unroll 4
-            for (int s = 0; s < pieces; ++s) mm = fmaxf(mm, __ldcg(&part_ml(slot_of(s))[r]).x);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-            for (int s = 0; s < pieces; ++s) {
-                const float2 x = __ldcg(&part_ml(slot_of(s))[r]);
-                ll += x.y * ex2_approx(x.x - ref);
-            }
-            if (p.lse && live && (both || w == 0))
-                p.lse[out_row(row)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-            const float iv = ll > 0.f ? 1.f / ll : 0.f;
-#pragma unroll 1
-            for (int x0 = 0; x0 < cols; x0 += 32) {
-                float o[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 2
-                for (int s = 0; s < pieces; ++s) {
-                    const int sl = slot_of(s);
-                    float4 y[8];
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = __ldcg(part_o(sl) + (x0 / 4 + e) * 128);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                    const float k = ex2_approx(__ldcg(&part_ml(sl)[r]).x - ref);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        o[4 * e] += y[e].x * k;
-                        o[4 * e + 1] += y[e].y * k;
-                        o[4 * e + 2] += y[e].z * k;
-                        o[4 * e + 3] += y[e].w * k;
-                    }
-                }
+            // quadrant of a group, one in each CTA, by themselves.  Reading one piece after
+            // another is bound by one SM's share of L2 (about 64 bytes a clock), so
+            // many pieces are first joined in groups, by different SMs: about 2 sqrt(n) pieces
+            // one after another instead of n.  Groups and order are fixed. ----
+            const int mine = static_cast<int>(blockIdx.x) - c0;          // this CTA's piece
+            int per = pieces;                                           // pieces in a group
+            if (pieces > kJoinFlat)
+                per = static_cast<int>(ceilf(sqrtf(static_cast<float>(pieces))));
+            int first = mine / per * per;                               // the group's first piece
+            int count = min(per, pieces - first), step = 1;
+            bool final = per == pieces;
+            while (true) {
+                int is_last = 1;
                 __syncwarp();
-                store32(o, iv, col0 + x0);
+                if (lane == 0 && count > 1) {
+                    int* counter = reinterpret_cast<int*>(p.ws + kCounterOff) +
+                                   16 * (c0 + first) + (final ? 8 : 0) + warp;
+                    __threadfence();
+                    is_last = atomicAdd(counter, 1) == count - 1;
+                    if (is_last) *counter = 0;
+                    __threadfence();
+                }
+                if (!__shfl_sync(0xffffffffu, is_last, 0)) break;
+                __syncwarp();
+                auto slot_of = [&](int i) {
+                    const int s = first + i * step;
+                    return 2 * (c0 + s) + (s == 0 ? 1 : 0);
+                };
+                if (count > 1) {
+                    float mm = -INFINITY, ll = 0.f;
+#pragma unroll 4
+                    for (int i = 0; i < count; ++i)
+                        mm = fmaxf(mm, __ldcg(&part_ml(slot_of(i))[r]).x);
+                    const float ref = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 4
+                    for (int i = 0; i < count; ++i) {
+                        const float2 x = __ldcg(&part_ml(slot_of(i))[r]);
+                        ll += x.y * ex2_approx(x.x - ref);
+                    }
+                    if (final && p.lse && live && (both || w == 0))
+                        p.lse[out_row(row)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
+                    const float iv = ll > 0.f ? 1.f / ll : 0.f;
+#pragma unroll 1
+                    for (int x0 = 0; x0 < cols; x0 += 32) {
+                        float o[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+#pragma unroll 2
+                        for (int i = 0; i < count; ++i) {
+                            const int sl = slot_of(i);
+                            float4 y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                y[e] = live ? __ldcg(part_o(sl) + (x0 / 4 + e) * 128)
+                                            : make_float4(0.f, 0.f, 0.f, 0.f);
+                            const float k = ex2_approx(__ldcg(&part_ml(sl)[r]).x - ref);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                o[4 * e] += y[e].x * k;
+                                o[4 * e + 1] += y[e].y * k;
+                                o[4 * e + 2] += y[e].z * k;
+                                o[4 * e + 3] += y[e].w * k;
+                            }
+                        }
+                        __syncwarp();
+                        if (final) {
+                            store32(o, iv, col0 + x0);
+                        } else if (live) {           // in the place of the group's first piece
+                            float4* dst = part_o(slot_of(0)) + x0 / 4 * 128;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e * 128] =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                    if (!final) part_ml(slot_of(0))[r] = make_float2(mm, ll);
+                }
+                if (final) break;
+                final = true;
+                first = 0;
+                step = per;
+                count = (pieces + per - 1) / per;
             }
         }
     }
