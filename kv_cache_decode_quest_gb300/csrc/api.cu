@@ -62,6 +62,20 @@ bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int head_
     return r == CUDA_SUCCESS;
 }
 
+bool encode_pages_map(CUtensorMap* map, const void* base, int64_t rows, int head_dim) {
+    if (!have_encode() || rows <= 0) return false;
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(head_dim / 64)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2, 128};
+    const cuuint32_t box[3] = {64, 16, static_cast<cuuint32_t>(head_dim / 64)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
 bool encode_heads_map(CUtensorMap* map, const void* base, int tokens, int heads, int64_t stride,
                       int group, int head_dim) {
     if (!have_encode() || tokens <= 0) return false;

@@ -456,14 +456,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 return (phys * H + it.h) * kPage;
             };
-            auto load = [&](const CUtensorMap* map, int row) -> bool {
+            // K's 64-column halves are regions of 128 rows (the tensor cores want all keys
+            // at one stride); V's are kept page by page, so one box brings a page
+            auto load = [&](bool keys, int row) -> bool {
                 const int st = seq % S::kStages;
                 if (!warp_wait(&c->empty[st], ((seq / S::kStages) & 1) ^ 1, c, status)) return false;
                 if (lane == 0) mbar_arrive_expect_tx(&c->full[st], S::kTile);
                 __syncwarp();
-                if (lane < 8 * S::kHalves)
-                    tma_load_2d(ring + st * S::kTile + (lane >> 3) * S::kRegion + (lane & 7) * 2048,
-                                map, &c->full[st], (lane >> 3) * 64, row);
+                uint8_t* to = ring + st * S::kTile;
+                if (keys && lane < 8 * S::kHalves)
+                    tma_load_2d(to + (lane >> 3) * S::kRegion + (lane & 7) * 2048, &tk, &c->full[st],
+                                (lane >> 3) * 64, row);
+                if (!keys && lane < 8)
+                    tma_load_3d(to + lane * (2048 * S::kHalves), &tv, &c->full[st], 0, row, 0);
                 ++seq;
                 return true;
             };
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++items;
             if (it.n == 0) break;
             int row_k = row_of(0, nxt1), row_v;
-            go = load(&tk, row_k);
+            go = load(true, row_k);
             if (go) {
                 go = warp_wait(&c->q_empty, (loads_q & 1) ^ 1, c, status);
                 if (go && lane == 0) {
@@ -497,9 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nxt2 = fetch(j + 2);
                 if (j + 1 < it.n) {
                     row_k = row_of(j + 1, nxt1);
-                    go = load(&tk, row_k);
+                    go = load(true, row_k);
                 }
-                if (go) go = load(&tv, row_v);
+                if (go) go = load(false, row_v);
             }
             // on to the next item: heads within the block, then the next block
             u = next;
@@ -524,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Descriptor words: the high one is the operand's layout, the low one
         // its address / 16 (and V's column stride), to which offsets are added.
         const uint64_t qd = umma_desc_sw128(smem_u32(qs)), kd = umma_desc_sw128(smem_u32(ring));
-        const uint64_t vd = umma_desc_mn_sw128(smem_u32(ring), S::kRegion);
+        const uint64_t vd = umma_desc_mn_sw128(smem_u32(ring), 2048);
         const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
         const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
         const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
@@ -551,13 +556,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ka + x * (S::kRegion / 16), k_hi, idesc_s, x > 0);
             umma_commit_warp(bar_s + w * 8);
         };
+        constexpr int kPageV = 2048 * S::kHalves;    // bytes of a page of V: 16 keys, one K step
         // O_w (+)= P_w V for the first / second 64 keys of the tile
         auto values = [&](uint32_t w, uint32_t stage, uint32_t acc, int half) {
-            const uint32_t va = v_lo + stage * (S::kTile / 16) + half * 512;
+            const uint32_t va = v_lo + stage * (S::kTile / 16) + half * (4 * kPageV / 16);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part)
-                umma_bf16_ts_warp4(tm + 256 + w * D, tm + w * 128 + part * 64 + half * 32, va, v_hi,
-                                   idesc_o, half + part > 0 ? 1u : acc);
+                umma_bf16_ts_warp4<kPageV / 16>(tm + 256 + w * D, tm + w * 128 + part * 64 + half * 32, va,
+                                                v_hi, idesc_o, half + part > 0 ? 1u : acc);
         };
         auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase) -> bool {
             if (!warp_wait(&c->p_half[w], phase, c, status)) return false;
@@ -588,12 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int tail_j =
                 len % kPage == 0 || (tail_t >= ts && tail_t < tl) ? -1 : tail_at - j0;
             auto clear_tail = [&](uint32_t stage) {
-                const int tail = len - tail_k0;
-                uint8_t* v = ring + stage * S::kTile;
-                const int r_end = (tail / kPage + 1) * kPage;
-                for (int i = lane; i < (r_end - tail) * 8 * S::kHalves; i += 32) {
-                    const int r = tail + i / (8 * S::kHalves), o = i % (8 * S::kHalves);
-                    *reinterpret_cast<uint4*>(v + (o >> 3) * S::kRegion + r * 128 + (o & 7) * 16) =
+                const int row = len % kPage;         // of the last page: 16 rows per half
+                uint8_t* v = ring + stage * S::kTile + (len - tail_k0) / kPage * kPageV;
+                for (int i = lane; i < (kPage - row) * 8 * S::kHalves; i += 32) {
+                    const int x = row + i / (8 * S::kHalves), o = i % (8 * S::kHalves);
+                    *reinterpret_cast<uint4*>(v + (o >> 3) * 2048 + x * 128 + (o & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
@@ -1062,7 +1067,7 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
     p.ws = static_cast<uint8_t*>(ws);
     CUtensorMap tq, tk, tv;
     if (!encode_rows_map(&tk, kv.k, (int64_t)kv.num_pages * H * kPage, D) ||
-        !encode_rows_map(&tv, kv.v, (int64_t)kv.num_pages * H * kPage, D) ||
+        !encode_pages_map(&tv, kv.v, (int64_t)kv.num_pages * H * kPage, D) ||
         !encode_heads_map(&tq, a.q, ck.max_tokens, a.Hq, a.q_stride, p.G, D))
         return cudaErrorInvalidValue;
     const int grid = std::min(num_sms(), kMaxCtas);

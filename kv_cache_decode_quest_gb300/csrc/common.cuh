@@ -510,7 +510,8 @@ __device__ __forceinline__ void umma_bf16_warp4(uint32_t tmem_d, uint32_t a_lo, 
         ::"r"(tmem_d), "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
 }
 // A from tensor memory (two K elements per 32-bit column: 16 of K are 8 columns), B
-// MN-major from shared memory (16 rows of K are 2048 bytes).
+// MN-major from shared memory, 16 rows of K STEP * 16 bytes from the next.
+template <int STEP>
 __device__ __forceinline__ void umma_bf16_ts_warp4(uint32_t tmem_d, uint32_t tmem_a, uint32_t b_lo,
                                                    uint32_t b_hi, uint32_t idesc,
                                                    uint32_t accumulate) {
@@ -521,13 +522,14 @@ __device__ __forceinline__ void umma_bf16_ts_warp4(uint32_t tmem_d, uint32_t tme
         "setp.eq.b32 t, 0, 0;\n\t"
         "mov.b64 b, {%2, %3};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t"
-        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, 128;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 8;\n\tadd.u32 y, %2, %6;\n\tmov.b64 b, {y, %3};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, 256;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 16;\n\tadd.u32 y, %2, %7;\n\tmov.b64 b, {y, %3};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t"
-        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, 384;\n\tmov.b64 b, {y, %3};\n\t"
+        "add.u32 x, %1, 24;\n\tadd.u32 y, %2, %8;\n\tmov.b64 b, {y, %3};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %4, t;\n\t}"
-        ::"r"(tmem_d), "r"(tmem_a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate));
+        ::"r"(tmem_d), "r"(tmem_a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "n"(STEP),
+          "n"(2 * STEP), "n"(3 * STEP));
 }
 __device__ __forceinline__ void umma_commit_warp(uint32_t bar) {
     asm volatile(

@@ -174,6 +174,9 @@ cudaError_t launch_h2o_step(const se_h2o_state& st, const void* q, const void* k
 // ---- tensor maps (api.cu) ----
 // 2-D bf16 map over [rows][head_dim] with 16-row x 64-column boxes, 128B swizzle.
 bool encode_rows_map(CUtensorMap* map, const void* base, int64_t rows, int head_dim);
+// The same rows as 3-D [head_dim / 64][rows][64] with boxes of all columns of 16 rows
+// (64-column halves one after another), 128B swizzle.
+bool encode_pages_map(CUtensorMap* map, const void* base, int64_t rows, int head_dim);
 // 3-D bf16 map over [tokens][heads][head_dim] (tokens `stride` elements apart) with boxes
 // of 64 columns x `group` heads x 128 / group tokens (128 rows), 128B swizzle.
 bool encode_heads_map(CUtensorMap* map, const void* base, int tokens, int heads, int64_t stride,
