@@ -49,9 +49,12 @@ constexpr int kRegsFew = 88, kRegsMany = 208;
 static_assert(kRegsFew * 128 + kRegsMany * 256 <= 168 * kThreads, "registers of the launch");
 constexpr int kItems = 4;                          // work items in flight between the roles
 constexpr int kMaxCtas = 256;
-constexpr int kBlockCost = 2;                      // a block's fixed work, in tiles
+// Units of work, about 700 clocks each: a tile for two row groups is bound by the tensor
+// cores and the softmax between them, one for a single group is shorter, and a block has a
+// fixed part (Q, the pipeline's fill, the rows' output).
+constexpr int kTileBoth = 4, kTileOne = 3, kBlockCost = 10;
 constexpr int kJoinFlat = 8;                       // pieces joined in one go at most
-constexpr int kMinShare = 4;                       // units a CTA takes at least
+constexpr int kMinShare = 16;                      // units a CTA takes at least (a tile or more)
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -82,7 +85,7 @@ struct Item {
     int ts, tl;        // tile j is key tile j (j < ts), else j - ts + tl
     int j0, n;         // this piece: tiles [j0, j0 + n); n = 0: no more work
     int split;         // the block is cut: this piece is partial
-    long long t0, t1;  // the block's tiles as units of work
+    long long t0, t1;  // first units of the block's first and last tile
 };
 
 struct Params {
@@ -168,7 +171,10 @@ struct Shares {
     }
 };
 
-__device__ __forceinline__ int block_cost(const Tiles& t) { return t.n > 0 ? t.n + kBlockCost : 0; }
+__device__ __forceinline__ int tile_cost(int rows) { return rows > 128 ? kTileBoth : kTileOne; }
+__device__ __forceinline__ int block_cost(const Tiles& t) {
+    return t.n > 0 ? t.n * tile_cost(t.rows) + kBlockCost : 0;
+}
 
 __device__ __forceinline__ int tile_of(const Item& it, int j) {
     return j < it.ts ? j : j - it.ts + it.tl;
@@ -314,8 +320,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         *sum = all;
         return before + x - v;
     };
-    // units: (tiles + the fixed cost) x heads, in the order (block, head, tile); the fixed
-    // cost comes before a block's first tile
+    // units in the order (block, head, tile); the fixed cost comes before a block's first
+    // tile, and a tile belongs to the share that holds its first unit
     long long total = 0, mine = 0;
     int nt = 0, my_b = 0;
     const int passes = (p.max_blocks + kThreads - 1) / kThreads;
@@ -417,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.b = b;
             it.n = 0;
             long long next = u1;
-            if (u < u1 && t.n > 0) {             // (n stays 0 if the share ends before a tile)
+            if (u < u1 && t.n > 0) {             // (n is 0 if the share ends before a tile)
                 if (first) {
                     h = static_cast<int>(udiv(u - pre * H, cost));
                     first = false;
@@ -432,11 +438,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 it.len = s.len;
                 it.ts = t.ts;
                 it.tl = t.tl;
-                it.j0 = static_cast<int>(max(0ll, u - t0));
-                it.n = static_cast<int>(max(0ll, next - t0)) - it.j0;
+                const int per = tile_cost(t.rows);
+                it.j0 = static_cast<int>(udiv(max(0ll, u - t0) + per - 1, per));
+                it.n = static_cast<int>(udiv(max(0ll, next - t0) + per - 1, per)) - it.j0;
                 it.split = it.n < t.n;
                 it.t0 = t0;
-                it.t1 = us + cost;
+                it.t1 = us + cost - per;             // the last tile's first unit
+            }
+            // on to the next item: heads within the block, then the next block
+            auto advance = [&]() {
+                u = next;
+                if (++h == H) {
+                    h = 0;
+                    pre += cost;
+                    ++blk;
+                }
+            };
+            if (it.n == 0 && next < u1) {            // the share begins inside the block's last tile
+                advance();
+                continue;
             }
             // lanes 0..15 issue a tile's boxes: page lane & 7, columns 64 * (lane >> 3)
             const int32_t* bt = p.kv.block_table + (int64_t)it.b * p.kv.max_pages_per_seq;
@@ -506,13 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (go) go = load(false, row_v);
             }
-            // on to the next item: heads within the block, then the next block
-            u = next;
-            if (++h == H) {
-                h = 0;
-                pre += cost;
-                ++blk;
-            }
+            advance();
         }
         if (lane == 0) {
             // every copy has landed before the block exits
@@ -882,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (it.split) {
                 const Shares sh(c->share_each, c->share_extra, 0);
                 c0 = sh.of(it.t0);
-                pieces = sh.of(it.t1 - 1) - c0 + 1;
+                pieces = sh.of(it.t1) - c0 + 1;
             }
             const int piece = 2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0);
             auto part_ml = [&](int s) {
