@@ -273,6 +273,12 @@ def quest_queries(w: QuestWorkload, tag: str = "") -> np.ndarray:
                        lead=2)
 
 
+def prompt_queries(w: QuestWorkload, tag: str = "") -> list:
+    """Per sequence, the queries of its prefill tokens: [ctx_b][Hq][D] bf16 bits."""
+    return [normal_bf16(w.seed, f"{w.name}{tag}/q_prompt/{b}",
+                        (w.ctx[b], w.num_q_heads, w.head_dim)) for b in range(w.batch)]
+
+
 def quest_inputs(w: QuestWorkload, tag: str = "") -> dict:
     """Logical tensors of a Quest decode run (bf16 bits, uint16).
 

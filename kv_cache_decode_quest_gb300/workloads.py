@@ -183,6 +183,106 @@ class QuestRun:
         return {"meta": meta, "kv": sel, "small": small, "total": meta + sel + small}
 
 
+class PromptRun:
+    """A Quest workload whose prompts go into the paged cache in chunks, pages handed
+    out on the GPU, and which then decodes with Quest from the cache they left.
+
+    prefill(): per chunk, se_chunk_plan (pages and rows of the next `chunk`
+    tokens of every sequence, fewer at its end), se_kv_append_chunk and
+    se_chunk_attn.  step(s): se_chunk_plan of one token per sequence (the page it may
+    need), then se_quest_select_append and se_sparse_decode.  release(): the
+    pages of finished sequences back to the pool."""
+
+    def __init__(self, w: synth.QuestWorkload, inputs: dict, prompt_q: list, chunk: int,
+                 device="cuda", out_dtype: int = 0, window: int = 0, sink: int = 0):
+        self.w, self.inputs, self.prompt_q, self.chunk_tokens = w, inputs, prompt_q, chunk
+        B, Hq, Hkv, D, S = w.batch, w.num_q_heads, w.num_kv_heads, w.head_dim, w.steps
+        self.B, self.Hq, self.Hkv, self.D, self.device = B, Hq, Hkv, D, device
+        self.scale = 1.0 / math.sqrt(D)
+        self.out_dtype, self.window, self.sink = out_dtype, window, sink
+        pages = [-(-(c + S) // PAGE) for c in w.ctx]
+        maxp, P = max(pages), sum(pages)
+        self.pool = se.PagePool.empty(B, P, maxp, device)
+        self.kv = se.PagedKV(
+            torch.zeros(P, Hkv, PAGE, D, dtype=torch.bfloat16, device=device),
+            torch.zeros(P, Hkv, PAGE, D, dtype=torch.bfloat16, device=device),
+            torch.zeros(B, maxp, Hkv, 2, D, dtype=torch.bfloat16, device=device),
+            self.pool.block_table, self.pool.ctx_len)
+        rows = B * chunk
+        self.chunk = se.Chunk.empty(B, rows, device)
+        self.one = se.Chunk.empty(B, B, device)
+        odt = torch.float32 if out_dtype == 1 else torch.bfloat16
+        self.out_rows = torch.zeros(rows, Hq, D, dtype=odt, device=device)
+        self.lse_rows = torch.zeros(rows, Hq, dtype=torch.float32, device=device)
+        units = B * Hkv
+        self.sel = torch.zeros(units, maxp, dtype=torch.int32, device=device)
+        self.n_sel = torch.zeros(units, dtype=torch.int32, device=device)
+        self.view = se.View.empty(units, maxp, device)
+        self.budget = torch.tensor([min(b, 2 ** 31 - 1) for b in w.budget], dtype=torch.int32,
+                                   device=device)
+        self.out = torch.zeros(B, Hq, D, dtype=odt, device=device)
+        self.lse = torch.zeros(B, Hq, dtype=torch.float32, device=device)
+        self.ws_pool = se.workspace(se.se_page_pool_workspace(B), device)
+        self.ws_small = se.workspace(se.se_small_workspace(), device)
+        self.ws_attn = se.workspace(se.se_chunk_attn_workspace(B, rows, Hkv, Hq, D), device)
+        self.ws_sel = se.workspace(se.se_quest_select_workspace(B, Hkv, maxp), device)
+        self.ws_dec = se.workspace(se.se_sparse_decode_workspace(units, Hq // Hkv, D), device)
+
+    def prefill(self):
+        """Yields (first positions, new tokens) per sequence after each chunk; its outputs are in
+        out_rows and lse_rows, packed by sequence."""
+        ctx = np.asarray(self.w.ctx)
+        done = np.zeros(self.B, dtype=np.int64)
+        nq, nk = self.Hq * self.D, self.Hkv * self.D
+        while np.any(done < ctx):
+            new = np.minimum(self.chunk_tokens, ctx - done)
+            # packed q | k | v rows, as a fused projection leaves them
+            rows = np.zeros((self.B * self.chunk_tokens, nq + 2 * nk), dtype=np.uint16)
+            at = 0
+            for b, n in enumerate(new):
+                t = slice(done[b], done[b] + n)
+                rows[at:at + n, :nq] = self.prompt_q[b][t].reshape(n, nq)
+                rows[at:at + n, nq:nq + nk] = self.inputs["k"][b][:, t].transpose(1, 0, 2).reshape(n, nk)
+                rows[at:at + n, nq + nk:] = self.inputs["v"][b][:, t].transpose(1, 0, 2).reshape(n, nk)
+                at += n
+            qkv = to_dev_bf16(rows, self.device).view(len(rows), -1, self.D)
+            self.chunk_step(qkv, torch.from_numpy(new.astype(np.int32)).to(self.device))
+            yield done.copy(), new
+            done += new
+
+    def chunk_step(self, qkv, new_len):
+        """One chunk of every sequence: qkv [rows][Hq + 2 Hkv][D]."""
+        Hq, H = self.Hq, self.Hkv
+        se.se_chunk_plan(self.pool, new_len, self.B, self.chunk, self.ws_pool)
+        se.se_kv_append_chunk(self.kv, qkv[:, Hq:Hq + H], qkv[:, Hq + H:], self.chunk, self.B,
+                              self.ws_small)
+        se.se_chunk_attn(self.kv, qkv[:, :Hq], self.chunk, self.B, Hq, self.scale, self.out_rows,
+                         self.lse_rows, self.ws_attn, out_dtype=self.out_dtype, window=self.window,
+                         sink=self.sink)
+
+    def step(self, s: int):
+        """One Quest decode step; the token's page comes from the pool."""
+        at = [c + s for c in self.w.ctx]
+        k, v = (to_dev_bf16(np.stack([self.inputs[x][b][:, at[b]] for b in range(self.B)]),
+                            self.device) for x in ("k", "v"))
+        q = to_dev_bf16(np.asarray(self.inputs["q"][s]), self.device)
+        se.se_chunk_plan(self.pool, torch.ones_like(self.pool.n_pages), self.B, self.one,
+                         self.ws_pool)
+        se.se_quest_select_append(self.kv, k, v, q, self.B, self.Hq, self.budget, self.sel,
+                                  self.n_sel, self.view, self.ws_sel)
+        se.se_sparse_decode(self.kv.k, self.kv.v, self.view, q, self.B, self.Hq, self.Hkv, self.D,
+                            self.scale, self.out, self.lse, self.ws_dec, out_dtype=self.out_dtype)
+
+    def release(self, done):
+        se.se_pages_release(self.pool, done, self.B, self.ws_pool)
+
+    def status(self) -> int:
+        st = 0
+        for ws in (self.ws_pool, self.ws_small, self.ws_attn, self.ws_sel, self.ws_dec):
+            st |= se.status_word(ws)
+        return st
+
+
 class OmniRun:
     """Cross-layer selection reuse over `layers` attention layers of one model:
     every layer keeps its own paged K/V (one block table for all), the filter
