@@ -292,7 +292,7 @@ int se_kv_append(const se_paged_kv* kv, const void* k_new, const void* v_new, in
  * and no rows (new_len < 0) or rows with pos = slot = -1.  A page outside [0, num_pages) met on the stack or in the block
  * table: SE_DEV_BAD_INDEX, the slots on it are -1.  ctx_len is not changed (the append commits it),
  * so a plan that is made again before the append finds its pages held and takes
- * no others.  Limits: 0 <= max_tokens <= 2^24.
+ * no others.  Limits: 0 <= max_tokens <= 2^24, num_pages and max_pages_per_seq < 2^27.
  * Workspace: se_page_pool_workspace(batch), zero-filled before its first use: it
  * holds an arrival counter, which every call leaves at zero. */
 int se_chunk_plan(const se_page_pool* pool, const int32_t* new_len, int batch,
@@ -336,10 +336,12 @@ int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_n
  * position at or past ctx_len[b]: SE_DEV_BAD_LENGTH, clamped.  start outside [0, max_tokens] or
  * descending: SE_DEV_BAD_LENGTH, clamped (a descending sequence has no rows).
  * Held keys and values are finite; what lies past ctx_len in a page may be anything.
- * scale finite; window, sink >= 0; 0 <= max_tokens <= 2^24.
+ * scale finite (0 and negative ones too); window, sink >= 0.  Limits: batch <= 8192,
+ * 0 <= max_tokens <= 2^24, max_pages_per_seq <= 2^26, else SE_ERR_UNSUPPORTED.
  * Workspace: se_chunk_attn_workspace(...), zero-filled before its first use:
  * it holds arrival counters at a fixed offset, which every call leaves at zero, so one
- * workspace serves calls of any shape whose size it covers. */
+ * workspace serves calls of any shape whose size it covers.  Clear it again after a
+ * call that set SE_DEV_TIMEOUT. */
 int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, int batch,
                   int num_q_heads, float scale, const se_chunk_attn_opts* opts, void* out,
                   float* lse, void* ws, size_t ws_bytes, se_stream_t stream);

@@ -92,7 +92,6 @@ struct Params {
     se_paged_kv kv;
     se_chunk ck;
     int batch, G, lg, Hq;          // G = 1 << lg query heads per KV head
-    int max_blocks;                // blocks numbered at most
     int window, sink;
     float scale_log2;              // > 0
     uint32_t negate;               // instruction descriptor bit for a negative scale
@@ -277,16 +276,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* sums = reinterpret_cast<int*>(smem);
     Seq* seqs = reinterpret_cast<Seq*>(smem + 1024);
     int* firsts = reinterpret_cast<int*>(smem + 1024 + (size_t)kMaxBatch * sizeof(Seq));
+    int max_blocks = 0;                              // blocks up to the last one with rows
     {
         int bad = 0;
         for (int b = threadIdx.x; b < p.batch; b += kThreads) {
             const Seq s = seq_info(p, b, bad);
             seqs[b] = s;
             firsts[b] = first_block(s.s0, G, b);
+            if (s.n > 0) max_blocks = first_block(s.s0 + s.n, G, b) + 1;
         }
         if (bad && blockIdx.x == 0) flag(status, bad);
+        max_blocks = __reduce_max_sync(0xffffffffu, max_blocks);
+        if (lane == 0) sums[32 + warp] = max_blocks;
     }
     __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) max_blocks = max(max_blocks, sums[32 + w]);
     auto find_seq = [&](int x) {                     // last sequence whose first number is <= x
         int lo = 0, hi = p.batch;
         while (hi - lo > 1) {
@@ -324,11 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // tile, and a tile belongs to the share that holds its first unit
     long long total = 0, mine = 0;
     int nt = 0, my_b = 0;
-    const int passes = (p.max_blocks + kThreads - 1) / kThreads;
+    const int passes = (max_blocks + kThreads - 1) / kThreads;
     for (int i = 0; i < passes; ++i) {
         const int x = i * kThreads + threadIdx.x;
         my_b = find_seq(x);
-        nt = x < p.max_blocks ? block_cost(block_tiles(p, seqs[my_b], x - firsts[my_b])) : 0;
+        nt = x < max_blocks ? block_cost(block_tiles(p, seqs[my_b], x - firsts[my_b])) : 0;
         long long sum;
         mine = scan(nt, &sum);
         total += sum;
@@ -347,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             long long sum;
             if (passes > 1) {
                 my_b = find_seq(x);
-                nt = x < p.max_blocks ? block_cost(block_tiles(p, seqs[my_b], x - firsts[my_b])) : 0;
+                nt = x < max_blocks ? block_cost(block_tiles(p, seqs[my_b], x - firsts[my_b])) : 0;
                 mine = scan(nt, &sum);
             } else {
                 sum = total;
@@ -1068,7 +1073,6 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
     p.G = a.Hq / H;
     for (p.lg = 0; 1 << p.lg < p.G;) ++p.lg;
     p.Hq = a.Hq;
-    p.max_blocks = static_cast<int>((int64_t)ck.max_tokens * p.G / kBlockRows) + batch;
     p.window = a.window;
     p.sink = a.sink;
     // a negative scale negates the products; a zero one becomes so small that

@@ -112,6 +112,8 @@ def test_attn(lib):
         assert call(o=opts(**bad)) == INVALID, bad
     assert call(c=chunk(max_tokens=(1 << 24) + 1)) == UNSUPPORTED
     assert call(batch=-1) == INVALID
+    assert call(batch=8193) == UNSUPPORTED
+    assert call(kv=paged(max_pages_per_seq=(1 << 26) + 1)) == UNSUPPORTED
     assert call(ws=None) == WORKSPACE and call(nbytes=need - 1) == WORKSPACE
     assert call(q=None, out=None, batch=0) == 0
     assert call(q=None, out=None, c=chunk(max_tokens=0, seq=None, pos=None, slot=None)) == 0

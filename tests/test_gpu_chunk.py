@@ -409,6 +409,66 @@ def test_long_context_split_over_the_gpu():
             a.check(chunk)
 
 
+@pytest.mark.parametrize("H,G,D,ctx,new", [
+    (1, 8, 128, [9000], [64]), (1, 1, 64, [7003], [300]), (1, 16, 128, [6000, 5000], [17, 3])])
+def test_blocks_cut_into_many_pieces(H, G, D, ctx, new):
+    """Few blocks over many keys: every SM takes a part, joined in two levels."""
+    g = np.random.default_rng([22, G])
+    c = held(g, len(ctx), H, D, ctx, new)
+    chunk = c.add(new)
+    for f32 in (False, True):
+        a = Attn(c, G, f32)
+        a.run(chunk)
+        a.check(chunk, rows=10)
+        first = a.out.clone()
+        a.call(chunk)
+        assert torch.equal(first, a.out)
+
+
+def test_many_sequences():
+    """More sequences than threads of a block: single tokens, empty ones, a few chunks."""
+    g = np.random.default_rng([23])
+    B = 900
+    ctx = g.integers(0, 60, B)
+    new = g.integers(0, 3, B)
+    new[[3, 400, 899]] = [70, 33, 17]
+    c = Cache(g, B, 1, 64, 10, int(sum(-(-(a + b) // PAGE) for a, b in zip(ctx, new))) + 1, False)
+    c.add(list(ctx))
+    chunk = c.add(list(new), pad=1)
+    a = Attn(c, 4)
+    a.run(chunk)
+    a.check(chunk, rows=8)
+    # the same rows in packed arrays with room for many more
+    wide = se.Chunk.empty(B, 60000)
+    wide.start.copy_(chunk.start)
+    for x in ("seq", "pos", "slot"):
+        getattr(wide, x)[:len(chunk.seq)] = getattr(chunk, x)
+    out, lse = a.out.clone(), a.lse.clone()
+    a.qt = torch.cat([a.qt, torch.zeros(60000 - len(a.qt), 4, 64, dtype=a.qt.dtype, device="cuda")])
+    a.out = torch.full((60000, 4, 64), 7.0, dtype=out.dtype, device="cuda")
+    a.lse = torch.full((60000, 4), 7.0, device="cuda")
+    a.ws = se.workspace(se.se_chunk_attn_workspace(B, 60000, 1, 4, 64))
+    a.call(wide)
+    assert torch.equal(a.out[:len(out)], out) and torch.equal(a.lse[:len(lse)], lse)
+    assert torch.all(a.out[len(out):] == 7.0) and torch.all(a.lse[len(out):] == 7.0)
+
+
+def test_rows_before_the_end_of_what_is_held():
+    """Positions in the middle of a longer history (the later keys are not seen)."""
+    g = np.random.default_rng([24])
+    c = held(g, 2, 2, 128, [500, 77], [1, 1])
+    chunk = c.add([1, 1])
+    n = [150, 20]
+    pos0 = [33, 50]
+    seq = np.repeat([0, 1], n)
+    pos = np.concatenate([p + np.arange(k) for p, k in zip(pos0, n)])
+    mid = se.Chunk(i32([0, 150, 170]), i32(seq), i32(pos), i32(np.zeros(170)))
+    for window in (0, 40):
+        a = Attn(c, 4, window=window)
+        a.run(mid)
+        a.check(mid, rows=30)
+
+
 def test_growing_maximum():
     """Keys whose logits grow along the sequence: every tile raises the running maximum."""
     g = np.random.default_rng([16])
