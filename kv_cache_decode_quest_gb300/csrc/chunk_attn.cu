@@ -219,6 +219,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* 
     return false;
 }
 
+// Two barriers at once.
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, Ctrl* c,
+                                           int* status) {
+#pragma unroll 1
+    for (uint32_t n = 0;; ++n) {
+        const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
+        if (__all_sync(0xffffffffu, x && y)) return true;
+        if (n == kWaitTries || __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->abort))) break;
+    }
+    *static_cast<volatile int*>(&c->abort) = 1;
+    flag(status, SE_DEV_TIMEOUT);
+    return false;
+}
+
 // 4 x 4 transpose of 16-byte units over each group of four lanes: lane i ends with
 // unit i of the rows that lanes 0..3 of the group held.
 __device__ __forceinline__ void transpose4(uint4 (&x)[4], int lane) {
@@ -591,7 +605,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!warp_wait(&c->p_full[w], phase, c, status)) return false;
             tc_fence_after();
             values(w, stage, acc, 1);
-            umma_commit_warp(bar_o + w * 8);
             return true;
         };
         for (int items = 0;; ++items) {
@@ -625,7 +638,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // The scores run `ahead` tiles before the products: both groups take every
             // tile, or tile j is group j & 1's.  Ring order: K0, then for each tile j:
-            // K_{j + 1}, V_j (the same order either way).
+            // K_{j + 1}, V_j (the same order either way).  This warp's own instructions are
+            // what bounds a tile (a wait that finds its barrier complete takes some 100
+            // clocks here, a commit 40): K and V are waited for together, before P.
             if (!warp_wait(&c->q_full, items & 1, c, status)) break;
             const int ahead = both ? 1 : 2;
             bool go = true;
@@ -634,18 +649,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool more = j + ahead < n;
                 uint32_t ks = st, kph = ph;
                 if (both && more) next_stage();
-                const uint32_t vs = st;
-                if (j >= 0) {
-                    go = wait_stage();
-                    if (!go) break;
-                    next_stage();
-                    if (j == tail_j) clear_tail(vs);
-                }
+                const uint32_t vs = st, vph = ph;
+                if (j >= 0) next_stage();
                 if (!both) {
                     ks = st;
                     kph = ph;
                     if (more) next_stage();
                 }
+                if (both || j < 0)
+                    go = warp_wait2(more ? &c->full[ks] : &c->full[vs], more ? kph : vph,
+                                    j >= 0 ? &c->full[vs] : &c->full[ks], j >= 0 ? vph : kph, c, status);
+                else
+                    go = warp_wait(&c->full[vs], vph, c, status);
+                if (!go) break;
+                tc_fence_after();
+                if (j >= 0 && j == tail_j) clear_tail(vs);
                 const uint32_t w_begin = both ? 0 : j & 1;
                 const uint32_t w_end = both ? 2 : (j & 1) + 1;
 #pragma unroll 1
@@ -657,12 +675,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (w + 1 == w_end) umma_commit_warp(bar_empty + vs * 8);
                     }
                     if (more) {
-                        if (w == w_begin) {
+                        if (!both && j >= 0) {
                             go = warp_wait(&c->full[ks], kph, c, status);
                             if (!go) break;
                             tc_fence_after();
                         }
                         scores(w, both ? w : 0, ks);
+                    } else if (j >= 0) {
+                        umma_commit_warp(bar_o + w * 8);      // the group's last product of the item
                     }
                 }
                 if (!go) break;
@@ -687,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lg = p.lg;
         const float sl2 = p.scale_log2;
         uint32_t ns = 0;                             // S tiles seen by this group
-        uint32_t no = 0;                             // P tiles handed to the tensor cores
+        uint32_t no = 0;                             // items with a product of this group's
         uint32_t n_ml = 0;
         for (int items = 0;; ++items) {
             const int slot = items % kItems;
@@ -796,10 +816,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float to = grow ? top : m;
                         const float alpha = to == m ? 1.f : ex2_approx(m - to);
                         if (i > 0) {
-                            // the previous product is complete before O is touched
-                            ok = warp_wait(&c->o_done[w], (no - 1) & 1, c, status);
-                            if (!ok) break;
-                            tc_fence_after();
+                            // (the previous product was issued before these scores, so it is
+                            // complete)
 #pragma unroll 1
                             for (int x = 0; x < D; x += 16) {
                                 uint32_t o[16];
@@ -816,7 +834,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         sum[0] = sum[1] = 0;
                         tmem_st_wait();
                     }
-                    if (!ok) break;
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -833,7 +850,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&c->p_full[w]);
-                ++no;
             }
             if (!ok) break;
             // ---- the item's rows ----
@@ -843,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n1 = both ? 0 : it.n / 2;      // tiles of group 1 (shared rows)
             float w0 = 1.f, w1 = 0.f;                // weights of the two accumulators
             // (each group has at least one tile, but group 1 of one shared tile)
-            if (mine_n > 0 && !warp_wait(&c->o_done[w], (no - 1) & 1, c, status)) break;
+            if (mine_n > 0 && !warp_wait(&c->o_done[w], no++ & 1, c, status)) break;
             if (!both) {
                 c->ml[w][r] = make_float2(m, l);
                 tc_fence_before();
