@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bar_q = smem_u32(&c->q_empty);
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         uint32_t st = 0, ph = 0;                     // ring stage and its phase
-        uint32_t np = 0;                             // bit w: phase of group w's P
+        uint32_t np0 = 0, np1 = 0;                   // phases of P of each group
         auto wait_stage = [&]() { return warp_wait(&c->full[st], ph, c, status); };
         auto next_stage = [&]() {
             if (++st == S::kStages) {
@@ -581,12 +581,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ph ^= 1;
             }
         };
-        auto scores = [&](uint32_t w, uint32_t qt, uint32_t stage) {      // S_w = Q_qt K^T
+        // S_w = Q_qt K^T; `beside` runs before the last four instructions, while those ahead of
+        // them are being carried out
+        auto scores = [&](uint32_t w, uint32_t qt, uint32_t stage, auto beside) {
             const uint32_t ka = k_lo + stage * (S::kTile / 16), qa = q_lo + qt * (S::kTile / 16);
 #pragma unroll
-            for (int x = 0; x < S::kHalves; ++x)
+            for (int x = 0; x < S::kHalves; ++x) {
+                if (x + 1 == S::kHalves) beside();
                 umma_bf16_warp4(tm + w * 128, qa + x * (S::kRegion / 16), q_hi,
                                 ka + x * (S::kRegion / 16), k_hi, idesc_s, x > 0);
+            }
             umma_commit_warp(bar_s + w * 8);
         };
         constexpr int kPageV = 2048 * S::kHalves;    // bytes of a page of V: 16 keys, one K step
@@ -598,14 +602,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 umma_bf16_ts_warp4<kPageV / 16>(tm + 256 + w * D, tm + w * 128 + part * 64 + half * 32, va,
                                                 v_hi, idesc_o, half + part > 0 ? 1u : acc);
         };
-        auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase) -> bool {
-            if (!warp_wait(&c->p_half[w], phase, c, status)) return false;
+        // `there`: the first half of P is known to be there
+        auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase, bool there) -> bool {
+            if (!there && !warp_wait(&c->p_half[w], phase, c, status)) return false;
             tc_fence_after();
             values(w, stage, acc, 0);
             if (!warp_wait(&c->p_full[w], phase, c, status)) return false;
             tc_fence_after();
             values(w, stage, acc, 1);
             return true;
+        };
+        auto test = [&](uint64_t* bar, uint32_t phase) {
+            return __all_sync(0xffffffffu, mbar_test_wait(bar, phase)) != 0;
         };
         for (int items = 0;; ++items) {
             const int slot = items % kItems;
@@ -636,58 +644,96 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            // The scores run `ahead` tiles before the products: both groups take every
-            // tile, or tile j is group j & 1's.  Ring order: K0, then for each tile j:
-            // K_{j + 1}, V_j (the same order either way).  This warp's own instructions are
-            // what bounds a tile (a wait that finds its barrier complete takes some 100
-            // clocks here, a commit 40): K and V are waited for together, before P.
-            if (!warp_wait(&c->q_full, items & 1, c, status)) break;
-            const int ahead = both ? 1 : 2;
+            // Ring order: K0, then for each tile j: K_{j + 1}, V_j.
+            // This warp's own instructions decide how well the tensor cores are fed: a wait
+            // that finds its barrier complete takes 100 to 160 clocks beside busy warps, and the
+            // queue holds some 250 clocks of work.  So barriers that are needed after a
+            // batch of instructions are tested before its end.
+            if (!warp_wait2(&c->q_full, items & 1, &c->full[st], ph, c, status)) break;
+            tc_fence_after();
+            auto nothing = [] {};
             bool go = true;
+            if (both) {
+                scores(0, 0, st, nothing);
+                scores(1, 1, st, nothing);
+                umma_commit_warp(bar_empty + st * 8);
+                if (n == 1) umma_commit_warp(bar_q);
+                next_stage();
+                bool kv = false, p0 = false, p1 = false;      // known to be there
 #pragma unroll 1
-            for (int j = -ahead; j < n; ++j) {
-                const bool more = j + ahead < n;
-                uint32_t ks = st, kph = ph;
-                if (both && more) next_stage();
-                const uint32_t vs = st, vph = ph;
-                if (j >= 0) next_stage();
-                if (!both) {
-                    ks = st;
-                    kph = ph;
+                for (int j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    const uint32_t ks = st, kph = ph;
                     if (more) next_stage();
-                }
-                if (both || j < 0)
-                    go = warp_wait2(more ? &c->full[ks] : &c->full[vs], more ? kph : vph,
-                                    j >= 0 ? &c->full[vs] : &c->full[ks], j >= 0 ? vph : kph, c, status);
-                else
-                    go = warp_wait(&c->full[vs], vph, c, status);
-                if (!go) break;
-                tc_fence_after();
-                if (j >= 0 && j == tail_j) clear_tail(vs);
-                const uint32_t w_begin = both ? 0 : j & 1;
-                const uint32_t w_end = both ? 2 : (j & 1) + 1;
-#pragma unroll 1
-                for (uint32_t w = w_begin; w < w_end; ++w) {
-                    if (j >= 0) {
-                        go = product(w, vs, j >= ahead, (np >> w) & 1);
-                        if (!go) break;
-                        np ^= 1u << w;
-                        if (w + 1 == w_end) umma_commit_warp(bar_empty + vs * 8);
-                    }
+                    const uint32_t vs = st, vph = ph;
+                    next_stage();
+                    if (!kv) go = warp_wait2(&c->full[ks], kph, &c->full[vs], vph, c, status);
+                    if (!go) break;
+                    if (j == tail_j) clear_tail(vs);
+                    go = product(0, vs, j > 0, np0, p0);
+                    if (!go) break;
+                    np0 ^= 1;
+                    if (more)
+                        scores(0, 0, ks, [&] { p1 = test(&c->p_half[1], np1); });
+                    else
+                        umma_commit_warp(bar_o);
+                    go = product(1, vs, j > 0, np1, more && p1);
+                    if (!go) break;
+                    np1 ^= 1;
+                    umma_commit_warp(bar_empty + vs * 8);
                     if (more) {
-                        if (!both && j >= 0) {
-                            go = warp_wait(&c->full[ks], kph, c, status);
-                            if (!go) break;
-                            tc_fence_after();
-                        }
-                        scores(w, both ? w : 0, ks);
-                    } else if (j >= 0) {
-                        umma_commit_warp(bar_o + w * 8);      // the group's last product of the item
+                        // K_{j + 2} and V_{j + 1} follow in the ring
+                        const uint32_t ka = st, kap = ph;
+                        const bool far = j + 2 < n;
+                        const uint32_t va = !far ? ka : ka + 1 == S::kStages ? 0 : ka + 1;
+                        const uint32_t vap = va < ka ? kap ^ 1 : kap;
+                        scores(1, 1, ks, [&] {
+                            kv = test(&c->full[ka], kap) && test(&c->full[va], vap);
+                            p0 = test(&c->p_half[0], np0);
+                        });
+                        umma_commit_warp(bar_empty + ks * 8);
+                        if (!far) umma_commit_warp(bar_q);
+                    } else {
+                        umma_commit_warp(bar_o + 8);
                     }
                 }
-                if (!go) break;
-                if (more) umma_commit_warp(bar_empty + ks * 8);
-                if (j + ahead == n - 1) umma_commit_warp(bar_q);
+            } else {
+                // tile j is group j & 1's; the scores run two tiles ahead
+                scores(0, 0, st, nothing);
+                umma_commit_warp(bar_empty + st * 8);
+                next_stage();
+                if (n > 1) {
+                    if (!wait_stage()) break;
+                    tc_fence_after();
+                    scores(1, 0, st, nothing);
+                    umma_commit_warp(bar_empty + st * 8);
+                    next_stage();
+                }
+                if (n <= 2) umma_commit_warp(bar_q);
+#pragma unroll 1
+                for (int j = 0; j < n; ++j) {
+                    const uint32_t w = j & 1, vs = st;
+                    go = wait_stage();
+                    if (!go) break;
+                    next_stage();
+                    if (j == tail_j) clear_tail(vs);
+                    go = product(w, vs, j > 1, w ? np1 : np0, false);
+                    if (!go) break;
+                    if (w) np1 ^= 1;
+                    else np0 ^= 1;
+                    umma_commit_warp(bar_empty + vs * 8);
+                    if (j + 2 < n) {
+                        go = wait_stage();
+                        if (!go) break;
+                        tc_fence_after();
+                        scores(w, 0, st, nothing);
+                        umma_commit_warp(bar_empty + st * 8);
+                        next_stage();
+                        if (j + 3 == n) umma_commit_warp(bar_q);
+                    } else {
+                        umma_commit_warp(bar_o + w * 8);
+                    }
+                }
             }
             if (!go) break;
         }
