@@ -21,9 +21,9 @@
 // each tile; a smaller one (short chunks, single tokens) gives them alternate
 // tiles of the same rows, joined at the end through tensor memory.  While one group
 // computes its exponentials, the tensor cores work for the other.  O stays in
-// tensor memory and is rescaled only when a row's maximum has grown by more than
-// 2^8 (the true maximum is not needed: any reference within 2^8 keeps P and l
-// far from overflow, and the same one divides out).
+// tensor memory and is rescaled only when a row's logits have outgrown the reference
+// (the true maximum is not needed: any reference near it keeps P and l far from
+// overflow, and the same one divides out).
 // A block cut between CTAs is joined by the last of them to finish, in the
 // order of its keys (the result does not depend on timing).
 #include <algorithm>
@@ -58,7 +58,7 @@ constexpr int kMinShare = 16;                      // units a CTA takes at least
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescale = 8.f;                    // log2 of the growth that rescales O
+constexpr float kGrowSum = 16384.f;                // a tile's row sum above this: the reference moves up
 
 // Workspace: status word, at byte 256 the arrival counters [kMaxCtas][2 levels][8 warps], then
 // the partial results: two pieces per CTA (the one it takes over and the one it hands
@@ -185,7 +185,7 @@ struct Ctrl {
     uint64_t q_full, q_empty;
     uint64_t s_full[2], o_done[2];
     uint64_t item_full[kItems], done;
-    uint64_t p_half[2], p_full[2];         // 4 warps each
+    uint64_t p_full[2];                    // 4 warps each
     uint64_t ml_full, ml_empty;            // a shared block's two groups: all softmax warps
     uint64_t item_empty[kItems];           // all softmax warps and the MMA warp
     uint32_t tmem;
@@ -196,10 +196,10 @@ struct Ctrl {
     float2 ml[2][128];                     // of a block that both groups share
 };
 
-constexpr int kBarriers = 10 + 10 + 2 + 2 + 2 + kItems + 1 + 2 + 2 + 2 + kItems;
+constexpr int kOnes = 10 + 10 + 2 + 2 + 2 + kItems + 1;
+constexpr int kBarriers = kOnes + 2 + 2 + kItems;
 __device__ __forceinline__ uint32_t barrier_count(int i) {
-    constexpr int kOnes = 10 + 10 + 2 + 2 + 2 + kItems + 1;
-    return i < kOnes ? 1 : i < kOnes + 4 ? 4 : i < kOnes + 6 ? kSoftWarps : kSoftWarps + 1;
+    return i < kOnes ? 1 : i < kOnes + 2 ? 4 : i < kOnes + 4 ? kSoftWarps : kSoftWarps + 1;
 }
 
 // Warp-uniform bounded wait.  Tries are counted (each is suspended by the hardware for
@@ -594,22 +594,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit_warp(bar_s + w * 8);
         };
         constexpr int kPageV = 2048 * S::kHalves;    // bytes of a page of V: 16 keys, one K step
-        // O_w (+)= P_w V for the first / second 64 keys of the tile
-        auto values = [&](uint32_t w, uint32_t stage, uint32_t acc, int half) {
-            const uint32_t va = v_lo + stage * (S::kTile / 16) + half * (4 * kPageV / 16);
+        // O_w (+)= P_w V; `there`: P is known to be there
+        auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase, bool there) -> bool {
+            if (!there && !warp_wait(&c->p_full[w], phase, c, status)) return false;
+            tc_fence_after();
+            const uint32_t va = v_lo + stage * (S::kTile / 16);
 #pragma unroll
             for (int part = 0; part < (F32 ? 2 : 1); ++part)
-                umma_bf16_ts_warp4<kPageV / 16>(tm + 256 + w * D, tm + w * 128 + part * 64 + half * 32, va,
-                                                v_hi, idesc_o, half + part > 0 ? 1u : acc);
-        };
-        // `there`: the first half of P is known to be there
-        auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase, bool there) -> bool {
-            if (!there && !warp_wait(&c->p_half[w], phase, c, status)) return false;
-            tc_fence_after();
-            values(w, stage, acc, 0);
-            if (!warp_wait(&c->p_full[w], phase, c, status)) return false;
-            tc_fence_after();
-            values(w, stage, acc, 1);
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+                    umma_bf16_ts_warp4<kPageV / 16>(tm + 256 + w * D,
+                                                    tm + w * 128 + part * 64 + half * 32,
+                                                    va + half * (4 * kPageV / 16), v_hi, idesc_o,
+                                                    half + part > 0 ? 1u : acc);
             return true;
         };
         auto test = [&](uint64_t* bar, uint32_t phase) {
@@ -674,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!go) break;
                     np0 ^= 1;
                     if (more)
-                        scores(0, 0, ks, [&] { p1 = test(&c->p_half[1], np1); });
+                        scores(0, 0, ks, [&] { p1 = test(&c->p_full[1], np1); });
                     else
                         umma_commit_warp(bar_o);
                     go = product(1, vs, j > 0, np1, more && p1);
@@ -689,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t vap = va < ka ? kap ^ 1 : kap;
                         scores(1, 1, ks, [&] {
                             kv = test(&c->full[ka], kap) && test(&c->full[va], vap);
-                            p0 = test(&c->p_half[0], np0);
+                            p0 = test(&c->p_full[0], np0);
                         });
                         umma_commit_warp(bar_empty + ks * 8);
                         if (!far) umma_commit_warp(bar_q);
@@ -815,10 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v[32 * x + e] = (see >> e) & 1 ? v[32 * x + e] : -INFINITY;
                         }
                     }
-                    // The first half of P is computed with the reference as it was, beside the
-                    // row's maximum (the one needs the exponential unit, the other does not).
-                    // Only where a row has outgrown its reference is it done again (and
-                    // for the first tile, which has none, only then); P goes to tensor
+                    // P is computed with the reference as it was, and its row sum, which is
+                    // needed anyway, shows whether that still serves: no logit is more than
+                    // log2(kGrowSum) above it if the sum is at most kGrowSum, and nothing comes
+                    // near overflow.  So no maximum is taken but for rows that have outgrown their
+                    // reference or have none yet; those are done again.  P goes to tensor
                     // memory, which nobody reads before it is handed over.
                     const uint64_t scale2 = f32x2(sl2, sl2);
                     uint64_t sum[2] = {0, 0};
@@ -841,13 +839,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
                     };
                     bool settled = false;
+                    float total;
+#pragma unroll 1
                     while (true) {                   // (one copy of the code: it is long)
                         if (settled || i > 0) {
-                            quarter(0);
-                            quarter(1);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) quarter(x);
+                            float s0, s1;
+                            f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
+                            total = s0 + s1;
                         }
                         if (settled) break;
                         settled = true;
+                        const bool grow = i == 0 || m == -INFINITY || !(total <= kGrowSum);
+                        if (!__any_sync(0xffffffffu, grow)) break;
                         float mx[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
                         for (int e = 4; e + 8 <= kKeys; e += 8)
@@ -857,13 +862,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], v[kKeys - 4 + x]);
                         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
-                        const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
-                        if (i > 0 && !__any_sync(0xffffffffu, grow)) break;
-                        const float to = grow ? top : m;
-                        const float alpha = to == m ? 1.f : ex2_approx(m - to);
+                        const float to = grow ? fmaxf(top, m) : m;
                         if (i > 0) {
                             // (the previous product was issued before these scores, so it is
                             // complete)
+                            const float alpha = to == m ? 1.f : ex2_approx(m - to);
 #pragma unroll 1
                             for (int x = 0; x < D; x += 16) {
                                 uint32_t o[16];
@@ -873,25 +876,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                                 tmem_st16(lane_base + 256 + w * D + x, o);
                             }
+                            l *= alpha;
                         }
-                        l *= alpha;
                         m = to;
                         neg = m == -INFINITY ? 0.f : -m;
                         sum[0] = sum[1] = 0;
                         tmem_st_wait();
                     }
+                    l += total;
                     tmem_st_wait();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&c->p_half[w]);
-                    quarter(2);
-                    quarter(3);
-                    float s0, s1;
-                    f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
-                    l += s0 + s1;
-                    tmem_st_wait();
-                } else if (lane == 0) {
-                    mbar_arrive(&c->p_half[w]);
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -491,6 +491,30 @@ def test_growing_maximum():
         a.check(chunk, rows=12)
 
 
+@pytest.mark.parametrize("jump", [20.0, 150.0, 3000.0])
+def test_sudden_jumps(jump):
+    """Single keys whose logits lie far above all before them, at the borders of tiles and
+    inside; behind the last one everything else vanishes."""
+    g = np.random.default_rng([25])
+    n, D = 700, 64
+    c = Cache(g, 1, 1, D, 45, 45)
+    q = np.ones((n, 2, D))
+    k = normal(g, n, 1, D) / 8
+    for i, at in enumerate((1, 127, 128, 200, 383, 511, 640)):
+        k[at] = oracle.widen(synth.f32_to_bf16_bits(np.full((1, D), (i + 1) * jump / 8, np.float32)))
+    v = normal(g, n, 1, D)
+    chunk = plan_both(c.o, c.pool, [n], n, c.ws_pool)
+    se.se_kv_append_chunk(c.kv, bf16(k), bf16(v), chunk, 1, c.ws)
+    oc.append(c.o, c.k, c.v, c.meta, k, v,
+              *(getattr(chunk, x).cpu().numpy() for x in ("start", "seq", "pos", "slot")))
+    for f32 in (False, True):
+        a = Attn(c, 2, f32)
+        a.run(chunk)
+        a.q, a.qt = q, bf16(q)
+        a.call(chunk)
+        a.check(chunk, rows=16)
+
+
 def test_refused_rows_and_missing_pages():
     g = np.random.default_rng([17])
     c = held(g, 3, 2, 128, [40, 0, 300], [5, 20, 5])
