@@ -821,22 +821,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint64_t scale2 = f32x2(sl2, sl2);
                     uint64_t sum[2] = {0, 0};
                     float neg = m == -INFINITY ? 0.f : -m;
-                    auto quarter = [&](int x) {
+                    // keys per store of P: the fewer stores, the less the exponentials ahead of
+                    // them drain (the two terms of fp32 output want the registers)
+                    constexpr int kRun = F32 ? 32 : 64;
+                    auto run_of = [&](int x) {
                         const uint64_t neg2 = f32x2(neg, neg);
-                        uint32_t hi[16], lo[16];
+                        uint32_t hi[kRun / 2], lo[kRun / 2];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
+                        for (int e = 0; e < kRun; e += 2) {
                             float a, d;
-                            f32x2_split(fma_f32x2(f32x2(v[32 * x + e], v[32 * x + e + 1]), scale2, neg2),
-                                        a, d);
+                            f32x2_split(
+                                fma_f32x2(f32x2(v[kRun * x + e], v[kRun * x + e + 1]), scale2, neg2), a, d);
                             a = ex2_approx(a);
                             d = ex2_approx(d);
                             sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(a, d));
                             hi[e / 2] = pack_bf16(a, d);
                             if (F32) lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
                         }
-                        tmem_st16(t_s + 16 * x, hi);
-                        if (F32) tmem_st16(t_s + 64 + 16 * x, lo);
+                        if constexpr (F32) {
+                            tmem_st16(t_s + 16 * x, hi);
+                            tmem_st16(t_s + 64 + 16 * x, lo);
+                        } else {
+                            tmem_st32(t_s + 32 * x, hi);
+                        }
                     };
                     bool settled = false;
                     float total;
@@ -844,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     while (true) {                   // (one copy of the code: it is long)
                         if (settled || i > 0) {
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) quarter(x);
+                            for (int x = 0; x < kKeys / kRun; ++x) run_of(x);
                             float s0, s1;
                             f32x2_split(add_f32x2(sum[0], sum[1]), s0, s1);
                             total = s0 + s1;

@@ -176,29 +176,45 @@ __global__ void __launch_bounds__(1024)
         __syncthreads();
         const int lo = max(r0, static_cast<int>(min(row_base, max_rows)));
         const int hi = min(r1, c_end);
-        for (int t = lo + threadIdx.x; t < hi; t += nt) {
+        // four rows a thread at once: their searches and loads overlap
+        for (int t0 = lo + threadIdx.x; t0 < hi; t0 += 4 * nt) {
+            int at[4], pos[4], phys[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) at[k] = 0;
             // the last sequence of the pass that starts at or before row t
-            int i = 0;
             for (int step = nt >> 1; step > 0; step >>= 1)
-                if (s_start[i + step] <= t) i += step;
-            const int q = b0 + i;
-            int pos = -1, slot = -1;
-            if (s_top[i] >= 0) {
-                pos = s_ctx[i] + (t - s_start[i]);
-                const int pg = pos / kPage;
-                int32_t* entry = pool.block_table + (int64_t)q * pool.max_pages_per_seq + pg;
-                const int fresh = pg - s_held[i];
-                int phys = fresh < 0 ? *entry : pool.free_pages[s_top[i] - fresh];
-                if (phys < 0 || phys >= pool.num_pages) {
-                    bad_flags |= SE_DEV_BAD_INDEX;
-                    phys = -1;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (s_start[at[k] + step] <= t0 + k * nt) at[k] += step;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = t0 + k * nt, i = at[k];
+                pos[k] = phys[k] = -1;
+                if (t < hi && s_top[i] >= 0) {
+                    pos[k] = s_ctx[i] + (t - s_start[i]);
+                    const int fresh = pos[k] / kPage - s_held[i];
+                    phys[k] = fresh < 0 ? pool.block_table[(int64_t)(b0 + i) * pool.max_pages_per_seq +
+                                                           pos[k] / kPage]
+                                        : pool.free_pages[s_top[i] - fresh];
                 }
-                if (fresh >= 0 && (pos % kPage == 0)) *entry = phys;
-                if (phys >= 0) slot = phys * kPage + pos % kPage;
             }
-            ck.seq[t] = q;
-            ck.pos[t] = pos;
-            ck.slot[t] = slot;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = t0 + k * nt, i = at[k];
+                if (t >= hi) break;
+                if (pos[k] >= 0) {
+                    if (phys[k] < 0 || phys[k] >= pool.num_pages) {
+                        bad_flags |= SE_DEV_BAD_INDEX;
+                        phys[k] = -1;
+                    }
+                    const int pg = pos[k] / kPage;
+                    if (pg >= s_held[i] && pos[k] % kPage == 0)
+                        pool.block_table[(int64_t)(b0 + i) * pool.max_pages_per_seq + pg] = phys[k];
+                }
+                ck.seq[t] = b0 + i;
+                ck.pos[t] = pos[k];
+                ck.slot[t] = phys[k] >= 0 ? phys[k] * kPage + pos[k] % kPage : -1;
+            }
         }
         row_base += rows;
         need_base += needs;
@@ -443,12 +459,15 @@ __global__ void __launch_bounds__(128)
 
 }  // namespace
 
+// A thread per sequence, up to 1024 of them in one pass.
+static int scan_threads(int batch) { return batch > 512 ? 1024 : batch > 256 ? 512 : 256; }
+
 size_t page_pool_ws_bytes() { return 512; }
 
 cudaError_t launch_chunk_plan(const se_page_pool& pool, const int32_t* new_len, int batch,
                               const se_chunk& ck, int* ws, cudaStream_t s) {
-    const int nt = batch > 256 ? 1024 : 256;
-    const int grid = max(1, min(num_sms(), (ck.max_tokens + 4 * nt - 1) / (4 * nt)));
+    const int nt = scan_threads(batch);
+    const int grid = max(1, min(num_sms(), (ck.max_tokens + 2 * nt - 1) / (2 * nt)));
     const int per = (ck.max_tokens + grid - 1) / grid;
     return launch_pdl(chunk_plan_kernel, dim3(grid), dim3(nt), (4 * nt + 1) * sizeof(int), s, pool,
                       new_len, batch, ck, per, ws);
@@ -456,7 +475,7 @@ cudaError_t launch_chunk_plan(const se_page_pool& pool, const int32_t* new_len, 
 
 cudaError_t launch_pages_release(const se_page_pool& pool, const int32_t* done, int batch, int* ws,
                                  cudaStream_t s) {
-    const int nt = batch > 256 ? 1024 : 256;
+    const int nt = scan_threads(batch);
     // a block for every 4096 table entries that could be released
     const int64_t most = std::min<int64_t>((int64_t)batch * pool.max_pages_per_seq, pool.num_pages);
     const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms(), most / 4096)));
