@@ -334,14 +334,14 @@ int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_n
  * split row are joined in a fixed order).  A block-table entry outside the pages sets SE_DEV_BAD_INDEX and its
  * keys count as absent; ctx_len outside [0, 16 * max_pages_per_seq], or a row
  * position at or past ctx_len[b]: SE_DEV_BAD_LENGTH, clamped.  start outside [0, max_tokens] or
- * descending: SE_DEV_BAD_LENGTH, clamped (a descending sequence has no rows).
+ * descending: SE_DEV_BAD_LENGTH, and the results are unspecified.
  * Held keys and values are finite; what lies past ctx_len in a page may be anything.
  * scale finite (0 and negative ones too); window, sink >= 0.  Limits: batch <= 8192,
  * 0 <= max_tokens <= 2^24, max_pages_per_seq <= 2^26, else SE_ERR_UNSUPPORTED.
  * Workspace: se_chunk_attn_workspace(...), zero-filled before its first use:
  * it holds arrival counters at a fixed offset, which every call leaves at zero, so one
  * workspace serves calls of any shape whose size it covers.  Clear it again after a
- * call that set SE_DEV_TIMEOUT. */
+ * call that set a device error bit. */
 int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, int batch,
                   int num_q_heads, float scale, const se_chunk_attn_opts* opts, void* out,
                   float* lse, void* ws, size_t ws_bytes, se_stream_t stream);

@@ -393,10 +393,11 @@ def se_pages_release(pool: PagePool, done, batch: int, ws, stream=None):
 def _token_stride(x, what: str) -> int:
     """Elements between tokens of a [tokens][heads][head_dim] tensor, which may be a
     slice of wider rows (a packed q/k/v projection)."""
-    if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise SparseEngineError(f"{what}: [tokens][heads][head_dim] with contiguous heads needed, "
-                                f"got shape {tuple(x.shape)} strides {x.stride()}")
-    return x.stride(0) if x.shape[0] > 1 else x.shape[1] * x.shape[2]
+                                f"got shape {tuple(shape)} strides {stride}")
+    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, stream=None):
