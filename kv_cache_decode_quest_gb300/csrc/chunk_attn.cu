@@ -1043,10 +1043,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0 && count > 1) {
                     int* counter = reinterpret_cast<int*>(p.ws + kCounterOff) +
                                    16 * (c0 + first) + (final ? 8 : 0) + warp;
-                    __threadfence();
-                    is_last = atomicAdd(counter, 1) == count - 1;
+                    // releases this warp's rows (ordered before it by the warp barrier) and
+                    // acquires those of the warps that arrived earlier
+                    int before;
+                    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+                                 : "=r"(before)
+                                 : "l"(counter)
+                                 : "memory");
+                    is_last = before == count - 1;
                     if (is_last) *counter = 0;
-                    __threadfence();
                 }
                 if (!__shfl_sync(0xffffffffu, is_last, 0)) break;
                 __syncwarp();
