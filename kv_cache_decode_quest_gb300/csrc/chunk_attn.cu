@@ -29,7 +29,7 @@
 //
 // Bound: 4 D flops per row and key on the tensor cores for chunks (32 MMAs of 64 clocks a
 // tile for 256 rows: 2060 clocks), K and V from HBM for few rows.  Measured on a GB300
-// (head_dim 128, 32 query heads, 4 KV heads, bf16): 2048 tokens behind 30720 in 660 us
+// (head_dim 128, 32 query heads, 4 KV heads, bf16): the last 2048 tokens of 32K in 660 us
 // (1.63 PFLOP/s), a prompt of 8192 in 367 us (1.50 PFLOP/s), 16 sequences of 32K checking
 // 8 tokens each in 169 us (6.4 TB/s).  A tile for 256 rows takes about 2950 clocks: without
 // its softmax 2370, without the tensor cores 2500, its loads alone 2000.  What was
@@ -83,7 +83,7 @@ struct Shape {
     static constexpr int kRegion = 128 * 128;               // 128 rows of 128 bytes
     static constexpr int kTile = kHalves * kRegion;         // 128 rows of Q, K or V
     static constexpr int kStages = D == 128 ? 5 : 10;
-    static constexpr size_t kCtrl = 3072;
+    static constexpr size_t kCtrl = 3 * 1024;
     static constexpr size_t kSmem = (size_t)(2 + kStages) * kTile + kCtrl;
 };
 
