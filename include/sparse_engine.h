@@ -289,10 +289,11 @@ int se_kv_append(const se_paged_kv* kv, const void* k_new, const void* v_new, in
  * page, its rows get pos = slot = -1, SE_DEV_CAPACITY (the latter two count as
  * need[b] = 0 for those behind).  A negative length, or n_pages[b] fewer than
  * ctx_len[b] needs (or more than max_pages_per_seq): SE_DEV_BAD_LENGTH, need[b] = 0
- * and no rows (new_len < 0) or rows with pos = slot = -1.  A page outside [0, num_pages) met on the stack or in the block
- * table: SE_DEV_BAD_INDEX, the slots on it are -1.  ctx_len is not changed (the append commits it),
- * so a plan that is made again before the append finds its pages held and takes
- * no others.  Limits: 0 <= max_tokens <= 2^24, num_pages and max_pages_per_seq < 2^27.
+ * and no rows (new_len < 0) or rows with pos = slot = -1.  A page outside
+ * [0, num_pages) met on the stack or in the block table: SE_DEV_BAD_INDEX, the slots
+ * on it are -1.  ctx_len is not changed (the append commits it), so a plan that is
+ * made again before the append finds its pages held and takes no others.
+ * Limits: 0 <= max_tokens <= 2^24, num_pages and max_pages_per_seq < 2^27.
  * Workspace: se_page_pool_workspace(batch), zero-filled before its first use: it
  * holds an arrival counter, which every call leaves at zero. */
 int se_chunk_plan(const se_page_pool* pool, const int32_t* new_len, int batch,
@@ -301,9 +302,9 @@ int se_chunk_plan(const se_page_pool* pool, const int32_t* new_len, int batch,
 /* Puts the pages of every sequence with done[b] != 0 (int32 [batch]) back on the
  * stack and sets its n_pages and ctx_len to 0.  The pages go back last page
  * first (the first released sequence's first page ends on top), so a plan that
- * takes as many takes them in the order of their sequences.  A stack that would pass num_pages entries (a page released
- * twice): SE_DEV_CAPACITY, nothing is released.  n_pages outside
- * [0, max_pages_per_seq]: SE_DEV_BAD_LENGTH, clamped.
+ * takes as many takes them in the order of their sequences.  A stack that would
+ * pass num_pages entries (a page released twice): SE_DEV_CAPACITY, nothing is
+ * released.  n_pages outside [0, max_pages_per_seq]: SE_DEV_BAD_LENGTH, clamped.
  * Workspace: as se_chunk_plan. */
 int se_pages_release(const se_page_pool* pool, const int32_t* done, int batch, void* ws,
                      size_t ws_bytes, se_stream_t stream);
@@ -330,11 +331,12 @@ int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_n
  * out and lse at and past start[batch] are left as they were.
  * q bf16 [max_tokens][num_q_heads][head_dim] (opts->q_stride); out bf16 or fp32
  * [max_tokens][num_q_heads][head_dim]; lse fp32 [max_tokens][num_q_heads] or NULL.
- * kv->meta is not used and may be NULL.  The results do not depend on timing (the pieces of a
- * split row are joined in a fixed order).  A block-table entry outside the pages sets SE_DEV_BAD_INDEX and its
- * keys count as absent; ctx_len outside [0, 16 * max_pages_per_seq], or a row
- * position at or past ctx_len[b]: SE_DEV_BAD_LENGTH, clamped.  start outside [0, max_tokens] or
- * descending: SE_DEV_BAD_LENGTH, and the results are unspecified.
+ * kv->meta is not used and may be NULL.  The results do not depend on timing (the
+ * pieces of a split row are joined in a fixed order).  A block-table entry outside
+ * the pages sets SE_DEV_BAD_INDEX and its keys count as absent; ctx_len outside
+ * [0, 16 * max_pages_per_seq], or a row position at or past ctx_len[b]:
+ * SE_DEV_BAD_LENGTH, clamped.  start outside [0, max_tokens] or descending:
+ * SE_DEV_BAD_LENGTH, and the results are unspecified.
  * Held keys and values are finite; what lies past ctx_len in a page may be anything.
  * scale finite (0 and negative ones too); window, sink >= 0.  Limits: batch <= 8192,
  * 0 <= max_tokens <= 2^24, max_pages_per_seq <= 2^26, else SE_ERR_UNSUPPORTED.

@@ -69,7 +69,7 @@ constexpr int kMinShare = 16;                      // units a CTA takes at least
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrowSum = 16384.f;                // a tile's row sum above this: the reference moves up
+constexpr float kGrowSum = 16384.f;                // a row sum of P above this moves the reference
 
 // Workspace: status word, at byte 256 the arrival counters [kMaxCtas][2 levels][8 warps], then
 // the partial results: two pieces per CTA (the one it takes over and the one it hands
@@ -106,7 +106,6 @@ struct Params {
     int window, sink;
     float scale_log2;              // > 0
     uint32_t negate;               // instruction descriptor bit for a negative scale
-    int out_f32;
     void* out;
     float* lse;
     uint8_t* ws;
@@ -173,12 +172,15 @@ struct Shares {
     long long each, extra;
     __device__ __forceinline__ Shares(long long U, long long n)
         : each(static_cast<long long>(udiv(U, n))), extra(U - each * n) {}
-    __device__ __forceinline__ Shares(long long each, long long extra, int) : each(each), extra(extra) {}
-    __device__ __forceinline__ long long begin(int c) const { return each * c + min((long long)c, extra); }
+    __device__ __forceinline__ Shares(long long each, long long extra, int)
+        : each(each), extra(extra) {}
+    __device__ __forceinline__ long long begin(int c) const {
+        return each * c + min((long long)c, extra);
+    }
     __device__ __forceinline__ int of(long long u) const {       // the CTA whose share holds unit u
         const long long big = extra * (each + 1);
         const long long c = u < big ? udiv(u, each + 1) : extra + udiv(u - big, each);
-        return static_cast<int>(min(c, (long long)kMaxCtas - 1));     // (in range whatever `start` holds)
+        return static_cast<int>(min(c, (long long)kMaxCtas - 1));   // (whatever `start` holds)
     }
 };
 
@@ -232,8 +234,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* 
 }
 
 // Two barriers at once.
-__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb, Ctrl* c,
-                                           int* status) {
+__device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b, uint32_t pb,
+                                           Ctrl* c, int* status) {
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
@@ -369,7 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long NC = min((long long)gridDim.x, (U + kMinShare - 1) / kMinShare);
     const Shares shares(U, max(1ll, NC));
     const bool idle = blockIdx.x >= NC;
-    const long long u0 = idle ? 0 : shares.begin(blockIdx.x), u1 = idle ? 0 : shares.begin(blockIdx.x + 1);
+    const long long u0 = idle ? 0 : shares.begin(blockIdx.x);
+    const long long u1 = idle ? 0 : shares.begin(blockIdx.x + 1);
     long long* s_start = reinterpret_cast<long long*>(smem + 256);   // sequence, block, prefix
     if (u0 < u1) {
         long long base = 0;
@@ -413,345 +416,347 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = c->tmem;
 
     if (warp >= kSoftWarps) {
-    regs_fewer<kRegsFew>();
-    if (warp == kSoftWarps) {
-        // ------------------------------ producer ------------------------------
-        fence_proxy_async_smem();                    // the staged lengths are read: TMA may write
-        if (lane == 0) {
-            prefetch_tmap(&tq);
-            prefetch_tmap(&tk);
-            prefetch_tmap(&tv);
-        }
-        uint32_t seq = 0;                            // ring positions used
-        int items = 0, loads_q = 0;
-        long long u = u0;
-        int h = 0;
-        bool first = true, go = true;
-        while (go) {
-            // the next block with tiles
-            Seq s = {0, 0, 0, 0};
-            Tiles t = {0, 0, 0, 0};
-            if (u < u1) {
-                while (true) {
-                    if (b >= b_win + 32) {
-                        b_win = b;
-                        int bad = 0;
-                        if (b + lane < p.batch) win = seq_info(p, b + lane, bad);
+        regs_fewer<kRegsFew>();
+        if (warp == kSoftWarps) {
+            // ------------------------------ producer ------------------------------
+            fence_proxy_async_smem();                    // the staged lengths are read: TMA may write
+            if (lane == 0) {
+                prefetch_tmap(&tq);
+                prefetch_tmap(&tk);
+                prefetch_tmap(&tv);
+            }
+            uint32_t seq = 0;                            // ring positions used
+            int items = 0, loads_q = 0;
+            long long u = u0;
+            int h = 0;
+            bool first = true, go = true;
+            while (go) {
+                // the next block with tiles
+                Seq s = {0, 0, 0, 0};
+                Tiles t = {0, 0, 0, 0};
+                if (u < u1) {
+                    while (true) {
+                        if (b >= b_win + 32) {
+                            b_win = b;
+                            int bad = 0;
+                            if (b + lane < p.batch) win = seq_info(p, b + lane, bad);
+                        }
+                        const int src = b - b_win;
+                        s.s0 = __shfl_sync(0xffffffffu, win.s0, src);
+                        s.n = __shfl_sync(0xffffffffu, win.n, src);
+                        s.p0 = __shfl_sync(0xffffffffu, win.p0, src);
+                        s.len = __shfl_sync(0xffffffffu, win.len, src);
+                        t = block_tiles(p, s, blk);
+                        if (t.n > 0 || b + 1 >= p.batch) break;
+                        ++b;
+                        blk = 0;
                     }
-                    const int src = b - b_win;
-                    s.s0 = __shfl_sync(0xffffffffu, win.s0, src);
-                    s.n = __shfl_sync(0xffffffffu, win.n, src);
-                    s.p0 = __shfl_sync(0xffffffffu, win.p0, src);
-                    s.len = __shfl_sync(0xffffffffu, win.len, src);
-                    t = block_tiles(p, s, blk);
-                    if (t.n > 0 || b + 1 >= p.batch) break;
-                    ++b;
-                    blk = 0;
                 }
-            }
-            const int cost = block_cost(t);
-            Item it = {};
-            it.b = b;
-            it.n = 0;
-            long long next = u1;
-            if (u < u1 && t.n > 0) {             // (n is 0 if the share ends before a tile)
-                if (first) {
-                    h = static_cast<int>(udiv(u - pre * H, cost));
-                    first = false;
+                const int cost = block_cost(t);
+                Item it = {};
+                it.b = b;
+                it.n = 0;
+                long long next = u1;
+                if (u < u1 && t.n > 0) {             // (n is 0 if the share ends before a tile)
+                    if (first) {
+                        h = static_cast<int>(udiv(u - pre * H, cost));
+                        first = false;
+                    }
+                    const long long us = pre * H + (long long)h * cost;      // the item's first unit
+                    const long long t0 = us + kBlockCost;                    // its first tile's
+                    next = min(u1, us + cost);
+                    it.h = h;
+                    it.tok0 = s.s0 + blk * (kBlockRows >> p.lg);
+                    it.rows = t.rows;
+                    it.pos0 = s.p0 + blk * (kBlockRows >> p.lg);
+                    it.len = s.len;
+                    it.ts = t.ts;
+                    it.tl = t.tl;
+                    const int per = tile_cost(t.rows);
+                    it.j0 = static_cast<int>(udiv(max(0ll, u - t0) + per - 1, per));
+                    it.n = static_cast<int>(udiv(max(0ll, next - t0) + per - 1, per)) - it.j0;
+                    it.split = it.n < t.n;
+                    it.t0 = t0;
+                    it.t1 = us + cost - per;             // the last tile's first unit
                 }
-                const long long us = pre * H + (long long)h * cost;      // the item's first unit
-                const long long t0 = us + kBlockCost;                    // its first tile's
-                next = min(u1, us + cost);
-                it.h = h;
-                it.tok0 = s.s0 + blk * (kBlockRows >> p.lg);
-                it.rows = t.rows;
-                it.pos0 = s.p0 + blk * (kBlockRows >> p.lg);
-                it.len = s.len;
-                it.ts = t.ts;
-                it.tl = t.tl;
-                const int per = tile_cost(t.rows);
-                it.j0 = static_cast<int>(udiv(max(0ll, u - t0) + per - 1, per));
-                it.n = static_cast<int>(udiv(max(0ll, next - t0) + per - 1, per)) - it.j0;
-                it.split = it.n < t.n;
-                it.t0 = t0;
-                it.t1 = us + cost - per;             // the last tile's first unit
-            }
-            // on to the next item: heads within the block, then the next block
-            auto advance = [&]() {
-                u = next;
-                if (++h == H) {
-                    h = 0;
-                    pre += cost;
-                    ++blk;
+                // on to the next item: heads within the block, then the next block
+                auto advance = [&]() {
+                    u = next;
+                    if (++h == H) {
+                        h = 0;
+                        pre += cost;
+                        ++blk;
+                    }
+                };
+                if (it.n == 0 && next < u1) {        // the share begins in the block's last tile
+                    advance();
+                    continue;
                 }
-            };
-            if (it.n == 0 && next < u1) {            // the share begins inside the block's last tile
+                // lanes 0..15 issue a tile's boxes: page lane & 7, columns 64 * (lane >> 3)
+                const int32_t* bt = p.kv.block_table + (int64_t)it.b * p.kv.max_pages_per_seq;
+                const int absent_row = p.kv.num_pages * H * kPage;     // past the map: reads zero
+                auto fetch = [&](int j) -> int {         // -1: a page past the end, or past the piece
+                    const int pg = tile_of(it, it.j0 + j) * kTilePages + (lane & 7);
+                    return (j < it.n && pg * kPage < it.len) ? bt[pg] : -1;
+                };
+                auto row_of = [&](int j, int phys) -> int {
+                    const int pg = tile_of(it, it.j0 + j) * kTilePages + (lane & 7);
+                    if (pg * kPage >= it.len) return absent_row;
+                    if (phys < 0 || phys >= p.kv.num_pages) {
+                        *static_cast<volatile int*>(&c->any_absent) = 1;
+                        __threadfence_block();
+                        flag(status, SE_DEV_BAD_INDEX);
+                        return absent_row;
+                    }
+                    return (phys * H + it.h) * kPage;
+                };
+                // K's 64-column halves are regions of 128 rows (the tensor cores want all keys
+                // at one stride); V's are kept page by page, so one box brings a page
+                auto load = [&](bool keys, int row) -> bool {
+                    const int st = seq % S::kStages;
+                    if (!warp_wait(&c->empty[st], ((seq / S::kStages) & 1) ^ 1, c, status))
+                        return false;
+                    if (lane == 0) mbar_arrive_expect_tx(&c->full[st], S::kTile);
+                    __syncwarp();
+                    uint8_t* to = ring + st * S::kTile;
+                    if (keys && lane < 8 * S::kHalves)
+                        tma_load_2d(to + (lane >> 3) * S::kRegion + (lane & 7) * 2048, &tk,
+                                    &c->full[st], (lane >> 3) * 64, row);
+                    if (!keys && lane < 8)
+                        tma_load_3d(to + lane * (2048 * S::kHalves), &tv, &c->full[st], 0, row, 0);
+                    ++seq;
+                    return true;
+                };
+                int nxt1 = fetch(0), nxt2 = fetch(1);
+                const int slot = items % kItems;
+                if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
+                if (lane == 0) {
+                    c->items[slot] = it;
+                    mbar_arrive(&c->item_full[slot]);
+                }
+                ++items;
+                if (it.n == 0) break;
+                int row_k = row_of(0, nxt1), row_v;
+                go = load(true, row_k);
+                if (go) {
+                    go = warp_wait(&c->q_empty, (loads_q & 1) ^ 1, c, status);
+                    if (go && lane == 0) {
+                        const int tiles = it.rows > 128 ? 2 : 1;
+                        mbar_arrive_expect_tx(&c->q_full, tiles * S::kTile);
+                        for (int w = 0; w < tiles; ++w)
+                            for (int hf = 0; hf < S::kHalves; ++hf)
+                                tma_load_3d(qs + w * S::kTile + hf * S::kRegion, &tq, &c->q_full,
+                                            hf * 64, it.h * G, it.tok0 + w * (128 >> p.lg));
+                    }
+                    __syncwarp();
+                    if (go) ++loads_q;
+                }
+                for (int j = 0; go && j < it.n; ++j) {   // K of tile j + 1, then V of tile j
+                    row_v = row_k;
+                    nxt1 = nxt2;
+                    nxt2 = fetch(j + 2);
+                    if (j + 1 < it.n) {
+                        row_k = row_of(j + 1, nxt1);
+                        go = load(true, row_k);
+                    }
+                    if (go) go = load(false, row_v);
+                }
                 advance();
-                continue;
             }
-            // lanes 0..15 issue a tile's boxes: page lane & 7, columns 64 * (lane >> 3)
-            const int32_t* bt = p.kv.block_table + (int64_t)it.b * p.kv.max_pages_per_seq;
-            const int absent_row = p.kv.num_pages * H * kPage;            // past the map: reads zero
-            auto fetch = [&](int j) -> int {         // -1: a page past the end, or past the piece
-                const int pg = tile_of(it, it.j0 + j) * kTilePages + (lane & 7);
-                return (j < it.n && pg * kPage < it.len) ? bt[pg] : -1;
-            };
-            auto row_of = [&](int j, int phys) -> int {
-                const int pg = tile_of(it, it.j0 + j) * kTilePages + (lane & 7);
-                if (pg * kPage >= it.len) return absent_row;
-                if (phys < 0 || phys >= p.kv.num_pages) {
-                    *static_cast<volatile int*>(&c->any_absent) = 1;
-                    __threadfence_block();
-                    flag(status, SE_DEV_BAD_INDEX);
-                    return absent_row;
+            if (lane == 0) {
+                // every copy has landed before the block exits
+                volatile int never = 0;
+                const uint32_t from = seq > (uint32_t)S::kStages ? seq - S::kStages : 0;
+                for (uint32_t i = from; i < seq; ++i)
+                    mbar_wait(&c->full[i % S::kStages], (i / S::kStages) & 1, &never);
+                if (loads_q > 0) mbar_wait(&c->q_full, (loads_q - 1) & 1, &never);
+            }
+            __syncwarp();
+        } else if (warp == kSoftWarps + 1) {
+            // ------------------------------ MMA issuer ------------------------------
+            // The whole warp runs this with the same values; an elected lane issues.
+            // Descriptor words: the high one is the operand's layout, the low one
+            // its address / 16 (and V's column stride), to which offsets are added.
+            const uint64_t qd = umma_desc_sw128(smem_u32(qs)), kd = umma_desc_sw128(smem_u32(ring));
+            const uint64_t vd = umma_desc_mn_sw128(smem_u32(ring), 2048);
+            const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
+            const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
+            const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
+            const uint32_t idesc_s = umma_idesc_bf16_f32(128, kKeys) | p.negate;
+            const uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | kUmmaBMnMajor;
+            const uint32_t bar_empty = smem_u32(&c->empty[0]);
+            const uint32_t bar_s = smem_u32(&c->s_full[0]), bar_o = smem_u32(&c->o_done[0]);
+            const uint32_t bar_q = smem_u32(&c->q_empty);
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            uint32_t st = 0, ph = 0;                     // ring stage and its phase
+            uint32_t np0 = 0, np1 = 0;                   // phases of P of each group
+            auto wait_stage = [&]() { return warp_wait(&c->full[st], ph, c, status); };
+            auto next_stage = [&]() {
+                if (++st == S::kStages) {
+                    st = 0;
+                    ph ^= 1;
                 }
-                return (phys * H + it.h) * kPage;
             };
-            // K's 64-column halves are regions of 128 rows (the tensor cores want all keys
-            // at one stride); V's are kept page by page, so one box brings a page
-            auto load = [&](bool keys, int row) -> bool {
-                const int st = seq % S::kStages;
-                if (!warp_wait(&c->empty[st], ((seq / S::kStages) & 1) ^ 1, c, status)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(&c->full[st], S::kTile);
-                __syncwarp();
-                uint8_t* to = ring + st * S::kTile;
-                if (keys && lane < 8 * S::kHalves)
-                    tma_load_2d(to + (lane >> 3) * S::kRegion + (lane & 7) * 2048, &tk, &c->full[st],
-                                (lane >> 3) * 64, row);
-                if (!keys && lane < 8)
-                    tma_load_3d(to + lane * (2048 * S::kHalves), &tv, &c->full[st], 0, row, 0);
-                ++seq;
+            // S_w = Q_qt K^T; `beside` runs before the last four instructions, while those ahead of
+            // them are being carried out
+            auto scores = [&](uint32_t w, uint32_t qt, uint32_t stage, auto beside) {
+                const uint32_t ka = k_lo + stage * (S::kTile / 16), qa = q_lo + qt * (S::kTile / 16);
+#pragma unroll
+                for (int x = 0; x < S::kHalves; ++x) {
+                    if (x + 1 == S::kHalves) beside();
+                    umma_bf16_warp4(tm + w * 128, qa + x * (S::kRegion / 16), q_hi,
+                                    ka + x * (S::kRegion / 16), k_hi, idesc_s, x > 0);
+                }
+                umma_commit_warp(bar_s + w * 8);
+            };
+            constexpr int kPageV = 2048 * S::kHalves;    // bytes of a page of V: 16 keys, one K step
+            // O_w (+)= P_w V; `there`: P is known to be there
+            auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase,
+                               bool there) -> bool {
+                if (!there && !warp_wait(&c->p_full[w], phase, c, status)) return false;
+                tc_fence_after();
+                const uint32_t va = v_lo + stage * (S::kTile / 16);
+#pragma unroll
+                for (int part = 0; part < (F32 ? 2 : 1); ++part)
+#pragma unroll
+                    for (int half = 0; half < 2; ++half)
+                        umma_bf16_ts_warp4<kPageV / 16>(tm + 256 + w * D,
+                                                        tm + w * 128 + part * 64 + half * 32,
+                                                        va + half * (4 * kPageV / 16), v_hi, idesc_o,
+                                                        half + part > 0 ? 1u : acc);
                 return true;
             };
-            int nxt1 = fetch(0), nxt2 = fetch(1);
-            const int slot = items % kItems;
-            if (!warp_wait(&c->item_empty[slot], ((items / kItems) & 1) ^ 1, c, status)) break;
-            if (lane == 0) {
-                c->items[slot] = it;
-                mbar_arrive(&c->item_full[slot]);
-            }
-            ++items;
-            if (it.n == 0) break;
-            int row_k = row_of(0, nxt1), row_v;
-            go = load(true, row_k);
-            if (go) {
-                go = warp_wait(&c->q_empty, (loads_q & 1) ^ 1, c, status);
-                if (go && lane == 0) {
-                    const int tiles = it.rows > 128 ? 2 : 1;
-                    mbar_arrive_expect_tx(&c->q_full, tiles * S::kTile);
-                    for (int w = 0; w < tiles; ++w)
-                        for (int hf = 0; hf < S::kHalves; ++hf)
-                            tma_load_3d(qs + w * S::kTile + hf * S::kRegion, &tq, &c->q_full, hf * 64,
-                                        it.h * G, it.tok0 + w * (128 >> p.lg));
-                }
-                __syncwarp();
-                if (go) ++loads_q;
-            }
-            for (int j = 0; go && j < it.n; ++j) {   // K of tile j + 1, then V of tile j
-                row_v = row_k;
-                nxt1 = nxt2;
-                nxt2 = fetch(j + 2);
-                if (j + 1 < it.n) {
-                    row_k = row_of(j + 1, nxt1);
-                    go = load(true, row_k);
-                }
-                if (go) go = load(false, row_v);
-            }
-            advance();
-        }
-        if (lane == 0) {
-            // every copy has landed before the block exits
-            volatile int never = 0;
-            const uint32_t from = seq > (uint32_t)S::kStages ? seq - S::kStages : 0;
-            for (uint32_t i = from; i < seq; ++i)
-                mbar_wait(&c->full[i % S::kStages], (i / S::kStages) & 1, &never);
-            if (loads_q > 0) mbar_wait(&c->q_full, (loads_q - 1) & 1, &never);
-        }
-        __syncwarp();
-    } else if (warp == kSoftWarps + 1) {
-        // ------------------------------ MMA issuer ------------------------------
-        // The whole warp runs this with the same values; an elected lane issues.
-        // Descriptor words: the high one is the operand's layout, the low one
-        // its address / 16 (and V's column stride), to which offsets are added.
-        const uint64_t qd = umma_desc_sw128(smem_u32(qs)), kd = umma_desc_sw128(smem_u32(ring));
-        const uint64_t vd = umma_desc_mn_sw128(smem_u32(ring), 2048);
-        const uint32_t q_lo = static_cast<uint32_t>(qd), q_hi = static_cast<uint32_t>(qd >> 32);
-        const uint32_t k_lo = static_cast<uint32_t>(kd), k_hi = static_cast<uint32_t>(kd >> 32);
-        const uint32_t v_lo = static_cast<uint32_t>(vd), v_hi = static_cast<uint32_t>(vd >> 32);
-        const uint32_t idesc_s = umma_idesc_bf16_f32(128, kKeys) | p.negate;
-        const uint32_t idesc_o = umma_idesc_bf16_f32(128, D) | kUmmaBMnMajor;
-        const uint32_t bar_empty = smem_u32(&c->empty[0]);
-        const uint32_t bar_s = smem_u32(&c->s_full[0]), bar_o = smem_u32(&c->o_done[0]);
-        const uint32_t bar_q = smem_u32(&c->q_empty);
-        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        uint32_t st = 0, ph = 0;                     // ring stage and its phase
-        uint32_t np0 = 0, np1 = 0;                   // phases of P of each group
-        auto wait_stage = [&]() { return warp_wait(&c->full[st], ph, c, status); };
-        auto next_stage = [&]() {
-            if (++st == S::kStages) {
-                st = 0;
-                ph ^= 1;
-            }
-        };
-        // S_w = Q_qt K^T; `beside` runs before the last four instructions, while those ahead of
-        // them are being carried out
-        auto scores = [&](uint32_t w, uint32_t qt, uint32_t stage, auto beside) {
-            const uint32_t ka = k_lo + stage * (S::kTile / 16), qa = q_lo + qt * (S::kTile / 16);
-#pragma unroll
-            for (int x = 0; x < S::kHalves; ++x) {
-                if (x + 1 == S::kHalves) beside();
-                umma_bf16_warp4(tm + w * 128, qa + x * (S::kRegion / 16), q_hi,
-                                ka + x * (S::kRegion / 16), k_hi, idesc_s, x > 0);
-            }
-            umma_commit_warp(bar_s + w * 8);
-        };
-        constexpr int kPageV = 2048 * S::kHalves;    // bytes of a page of V: 16 keys, one K step
-        // O_w (+)= P_w V; `there`: P is known to be there
-        auto product = [&](uint32_t w, uint32_t stage, uint32_t acc, uint32_t phase, bool there) -> bool {
-            if (!there && !warp_wait(&c->p_full[w], phase, c, status)) return false;
-            tc_fence_after();
-            const uint32_t va = v_lo + stage * (S::kTile / 16);
-#pragma unroll
-            for (int part = 0; part < (F32 ? 2 : 1); ++part)
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-                    umma_bf16_ts_warp4<kPageV / 16>(tm + 256 + w * D,
-                                                    tm + w * 128 + part * 64 + half * 32,
-                                                    va + half * (4 * kPageV / 16), v_hi, idesc_o,
-                                                    half + part > 0 ? 1u : acc);
-            return true;
-        };
-        auto test = [&](uint64_t* bar, uint32_t phase) {
-            return __all_sync(0xffffffffu, mbar_test_wait(bar, phase)) != 0;
-        };
-        for (int items = 0;; ++items) {
-            const int slot = items % kItems;
-            if (!warp_wait(&c->item_full[slot], (items / kItems) & 1, c, status)) break;
-            const Item* ip = &c->items[slot];
-            const int n = __shfl_sync(0xffffffffu, ip->n, 0);
-            const bool both = __shfl_sync(0xffffffffu, ip->rows, 0) > 128;   // rows of its own each
-            const int len = ip->len, ts = ip->ts, tl = ip->tl, j0 = ip->j0;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c->item_empty[slot]);
-            if (n == 0) break;
-            // rows of the last page past the held tokens may be anything, and 0 * NaN is
-            // not 0: V's are cleared before the product.  They are in the piece's tile
-            // `tail_j`, if any (the tiles of a block are in key order).
-            const int tail_k0 = len / kKeys * kKeys;
-            const int tail_t = tail_k0 / kKeys;
-            const int tail_at = tail_t < ts ? tail_t : tail_t - tl + ts;
-            const int tail_j =
-                len % kPage == 0 || (tail_t >= ts && tail_t < tl) ? -1 : tail_at - j0;
-            auto clear_tail = [&](uint32_t stage) {
-                const int row = len % kPage;         // of the last page: 16 rows per half
-                uint8_t* v = ring + stage * S::kTile + (len - tail_k0) / kPage * kPageV;
-                for (int i = lane; i < (kPage - row) * 8 * S::kHalves; i += 32) {
-                    const int x = row + i / (8 * S::kHalves), o = i % (8 * S::kHalves);
-                    *reinterpret_cast<uint4*>(v + (o >> 3) * 2048 + x * 128 + (o & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
+            auto test = [&](uint64_t* bar, uint32_t phase) {
+                return __all_sync(0xffffffffu, mbar_test_wait(bar, phase)) != 0;
             };
-            // Ring order: K0, then for each tile j: K_{j + 1}, V_j.
-            // This warp's own instructions decide how well the tensor cores are fed: a wait
-            // that finds its barrier complete takes 100 to 160 clocks beside busy warps, and the
-            // queue holds some 250 clocks of work.  So barriers that are needed after a
-            // batch of instructions are tested before its end.
-            if (!warp_wait2(&c->q_full, items & 1, &c->full[st], ph, c, status)) break;
-            tc_fence_after();
-            auto nothing = [] {};
-            bool go = true;
-            if (both) {
-                scores(0, 0, st, nothing);
-                scores(1, 1, st, nothing);
-                umma_commit_warp(bar_empty + st * 8);
-                if (n == 1) umma_commit_warp(bar_q);
-                next_stage();
-                bool kv = false, p0 = false, p1 = false;      // known to be there
-#pragma unroll 1
-                for (int j = 0; j < n; ++j) {
-                    const bool more = j + 1 < n;
-                    const uint32_t ks = st, kph = ph;
-                    if (more) next_stage();
-                    const uint32_t vs = st, vph = ph;
-                    next_stage();
-                    if (!kv) go = warp_wait2(&c->full[ks], kph, &c->full[vs], vph, c, status);
-                    if (!go) break;
-                    if (j == tail_j) clear_tail(vs);
-                    go = product(0, vs, j > 0, np0, p0);
-                    if (!go) break;
-                    np0 ^= 1;
-                    if (more)
-                        scores(0, 0, ks, [&] { p1 = test(&c->p_full[1], np1); });
-                    else
-                        umma_commit_warp(bar_o);
-                    go = product(1, vs, j > 0, np1, more && p1);
-                    if (!go) break;
-                    np1 ^= 1;
-                    umma_commit_warp(bar_empty + vs * 8);
-                    if (more) {
-                        // K_{j + 2} and V_{j + 1} follow in the ring
-                        const uint32_t ka = st, kap = ph;
-                        const bool far = j + 2 < n;
-                        const uint32_t va = !far ? ka : ka + 1 == S::kStages ? 0 : ka + 1;
-                        const uint32_t vap = va < ka ? kap ^ 1 : kap;
-                        scores(1, 1, ks, [&] {
-                            kv = test(&c->full[ka], kap) && test(&c->full[va], vap);
-                            p0 = test(&c->p_full[0], np0);
-                        });
-                        umma_commit_warp(bar_empty + ks * 8);
-                        if (!far) umma_commit_warp(bar_q);
-                    } else {
-                        umma_commit_warp(bar_o + 8);
+            for (int items = 0;; ++items) {
+                const int slot = items % kItems;
+                if (!warp_wait(&c->item_full[slot], (items / kItems) & 1, c, status)) break;
+                const Item* ip = &c->items[slot];
+                const int n = __shfl_sync(0xffffffffu, ip->n, 0);
+                const bool both = __shfl_sync(0xffffffffu, ip->rows, 0) > 128;   // own rows each
+                const int len = ip->len, ts = ip->ts, tl = ip->tl, j0 = ip->j0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c->item_empty[slot]);
+                if (n == 0) break;
+                // rows of the last page past the held tokens may be anything, and 0 * NaN is
+                // not 0: V's are cleared before the product.  They are in the piece's tile
+                // `tail_j`, if any (the tiles of a block are in key order).
+                const int tail_k0 = len / kKeys * kKeys;
+                const int tail_t = tail_k0 / kKeys;
+                const int tail_at = tail_t < ts ? tail_t : tail_t - tl + ts;
+                const int tail_j =
+                    len % kPage == 0 || (tail_t >= ts && tail_t < tl) ? -1 : tail_at - j0;
+                auto clear_tail = [&](uint32_t stage) {
+                    const int row = len % kPage;         // of the last page: 16 rows per half
+                    uint8_t* v = ring + stage * S::kTile + (len - tail_k0) / kPage * kPageV;
+                    for (int i = lane; i < (kPage - row) * 8 * S::kHalves; i += 32) {
+                        const int x = row + i / (8 * S::kHalves), o = i % (8 * S::kHalves);
+                        *reinterpret_cast<uint4*>(v + (o >> 3) * 2048 + x * 128 + (o & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
                     }
-                }
-            } else {
-                // tile j is group j & 1's; the scores run two tiles ahead
-                scores(0, 0, st, nothing);
-                umma_commit_warp(bar_empty + st * 8);
-                next_stage();
-                if (n > 1) {
-                    if (!wait_stage()) break;
-                    tc_fence_after();
-                    scores(1, 0, st, nothing);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                };
+                // Ring order: K0, then for each tile j: K_{j + 1}, V_j.
+                // This warp's own instructions decide how well the tensor cores are fed: a wait
+                // that finds its barrier complete takes 100 to 160 clocks beside busy warps, and the
+                // queue holds some 250 clocks of work.  So barriers that are needed after a
+                // batch of instructions are tested before its end.
+                if (!warp_wait2(&c->q_full, items & 1, &c->full[st], ph, c, status)) break;
+                tc_fence_after();
+                auto nothing = [] {};
+                bool go = true;
+                if (both) {
+                    scores(0, 0, st, nothing);
+                    scores(1, 1, st, nothing);
+                    umma_commit_warp(bar_empty + st * 8);
+                    if (n == 1) umma_commit_warp(bar_q);
+                    next_stage();
+                    bool kv = false, p0 = false, p1 = false;      // known to be there
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const uint32_t ks = st, kph = ph;
+                        if (more) next_stage();
+                        const uint32_t vs = st, vph = ph;
+                        next_stage();
+                        if (!kv) go = warp_wait2(&c->full[ks], kph, &c->full[vs], vph, c, status);
+                        if (!go) break;
+                        if (j == tail_j) clear_tail(vs);
+                        go = product(0, vs, j > 0, np0, p0);
+                        if (!go) break;
+                        np0 ^= 1;
+                        if (more)
+                            scores(0, 0, ks, [&] { p1 = test(&c->p_full[1], np1); });
+                        else
+                            umma_commit_warp(bar_o);
+                        go = product(1, vs, j > 0, np1, more && p1);
+                        if (!go) break;
+                        np1 ^= 1;
+                        umma_commit_warp(bar_empty + vs * 8);
+                        if (more) {
+                            // K_{j + 2} and V_{j + 1} follow in the ring
+                            const uint32_t ka = st, kap = ph;
+                            const bool far = j + 2 < n;
+                            const uint32_t va = !far ? ka : ka + 1 == S::kStages ? 0 : ka + 1;
+                            const uint32_t vap = va < ka ? kap ^ 1 : kap;
+                            scores(1, 1, ks, [&] {
+                                kv = test(&c->full[ka], kap) && test(&c->full[va], vap);
+                                p0 = test(&c->p_full[0], np0);
+                            });
+                            umma_commit_warp(bar_empty + ks * 8);
+                            if (!far) umma_commit_warp(bar_q);
+                        } else {
+                            umma_commit_warp(bar_o + 8);
+                        }
+                    }
+                } else {
+                    // tile j is group j & 1's; the scores run two tiles ahead
+                    scores(0, 0, st, nothing);
                     umma_commit_warp(bar_empty + st * 8);
                     next_stage();
-                }
-                if (n <= 2) umma_commit_warp(bar_q);
-#pragma unroll 1
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t w = j & 1, vs = st;
-                    go = wait_stage();
-                    if (!go) break;
-                    next_stage();
-                    if (j == tail_j) clear_tail(vs);
-                    go = product(w, vs, j > 1, w ? np1 : np0, false);
-                    if (!go) break;
-                    if (w) np1 ^= 1;
-                    else np0 ^= 1;
-                    umma_commit_warp(bar_empty + vs * 8);
-                    if (j + 2 < n) {
-                        go = wait_stage();
-                        if (!go) break;
+                    if (n > 1) {
+                        if (!wait_stage()) break;
                         tc_fence_after();
-                        scores(w, 0, st, nothing);
+                        scores(1, 0, st, nothing);
                         umma_commit_warp(bar_empty + st * 8);
                         next_stage();
-                        if (j + 3 == n) umma_commit_warp(bar_q);
-                    } else {
-                        umma_commit_warp(bar_o + w * 8);
+                    }
+                    if (n <= 2) umma_commit_warp(bar_q);
+#pragma unroll 1
+                    for (int j = 0; j < n; ++j) {
+                        const uint32_t w = j & 1, vs = st;
+                        go = wait_stage();
+                        if (!go) break;
+                        next_stage();
+                        if (j == tail_j) clear_tail(vs);
+                        go = product(w, vs, j > 1, w ? np1 : np0, false);
+                        if (!go) break;
+                        if (w) np1 ^= 1;
+                        else np0 ^= 1;
+                        umma_commit_warp(bar_empty + vs * 8);
+                        if (j + 2 < n) {
+                            go = wait_stage();
+                            if (!go) break;
+                            tc_fence_after();
+                            scores(w, 0, st, nothing);
+                            umma_commit_warp(bar_empty + st * 8);
+                            next_stage();
+                            if (j + 3 == n) umma_commit_warp(bar_q);
+                        } else {
+                            umma_commit_warp(bar_o + w * 8);
+                        }
                     }
                 }
+                if (!go) break;
             }
-            if (!go) break;
+            __syncwarp();
+            umma_commit_warp(smem_u32(&c->done));        // every MMA of this CTA has finished
+            volatile int never = 0;
+            mbar_wait(&c->done, 0, &never);
+            __syncwarp();
         }
-        __syncwarp();
-        umma_commit_warp(smem_u32(&c->done));        // every MMA of this CTA has finished
-        volatile int never = 0;
-        mbar_wait(&c->done, 0, &never);
-        __syncwarp();
-    }
     } else {
         // ------------------------------ softmax ------------------------------
         regs_more<kRegsMany>();
@@ -842,13 +847,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int e = 0; e < kRun; e += 2) {
                             float a, d;
-                            f32x2_split(
-                                fma_f32x2(f32x2(v[kRun * x + e], v[kRun * x + e + 1]), scale2, neg2), a, d);
+                            const uint64_t s2 = f32x2(v[kRun * x + e], v[kRun * x + e + 1]);
+                            f32x2_split(fma_f32x2(s2, scale2, neg2), a, d);
                             a = ex2_approx(a);
                             d = ex2_approx(d);
                             sum[(e >> 1) & 1] = add_f32x2(sum[(e >> 1) & 1], f32x2(a, d));
                             hi[e / 2] = pack_bf16(a, d);
-                            if (F32) lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
+                            if (F32)
+                                lo[e / 2] = pack_bf16(a - bf_lo(hi[e / 2]), d - bf_hi(hi[e / 2]));
                         }
                         if constexpr (F32) {
                             tmem_st16(t_s + 16 * x, hi);
@@ -951,18 +957,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             u[e] = make_uint4(__float_as_uint(f[0] * k), __float_as_uint(f[1] * k),
                                               __float_as_uint(f[2] * k), __float_as_uint(f[3] * k));
                         else
-                            u[e] = make_uint4(pack_bf16(f[0] * k, f[1] * k), pack_bf16(f[2] * k, f[3] * k),
-                                              pack_bf16(f[4] * k, f[5] * k), pack_bf16(f[6] * k, f[7] * k));
+                            u[e] = make_uint4(
+                                pack_bf16(f[0] * k, f[1] * k), pack_bf16(f[2] * k, f[3] * k),
+                                pack_bf16(f[4] * k, f[5] * k), pack_bf16(f[6] * k, f[7] * k));
                     }
                     transpose4(u, lane);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int x_row = wrow0 + q4 * 32 + (lane & ~3) + e;
-                        if (x_row < it.rows)
-                            reinterpret_cast<uint4*>(
-                                static_cast<uint8_t*>(p.out) +
-                                (out_row(x_row) * D + x + (F32 ? 16 * part : 0)) * (F32 ? 4 : 2))[lane & 3] =
-                                u[e];
+                        const int64_t at = out_row(x_row) * D + x + (F32 ? 16 * part : 0);
+                        uint8_t* to = static_cast<uint8_t*>(p.out) + at * (F32 ? 4 : 2);
+                        if (x_row < it.rows) reinterpret_cast<uint4*>(to)[lane & 3] = u[e];
                     }
                 }
             };
@@ -1158,7 +1163,6 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
     // every logit is zero to fp32 (masked ones stay -inf)
     p.scale_log2 = std::max(std::abs(a.scale) * kLog2e, 1e-37f);
     p.negate = a.scale < 0.f ? kUmmaNegateA : 0u;
-    p.out_f32 = a.out_dtype;
     p.out = a.out;
     p.lse = a.lse;
     p.ws = static_cast<uint8_t*>(ws);

@@ -97,7 +97,8 @@ __device__ __forceinline__ SeqPlan seq_plan(const se_page_pool& p, const int32_t
         s.ok = false;
         s.flags = SE_DEV_CAPACITY;
     } else {
-        s.need = max(0, static_cast<int>((static_cast<long long>(s.ctx) + s.n + kPage - 1) / kPage) - s.held);
+        const int pages = static_cast<int>((static_cast<long long>(s.ctx) + s.n + kPage - 1) / kPage);
+        s.need = max(0, pages - s.held);
     }
     return s;
 }
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(1024)
         }
         return n;
     };
-    long long total = 0, mine = 0;                 // mine: in one pass, pages before this sequence's
+    long long total = 0, mine = 0;             // mine: in one pass, pages before this sequence's
     for (int b0 = 0; b0 < batch; b0 += nt) {
         long long none = 0, sum = 0, nones = 0;
         mine = held_of(b0 + threadIdx.x);
@@ -478,7 +479,8 @@ cudaError_t launch_pages_release(const se_page_pool& pool, const int32_t* done, 
     const int nt = scan_threads(batch);
     // a block for every 4096 table entries that could be released
     const int64_t most = std::min<int64_t>((int64_t)batch * pool.max_pages_per_seq, pool.num_pages);
-    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms(), most / 4096)));
+    const int grid =
+        static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(num_sms(), most / 4096)));
     return launch_pdl(pages_release_kernel, dim3(grid), dim3(nt), (nt + 1) * sizeof(long long), s,
                       pool, done, batch, ws);
 }
