@@ -1065,44 +1065,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return 2 * (c0 + s) + (s == 0 ? 1 : 0);
                 };
                 if (count > 1) {
-                    float mm = -INFINITY, ll = 0.f;
-#pragma unroll 4
-                    for (int i = 0; i < count; ++i)
-                        mm = fmaxf(mm, __ldcg(&part_ml(slot_of(i))[r]).x);
-                    const float ref = mm == -INFINITY ? 0.f : mm;
-#pragma unroll 4
-                    for (int i = 0; i < count; ++i) {
-                        const float2 x = __ldcg(&part_ml(slot_of(i))[r]);
-                        ll += x.y * ex2_approx(x.x - ref);
-                    }
-                    if (final && p.lse && live && (both || w == 0))
-                        p.lse[out_row(row)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
-                    const float iv = ll > 0.f ? 1.f / ll : 0.f;
+                    // one pass over the pieces with a running reference: their loads overlap
+                    float mm, ll;
 #pragma unroll 1
                     for (int x0 = 0; x0 < cols; x0 += 32) {
                         float o[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        mm = -INFINITY;
+                        ll = 0.f;
 #pragma unroll 2
                         for (int i = 0; i < count; ++i) {
                             const int sl = slot_of(i);
+                            const float2 x = __ldcg(&part_ml(sl)[r]);
                             float4 y[8];
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 y[e] = live ? __ldcg(part_o(sl) + (x0 / 4 + e) * 128)
                                             : make_float4(0.f, 0.f, 0.f, 0.f);
-                            const float k = ex2_approx(__ldcg(&part_ml(sl)[r]).x - ref);
+                            const float up = fmaxf(mm, x.x), ref = up == -INFINITY ? 0.f : up;
+                            const float was = ex2_approx(mm - ref), k = ex2_approx(x.x - ref);
+                            mm = up;
+                            ll = ll * was + x.y * k;
 #pragma unroll
                             for (int e = 0; e < 8; ++e) {
-                                o[4 * e] += y[e].x * k;
-                                o[4 * e + 1] += y[e].y * k;
-                                o[4 * e + 2] += y[e].z * k;
-                                o[4 * e + 3] += y[e].w * k;
+                                o[4 * e] = o[4 * e] * was + y[e].x * k;
+                                o[4 * e + 1] = o[4 * e + 1] * was + y[e].y * k;
+                                o[4 * e + 2] = o[4 * e + 2] * was + y[e].z * k;
+                                o[4 * e + 3] = o[4 * e + 3] * was + y[e].w * k;
                             }
                         }
                         __syncwarp();
                         if (final) {
-                            store32(o, iv, col0 + x0);
+                            store32(o, ll > 0.f ? 1.f / ll : 0.f, col0 + x0);
                         } else if (live) {           // in the place of the group's first piece
                             float4* dst = part_o(slot_of(0)) + x0 / 4 * 128;
 #pragma unroll
@@ -1111,7 +1106,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     }
-                    if (!final) part_ml(slot_of(0))[r] = make_float2(mm, ll);
+                    if (!final)
+                        part_ml(slot_of(0))[r] = make_float2(mm, ll);
+                    else if (p.lse && live && (both || w == 0))
+                        p.lse[out_row(row)] = ll > 0.f ? (mm + log2f(ll)) * kLn2 : -INFINITY;
                 }
                 if (final) break;
                 final = true;
