@@ -65,7 +65,10 @@ constexpr int kMaxCtas = 256;
 // fixed part (Q, the pipeline's fill, the rows' output).
 constexpr int kTileBoth = 4, kTileOne = 3, kBlockCost = 10;
 constexpr int kJoinFlat = 8;                       // pieces joined in one go at most
-constexpr int kMinShare = 16;                      // units a CTA takes at least (a tile or more)
+// Units a CTA takes at least (more than a tile's): 8 suits a single query (11.9 us against
+// 12.4 over 2K) and costs where there are several heads (24.0 against 22.9 over 16K); 24
+// costs both (13.9, 25.4).
+constexpr int kMinShare = 12;
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
