@@ -29,11 +29,11 @@
 //
 // Bound: 4 D flops per row and key on the tensor cores for chunks (32 MMAs of 64 clocks a
 // tile for 256 rows: 2060 clocks), K and V from HBM for few rows.  Measured on a GB300
-// (head_dim 128, 32 query heads, 4 KV heads, bf16): the last 2048 tokens of 32K in 660 us
-// (1.63 PFLOP/s), a prompt of 8192 in 367 us (1.50 PFLOP/s), 16 sequences of 32K checking
+// (head_dim 128, 32 query heads, 4 KV heads, bf16): the last 2048 tokens of 32K in 665 us
+// (1.61 PFLOP/s), a prompt of 8192 in 365 us (1.51 PFLOP/s), 16 sequences of 32K checking
 // 8 tokens each in 169 us (6.4 TB/s).  A tile for 256 rows takes about 2950 clocks: without
 // its softmax 2370, without the tensor cores 2500, its loads alone 2000.  What was
-// measured and not kept: sixteen softmax warps, two threads a row (713 us against 655: issue
+// measured and not kept: sixteen softmax warps, two threads a row (690 us against 665: issue
 // slots, not latency, are short); an MMA warp for each group (789 us: the two fall into step
 // instead of alternating); handing P over in halves (no difference); the running maximum in
 // every tile (the row sum does: 2% on a mixed batch).
