@@ -397,7 +397,16 @@ def _token_stride(x, what: str) -> int:
     if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
         raise SparseEngineError(f"{what}: [tokens][heads][head_dim] with contiguous heads needed, "
                                 f"got shape {tuple(shape)} strides {stride}")
+    if shape[0] > 1 and stride[0] < shape[1] * shape[2]:
+        raise SparseEngineError(f"{what}: tokens overlap (an expanded tensor?), strides {stride}")
     return stride[0] if shape[0] > 1 else shape[1] * shape[2]
+
+
+def _check_tokens(x, tokens: int, heads: int, head_dim: int, what: str):
+    """The kernels reach every row up to the chunk's max_tokens."""
+    if x.shape[0] < tokens or x.shape[1] != heads or x.shape[2] != head_dim:
+        raise SparseEngineError(f"{what}: shape {tuple(x.shape)}, needed is at least "
+                                f"[{tokens}][{heads}][{head_dim}]")
 
 
 def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, stream=None):
@@ -407,6 +416,8 @@ def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, 
     stride = _token_stride(k_new, "se_kv_append_chunk k_new")
     if stride != _token_stride(v_new, "se_kv_append_chunk v_new"):
         raise SparseEngineError("se_kv_append_chunk: k_new and v_new strides differ")
+    for x, what in ((k_new, "k_new"), (v_new, "v_new")):
+        _check_tokens(x, cc.max_tokens, c.num_kv_heads, c.head_dim, "se_kv_append_chunk " + what)
     _check(load().se_kv_append_chunk(ctypes.byref(c), _p(k_new), _p(v_new), stride,
                                      ctypes.byref(cc), batch, _p(ws), ws.numel(),
                                      _stream(stream)), "se_kv_append_chunk")
@@ -418,7 +429,14 @@ def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, sc
     """Causal attention of the chunk's tokens over the paged cache; q
     [max_tokens][Hq][D] may be a slice of wider rows."""
     c, cc = kv.c, chunk.c
-    opts = ChunkAttnOptsC(out_dtype, window, sink, _token_stride(q, "se_chunk_attn q"),
+    stride = _token_stride(q, "se_chunk_attn q")
+    _check_tokens(q, cc.max_tokens, num_q_heads, c.head_dim, "se_chunk_attn q")
+    _check_tokens(out, cc.max_tokens, num_q_heads, c.head_dim, "se_chunk_attn out")
+    if not out.is_contiguous() or out.element_size() != (4 if out_dtype else 2):
+        raise SparseEngineError("se_chunk_attn: out is not contiguous or not of out_dtype")
+    if lse is not None and (lse.numel() < cc.max_tokens * num_q_heads or not lse.is_contiguous()):
+        raise SparseEngineError("se_chunk_attn: lse of [max_tokens][num_q_heads] needed")
+    opts = ChunkAttnOptsC(out_dtype, window, sink, stride,
                           ev_begin.cuda_event if ev_begin is not None else None,
                           ev_end.cuda_event if ev_end is not None else None)
     _check(load().se_chunk_attn(ctypes.byref(c), _p(q), ctypes.byref(cc), batch, num_q_heads,

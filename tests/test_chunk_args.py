@@ -129,3 +129,37 @@ def test_binding_refuses_layouts_it_cannot_pass(lib):
     for bad in (x.transpose(1, 2), x[:, :, ::2], x[:, ::2], x.view(16, 128)):
         with pytest.raises(binding.SparseEngineError):
             binding._token_stride(bad, "x")
+
+
+def test_binding_refuses_rows_that_are_not_there(lib):
+    """Expanded or too short tensors never reach the library (every pointer here is a CPU one)."""
+    with pytest.raises(binding.SparseEngineError, match="overlap"):
+        binding._token_stride(torch.zeros(1, 4, 128).expand(8, 4, 128), "x")
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    kv = binding.PagedKV(z(4, 2, 16, 64), z(4, 2, 16, 64), None, i(2, 4), i(2))
+    c = binding.Chunk.empty(2, 8, "cpu")
+    ws = torch.zeros(1 << 10, dtype=torch.uint8)
+    good = z(8, 2, 64)
+    for bad in (z(7, 2, 64), z(8, 4, 64), z(8, 1, 64), z(8, 2, 128)):
+        for k, v in ((bad, bad), (good, z(7, 2, 64))):
+            with pytest.raises(binding.SparseEngineError, match="needed|differ"):
+                binding.se_kv_append_chunk(kv, k, v, c, 2, ws, stream=NoStream)
+    for bad in (z(7, 4, 64), z(8, 2, 64), z(8, 4, 128), z(1, 4, 64).expand(8, 4, 64)):
+        with pytest.raises(binding.SparseEngineError, match="needed|overlap"):
+            binding.se_chunk_attn(kv, bad, c, 2, 4, 1.0, z(8, 4, 64), None, ws, stream=NoStream)
+
+    q = z(8, 4, 64)
+    for out, f32 in ((z(7, 4, 64), 0), (z(8, 4, 64), 1), (z(8, 4, 128)[:, :, :64], 0),
+                     (torch.zeros(8, 4, 64), 0)):
+        with pytest.raises(binding.SparseEngineError, match="needed|contiguous"):
+            binding.se_chunk_attn(kv, q, c, 2, 4, 1.0, out, None, ws, out_dtype=f32,
+                                  stream=NoStream)
+    for lse in (torch.zeros(7, 4), torch.zeros(8, 8)[:, :4]):
+        with pytest.raises(binding.SparseEngineError, match="lse"):
+            binding.se_chunk_attn(kv, q, c, 2, 4, 1.0, q.clone(), lse, ws, stream=NoStream)
+
+
+
+class NoStream:
+    cuda_stream = None
