@@ -390,34 +390,38 @@ def se_pages_release(pool: PagePool, done, batch: int, ws, stream=None):
                                    _stream(stream)), "se_pages_release")
 
 
-def _token_stride(x, what: str) -> int:
+def _token_stride(x, what: str, tokens: int = 0, heads: int = 0, head_dim: int = 0):
     """Elements between tokens of a [tokens][heads][head_dim] tensor, which may be a
-    slice of wider rows (a packed q/k/v projection)."""
+    slice of wider rows (a packed q/k/v projection).  With `heads` the shape is checked too:
+    the kernels reach every row up to the chunk's max_tokens."""
     shape, stride = x.shape, x.stride()
-    if len(shape) != 3 or stride[2] != 1 or (stride[1] != shape[2] and shape[1] > 1):
+    try:
+        n, h, d = shape
+        sn, sh, sd = stride
+        ok = sd == 1 and (sh == d or h == 1)
+    except ValueError:
+        ok = False
+    if not ok:
         raise SparseEngineError(f"{what}: [tokens][heads][head_dim] with contiguous heads needed, "
                                 f"got shape {tuple(shape)} strides {stride}")
-    if shape[0] > 1 and stride[0] < shape[1] * shape[2]:
-        raise SparseEngineError(f"{what}: tokens overlap (an expanded tensor?), strides {stride}")
-    return stride[0] if shape[0] > 1 else shape[1] * shape[2]
-
-
-def _check_tokens(x, tokens: int, heads: int, head_dim: int, what: str):
-    """The kernels reach every row up to the chunk's max_tokens."""
-    if x.shape[0] < tokens or x.shape[1] != heads or x.shape[2] != head_dim:
-        raise SparseEngineError(f"{what}: shape {tuple(x.shape)}, needed is at least "
+    if heads and (h != heads or d != head_dim or n < tokens):
+        raise SparseEngineError(f"{what}: shape {tuple(shape)}, needed is at least "
                                 f"[{tokens}][{heads}][{head_dim}]")
+    if n <= 1:
+        return h * d
+    if sn < h * d:
+        raise SparseEngineError(f"{what}: tokens overlap (an expanded tensor?), strides {stride}")
+    return sn
 
 
 def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, stream=None):
     """Append the chunk's rows; k_new and v_new [max_tokens][Hkv][D] may be slices
     of wider rows."""
     c, cc = kv.c, chunk.c
-    stride = _token_stride(k_new, "se_kv_append_chunk k_new")
-    if stride != _token_stride(v_new, "se_kv_append_chunk v_new"):
+    rows, heads, dim = cc.max_tokens, c.num_kv_heads, c.head_dim
+    stride = _token_stride(k_new, "se_kv_append_chunk k_new", rows, heads, dim)
+    if stride != _token_stride(v_new, "se_kv_append_chunk v_new", rows, heads, dim):
         raise SparseEngineError("se_kv_append_chunk: k_new and v_new strides differ")
-    for x, what in ((k_new, "k_new"), (v_new, "v_new")):
-        _check_tokens(x, cc.max_tokens, c.num_kv_heads, c.head_dim, "se_kv_append_chunk " + what)
     _check(load().se_kv_append_chunk(ctypes.byref(c), _p(k_new), _p(v_new), stride,
                                      ctypes.byref(cc), batch, _p(ws), ws.numel(),
                                      _stream(stream)), "se_kv_append_chunk")
@@ -429,12 +433,12 @@ def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, sc
     """Causal attention of the chunk's tokens over the paged cache; q
     [max_tokens][Hq][D] may be a slice of wider rows."""
     c, cc = kv.c, chunk.c
-    stride = _token_stride(q, "se_chunk_attn q")
-    _check_tokens(q, cc.max_tokens, num_q_heads, c.head_dim, "se_chunk_attn q")
-    _check_tokens(out, cc.max_tokens, num_q_heads, c.head_dim, "se_chunk_attn out")
+    rows, dim = cc.max_tokens, c.head_dim
+    stride = _token_stride(q, "se_chunk_attn q", rows, num_q_heads, dim)
+    _token_stride(out, "se_chunk_attn out", rows, num_q_heads, dim)
     if not out.is_contiguous() or out.element_size() != (4 if out_dtype else 2):
         raise SparseEngineError("se_chunk_attn: out is not contiguous or not of out_dtype")
-    if lse is not None and (lse.numel() < cc.max_tokens * num_q_heads or not lse.is_contiguous()):
+    if lse is not None and (lse.numel() < rows * num_q_heads or not lse.is_contiguous()):
         raise SparseEngineError("se_chunk_attn: lse of [max_tokens][num_q_heads] needed")
     opts = ChunkAttnOptsC(out_dtype, window, sink, stride,
                           ev_begin.cuda_event if ev_begin is not None else None,
