@@ -295,7 +295,9 @@ int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, i
     a.q_stride = o.q_stride;
     a.Hq = num_q_heads;
     a.scale = scale;
-    a.window = o.window;
+    // positions are below 2^30, so a longer window sees the same; the kernel's sums of
+    // positions and window then stay within 32 bits
+    a.window = std::min(o.window, kMaxChunkPages * SE_PAGE_SIZE);
     a.sink = o.sink;
     a.out_dtype = o.out_dtype;
     a.out = out;

@@ -469,6 +469,23 @@ def test_rows_before_the_end_of_what_is_held():
         a.check(mid, rows=30)
 
 
+def test_longest_window_and_sink():
+    """Window and sink of 2^31 - 1, alone and together, see what no window does."""
+    g = np.random.default_rng([25])
+    c = held(g, 2, 2, 64, [700, 0], [40, 130])
+    chunk = c.add([40, 130])
+    a = Attn(c, 4)
+    a.run(chunk)
+    a.check(chunk, rows=20)
+    out, lse = a.out.clone(), a.lse.clone()
+    for a.window, a.sink in ((2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (1, 2 ** 31 - 1)):
+        a.out.fill_(7.0)
+        a.lse.fill_(7.0)
+        a.call(chunk)
+        assert se.status_word(a.ws) == 0
+        assert torch.equal(a.out, out) and torch.equal(a.lse, lse), (a.window, a.sink)
+
+
 def test_growing_maximum():
     """Keys whose logits grow along the sequence: every tile raises the running maximum."""
     g = np.random.default_rng([16])
