@@ -314,7 +314,8 @@ int se_pages_release(const se_page_pool* pool, const int32_t* done, int batch, v
  * apart; 0: num_kv_heads * head_dim; a multiple of 8) go to the cache row of slot[t]
  * and the key is folded into the summary of its page (a page whose first token
  * is among the rows is set anew); ctx_len[seq[t]] becomes pos[t] + 1 of the
- * sequence's last row.  The same result as se_kv_append token by token.  kv->meta
+ * sequence's last row that has a slot and is not dropped, whatever rows before it
+ * have none.  The same result as se_kv_append token by token.  kv->meta
  * may be NULL (no summaries are kept).  A slot outside the pages, or a seq or pos outside
  * the block table: SE_DEV_BAD_INDEX, row dropped.  Workspace: se_small_workspace(). */
 int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_new,

@@ -337,6 +337,56 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) ws[kCounterWord] = 0;
 }
 
+// Row t of a chunk: slot is -1 where it has none, where it is dropped (`bad`: the slot
+// is outside the pages, or seq or pos outside the block table) and past the arrays.
+struct ChunkRow {
+    int slot, pos, seq;
+    bool bad;
+};
+__device__ __forceinline__ ChunkRow chunk_row(const se_paged_kv& kv, const se_chunk& ck, int batch,
+                                              int t) {
+    ChunkRow r = {-1, -1, -1, false};
+    if (t < 0 || t >= ck.max_tokens) return r;
+    r.slot = ck.slot[t];
+    r.pos = ck.pos[t];
+    r.seq = ck.seq[t];
+    r.bad = r.slot != -1 &&
+            (r.slot < 0 || r.slot / kPage >= kv.num_pages || r.seq < 0 || r.seq >= batch ||
+             r.pos < 0 || r.pos / kPage >= kv.max_pages_per_seq ||
+             r.pos % kPage != r.slot % kPage);
+    if (r.bad) r.slot = -1;
+    return r;
+}
+
+// Lengths: each sequence's last row with a slot sets ctx_len, and no other row writes it.  Lane l holds
+// row t of 32; lanes 1..16 hold the rows this warp answers for.  The row after
+// such a row tells, unless that one has no slot (a page that was not found, a dropped
+// row): then the warp looks on, past rows without a slot that are the same sequence's or
+// name none that exists, 32 at a time, to the next row that decides.
+__device__ __forceinline__ void commit_lengths(const se_paged_kv& kv, const se_chunk& ck, int batch,
+                                               int t, int lane, const ChunkRow& row) {
+    const bool mine = row.slot >= 0 && lane >= 1 && lane <= kPage;
+    const int nslot = __shfl_down_sync(0xffffffffu, row.slot, 1);
+    const int nseq = __shfl_down_sync(0xffffffffu, row.seq, 1);
+    auto passes = [&](int s, int b) { return s == b || s < -1 || s >= batch; };
+    const bool hole = mine && nslot < 0 && passes(nseq, row.seq);
+    if (mine && !hole && (nslot < 0 || nseq != row.seq)) kv.ctx_len[row.seq] = row.pos + 1;
+    for (uint32_t m = __ballot_sync(0xffffffffu, hole); m != 0; m &= m - 1) {
+        const int f = __ffs(m) - 1;
+        const int b = __shfl_sync(0xffffffffu, row.seq, f);
+        const int len = __shfl_sync(0xffffffffu, row.pos, f) + 1;
+        uint32_t more, end;                         // rows that go on, rows that are another's or none's
+        for (int r = __shfl_sync(0xffffffffu, t, f) + 1;; r += 32) {
+            const ChunkRow x = chunk_row(kv, ck, batch, r + lane);
+            more = __ballot_sync(0xffffffffu, x.slot >= 0 && x.seq == b);
+            end = __ballot_sync(0xffffffffu,
+                                x.slot >= 0 ? x.seq != b : !passes(x.seq, b));
+            if ((more | end) != 0) break;           // (rows past max_tokens end it)
+        }
+        if (lane == 0 && __ffs(more | end) == __ffs(end)) kv.ctx_len[b] = len;
+    }
+}
+
 // Append of packed rows.  Block i looks at rows [16i, 16i + 16); a run of rows
 // that lie one after another in one page is a piece (at most 16 rows), the work of one
 // warp for one KV head, which owns that page's summary while it works: no
@@ -356,18 +406,9 @@ __global__ void __launch_bounds__(128)
     const int H = kv.num_kv_heads;
     // lane l looks at row 16i - 1 + l
     const int t = static_cast<int>(blockIdx.x) * kPage - 1 + lane;
-    int slot = -1, pos = -1, seq = -1;
-    if (t >= 0 && t < ck.max_tokens) {
-        slot = ck.slot[t];
-        pos = ck.pos[t];
-        seq = ck.seq[t];
-        if (slot != -1 &&
-            (slot < 0 || slot / kPage >= kv.num_pages || seq < 0 || seq >= batch || pos < 0 ||
-             pos / kPage >= kv.max_pages_per_seq || pos % kPage != slot % kPage)) {
-            if (lane >= 1 && lane <= kPage && warp == 0) flag(status, SE_DEV_BAD_INDEX);
-            slot = -1;
-        }
-    }
+    const ChunkRow row = chunk_row(kv, ck, batch, t);
+    if (row.bad && lane >= 1 && lane <= kPage && warp == 0) flag(status, SE_DEV_BAD_INDEX);
+    const int slot = row.slot, pos = row.pos, seq = row.seq;
     const bool valid = slot >= 0;
     const int pslot = __shfl_up_sync(0xffffffffu, slot, 1);
     const int pseq = __shfl_up_sync(0xffffffffu, seq, 1);
@@ -376,9 +417,7 @@ __global__ void __launch_bounds__(128)
                       pslot + 1 == slot && pos % kPage != 0;
     const uint32_t cont_m = __ballot_sync(0xffffffffu, cont);
     const uint32_t lead_m = __ballot_sync(0xffffffffu, valid && !cont) & 0x1fffeu;
-    const int nseq = __shfl_down_sync(0xffffffffu, valid ? seq : -1, 1);
-    if (warp == 0 && blockIdx.y == 0 && valid && lane >= 1 && lane <= kPage && nseq != seq)
-        kv.ctx_len[seq] = pos + 1;
+    if (warp == 0 && blockIdx.y == 0) commit_lengths(kv, ck, batch, t, lane, row);
     const int seg = lane % SEGS, rp = lane / SEGS;
     uint4* K = static_cast<uint4*>(kv.k);
     uint4* V = static_cast<uint4*>(kv.v);

@@ -1,0 +1,101 @@
+"""Appends of chunks some of whose rows have no slot or are dropped, between rows that have
+one: lengths, rows and page summaries are the oracle's, every time."""
+import numpy as np
+import pytest
+import torch
+
+from kv_cache_decode_quest_gb300 import binding as se
+from oracle import chunk as oc
+from tests.test_gpu_chunk import BAD_INDEX, PAGE, Cache, bf16, f64, i32, normal
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _lib(lib):
+    return lib
+
+
+def append_rows(c, start, seq, pos, slot, status=0, kept=None):
+    """Appends the rows on both sides; `kept`: the slots that the oracle writes."""
+    kn, vn = normal(c.g, len(slot), c.H, c.D), normal(c.g, len(slot), c.H, c.D)
+    lengths = c.pool.ctx_len.clone()
+    oc.append(c.o, c.k, c.v, c.meta, kn, vn, start, seq, pos, slot if kept is None else kept)
+    chunk = se.Chunk(i32(start), i32(seq), i32(pos), i32(slot))
+    meta = None if c.meta is None else c.kv.meta.clone()
+    for _ in range(8):
+        c.pool.ctx_len.copy_(lengths)
+        if meta is not None:
+            c.kv.meta.copy_(meta)
+        se.se_kv_append_chunk(c.kv, bf16(kn), bf16(vn), chunk, c.B, c.ws)
+        assert se.status_word(c.ws) == status
+        c.check()
+    c.ws[:4] = 0
+
+
+def planned(c, new, pad=0):
+    """start, seq, pos, slot of `new` tokens per sequence, pages taken on both sides."""
+    rows = int(sum(new)) + pad
+    start, seq, pos, slot, flags = oc.plan(c.o, new, rows)
+    assert flags == 0
+    c.pool.block_table.copy_(i32(c.o.block_table))
+    c.pool.n_pages.copy_(i32(c.o.n_pages))
+    c.pool.n_free.fill_(len(c.o.free))
+    return start, seq, pos, slot
+
+
+# (tokens held, new tokens, holes as (sequence, first page of its new tokens, pages)):
+# one page, many, the first, the last, up to the next sequence, all of a sequence
+PAGE_HOLES = [
+    ([0], [48], [(0, 1, 1)]), ([0], [33], [(0, 1, 1)]), ([5], [100], [(0, 1, 2), (0, 5, 1)]),
+    ([0, 3], [700, 20], [(0, 1, 40), (1, 0, 1)]), ([16, 0], [64, 16], [(0, 3, 1), (1, 0, 1)]),
+    ([0, 7, 9], [32, 90, 5], [(0, 0, 2), (1, 1, 3), (2, 0, 1)]),
+    ([1, 1], [47, 47], [(0, 2, 1), (1, 0, 1)]),
+]
+
+
+@pytest.mark.parametrize("pad", [0, 3, 200])
+@pytest.mark.parametrize("held,new,holes", PAGE_HOLES)
+def test_pages_that_were_not_found(held, new, holes, pad):
+    """Rows of whole pages have no slot: the last row that has one sets the length."""
+    g = np.random.default_rng([31, len(new), new[0], pad])
+    c = Cache(g, len(new), 2, 64, 48, 120)
+    if any(held):
+        c.add(held)
+    start, seq, pos, slot = planned(c, new, pad)
+    for b, first, pages in holes:
+        at = held[b] // PAGE + first
+        slot[(seq == b) & (pos >= at * PAGE) & (pos < (at + pages) * PAGE)] = -1
+    assert (slot[:start[-1]] == -1).any()
+    append_rows(c, start, seq, pos, slot)
+
+
+@pytest.mark.parametrize("what", ["seq", "slot", "pos"])
+def test_dropped_rows_in_the_middle(what):
+    """Rows dropped for a bad seq, slot or pos are no end of their sequence."""
+    g = np.random.default_rng([32])
+    c = Cache(g, 2, 2, 64, 40, 80)
+    start, seq, pos, slot = planned(c, [200, 50], 5)
+    kept = slot.copy()
+    for a, z in ((16, 32), (48, 128), (200 + 16, 200 + 32)):
+        kept[a:z] = -1
+        (seq if what == "seq" else slot if what == "slot" else pos)[a:z] = \
+            {"seq": 2, "slot": 80 * PAGE, "pos": 40 * PAGE}[what]
+    append_rows(c, start, seq, pos, slot, BAD_INDEX, kept)
+
+
+def test_plan_with_bad_pages_then_append():
+    """Pages outside the cache met on the stack: se_chunk_plan's rows of them have no slot, and the
+    append behind it commits the length of the last row that has one."""
+    g = np.random.default_rng([33])
+    c = Cache(g, 2, 2, 64, 8, 16, summaries=False)
+    c.pool.free_pages[13:15] = i32([16, -5])             # second and third page handed out
+    chunk = se.Chunk.empty(2, 90)
+    se.se_chunk_plan(c.pool, i32([70, 18]), 2, chunk, c.ws_pool)
+    assert se.status_word(c.ws_pool) == BAD_INDEX
+    start, seq, pos, slot = (getattr(chunk, x).cpu().numpy() for x in ("start", "seq", "pos", "slot"))
+    assert (slot[16:48] == -1).all() and (slot[:16] >= 0).all() and (slot[48:88] >= 0).all()
+    c.o.n_pages[:] = c.pool.n_pages.tolist()
+    c.o.block_table[:] = c.pool.block_table.cpu().numpy()
+    append_rows(c, start, seq, pos, slot)
+    assert c.pool.ctx_len.tolist() == [70, 18]
