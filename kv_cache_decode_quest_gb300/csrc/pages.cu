@@ -387,9 +387,9 @@ __device__ __forceinline__ void commit_lengths(const se_paged_kv& kv, const se_c
     }
 }
 
-// Append of packed rows.  Block i looks at rows [16i, 16i + 16); a run of rows
-// that lie one after another in one page is a piece (at most 16 rows), the work of one
-// warp for one KV head, which owns that page's summary while it works: no
+// Append of packed rows.  Block i looks at rows [16i, 16i + 16); the rows of one sequence that
+// lie in one page are a piece (at most 16 rows apart, whatever rows between them have no
+// slot), the work of one warp for one KV head, which owns that page's summary: no
 // atomics and a fixed result.  Each warp finds the pieces that begin in the block
 // from the slots of 32 rows around it (ballots).  A row is D/8 16-byte vectors, so
 // RP rows move side by side; all loads of a piece are in flight before the
@@ -413,10 +413,33 @@ __global__ void __launch_bounds__(128)
     const int pslot = __shfl_up_sync(0xffffffffu, slot, 1);
     const int pseq = __shfl_up_sync(0xffffffffu, seq, 1);
     const int ppos = __shfl_up_sync(0xffffffffu, pos, 1);
-    const bool cont = valid && lane > 0 && pslot >= 0 && pseq == seq && ppos + 1 == pos &&
-                      pslot + 1 == slot && pos % kPage != 0;
-    const uint32_t cont_m = __ballot_sync(0xffffffffu, cont);
-    const uint32_t lead_m = __ballot_sync(0xffffffffu, valid && !cont) & 0x1fffeu;
+    const bool begins = valid && lane >= 1 && lane <= kPage &&
+                        !(pslot >= 0 && pseq == seq && ppos + 1 == pos && pslot + 1 == slot &&
+                          pos % kPage != 0);
+    // rows of a piece: slot and position go with the row
+    auto same_piece = [&](int d, int slot_d, int pos_d, int seq_d, int slot0, int pos0, int seq0) {
+        return slot_d >= 0 && seq_d == seq0 && slot_d - slot0 == d && pos_d - pos0 == d &&
+               pos_d / kPage == pos0 / kPage;
+    };
+    uint32_t lead_m = __ballot_sync(0xffffffffu, begins);
+    // behind rows without a slot a page may have begun before them: up to 15 rows back
+    const bool unsure = begins && pslot < 0 && t > 0 && pos % kPage != 0 &&
+                        (pseq == seq || pseq < 0 || pseq >= batch);
+    uint32_t look = __ballot_sync(0xffffffffu, unsure);
+    if (look != 0) {
+        const ChunkRow far = chunk_row(kv, ck, batch, t - 32);
+        for (; look != 0; look &= look - 1) {
+            const int f = __ffs(look) - 1;
+            const int slot0 = __shfl_sync(0xffffffffu, slot, f);
+            const int pos0 = __shfl_sync(0xffffffffu, pos, f);
+            const int seq0 = __shfl_sync(0xffffffffu, seq, f);
+            if (__any_sync(0xffffffffu,
+                           (lane < f && same_piece(lane - f, slot, pos, seq, slot0, pos0, seq0)) ||
+                               same_piece(lane - 32 - f, far.slot, far.pos, far.seq, slot0, pos0,
+                                          seq0)))
+                lead_m &= ~(1u << f);
+        }
+    }
     if (warp == 0 && blockIdx.y == 0) commit_lengths(kv, ck, batch, t, lane, row);
     const int seg = lane % SEGS, rp = lane / SEGS;
     uint4* K = static_cast<uint4*>(kv.k);
@@ -429,17 +452,19 @@ __global__ void __launch_bounds__(128)
         uint32_t rest = lead_m;
         for (int i = u / H; i > 0; --i) rest &= rest - 1;
         const int f = __ffs(rest) - 1;                              // lane of the piece's first row
-        const int len = min(kPage, 1 + __ffs(~(cont_m >> (f + 1))) - 1);
         const int slot0 = __shfl_sync(0xffffffffu, slot, f);
         const int pos0 = __shfl_sync(0xffffffffu, pos, f);
         const int seq0 = __shfl_sync(0xffffffffu, seq, f);
+        // bit r: row r behind the first is of the piece
+        const uint32_t rows =
+            __ballot_sync(0xffffffffu, same_piece(lane - f, slot, pos, seq, slot0, pos0, seq0)) >> f;
         const int64_t src = (int64_t)(static_cast<int>(blockIdx.x) * kPage - 1 + f) * row_stride +
                             h * SEGS + seg;
         uint4 k[IT], v[IT];
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r = i * RP + rp;
-            if (r < len) {
+            if ((rows >> r) & 1) {
                 k[i] = k_new[src + r * row_stride];
                 v[i] = v_new[src + r * row_stride];
             }
@@ -463,7 +488,7 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r = i * RP + rp;
-            if (r < len) {
+            if ((rows >> r) & 1) {
                 K[dst + r * SEGS] = k[i];
                 V[dst + r * SEGS] = v[i];
                 const Bf8 x = unpack8(k[i]);

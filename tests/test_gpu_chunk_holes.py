@@ -99,3 +99,62 @@ def test_plan_with_bad_pages_then_append():
     c.o.block_table[:] = c.pool.block_table.cpu().numpy()
     append_rows(c, start, seq, pos, slot)
     assert c.pool.ctx_len.tolist() == [70, 18]
+
+
+# rows of one sequence that have no slot: inside a page, at its first or last token, across the
+# 16-row groups that the kernel's blocks look at
+ROW_HOLES = [
+    ([0], [16], [5]), ([0], [16], [0]), ([0], [32], [15, 16]), ([3], [40], [7, 8, 9]),
+    ([9], [100], [6, 22, 38, 54, 70]), ([0, 11], [7, 90], [3, 7 + 1, 7 + 5, 7 + 20, 7 + 21, 7 + 36]),
+    ([5, 2], [15, 15], [*range(1, 10), *range(16, 29)]), ([0], [64], [*range(1, 64, 2)]),
+    ([14], [70], [*range(3, 17), *range(20, 33)]),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("held,new,rows", ROW_HOLES)
+def test_rows_without_a_slot_inside_pages(held, new, rows, D):
+    """The rows of a page around a hole are folded into its summary by one warp."""
+    g = np.random.default_rng([34, len(new), new[0], len(rows)])
+    c = Cache(g, len(new), 3, D, 16, 40)
+    c.meta[:] = c.g.choice([-0.25, 0.25, 1.0], c.meta.shape)      # what earlier users left
+    c.kv.meta.copy_(bf16(c.meta))
+    if any(held):
+        c.add(held)
+    start, seq, pos, slot = planned(c, new, 2)
+    slot[rows] = -1
+    append_rows(c, start, seq, pos, slot)
+    # the same holes by rows that name no position, in the next tokens
+    start, seq, pos, slot = planned(c, new, 1)
+    slot[rows] = pos[rows] = -1
+    append_rows(c, start, seq, pos, slot)
+
+
+@pytest.mark.parametrize("what", ["seq", "slot", "offset"])
+def test_dropped_rows_inside_pages(what):
+    g = np.random.default_rng([35])
+    c = Cache(g, 2, 4, 64, 20, 40)
+    c.add([21, 0])
+    start, seq, pos, slot = planned(c, [60, 33])
+    kept = slot.copy()
+    at = np.array([2, 3, 14, 30, 60 + 4, 60 + 15, 60 + 16])
+    kept[at] = -1
+    if what == "seq":
+        seq[at] = [2, -3, 7, 2, 2, -9, 2]
+    elif what == "slot":
+        slot[at] = 40 * PAGE + 3
+    else:
+        slot[at] ^= 1                                        # another row of the page than pos says
+    append_rows(c, start, seq, pos, slot, BAD_INDEX, kept)
+
+
+def test_holes_between_other_sequences_rows():
+    """Single tokens in the middle of a page behind a request that found no page."""
+    g = np.random.default_rng([36])
+    c = Cache(g, 40, 2, 64, 3, 70)
+    held = [int(x) for x in g.integers(0, 30, 40)]
+    c.add(held)
+    start, seq, pos, slot = planned(c, [1, 3] * 20, 4)
+    for b in range(1, 40, 4):
+        pos[seq == b] = slot[seq == b] = -1
+    append_rows(c, start, seq, pos, slot)
