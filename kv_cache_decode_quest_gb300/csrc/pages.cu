@@ -3,6 +3,8 @@
 // rows with their page summaries (se_kv_append_chunk).  Pages of 16 tokens
 // with a token->page table follow the paged KV layout of "长程 agent 把显存撑爆以后",
 // section "四、为什么进不了 vLLM 一类的引擎".
+#include <math_constants.h>
+
 #include <algorithm>
 
 #include "append.cuh"
@@ -481,10 +483,8 @@ __global__ void __launch_bounds__(128)
             (((int64_t)(slot0 / kPage) * H + h) * kPage + slot0 % kPage) * SEGS + seg;
         Bf8 mn, mx;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            mn.x[e] = INFINITY;
-            mx.x[e] = -INFINITY;
-        }
+        for (int e = 0; e < 8; ++e)              // nothing yet: min and max pass a NaN over, and
+            mn.x[e] = mx.x[e] = CUDART_NAN_F;    // one stays where there is no other key
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r = i * RP + rp;

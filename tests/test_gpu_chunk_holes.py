@@ -158,3 +158,35 @@ def test_holes_between_other_sequences_rows():
     for b in range(1, 40, 4):
         pos[seq == b] = slot[seq == b] = -1
     append_rows(c, start, seq, pos, slot)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_that_are_no_numbers_fold_as_one_by_one(D):
+    """NaN and infinite keys give the summaries that se_kv_append gives token by token: a NaN
+    is passed over unless the page holds nothing else in that channel."""
+    g = np.random.default_rng([37, D])
+    n = 40
+    c = Cache(g, 2, 2, D, 6, 12)
+    other = se.PagedKV(c.kv.k.clone(), c.kv.v.clone(), c.kv.meta.clone(), c.kv.block_table,
+                       c.kv.ctx_len.clone())
+    k = normal(g, 2 * n, 2, D)
+    k[g.random(k.shape) < 0.5] = np.nan
+    k[:16, 0, :8] = k[n:n + 3, 1] = np.nan
+    k[5, 1, 3], k[6, 1, 4] = np.inf, -np.inf
+    k, v = bf16(k), bf16(normal(g, 2 * n, 2, D))
+    at = [0, 0]
+    for new in ([1, 3], [20, 1], [19, 36]):
+        start, seq, pos, slot = planned(c, new)
+        rows = np.concatenate([np.arange(b * n + at[b], b * n + at[b] + new[b]) for b in range(2)])
+        se.se_kv_append_chunk(c.kv, k[rows], v[rows], se.Chunk(i32(start), i32(seq), i32(pos), i32(slot)),
+                              2, c.ws)
+        at = [a + x for a, x in zip(at, new)]
+        c.o.ctx[:] = at
+    for b in range(2):                                        # one token of one sequence a call
+        one = se.PagedKV(other.k, other.v, other.meta[b:], other.block_table[b:], other.ctx_len[b:])
+        for i in range(n):
+            se.se_kv_append(one, k[b * n + i:b * n + i + 1], v[b * n + i:b * n + i + 1], 1, c.ws)
+    assert se.status_word(c.ws) == 0 and c.kv.ctx_len.tolist() == other.ctx_len.tolist() == [n, n]
+    assert np.array_equal(f64(c.kv.k), f64(other.k), equal_nan=True)
+    assert np.isnan(f64(other.meta[0, 0, 0, :, :8])).all() and np.isinf(f64(other.meta)).any()
+    assert np.array_equal(f64(c.kv.meta), f64(other.meta), equal_nan=True)
