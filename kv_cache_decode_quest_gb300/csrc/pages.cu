@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(1024)
                       int rows_per_block, int* ws) {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ int smem[];
+    extern __shared__ __align__(16) int smem[];
     const int nt = blockDim.x;
     int* s_start = smem;            // [nt + 1] first row of each sequence of the pass
     int* s_ctx = s_start + nt + 1;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(1024)
     pages_release_kernel(se_page_pool pool, const int32_t* done, int batch, int* ws) {
     pdl_wait();
     pdl_trigger();
-    extern __shared__ int smem[];
+    extern __shared__ __align__(16) int smem[];
     const int nt = blockDim.x;
     long long* s_first = reinterpret_cast<long long*>(smem);    // [nt + 1]
     __shared__ long long tmp[66];
