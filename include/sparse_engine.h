@@ -222,6 +222,10 @@ typedef struct se_chunk_attn_opts {
     void* ev_kernel_begin;    /* NULL or a cudaEvent_t recorded right before / */
     void* ev_kernel_end;      /* right after the attention kernel (timing only;
                                  captured as external event-record nodes) */
+    int32_t wait_limit_ns;    /* bound of each wait inside a block, counted in tries of
+                                 about 4 us (0: one second); for tests.  A wait that runs
+                                 out sets SE_DEV_TIMEOUT and its block returns; the
+                                 call's results are then invalid */
 } se_chunk_attn_opts;
 
 /* ---- library ------------------------------------------------------------ */

@@ -63,7 +63,8 @@ class ChunkC(ctypes.Structure):
 class ChunkAttnOptsC(ctypes.Structure):
     _fields_ = [("out_dtype", ctypes.c_int32), ("window", ctypes.c_int32),
                 ("sink", ctypes.c_int32), ("q_stride", ctypes.c_int64),
-                ("ev_kernel_begin", ctypes.c_void_p), ("ev_kernel_end", ctypes.c_void_p)]
+                ("ev_kernel_begin", ctypes.c_void_p), ("ev_kernel_end", ctypes.c_void_p),
+                ("wait_limit_ns", ctypes.c_int32)]
 
 
 class DecodeOptsC(ctypes.Structure):
@@ -429,7 +430,7 @@ def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, 
 
 def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, scale: float, out,
                   lse, ws, out_dtype: int = 0, window: int = 0, sink: int = 0, ev_begin=None,
-                  ev_end=None, stream=None):
+                  ev_end=None, stream=None, wait_limit_ns: int = 0):
     """Causal attention of the chunk's tokens over the paged cache; q
     [max_tokens][Hq][D] may be a slice of wider rows."""
     c, cc = kv.c, chunk.c
@@ -442,7 +443,7 @@ def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, sc
         raise SparseEngineError("se_chunk_attn: lse of [max_tokens][num_q_heads] needed")
     opts = ChunkAttnOptsC(out_dtype, window, sink, stride,
                           ev_begin.cuda_event if ev_begin is not None else None,
-                          ev_end.cuda_event if ev_end is not None else None)
+                          ev_end.cuda_event if ev_end is not None else None, wait_limit_ns)
     _check(load().se_chunk_attn(ctypes.byref(c), _p(q), ctypes.byref(cc), batch, num_q_heads,
                                 scale, ctypes.byref(opts), _p(out), _p(lse), _p(ws), ws.numel(),
                                 _stream(stream)), "se_chunk_attn")

@@ -275,12 +275,12 @@ int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, i
     if (num_q_heads % kv->num_kv_heads || !group_ok(num_q_heads / kv->num_kv_heads))
         return SE_ERR_UNSUPPORTED;
     if (!std::isfinite(scale)) return SE_ERR_INVALID_ARG;
-    se_chunk_attn_opts o = {0, 0, 0, 0, nullptr, nullptr};
+    se_chunk_attn_opts o = {0, 0, 0, 0, nullptr, nullptr, 0};
     if (opts) o = *opts;
     const int64_t row = (int64_t)num_q_heads * kv->head_dim;
     if (o.q_stride == 0) o.q_stride = row;
     if (o.out_dtype != 0 && o.out_dtype != 1) return SE_ERR_INVALID_ARG;
-    if (o.window < 0 || o.sink < 0) return SE_ERR_INVALID_ARG;
+    if (o.window < 0 || o.sink < 0 || o.wait_limit_ns < 0) return SE_ERR_INVALID_ARG;
     if (o.q_stride < row || o.q_stride % 8) return SE_ERR_INVALID_ARG;
     if (kv->max_pages_per_seq > kMaxChunkPages || batch > chunk_attn_max_batch())
         return SE_ERR_UNSUPPORTED;
@@ -300,6 +300,7 @@ int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, i
     a.window = std::min(o.window, kMaxChunkPages * SE_PAGE_SIZE);
     a.sink = o.sink;
     a.out_dtype = o.out_dtype;
+    a.wait_limit_ns = o.wait_limit_ns;
     a.out = out;
     a.lse = lse;
     return cuda_status(launch_chunk_attn(*kv, *chunk, batch, a, ws,

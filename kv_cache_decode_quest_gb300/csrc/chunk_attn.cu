@@ -109,6 +109,7 @@ struct Params {
     int window, sink;
     float scale_log2;              // > 0
     uint32_t negate;               // instruction descriptor bit for a negative scale
+    uint32_t wait_tries;           // a wait's failed tries before it gives up
     void* out;
     float* lse;
     uint8_t* ws;
@@ -207,6 +208,7 @@ struct Ctrl {
     uint64_t item_empty[kItems];           // all softmax warps and the MMA warp
     uint32_t tmem;
     int abort;
+    uint32_t wait_tries;                   // Params::wait_tries, beside the flag it is looked at with
     int any_absent;                        // a block-table entry named no page
     long long share_each, share_extra;
     Item items[kItems];
@@ -219,17 +221,19 @@ __device__ __forceinline__ uint32_t barrier_count(int i) {
     return i < kOnes ? 1 : i < kOnes + 2 ? 4 : i < kOnes + 4 ? kSoftWarps : kSoftWarps + 1;
 }
 
-// Warp-uniform bounded wait.  Tries are counted (each is suspended by the hardware for
-// some time of its own choice) rather than a clock read: that keeps the code of the
-// many waits short, and a first pass through this kernel runs at the rate its
-// code arrives.  A suspension hint, or polling without one, made a chunk of 2048 at
-// 32K 5% slower than this form.
-constexpr uint32_t kWaitTries = 1u << 20;
+// Warp-uniform bounded wait.  Tries are counted rather than a clock read: that keeps the code
+// of the many waits short, and a first pass through this kernel runs at the rate its
+// code arrives.  A try that fails has been suspended by the hardware for a fixed time (3.75 us
+// measured on a GB300), so the count is a time.  A suspension hint, or polling without one,
+// made a chunk of 2048 at 32K 5% slower than this form.
+constexpr int kTryNs = 3750;
+constexpr int kWaitLimitDefaultNs = 1000 * 1000 * 1000;
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Ctrl* c, int* status) {
 #pragma unroll 1
     for (uint32_t n = 0;; ++n) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if (n == kWaitTries || __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->abort))) break;
+        if (n >= c->wait_tries || __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->abort)))
+            break;
     }
     *static_cast<volatile int*>(&c->abort) = 1;
     flag(status, SE_DEV_TIMEOUT);
@@ -243,7 +247,8 @@ __device__ __forceinline__ bool warp_wait2(uint64_t* a, uint32_t pa, uint64_t* b
     for (uint32_t n = 0;; ++n) {
         const bool x = mbar_try_wait(a, pa), y = mbar_try_wait(b, pb);
         if (__all_sync(0xffffffffu, x && y)) return true;
-        if (n == kWaitTries || __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->abort))) break;
+        if (n >= c->wait_tries || __any_sync(0xffffffffu, *static_cast<volatile int*>(&c->abort)))
+            break;
     }
     *static_cast<volatile int*>(&c->abort) = 1;
     flag(status, SE_DEV_TIMEOUT);
@@ -297,6 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 0) {
         c->abort = 0;
+        c->wait_tries = p.wait_tries;
         c->any_absent = 0;
     }
     if (warp == kSoftWarps + 1) tmem_alloc(&c->tmem, 512);
@@ -1164,6 +1170,8 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
     // every logit is zero to fp32 (masked ones stay -inf)
     p.scale_log2 = std::max(std::abs(a.scale) * kLog2e, 1e-37f);
     p.negate = a.scale < 0.f ? kUmmaNegateA : 0u;
+    p.wait_tries =
+        static_cast<uint32_t>((a.wait_limit_ns > 0 ? a.wait_limit_ns : kWaitLimitDefaultNs) / kTryNs);
     p.out = a.out;
     p.lse = a.lse;
     p.ws = static_cast<uint8_t*>(ws);

@@ -86,6 +86,7 @@ struct ChunkAttnArgs {
     float scale;
     int window, sink;
     int out_dtype;
+    int wait_limit_ns;       // 0: the default
     void* out;
     float* lse;
 };

@@ -163,3 +163,12 @@ def test_binding_refuses_rows_that_are_not_there(lib):
 
 class NoStream:
     cuda_stream = None
+
+
+def test_attn_wait_limit(lib):
+    need = lib.se_chunk_attn_workspace(2, 32, 4, 32, 128)
+    for limit, rc in ((-1, INVALID), (-2 ** 31, INVALID), (0, 0), (1, 0), (2 ** 31 - 1, 0)):
+        o = binding.ChunkAttnOptsC(0, 0, 0, 0, None, None, limit)
+        empty = chunk(max_tokens=0, seq=None, pos=None, slot=None)
+        assert lib.se_chunk_attn(paged(), None, empty, 2, 32, 0.1, ctypes.byref(o), None, None, P,
+                                 need, None) == rc, limit
