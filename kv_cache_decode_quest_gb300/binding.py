@@ -136,6 +136,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 
 
 def library_path() -> str:
@@ -185,13 +186,46 @@ def _ref(x):
 # holders: keep the tensors alive next to the C struct that points at them
 # ---------------------------------------------------------------------------
 
+class _Measured:
+    """A holder of tensors whose types and lengths the calls on chunks look at once after each
+    assignment, not in every call (`_measure`: the sequences it holds, or an error)."""
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__["_sequences"] = None
+
+
+def _int32_fields(holder):
+    # the kernels take bare pointers: another type would be read as pairs or quarters of words
+    for f in dataclasses.fields(holder):
+        t = getattr(holder, f.name)
+        if t.dtype is not torch.int32 or not t.is_contiguous():
+            raise SparseEngineError(f"{type(holder).__name__}.{f.name}: contiguous int32 tensor "
+                                    f"needed, got {t.dtype}, strides {t.stride()}")
+
+
+def _holds(holder: _Measured, batch: int, what: str):
+    n = holder._sequences
+    if n is None:
+        n = holder.__dict__["_sequences"] = holder._measure()
+    if n < batch:
+        raise SparseEngineError(f"{what}: the {type(holder).__name__}'s tensors are too short for "
+                                f"{batch} sequences")
+
+
 @dataclasses.dataclass
-class PagedKV:
+class PagedKV(_Measured):
     k: torch.Tensor            # bf16 [num_pages][Hkv][16][D]
     v: torch.Tensor
     meta: torch.Tensor         # bf16 [B][max_pages][Hkv][2][D], logical page order
     block_table: torch.Tensor  # int32 [B][max_pages]
     ctx_len: torch.Tensor      # int32 [B]
+
+    def _measure(self) -> int:
+        for t in (self.k, self.v, self.meta):
+            if t is not None and t.dtype is not torch.bfloat16:
+                raise SparseEngineError(f"PagedKV: a bfloat16 cache is needed, got {t.dtype}")
+        return min(self.ctx_len.numel(), self.block_table.shape[0])
 
     @property
     def c(self) -> PagedKVC:
@@ -262,17 +296,24 @@ class H2OState:
 
 
 @dataclasses.dataclass
-class PagePool:
+class PagePool(_Measured):
     free_pages: torch.Tensor   # int32 [num_pages], the first n_free entries are free
     n_free: torch.Tensor       # int32 [1]
     n_pages: torch.Tensor      # int32 [B]
     block_table: torch.Tensor  # int32 [B][max_pages], the PagedKV's
     ctx_len: torch.Tensor      # int32 [B], the PagedKV's
 
+    def _measure(self) -> int:
+        _int32_fields(self)
+        if self.n_free.numel() < 1:
+            raise SparseEngineError("PagePool.n_free: one word needed")
+        return min(self.n_pages.numel(), self.ctx_len.numel(), self.block_table.shape[0])
+
     @property
     def c(self) -> PagePoolC:
-        return PagePoolC(_p(self.free_pages), _p(self.n_free), _p(self.n_pages),
-                         _p(self.block_table), _p(self.ctx_len), self.free_pages.numel(),
+        return PagePoolC(self.free_pages.data_ptr(), self.n_free.data_ptr(),
+                         self.n_pages.data_ptr(), self.block_table.data_ptr(),
+                         self.ctx_len.data_ptr(), self.free_pages.numel(),
                          self.block_table.shape[1])
 
     @staticmethod
@@ -287,15 +328,22 @@ class PagePool:
 
 
 @dataclasses.dataclass
-class Chunk:
+class Chunk(_Measured):
     start: torch.Tensor        # int32 [B + 1]
     seq: torch.Tensor          # int32 [max_tokens]
     pos: torch.Tensor          # int32 [max_tokens]
     slot: torch.Tensor         # int32 [max_tokens]
 
+    def _measure(self) -> int:
+        _int32_fields(self)
+        if min(self.pos.numel(), self.slot.numel()) < self.seq.numel():
+            raise SparseEngineError("Chunk: fewer entries in pos or slot than rows in seq")
+        return self.start.numel() - 1
+
     @property
     def c(self) -> ChunkC:
-        return ChunkC(_p(self.start), _p(self.seq), _p(self.pos), _p(self.slot), self.seq.numel())
+        return ChunkC(self.start.data_ptr(), self.seq.data_ptr(), self.pos.data_ptr(),
+                      self.slot.data_ptr(), self.seq.numel())
 
     @staticmethod
     def empty(batch: int, max_tokens: int, device="cuda") -> "Chunk":
@@ -377,9 +425,19 @@ def se_chunk_attn_workspace(batch, max_tokens, num_kv_heads, num_q_heads, head_d
     return load().se_chunk_attn_workspace(batch, max_tokens, num_kv_heads, num_q_heads, head_dim)
 
 
+def _per_sequence(t, batch: int, what: str):
+    """An int32 word for each of `batch` sequences (None: the library's check)."""
+    if t is not None and (t.dtype is not _I32 or t.numel() < batch or not t.is_contiguous()):
+        raise SparseEngineError(f"{what}: contiguous int32 of at least {batch} entries needed, got "
+                                f"{t.dtype} of shape {tuple(t.shape)}")
+
+
 def se_chunk_plan(pool: PagePool, new_len, batch: int, chunk: Chunk, ws, stream=None):
     """Pages, positions and cache rows of each sequence's new tokens."""
     c, cc = pool.c, chunk.c
+    _per_sequence(new_len, batch, "se_chunk_plan new_len")
+    _holds(pool, batch, "se_chunk_plan")
+    _holds(chunk, batch, "se_chunk_plan")
     _check(load().se_chunk_plan(ctypes.byref(c), _p(new_len), batch, ctypes.byref(cc), _p(ws),
                                 ws.numel(), _stream(stream)), "se_chunk_plan")
 
@@ -387,6 +445,8 @@ def se_chunk_plan(pool: PagePool, new_len, batch: int, chunk: Chunk, ws, stream=
 def se_pages_release(pool: PagePool, done, batch: int, ws, stream=None):
     """Pages of the sequences with done[b] != 0 back onto the free stack."""
     c = pool.c
+    _per_sequence(done, batch, "se_pages_release done")
+    _holds(pool, batch, "se_pages_release")
     _check(load().se_pages_release(ctypes.byref(c), _p(done), batch, _p(ws), ws.numel(),
                                    _stream(stream)), "se_pages_release")
 
@@ -423,6 +483,10 @@ def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, 
     stride = _token_stride(k_new, "se_kv_append_chunk k_new", rows, heads, dim)
     if stride != _token_stride(v_new, "se_kv_append_chunk v_new", rows, heads, dim):
         raise SparseEngineError("se_kv_append_chunk: k_new and v_new strides differ")
+    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16:
+        raise SparseEngineError("se_kv_append_chunk: bfloat16 k_new and v_new needed")
+    _holds(kv, batch, "se_kv_append_chunk")
+    _holds(chunk, 0, "se_kv_append_chunk")
     _check(load().se_kv_append_chunk(ctypes.byref(c), _p(k_new), _p(v_new), stride,
                                      ctypes.byref(cc), batch, _p(ws), ws.numel(),
                                      _stream(stream)), "se_kv_append_chunk")
@@ -437,10 +501,15 @@ def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, sc
     rows, dim = cc.max_tokens, c.head_dim
     stride = _token_stride(q, "se_chunk_attn q", rows, num_q_heads, dim)
     _token_stride(out, "se_chunk_attn out", rows, num_q_heads, dim)
-    if not out.is_contiguous() or out.element_size() != (4 if out_dtype else 2):
+    if q.dtype is not _BF16:
+        raise SparseEngineError("se_chunk_attn: bfloat16 q needed")
+    if not out.is_contiguous() or out.dtype is not (_F32 if out_dtype else _BF16):
         raise SparseEngineError("se_chunk_attn: out is not contiguous or not of out_dtype")
-    if lse is not None and (lse.numel() < rows * num_q_heads or not lse.is_contiguous()):
-        raise SparseEngineError("se_chunk_attn: lse of [max_tokens][num_q_heads] needed")
+    if lse is not None and (lse.numel() < rows * num_q_heads or not lse.is_contiguous() or
+                            lse.dtype is not _F32):
+        raise SparseEngineError("se_chunk_attn: float32 lse of [max_tokens][num_q_heads] needed")
+    _holds(kv, batch, "se_chunk_attn")
+    _holds(chunk, batch, "se_chunk_attn")
     opts = ChunkAttnOptsC(out_dtype, window, sink, stride,
                           ev_begin.cuda_event if ev_begin is not None else None,
                           ev_end.cuda_event if ev_end is not None else None, wait_limit_ns)

@@ -172,3 +172,107 @@ def test_attn_wait_limit(lib):
         empty = chunk(max_tokens=0, seq=None, pos=None, slot=None)
         assert lib.se_chunk_attn(paged(), None, empty, 2, 32, 0.1, ctypes.byref(o), None, None, P,
                                  need, None) == rc, limit
+
+
+def chunk_of(rows=8, batch=2, **kw):
+    t = dict(start=torch.zeros(batch + 1, dtype=torch.int32),
+             **{x: torch.zeros(rows, dtype=torch.int32) for x in ("seq", "pos", "slot")})
+    return binding.Chunk(**{**t, **kw})
+
+
+def pool_of(batch=2, **kw):
+    p = binding.PagePool.empty(batch, 6, 4, "cpu")
+    for k, v in kw.items():
+        setattr(p, k, v)
+    return p
+
+
+def cache_of(batch=2, dtype=torch.bfloat16, meta=None):
+    z = torch.zeros(4, 2, 16, 64, dtype=dtype)
+    return binding.PagedKV(z, z.clone(), meta, torch.zeros(batch, 4, dtype=torch.int32),
+                           torch.zeros(batch, dtype=torch.int32))
+
+
+def test_binding_refuses_integers_of_another_type(lib):
+    """A bool, int64 or strided table of a holder is refused, also when it is put there later."""
+    good, ws = torch.zeros(8, dtype=torch.int32), torch.zeros(1 << 10, dtype=torch.uint8)
+
+    def plan(p, c):
+        binding.se_chunk_plan(p, good, 2, c, ws, stream=NoStream)
+    for bad in (good.bool(), good.long(), good.short(), good.float(),
+                torch.zeros(16, dtype=torch.int32)[::2]):
+        for field in ("start", "seq", "pos", "slot"):
+            with pytest.raises(binding.SparseEngineError, match=f"Chunk.{field}.*int32"):
+                plan(pool_of(), chunk_of(**{field: bad}))
+        for field in ("free_pages", "n_free", "n_pages", "ctx_len"):
+            with pytest.raises(binding.SparseEngineError, match=f"PagePool.{field}.*int32"):
+                plan(pool_of(**{field: bad}), chunk_of())
+        with pytest.raises(binding.SparseEngineError, match="PagePool.block_table.*int32"):
+            plan(pool_of(block_table=bad.view(2, 4) if bad.is_contiguous() else bad[:, None]),
+                 chunk_of())
+    c = chunk_of()
+    with pytest.raises(binding.SparseEngineError, match="workspace"):       # all that is wrong here
+        binding.se_chunk_plan(pool_of(), good, 2, c, ws[:8], stream=NoStream)
+    c.pos = c.pos.long()
+    with pytest.raises(binding.SparseEngineError, match="Chunk.pos.*int32"):
+        plan(pool_of(), c)
+
+
+def test_binding_refuses_tables_that_are_too_short(lib):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    ws = torch.zeros(1 << 10, dtype=torch.uint8)
+    refused = lambda m: pytest.raises(binding.SparseEngineError, match=m)
+
+    def plan(pool=None, new=i(2), batch=2, c=None):
+        binding.se_chunk_plan(pool or pool_of(), new, batch, c or chunk_of(), ws, stream=NoStream)
+
+    def release(pool=None, done=i(2), batch=2):
+        binding.se_pages_release(pool or pool_of(), done, batch, ws, stream=NoStream)
+    for bad in (i(1), torch.zeros(2, dtype=torch.bool), torch.zeros(2, dtype=torch.int64), i(4)[::2]):
+        with refused("new_len.*int32"):
+            plan(new=bad)
+        with refused("done.*int32"):
+            release(done=bad)
+    for bad in (dict(n_pages=i(1)), dict(ctx_len=i(1)), dict(block_table=i(1, 4)), dict(n_free=i(0))):
+        with refused("PagePool.*too short for 2 sequences|n_free: one word"):
+            plan(pool_of(**bad))
+        with refused("PagePool.*too short for 2 sequences|n_free: one word"):
+            release(pool_of(**bad))
+    kv, q, k = cache_of(), torch.zeros(8, 4, 64, dtype=torch.bfloat16), torch.zeros(8, 2, 64).bfloat16()
+    for bad in (chunk_of(pos=i(7)), chunk_of(slot=i(7)), chunk_of(start=i(2))):
+        with refused("Chunk.*too short for 2 sequences|Chunk: fewer entries"):
+            plan(c=bad)
+        with refused("Chunk.*too short for 2 sequences|Chunk: fewer entries"):
+            binding.se_chunk_attn(kv, q, bad, 2, 4, 1.0, q.clone(), None, ws, stream=NoStream)
+    for bad in (chunk_of(pos=i(7)), chunk_of(slot=i(7))):
+        with refused("Chunk.*too short for 2 sequences|Chunk: fewer entries"):
+            binding.se_kv_append_chunk(kv, k, k, bad, 2, ws, stream=NoStream)
+    three = chunk_of(batch=3)
+    with refused("PagedKV.*too short for 3 sequences"):
+        binding.se_kv_append_chunk(kv, k, k, three, 3, ws, stream=NoStream)
+    with refused("PagedKV.*too short for 3 sequences"):
+        binding.se_chunk_attn(kv, q, three, 3, 4, 1.0, q.clone(), None, ws, stream=NoStream)
+
+
+def test_binding_refuses_numbers_of_another_type(lib):
+    ws = torch.zeros(1 << 10, dtype=torch.uint8)
+    kv, c = cache_of(), chunk_of()
+    q, k = torch.zeros(8, 4, 64, dtype=torch.bfloat16), torch.zeros(8, 2, 64, dtype=torch.bfloat16)
+
+    def attn(kv=kv, q=q, out=q.clone(), lse=None, f32=0):
+        binding.se_chunk_attn(kv, q, c, 2, 4, 1.0, out, lse, ws, out_dtype=f32, stream=NoStream)
+
+    def append(kv=kv, k=k, v=k):
+        binding.se_kv_append_chunk(kv, k, v, c, 2, ws, stream=NoStream)
+    for dt in (torch.float16, torch.float32, torch.int16):
+        for call in (lambda: attn(q=q.to(dt)), lambda: append(k=k.to(dt)), lambda: append(v=k.to(dt)),
+                     lambda: attn(kv=cache_of(dtype=dt)), lambda: append(kv=cache_of(dtype=dt)),
+                     lambda: append(kv=cache_of(meta=torch.zeros(2, 4, 2, 2, 64, dtype=dt)))):
+            with pytest.raises(binding.SparseEngineError, match="bfloat16"):
+                call()
+    for out, f32 in ((q.half(), 0), (q.short(), 0), (q.int(), 1), (q.float(), 0), (q, 1)):
+        with pytest.raises(binding.SparseEngineError, match="out_dtype"):
+            attn(out=out, f32=f32)
+    for lse in (torch.zeros(8, 4, dtype=torch.float64), torch.zeros(8, 4, dtype=torch.int32)):
+        with pytest.raises(binding.SparseEngineError, match="float32 lse"):
+            attn(lse=lse)
