@@ -171,11 +171,17 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle alone (building the torch.cuda.Stream object costs as much as a
+# launch).  The function is private to torch: where it is missing, the object is built.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        # the handle alone: building the torch.cuda.Stream object costs as much as a launch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
-    return stream.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _ref(x):
