@@ -65,10 +65,14 @@ constexpr int kMaxCtas = 256;
 // fixed part (Q, the pipeline's fill, the rows' output).
 constexpr int kTileBoth = 4, kTileOne = 3, kBlockCost = 10;
 constexpr int kJoinFlat = 8;                       // pieces joined in one go at most
-// Units a CTA takes at least (more than a tile's): 8 suits a single query (11.9 us against
-// 12.4 over 2K) and costs where there are several heads (24.0 against 22.9 over 16K); 24
-// costs both (13.9, 25.4).
+// Units that a CTA should take: 8 suits a single query (11.9 us against 12.4 over 2K) and
+// costs where there are several heads (24.0 against 22.9 over 16K); 24 costs both (13.9,
+// 25.4).  U units go to ceil(U / kMinShare) CTAs at most, so a share is smaller where they do not
+// divide: floor(U / n) for U >= kMinShare (n - 1) + 1, at the least (kMinShare + 1) / 2, with two
+// CTAs.  That is more than a tile's units, which the joins rely on: every CTA between a cut
+// block's first tile and its last holds one of them.
 constexpr int kMinShare = 12;
+static_assert((kMinShare + 1) / 2 >= kTileBoth, "a share holds a tile's first unit");
 constexpr int kMaxBatch = 8192;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -375,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mine = scan(nt, &sum);
         total += sum;
     }
-    // (no share is empty: a block's pieces are those of consecutive CTAs)
+    // (every share has units for a tile: a block's pieces are those of consecutive CTAs)
     const long long U = total * H;
     const long long NC = min((long long)gridDim.x, (U + kMinShare - 1) / kMinShare);
     const Shares shares(U, max(1ll, NC));
