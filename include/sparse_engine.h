@@ -343,9 +343,15 @@ int se_kv_append_chunk(const se_paged_kv* kv, const void* k_new, const void* v_n
  * SE_DEV_BAD_LENGTH, clamped.  start outside [0, max_tokens] or descending:
  * SE_DEV_BAD_LENGTH, and the results are unspecified.
  * Held keys and values are finite; what lies past ctx_len in a page may be anything.
- * scale finite (0 and negative ones too); window, sink >= 0.  Limits: batch <= 8192,
+ * scale finite (0 and negative ones too), |s[j]| < 2^30; window, sink >= 0.
+ * Logits, the softmax's reference and sum and the sums of v are fp32 (sums on the tensor
+ * cores, which round them toward zero).  As in se_sparse_decode the weights are rounded before
+ * the product with v: to bf16 for bf16 output (the output is then off by 2.2 to
+ * 2.4e-3 of its norm, its own rounding alone is 1.7e-3), to two bf16 terms for fp32 output
+ * (2e-6 over 2K tokens, up to 6e-5 over 32K, where the rounded sums are long).  Limits: batch <= 8192,
  * 0 <= max_tokens <= 2^24, max_pages_per_seq <= 2^26, else SE_ERR_UNSUPPORTED.
- * Workspace: se_chunk_attn_workspace(...), zero-filled before its first use:
+ * Workspace: se_chunk_attn_workspace(...) (68 MB for head_dim 128, 35 MB for 64, whatever the
+ * batch: two partial results for each of 256 blocks), zero-filled before its first use:
  * it holds arrival counters at a fixed offset, which every call leaves at zero, so one
  * workspace serves calls of any shape whose size it covers.  Clear it again after a
  * call that set a device error bit. */

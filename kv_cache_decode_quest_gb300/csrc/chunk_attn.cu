@@ -8,6 +8,10 @@
 // exp2(m - m') first; at the end out = O / l and lse = ln 2 (m + log2 l).  Every running
 // value is fp32; P is rounded to bf16 for the product with V (bf16 output: the result is
 // rounded as coarsely anyway) or split into two bf16 terms (fp32 output: 16 mantissa bits).
+// Relative L2 error of the output: 2.2 to 2.4e-3 for bf16, where rounding the output alone gives
+// 1.7e-3 (two terms would bring it there for half as many MMAs again); for fp32 2e-6
+// over 2K keys, 6e-5 over 32K in one accumulator, which the tensor cores round toward zero
+// in every step of 16 keys.
 //
 // One resident CTA per SM takes an equal share of all key tiles of all blocks
 // (a share may begin and end inside a block's keys), found from the lengths on the
@@ -29,11 +33,12 @@
 //
 // Bound: 4 D flops per row and key on the tensor cores for chunks (32 MMAs of 64 clocks a
 // tile for 256 rows: 2060 clocks), K and V from HBM for few rows.  Measured on a GB300
-// (head_dim 128, 32 query heads, 4 KV heads, bf16): the last 2048 tokens of 32K in 665 us
-// (1.61 PFLOP/s), a prompt of 8192 in 365 us (1.51 PFLOP/s), 16 sequences of 32K checking
-// 8 tokens each in 169 us (6.4 TB/s).  A tile for 256 rows takes about 2950 clocks: without
+// (head_dim 128, 32 query heads, 4 KV heads, bf16; 20 calls after a rest / for two seconds on end,
+// where the GPU is at its power limit): the last 2048 tokens of 32K in 650 / 696 us (1.65 /
+// 1.54 PFLOP/s), a prompt of 8192 in 369 / 389 us (1.49 / 1.41 PFLOP/s); 16 sequences of 32K
+// checking 8 tokens each in 169 us (6.4 TB/s).  A tile for 256 rows takes about 2950 clocks: without
 // its softmax 2370, without the tensor cores 2500, its loads alone 2000.  What was
-// measured and not kept: sixteen softmax warps, two threads a row (690 us against 665: issue
+// measured (in bursts) and not kept: sixteen softmax warps, two threads a row (690 us against 665: issue
 // slots, not latency, are short); an MMA warp for each group (789 us: the two fall into step
 // instead of alternating); handing P over in halves (no difference); the running maximum in
 // every tile (the row sum does: 2% on a mixed batch).
