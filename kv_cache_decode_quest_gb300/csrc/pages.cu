@@ -356,12 +356,15 @@ __device__ __forceinline__ ChunkRow chunk_row(const se_paged_kv& kv, const se_ch
             (r.slot < 0 || r.slot / kPage >= kv.num_pages || r.seq < 0 || r.seq >= batch ||
              r.pos < 0 || r.pos / kPage >= kv.max_pages_per_seq ||
              r.pos % kPage != r.slot % kPage);
-    if (r.bad) r.slot = -1;
+    if (r.bad) {
+        r.slot = -1;
+        if (r.seq == -1) r.seq = -2;                // names none, but is no row past the last sequence
+    }
     return r;
 }
 
-// Lengths: each sequence's last row with a slot sets ctx_len, and no other row writes it.  Lane l holds
-// row t of 32; lanes 1..16 hold the rows this warp answers for.  The row after
+// Lengths: each sequence's last row with a slot sets ctx_len, and no other row writes it.
+// Lane l holds row t of 32; lanes 1..16 hold the rows this warp answers for.  The row after
 // such a row tells, unless that one has no slot (a page that was not found, a dropped
 // row): then the warp looks on, past rows without a slot that are the same sequence's or
 // name none that exists, 32 at a time, to the next row that decides.
@@ -483,8 +486,8 @@ __global__ void __launch_bounds__(128)
             (((int64_t)(slot0 / kPage) * H + h) * kPage + slot0 % kPage) * SEGS + seg;
         Bf8 mn, mx;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)              // nothing yet: min and max pass a NaN over, and
-            mn.x[e] = mx.x[e] = CUDART_NAN_F;    // one stays where there is no other key
+        for (int e = 0; e < 8; ++e)              // none yet: min and max pass a NaN over
+            mn.x[e] = mx.x[e] = CUDART_NAN_F;
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r = i * RP + rp;

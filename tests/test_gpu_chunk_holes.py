@@ -190,3 +190,17 @@ def test_keys_that_are_no_numbers_fold_as_one_by_one(D):
     assert np.array_equal(f64(c.kv.k), f64(other.k), equal_nan=True)
     assert np.isnan(f64(other.meta[0, 0, 0, :, :8])).all() and np.isinf(f64(other.meta)).any()
     assert np.array_equal(f64(c.kv.meta), f64(other.meta), equal_nan=True)
+
+
+@pytest.mark.parametrize("whole_page", [False, True])
+def test_dropped_rows_that_name_no_sequence(whole_page):
+    """A seq of -1 beside a slot is a dropped row like any other, not the end of the rows."""
+    g = np.random.default_rng([38])
+    c = Cache(g, 2, 2, 64, 10, 20)
+    c.add([3, 0])
+    start, seq, pos, slot = planned(c, [90, 40], 6)
+    kept = slot.copy()
+    at = np.r_[13:29, 45:61] if whole_page else np.array([5, 20, 21, 44, 90 + 1, 90 + 30])
+    kept[at] = -1
+    seq[at] = -1
+    append_rows(c, start, seq, pos, slot, BAD_INDEX, kept)
