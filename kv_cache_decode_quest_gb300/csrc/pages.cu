@@ -8,72 +8,13 @@
 #include <algorithm>
 
 #include "append.cuh"
+#include "chunk_rows.cuh"
 #include "common.cuh"
 #include "internal.h"
+#include "page_tables.cuh"
 
 namespace se {
 namespace {
-
-// Workspace: the status word, then at byte 256 the arrival counter of the
-// kernel's blocks (zero between calls).
-constexpr int kCounterWord = 64;
-
-// Exclusive block-wide sums of two 64-bit values per thread (lengths come from
-// the device and may be anything: 64 bits hold the sum of any 1024 of them).
-// `tmp` holds 2 * 33 values.  All threads call it; *ta, *tb receive the totals.
-__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long* tmp,
-                                            long long* ta, long long* tb) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    long long x = a, y = b;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, x, o);
-        const long long v = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-            x += u;
-            y += v;
-        }
-    }
-    if (lane == 31) {
-        tmp[warp] = x;
-        tmp[33 + warp] = y;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        long long p = lane < nw ? tmp[lane] : 0, q = lane < nw ? tmp[33 + lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long u = __shfl_up_sync(0xffffffffu, p, o);
-            const long long v = __shfl_up_sync(0xffffffffu, q, o);
-            if (lane >= o) {
-                p += u;
-                q += v;
-            }
-        }
-        if (lane < nw) {
-            tmp[lane] = p;
-            tmp[33 + lane] = q;
-        }
-    }
-    __syncthreads();
-    *ta = tmp[nw - 1];
-    *tb = tmp[33 + nw - 1];
-    a = x - a + (warp > 0 ? tmp[warp - 1] : 0);
-    b = y - b + (warp > 0 ? tmp[33 + warp - 1] : 0);
-    __syncthreads();
-}
-
-// True in every thread of the last block of the grid to get here; what the
-// other blocks read before is then read, and their writes are visible.
-__device__ __forceinline__ bool last_block(int* counter) {
-    __shared__ int s_last;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    __threadfence();
-    return s_last != 0;
-}
 
 struct SeqPlan {
     int ctx, held, n;       // tokens and pages held, new tokens (rows in the packed arrays)
@@ -339,64 +280,10 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) ws[kCounterWord] = 0;
 }
 
-// Row t of a chunk: slot is -1 where it has none, where it is dropped (`bad`: the slot
-// is outside the pages, or seq or pos outside the block table) and past the arrays.
-struct ChunkRow {
-    int slot, pos, seq;
-    bool bad;
-};
-__device__ __forceinline__ ChunkRow chunk_row(const se_paged_kv& kv, const se_chunk& ck, int batch,
-                                              int t) {
-    ChunkRow r = {-1, -1, -1, false};
-    if (t < 0 || t >= ck.max_tokens) return r;
-    r.slot = ck.slot[t];
-    r.pos = ck.pos[t];
-    r.seq = ck.seq[t];
-    r.bad = r.slot != -1 &&
-            (r.slot < 0 || r.slot / kPage >= kv.num_pages || r.seq < 0 || r.seq >= batch ||
-             r.pos < 0 || r.pos / kPage >= kv.max_pages_per_seq ||
-             r.pos % kPage != r.slot % kPage);
-    if (r.bad) {
-        r.slot = -1;
-        if (r.seq == -1) r.seq = -2;                // names none, but is no row past the last sequence
-    }
-    return r;
-}
-
-// Lengths: each sequence's last row with a slot sets ctx_len, and no other row writes it.
-// Lane l holds row t of 32; lanes 1..16 hold the rows this warp answers for.  The row after
-// such a row tells, unless that one has no slot (a page that was not found, a dropped
-// row): then the warp looks on, past rows without a slot that are the same sequence's or
-// name none that exists, 32 at a time, to the next row that decides.
-__device__ __forceinline__ void commit_lengths(const se_paged_kv& kv, const se_chunk& ck, int batch,
-                                               int t, int lane, const ChunkRow& row) {
-    const bool mine = row.slot >= 0 && lane >= 1 && lane <= kPage;
-    const int nslot = __shfl_down_sync(0xffffffffu, row.slot, 1);
-    const int nseq = __shfl_down_sync(0xffffffffu, row.seq, 1);
-    auto passes = [&](int s, int b) { return s == b || s < -1 || s >= batch; };
-    const bool hole = mine && nslot < 0 && passes(nseq, row.seq);
-    if (mine && !hole && (nslot < 0 || nseq != row.seq)) kv.ctx_len[row.seq] = row.pos + 1;
-    for (uint32_t m = __ballot_sync(0xffffffffu, hole); m != 0; m &= m - 1) {
-        const int f = __ffs(m) - 1;
-        const int b = __shfl_sync(0xffffffffu, row.seq, f);
-        const int len = __shfl_sync(0xffffffffu, row.pos, f) + 1;
-        uint32_t more, end;                         // rows that go on, rows that are another's or none's
-        for (int r = __shfl_sync(0xffffffffu, t, f) + 1;; r += 32) {
-            const ChunkRow x = chunk_row(kv, ck, batch, r + lane);
-            more = __ballot_sync(0xffffffffu, x.slot >= 0 && x.seq == b);
-            end = __ballot_sync(0xffffffffu,
-                                x.slot >= 0 ? x.seq != b : !passes(x.seq, b));
-            if ((more | end) != 0) break;           // (rows past max_tokens end it)
-        }
-        if (lane == 0 && __ffs(more | end) == __ffs(end)) kv.ctx_len[b] = len;
-    }
-}
-
 // Append of packed rows.  Block i looks at rows [16i, 16i + 16); the rows of one sequence that
 // lie in one page are a piece (at most 16 rows apart, whatever rows between them have no
 // slot), the work of one warp for one KV head, which owns that page's summary: no
-// atomics and a fixed result.  Each warp finds the pieces that begin in the block
-// from the slots of 32 rows around it (ballots).  A row is D/8 16-byte vectors, so
+// atomics and a fixed result.  A row is D/8 16-byte vectors, so
 // RP rows move side by side; all loads of a piece are in flight before the
 // first store.  HBM bound for long chunks (each byte read once and written once),
 // latency bound for a few rows.
@@ -409,60 +296,20 @@ __global__ void __launch_bounds__(128)
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int H = kv.num_kv_heads;
-    // lane l looks at row 16i - 1 + l
-    const int t = static_cast<int>(blockIdx.x) * kPage - 1 + lane;
-    const ChunkRow row = chunk_row(kv, ck, batch, t);
-    if (row.bad && lane >= 1 && lane <= kPage && warp == 0) flag(status, SE_DEV_BAD_INDEX);
-    const int slot = row.slot, pos = row.pos, seq = row.seq;
-    const bool valid = slot >= 0;
-    const int pslot = __shfl_up_sync(0xffffffffu, slot, 1);
-    const int pseq = __shfl_up_sync(0xffffffffu, seq, 1);
-    const int ppos = __shfl_up_sync(0xffffffffu, pos, 1);
-    const bool begins = valid && lane >= 1 && lane <= kPage &&
-                        !(pslot >= 0 && pseq == seq && ppos + 1 == pos && pslot + 1 == slot &&
-                          pos % kPage != 0);
-    // rows of a piece: slot and position go with the row
-    auto same_piece = [&](int d, int slot_d, int pos_d, int seq_d, int slot0, int pos0, int seq0) {
-        return slot_d >= 0 && seq_d == seq0 && slot_d - slot0 == d && pos_d - pos0 == d &&
-               pos_d / kPage == pos0 / kPage;
-    };
-    uint32_t lead_m = __ballot_sync(0xffffffffu, begins);
-    // behind rows without a slot a page may have begun before them: up to 15 rows back
-    const bool unsure = begins && pslot < 0 && t > 0 && pos % kPage != 0 &&
-                        (pseq == seq || pseq < 0 || pseq >= batch);
-    uint32_t look = __ballot_sync(0xffffffffu, unsure);
-    if (look != 0) {
-        const ChunkRow far = chunk_row(kv, ck, batch, t - 32);
-        for (; look != 0; look &= look - 1) {
-            const int f = __ffs(look) - 1;
-            const int slot0 = __shfl_sync(0xffffffffu, slot, f);
-            const int pos0 = __shfl_sync(0xffffffffu, pos, f);
-            const int seq0 = __shfl_sync(0xffffffffu, seq, f);
-            if (__any_sync(0xffffffffu,
-                           (lane < f && same_piece(lane - f, slot, pos, seq, slot0, pos0, seq0)) ||
-                               same_piece(lane - 32 - f, far.slot, far.pos, far.seq, slot0, pos0,
-                                          seq0)))
-                lead_m &= ~(1u << f);
-        }
-    }
-    if (warp == 0 && blockIdx.y == 0) commit_lengths(kv, ck, batch, t, lane, row);
+    const Pieces pieces = find_pieces(kv, ck, batch, static_cast<int>(blockIdx.x), lane);
+    if (pieces.row.bad && lane >= 1 && lane <= kPage && warp == 0) flag(status, SE_DEV_BAD_INDEX);
+    if (warp == 0 && blockIdx.y == 0) commit_lengths(kv, ck, batch, pieces.t, lane, pieces.row);
     const int seg = lane % SEGS, rp = lane / SEGS;
     uint4* K = static_cast<uint4*>(kv.k);
     uint4* V = static_cast<uint4*>(kv.v);
     uint4* M = static_cast<uint4*>(kv.meta);
-    const int units = __popc(lead_m) * H;
+    const int units = __popc(pieces.lead) * H;
     const int nw = (blockDim.x >> 5) * gridDim.y;
     for (int u = warp + (blockDim.x >> 5) * blockIdx.y; u < units; u += nw) {
         const int h = u % H;
-        uint32_t rest = lead_m;
-        for (int i = u / H; i > 0; --i) rest &= rest - 1;
-        const int f = __ffs(rest) - 1;                              // lane of the piece's first row
-        const int slot0 = __shfl_sync(0xffffffffu, slot, f);
-        const int pos0 = __shfl_sync(0xffffffffu, pos, f);
-        const int seq0 = __shfl_sync(0xffffffffu, seq, f);
-        // bit r: row r behind the first is of the piece
-        const uint32_t rows =
-            __ballot_sync(0xffffffffu, same_piece(lane - f, slot, pos, seq, slot0, pos0, seq0)) >> f;
+        const Piece pc = piece_at(pieces, u / H, lane);
+        const int f = pc.f, slot0 = pc.slot0, pos0 = pc.pos0, seq0 = pc.seq0;
+        const uint32_t rows = pc.rows;                  // bit r: row r behind the first is of the piece
         const int64_t src = (int64_t)(static_cast<int>(blockIdx.x) * kPage - 1 + f) * row_stride +
                             h * SEGS + seg;
         uint4 k[IT], v[IT];
