@@ -67,6 +67,22 @@ class ChunkAttnOptsC(ctypes.Structure):
                 ("wait_limit_ns", ctypes.c_int32)]
 
 
+class RopeC(ctypes.Structure):
+    _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p)]
+
+
+class RopeScalingC(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("factor", ctypes.c_float),
+                ("original_len", ctypes.c_float), ("low", ctypes.c_float),
+                ("high", ctypes.c_float)]
+
+
+class PageCarryC(ctypes.Structure):
+    _fields_ = [("from_seq", ctypes.c_void_p), ("from_page", ctypes.c_void_p)]
+
+
 class DecodeOptsC(ctypes.Structure):
     _fields_ = [("out_dtype", ctypes.c_int32), ("max_splits", ctypes.c_int32),
                 ("logits_out", ctypes.c_void_p), ("logits_stride", ctypes.c_int32),
@@ -78,6 +94,8 @@ class SelectOptsC(ctypes.Structure):
 
 
 SE_AGG_SUM, SE_AGG_MAX = 0, 1
+SE_ROPE_HALVES, SE_ROPE_PAIRS = 0, 1
+SE_ROPE_PLAIN, SE_ROPE_LINEAR, SE_ROPE_NTK, SE_ROPE_YARN, SE_ROPE_BANDS = range(5)
 
 
 class QuestStepOptsC(ctypes.Structure):
@@ -88,6 +106,7 @@ class QuestStepOptsC(ctypes.Structure):
 
 # C entry points: name -> (restype, argtypes)
 _VP, _I, _SZ, _F, _I64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float, ctypes.c_int64
+_F64 = ctypes.c_double
 SIGNATURES = {
     "se_status_str": (ctypes.c_char_p, [_I]),
     "se_version": (_I, []),
@@ -104,6 +123,18 @@ SIGNATURES = {
     "se_pages_release": (_I, [_VP, _VP, _I, _VP, _SZ, _VP]),
     "se_kv_append_chunk": (_I, [_VP, _VP, _VP, _I64, _VP, _I, _VP, _SZ, _VP]),
     "se_chunk_attn": (_I, [_VP, _VP, _VP, _I, _I, _F, _VP, _VP, _VP, _VP, _SZ, _VP]),
+    "se_rope_turns": (_I, [_F64, _I, _VP, _VP, _VP]),
+    "se_qk_rope": (_I, [_VP, _VP, _I, _I, _I, _I, _VP, _I64, _VP, _I64, _VP, _I64, _VP, _I64, _VP,
+                        _SZ, _VP]),
+    "se_rope_append_chunk": (_I, [_VP, _VP, _VP, _I64, _I, _VP, _VP, _I64, _VP, _I64, _VP, _I, _VP,
+                                  _SZ, _VP]),
+    "se_draft_verify_workspace": (_SZ, [_I, _I]),
+    "se_draft_verify": (_I, [_VP, _VP, _I64, _I, _I, _VP, _VP, _VP, _VP, _I, _VP, _VP, _VP, _VP,
+                             _SZ, _VP]),
+    "se_pages_truncate_workspace": (_SZ, [_I, _I]),
+    "se_pages_fork": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _SZ, _VP]),
+    "se_pages_truncate": (_I, [_VP, _VP, _VP, _I, _VP, _VP, _SZ, _VP]),
+    "se_pages_carry": (_I, [_VP, _VP, _I, _VP, _SZ, _VP]),
     "se_page_meta_build": (_I, [_VP, _I, _VP, _SZ, _VP]),
     "se_kv_append": (_I, [_VP, _VP, _VP, _I, _VP, _SZ, _VP]),
     "se_quest_select": (_I, [_VP, _VP, _I, _I, _VP, _VP, _VP, _VP, _VP, _SZ, _VP]),
@@ -358,6 +389,72 @@ class Chunk(_Measured):
                      rows[2])
 
 
+@dataclasses.dataclass
+class Carry(_Measured):
+    """What each layer's cache takes over after se_pages_fork or se_pages_truncate."""
+    from_seq: torch.Tensor     # int32 [B]
+    from_page: torch.Tensor    # int32 [B]
+
+    def _measure(self) -> int:
+        _int32_fields(self)
+        return min(self.from_seq.numel(), self.from_page.numel())
+
+    @property
+    def c(self) -> PageCarryC:
+        return PageCarryC(self.from_seq.data_ptr(), self.from_page.data_ptr())
+
+    @staticmethod
+    def empty(batch: int, device="cuda") -> "Carry":
+        t = torch.full((2, batch), -1, dtype=torch.int32, device=device)
+        return Carry(t[0], t[1])
+
+
+@dataclasses.dataclass
+class Rope(_Measured):
+    """A layer's rotation and the norms ahead of it (Rope.make)."""
+    turns: torch.Tensor | None           # int64 [rot_dim / 2], the 64 bits of turns per position
+    rot_dim: int
+    layout: int = SE_ROPE_HALVES
+    amplitude: float = 1.0
+    eps: float = 1e-6
+    q_weight: torch.Tensor | None = None     # bf16 [D]
+    k_weight: torch.Tensor | None = None     # bf16 [D]
+
+    def _measure(self) -> int:
+        t = self.turns
+        if t is not None and (t.dtype is not torch.int64 or not t.is_contiguous()):
+            raise SparseEngineError(f"Rope.turns: contiguous int64 tensor needed, got {t.dtype}")
+        if self.rot_dim and (t is None or 2 * t.numel() < self.rot_dim):
+            raise SparseEngineError(f"Rope.turns: {self.rot_dim // 2} entries needed")
+        widths = {1 << 20}
+        for name in ("q_weight", "k_weight"):
+            w = getattr(self, name)
+            if w is not None:
+                if w.dtype is not _BF16 or not w.is_contiguous() or w.dim() != 1:
+                    raise SparseEngineError(f"Rope.{name}: contiguous bfloat16 [head_dim] needed, got "
+                                            f"{w.dtype} of shape {tuple(w.shape)}")
+                widths.add(w.numel())
+        return min(widths)
+
+    @property
+    def c(self) -> RopeC:
+        return RopeC(_p(self.turns), self.rot_dim, self.layout, self.amplitude, self.eps,
+                     _p(self.q_weight), _p(self.k_weight))
+
+    @staticmethod
+    def make(rot_dim: int, base: float = 10000.0, scaling: int = SE_ROPE_PLAIN, factor: float = 1.0,
+             original_len: float = 0.0, low: float = 1.0, high: float = 32.0,
+             layout: int = SE_ROPE_HALVES, q_weight=None, k_weight=None, eps: float = 1e-6,
+             amplitude: float | None = None, device="cuda") -> "Rope":
+        """The rotation of rot_dim channels (0: norms alone); amplitude None: the scaling's own."""
+        turns, amp = None, 1.0
+        if rot_dim:
+            turns, amp = se_rope_turns(rot_dim, base, scaling, factor, original_len, low, high)
+            turns = turns.to(device)
+        return Rope(turns, rot_dim, layout, amp if amplitude is None else amplitude, eps, q_weight,
+                    k_weight)
+
+
 def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     """A zeroed device workspace (status word cleared)."""
     return torch.zeros(max(256, int(nbytes)), dtype=torch.uint8, device=device)
@@ -465,7 +562,7 @@ def _token_stride(x, what: str, tokens: int = 0, heads: int = 0, head_dim: int =
     try:
         n, h, d = shape
         sn, sh, sd = stride
-        ok = sd == 1 and (sh == d or h == 1)
+        ok = n == 0 or sd == 1 and (sh == d or h == 1)     # (no rows: strides mean nothing)
     except ValueError:
         ok = False
     if not ok:
@@ -522,6 +619,164 @@ def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, sc
     _check(load().se_chunk_attn(ctypes.byref(c), _p(q), ctypes.byref(cc), batch, num_q_heads,
                                 scale, ctypes.byref(opts), _p(out), _p(lse), _p(ws), ws.numel(),
                                 _stream(stream)), "se_chunk_attn")
+
+
+def _on_device(what: str, *tensors):
+    """Refuses tensors that the kernels cannot reach: the calls run on the current device."""
+    here = None
+    for t in tensors:
+        if t is None:
+            continue
+        at = t.get_device()
+        if here is None:
+            here = torch.cuda.current_device() if at >= 0 else 0
+        if at != here:
+            raise SparseEngineError(f"{what}: a tensor is on {t.device}, not on the current CUDA device")
+
+
+def se_rope_turns(rot_dim: int, base: float = 10000.0, scaling: int = SE_ROPE_PLAIN,
+                  factor: float = 1.0, original_len: float = 0.0, low: float = 1.0,
+                  high: float = 32.0):
+    """(turns, amplitude): the frequencies of a rotation as int64 (CPU) and the factor on its cosines."""
+    turns = torch.zeros(max(0, rot_dim // 2), dtype=torch.int64)
+    amplitude = ctypes.c_float(1.0)
+    s = RopeScalingC(scaling, factor, original_len, low, high)
+    _check(load().se_rope_turns(base, rot_dim, ctypes.byref(s), _p(turns), ctypes.byref(amplitude)),
+           "se_rope_turns")
+    return turns, amplitude.value
+
+
+def _rotated(x, out, rows: int, what: str):
+    """(heads, head_dim, stride, out stride) of rows of heads and the tensor they go to."""
+    if x is None or out is None:
+        if x is not None or out is not None:
+            raise SparseEngineError(f"{what}: rows without a tensor to go to, or the other way round")
+        return 0, 0, 0, 0
+    if x.dtype is not _BF16 or out.dtype is not _BF16:
+        raise SparseEngineError(f"{what}: bfloat16 needed, got {x.dtype} and {out.dtype}")
+    stride = _token_stride(x, what, rows, x.shape[1] if x.dim() == 3 else 0, x.shape[-1])
+    return x.shape[1], x.shape[2], stride, _token_stride(out, f"{what}_out", rows, *x.shape[1:])
+
+
+def se_qk_rope(rope: Rope, pos, q, k, q_out, k_out, ws, stream=None):
+    """Queries [rows][Hq][D] and keys [rows][Hkv][D] (or one of them, the other None) normalised per
+    head and rotated to the positions pos (int32 [rows], negative: the row is left out); q_out may be q
+    and k_out k, and all may be slices of wider rows."""
+    rows = pos.numel()
+    _per_sequence(pos, rows, "se_qk_rope pos")
+    hq, dim, sq, oq = _rotated(q, q_out, rows, "se_qk_rope q")
+    hk, dim_k, sk, ok = _rotated(k, k_out, rows, "se_qk_rope k")
+    if hq and hk and dim != dim_k:
+        raise SparseEngineError(f"se_qk_rope: q of {dim} channels a head, k of {dim_k}")
+    dim = dim or dim_k
+    _holds(rope, dim, "se_qk_rope: head_dim")
+    _on_device("se_qk_rope", pos, q, k, q_out, k_out, ws, rope.turns, rope.q_weight, rope.k_weight)
+    c = rope.c
+    _check(load().se_qk_rope(ctypes.byref(c), _p(pos), rows, hq, hk, dim, _p(q), sq, _p(k), sk,
+                             _p(q_out), oq, _p(k_out), ok, _p(ws), ws.numel(), _stream(stream)),
+           "se_qk_rope")
+
+
+def se_rope_append_chunk(kv: PagedKV, rope: Rope, q, k_new, v_new, q_out, chunk: Chunk, batch: int,
+                         ws, stream=None):
+    """se_qk_rope of the chunk's rows and se_kv_append_chunk of the rotated keys and of v_new in one
+    pass; q, q_out None: keys alone.  All rows may be slices of wider rows."""
+    c, cc = kv.c, chunk.c
+    rows, heads, dim = cc.max_tokens, c.num_kv_heads, c.head_dim
+    stride = _token_stride(k_new, "se_rope_append_chunk k_new", rows, heads, dim)
+    if stride != _token_stride(v_new, "se_rope_append_chunk v_new", rows, heads, dim):
+        raise SparseEngineError("se_rope_append_chunk: k_new and v_new strides differ")
+    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16:
+        raise SparseEngineError("se_rope_append_chunk: bfloat16 k_new and v_new needed")
+    hq, dim_q, sq, oq = _rotated(q, q_out, rows, "se_rope_append_chunk q")
+    if hq and dim_q != dim:
+        raise SparseEngineError(f"se_rope_append_chunk: q of {dim_q} channels a head, the cache of {dim}")
+    _holds(rope, dim, "se_rope_append_chunk: head_dim")
+    _holds(kv, batch, "se_rope_append_chunk")
+    _holds(chunk, 0, "se_rope_append_chunk")
+    _on_device("se_rope_append_chunk", kv.k, kv.v, kv.meta, kv.ctx_len, q, k_new, v_new, q_out,
+               chunk.slot, ws, rope.turns, rope.q_weight, rope.k_weight)
+    rc = rope.c
+    _check(load().se_rope_append_chunk(ctypes.byref(c), ctypes.byref(rc), _p(q), sq, hq, _p(k_new),
+                                       _p(v_new), stride, _p(q_out), oq, ctypes.byref(cc), batch,
+                                       _p(ws), ws.numel(), _stream(stream)), "se_rope_append_chunk")
+
+
+def se_draft_verify_workspace(batch: int, vocab: int) -> int:
+    return load().se_draft_verify_workspace(batch, vocab)
+
+
+def se_draft_verify(probs, draft_probs, tokens, accept_u, sample_u, chunk: Chunk, batch: int,
+                    n_accepted, next_token, keep, ws, stream=None):
+    """Which of the chunk's drafted tokens stay and the token behind them; probs and draft_probs (or
+    None) [max_tokens][vocab] bf16 or fp32, keep: the lengths for se_pages_truncate."""
+    what, rows = "se_draft_verify", chunk.seq.numel()
+    for t in (probs, draft_probs):
+        if t is None:
+            continue
+        if t.dtype is not probs.dtype or t.dtype not in (_BF16, _F32):
+            raise SparseEngineError(f"{what}: probabilities in bfloat16 or float32 needed, one type for "
+                                    f"both, got {t.dtype}")
+        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != probs.shape[1] or \
+                (rows > 0 and t.shape[1] > 1 and t.stride(1) != 1) or \
+                (rows > 1 and (t.stride(0) != probs.stride(0) or t.stride(0) < t.shape[1])):
+            raise SparseEngineError(f"{what}: probabilities of at least [{rows}][vocab] with equal row "
+                                    f"strides needed, got shape {tuple(t.shape)} strides {t.stride()}")
+    _per_sequence(tokens, rows, f"{what} tokens")
+    for t, n, name in ((accept_u, rows, "accept_u"), (sample_u, batch, "sample_u")):
+        if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
+            raise SparseEngineError(f"{what} {name}: contiguous float32 of at least {n} entries needed, "
+                                    f"got {t.dtype} of shape {tuple(t.shape)}")
+    for t, name in ((n_accepted, "n_accepted"), (next_token, "next_token"), (keep, "keep")):
+        _per_sequence(t, batch, f"{what} {name}")
+    _holds(chunk, batch, what)
+    _on_device(what, probs, draft_probs, tokens, accept_u, sample_u, chunk.start, chunk.pos, n_accepted,
+               next_token, keep, ws)
+    cc, vocab = chunk.c, probs.shape[1]
+    stride = probs.stride(0) if rows > 1 else vocab
+    _check(load().se_draft_verify(_p(probs), _p(draft_probs), stride, int(probs.dtype is _F32), vocab,
+                                  _p(tokens), _p(accept_u), _p(sample_u), ctypes.byref(cc), batch,
+                                  _p(n_accepted), _p(next_token), _p(keep), _p(ws), ws.numel(),
+                                  _stream(stream)), what)
+
+
+def se_pages_truncate_workspace(batch: int, num_pages: int) -> int:
+    return load().se_pages_truncate_workspace(batch, num_pages)
+
+
+def _table_edit(name: str, pool: PagePool, page_refs, words, batch: int, carry: Carry, ws, stream):
+    _per_sequence(words, batch, name)
+    _per_sequence(page_refs, pool.free_pages.numel(), f"{name} page_refs")
+    _holds(pool, batch, name)
+    _holds(carry, batch, name)
+    _on_device(name, pool.free_pages, pool.block_table, pool.ctx_len, page_refs, words, carry.from_seq,
+               carry.from_page, ws)
+    c, cc = pool.c, carry.c
+    _check(getattr(load(), name)(ctypes.byref(c), _p(page_refs), _p(words), batch, ctypes.byref(cc),
+                                 _p(ws), ws.numel(), _stream(stream)), name)
+
+
+def se_pages_fork(pool: PagePool, page_refs, src, batch: int, carry: Carry, ws, stream=None):
+    """Every sequence b with src[b] >= 0 becomes a copy of sequence src[b] that shares its full pages;
+    page_refs int32 [num_pages] counts the holders beside the first."""
+    _table_edit("se_pages_fork", pool, page_refs, src, batch, carry, ws, stream)
+
+
+def se_pages_truncate(pool: PagePool, page_refs, keep, batch: int, carry: Carry, ws, stream=None):
+    """Cuts every sequence b with keep[b] >= 0 to keep[b] tokens; pages that nobody holds any more go
+    back on the stack.  page_refs None: no pages are shared."""
+    _table_edit("se_pages_truncate", pool, page_refs, keep, batch, carry, ws, stream)
+
+
+def se_pages_carry(kv: PagedKV, carry: Carry, batch: int, ws, stream=None):
+    """One layer's cache follows a fork or a truncation: last pages' rows and page summaries."""
+    _holds(kv, batch, "se_pages_carry")
+    _holds(carry, batch, "se_pages_carry")
+    _on_device("se_pages_carry", kv.k, kv.v, kv.meta, kv.block_table, kv.ctx_len, carry.from_seq,
+               carry.from_page, ws)
+    c, cc = kv.c, carry.c
+    _check(load().se_pages_carry(ctypes.byref(c), ctypes.byref(cc), batch, _p(ws), ws.numel(),
+                                 _stream(stream)), "se_pages_carry")
 
 
 def se_quest_select(kv: PagedKV, q, batch: int, num_q_heads: int, budget_tokens, sel_pages,

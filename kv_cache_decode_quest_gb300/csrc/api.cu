@@ -150,6 +150,36 @@ int check_chunk(const se_chunk* c) {
     return SE_OK;
 }
 
+constexpr int kMaxRopeHeads = 1024;
+constexpr int kMaxVocab = 1 << 22;
+
+int check_rope(const se_rope* r, int head_dim) {
+    if (!r) return SE_ERR_INVALID_ARG;
+    if (!head_dim_ok(head_dim)) return SE_ERR_UNSUPPORTED;
+    if (r->rot_dim < 0 || r->rot_dim > head_dim || r->rot_dim % 16) return SE_ERR_INVALID_ARG;
+    if (r->rot_dim > 0 && (!r->turns || !aligned(r->turns, 8))) return SE_ERR_INVALID_ARG;
+    if (r->layout != SE_ROPE_HALVES && r->layout != SE_ROPE_PAIRS) return SE_ERR_INVALID_ARG;
+    if (!std::isfinite(r->amplitude) || !std::isfinite(r->eps) || r->eps < 0)
+        return SE_ERR_INVALID_ARG;
+    if (!aligned(r->q_weight, 16) || !aligned(r->k_weight, 16)) return SE_ERR_INVALID_ARG;
+    return SE_OK;
+}
+
+// Rows of heads, in and out (strides 0: dense).
+int check_heads(HeadArgs& a, int head_dim) {
+    if (a.heads < 0) return SE_ERR_INVALID_ARG;
+    if (a.heads > kMaxRopeHeads) return SE_ERR_UNSUPPORTED;
+    if (a.heads == 0) return SE_OK;
+    const int64_t row = (int64_t)a.heads * head_dim;
+    if (a.in_stride == 0) a.in_stride = row;
+    if (a.out_stride == 0) a.out_stride = row;
+    if (!a.in || !a.out || !aligned(a.in, 16) || !aligned(a.out, 16)) return SE_ERR_INVALID_ARG;
+    if (a.in_stride < row || a.in_stride % 8 || a.out_stride < row || a.out_stride % 8)
+        return SE_ERR_INVALID_ARG;
+    if (a.in == a.out && a.in_stride != a.out_stride) return SE_ERR_INVALID_ARG;
+    return SE_OK;
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? SE_OK : SE_ERR_CUDA; }
 
 }  // namespace
@@ -177,7 +207,8 @@ int se_sync_status(const void* ws, se_stream_t stream) {
     int32_t word = 0;
     if (cudaMemcpy(&word, ws, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
         return SE_ERR_CUDA;
-    return word & (SE_DEV_BAD_INDEX | SE_DEV_CAPACITY | SE_DEV_BAD_LENGTH | SE_DEV_TIMEOUT);
+    return word & (SE_DEV_BAD_INDEX | SE_DEV_CAPACITY | SE_DEV_BAD_LENGTH | SE_DEV_TIMEOUT |
+                   SE_DEV_BAD_VALUE);
 }
 
 size_t se_small_workspace(void) { return 256; }
@@ -307,6 +338,170 @@ int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, i
                                          static_cast<cudaEvent_t>(o.ev_kernel_begin),
                                          static_cast<cudaEvent_t>(o.ev_kernel_end),
                                          static_cast<cudaStream_t>(stream)));
+}
+
+int se_rope_turns(double base, int rot_dim, const se_rope_scaling* scaling, uint64_t* turns,
+                  float* amplitude) {
+    constexpr double kPi = 3.14159265358979323846;
+    se_rope_scaling sc = {SE_ROPE_PLAIN, 1.f, 0.f, 0.f, 0.f};
+    if (scaling) sc = *scaling;
+    if (!turns || !std::isfinite(base) || !(base > 1) || rot_dim < 16 || rot_dim > 128 || rot_dim % 16)
+        return SE_ERR_INVALID_ARG;
+    if (sc.kind < SE_ROPE_PLAIN || sc.kind > SE_ROPE_BANDS) return SE_ERR_INVALID_ARG;
+    const double s = sc.kind == SE_ROPE_PLAIN ? 1.0 : sc.factor, L = sc.original_len;
+    if (!std::isfinite(s) || !(s >= 1)) return SE_ERR_INVALID_ARG;
+    if (sc.kind == SE_ROPE_YARN || sc.kind == SE_ROPE_BANDS)
+        if (!std::isfinite(L) || !(L > 0) || !(sc.low > 0) || !std::isfinite(sc.high) ||
+            !(sc.low < sc.high))
+            return SE_ERR_INVALID_ARG;
+    if (sc.kind == SE_ROPE_NTK) {
+        base *= std::pow(s, rot_dim / (rot_dim - 2.0));
+        if (!std::isfinite(base)) return SE_ERR_INVALID_ARG;
+    }
+    double lo = 0, hi = 0;
+    if (sc.kind == SE_ROPE_YARN) {
+        auto at = [&](double x) {
+            return rot_dim * std::log(L / (2 * kPi * x)) / (2 * std::log(base));
+        };
+        lo = std::max(0.0, std::floor(at(sc.high)));
+        hi = std::min(rot_dim - 1.0, std::ceil(at(sc.low)));
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2.0 * i / rot_dim);
+        if (sc.kind == SE_ROPE_LINEAR) {
+            f /= s;
+        } else if (sc.kind == SE_ROPE_YARN) {
+            const double r = std::min(1.0, std::max(0.0, (i - lo) / std::max(hi - lo, 0.001)));
+            f = f * (1 - r) + f / s * r;
+        } else if (sc.kind == SE_ROPE_BANDS) {
+            const double r = std::min(
+                1.0, std::max(0.0, (L * f / (2 * kPi) - sc.low) / ((double)sc.high - sc.low)));
+            f = f * r + f / s * (1 - r);
+        }
+        turns[i] = static_cast<uint64_t>(std::nearbyint(std::ldexp(f / (2 * kPi), 64)));
+    }
+    if (amplitude)
+        *amplitude = sc.kind == SE_ROPE_YARN ? static_cast<float>(0.1 * std::log(s) + 1) : 1.f;
+    return SE_OK;
+}
+
+int se_qk_rope(const se_rope* rope, const int32_t* pos, int rows, int num_q_heads, int num_kv_heads,
+               int head_dim, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+               void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* ws,
+               size_t ws_bytes, se_stream_t stream) {
+    int rc = check_rope(rope, head_dim);
+    if (rc) return rc;
+    if (rows < 0) return SE_ERR_INVALID_ARG;
+    if (rows > kMaxChunkTokens) return SE_ERR_UNSUPPORTED;
+    if ((rc = check_ws(ws, ws_bytes, se_small_workspace()))) return rc;
+    if (rows == 0) return SE_OK;
+    HeadArgs qa = {q, q_out, q_stride, q_out_stride, num_q_heads};
+    HeadArgs ka = {k, k_out, k_stride, k_out_stride, num_kv_heads};
+    if ((rc = check_heads(qa, head_dim)) || (rc = check_heads(ka, head_dim))) return rc;
+    if (!pos) return SE_ERR_INVALID_ARG;
+    return cuda_status(
+        launch_qk_rope(*rope, pos, rows, head_dim, qa, ka, static_cast<cudaStream_t>(stream)));
+}
+
+int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void* q, int64_t q_stride,
+                         int num_q_heads, const void* k_new, const void* v_new, int64_t kv_stride,
+                         void* q_out, int64_t q_out_stride, const se_chunk* chunk, int batch,
+                         void* ws, size_t ws_bytes, se_stream_t stream) {
+    int rc = check_paged(kv, false);
+    if (rc) return rc;
+    if ((rc = check_rope(rope, kv->head_dim)) || (rc = check_chunk(chunk))) return rc;
+    if (batch < 0) return SE_ERR_INVALID_ARG;
+    if (kv->num_kv_heads > kMaxRopeHeads) return SE_ERR_UNSUPPORTED;
+    if (batch > 0 && chunk->max_tokens > 0 && (!k_new || !v_new)) return SE_ERR_INVALID_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16)) return SE_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)kv->num_kv_heads * kv->head_dim;
+    if (kv_stride == 0) kv_stride = row;
+    if (kv_stride < row || kv_stride % 8) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_small_workspace()))) return rc;
+    if (batch == 0 || chunk->max_tokens == 0) return SE_OK;
+    HeadArgs qa = {q, q_out, q_stride, q_out_stride, num_q_heads};
+    if ((rc = check_heads(qa, kv->head_dim))) return rc;
+    return cuda_status(launch_rope_append_chunk(*kv, *rope, qa, k_new, v_new, kv_stride, *chunk, batch,
+                                                static_cast<int*>(ws),
+                                                static_cast<cudaStream_t>(stream)));
+}
+
+size_t se_draft_verify_workspace(int batch, int vocab) {
+    if (batch < 0 || batch > draft_verify_max_batch() || vocab < 1 || vocab > kMaxVocab) return 0;
+    return draft_verify_ws_bytes(batch, vocab);
+}
+
+int se_draft_verify(const void* probs, const void* draft_probs, int64_t row_stride, int prob_dtype,
+                    int vocab, const int32_t* tokens, const float* accept_u, const float* sample_u,
+                    const se_chunk* chunk, int batch, int32_t* n_accepted, int32_t* next_token,
+                    int32_t* keep, void* ws, size_t ws_bytes, se_stream_t stream) {
+    int rc;
+    if (!chunk || !chunk->start || chunk->max_tokens < 0) return SE_ERR_INVALID_ARG;
+    if (chunk->max_tokens > kMaxChunkTokens) return SE_ERR_UNSUPPORTED;
+    if (batch < 0 || vocab < 1 || (prob_dtype != 0 && prob_dtype != 1)) return SE_ERR_INVALID_ARG;
+    if (batch > draft_verify_max_batch() || vocab > kMaxVocab) return SE_ERR_UNSUPPORTED;
+    if (row_stride == 0) row_stride = vocab;
+    if (row_stride < vocab) return SE_ERR_INVALID_ARG;
+    if (batch == 0) return SE_OK;
+    if (!sample_u || !n_accepted || !next_token || !keep) return SE_ERR_INVALID_ARG;
+    if (chunk->max_tokens > 0 && (!probs || !tokens || !accept_u || !chunk->pos))
+        return SE_ERR_INVALID_ARG;
+    if (!aligned(probs, 16) || !aligned(draft_probs, 16)) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_draft_verify_workspace(batch, vocab)))) return rc;
+    return cuda_status(launch_draft_verify(probs, draft_probs, row_stride, prob_dtype, vocab, tokens,
+                                           accept_u, sample_u, *chunk, batch, n_accepted, next_token,
+                                           keep, static_cast<int*>(ws),
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+size_t se_pages_truncate_workspace(int batch, int num_pages) {
+    if (batch < 0 || batch > page_share_max_batch() || num_pages <= 0 ||
+        num_pages > INT32_MAX / SE_PAGE_SIZE)
+        return 0;
+    return pages_truncate_ws_bytes(num_pages);
+}
+
+int se_pages_fork(const se_page_pool* pool, int32_t* page_refs, const int32_t* src, int batch,
+                  const se_page_carry* carry, void* ws, size_t ws_bytes, se_stream_t stream) {
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if (batch < 0) return SE_ERR_INVALID_ARG;
+    if (batch > page_share_max_batch()) return SE_ERR_UNSUPPORTED;
+    if (!page_refs || !carry || !carry->from_seq || !carry->from_page) return SE_ERR_INVALID_ARG;
+    if (batch > 0 && !src) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_page_pool_workspace(batch)))) return rc;
+    if (batch == 0) return SE_OK;
+    return cuda_status(launch_pages_fork(*pool, page_refs, src, batch, *carry, static_cast<int*>(ws),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int se_pages_truncate(const se_page_pool* pool, int32_t* page_refs, const int32_t* keep, int batch,
+                      const se_page_carry* carry, void* ws, size_t ws_bytes, se_stream_t stream) {
+    int rc = check_pool(pool);
+    if (rc) return rc;
+    if (batch < 0) return SE_ERR_INVALID_ARG;
+    if (batch > page_share_max_batch()) return SE_ERR_UNSUPPORTED;
+    if (!carry || !carry->from_seq || !carry->from_page) return SE_ERR_INVALID_ARG;
+    if (batch > 0 && !keep) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_pages_truncate_workspace(batch, pool->num_pages)))) return rc;
+    if (batch == 0) return SE_OK;
+    return cuda_status(launch_pages_truncate(*pool, page_refs, keep, batch, *carry,
+                                             static_cast<int*>(ws),
+                                             static_cast<cudaStream_t>(stream)));
+}
+
+int se_pages_carry(const se_paged_kv* kv, const se_page_carry* carry, int batch, void* ws,
+                   size_t ws_bytes, se_stream_t stream) {
+    int rc = check_paged(kv, false);
+    if (rc) return rc;
+    if (batch < 0) return SE_ERR_INVALID_ARG;
+    if (batch > page_share_max_batch() || kv->max_pages_per_seq > kMaxChunkPages)
+        return SE_ERR_UNSUPPORTED;
+    if (!carry || !carry->from_seq || !carry->from_page) return SE_ERR_INVALID_ARG;
+    if ((rc = check_ws(ws, ws_bytes, se_small_workspace()))) return rc;
+    if (batch == 0) return SE_OK;
+    return cuda_status(launch_pages_carry(*kv, *carry, batch, static_cast<int*>(ws),
+                                          static_cast<cudaStream_t>(stream)));
 }
 
 int se_quest_select(const se_paged_kv* kv, const void* q, int batch, int num_q_heads,

@@ -1,0 +1,519 @@
+// Sequences that share pages: forks (se_pages_fork), lengths cut back with the pages that nobody
+// holds any more going back on the stack (se_pages_truncate), and what each layer's cache takes
+// over (se_pages_carry).  Pages of 16 tokens with a token->page table follow the paged KV
+// layout of "长程 agent 把显存撑爆以后", section "四、为什么进不了 vLLM 一类的引擎".
+//
+// One rule keeps every append away from shared pages: a sequence's last, partly filled page is its
+// own.  Full pages may be shared (page_refs counts the holders beside the first); a fork takes a
+// page for the part that is not full, and so does a cut that ends inside a shared page.
+#include <math_constants.h>
+
+#include <algorithm>
+
+#include "append.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "page_tables.cuh"
+
+namespace se {
+namespace {
+
+constexpr int kMaxBatch = 8192;              // first entry and state of every sequence in shared memory
+constexpr int kWhoWord = 128;                // workspace words of the pages (se_pages_truncate), zero between calls
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// A word of another block's shared memory, of the same variable as `p` here.
+__device__ __forceinline__ int cluster_peek(const int* p, uint32_t rank) {
+    uint32_t a;
+    int v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ int clamped_free(const se_page_pool& pool, int& flags) {
+    const int n = *pool.n_free;
+    if (n >= 0 && n <= pool.num_pages) return n;
+    flags |= SE_DEV_BAD_LENGTH;
+    return n < 0 ? 0 : pool.num_pages;
+}
+__device__ __forceinline__ bool in_pool(const se_page_pool& pool, int page) {
+    return page >= 0 && page < pool.num_pages;
+}
+// Whether ctx tokens in `held` pages make sense.
+__device__ __forceinline__ bool consistent(const se_page_pool& pool, int ctx, int held) {
+    return ctx >= 0 && held >= 0 && held <= pool.max_pages_per_seq &&
+           ctx <= (long long)pool.max_pages_per_seq * kPage && held >= (ctx + kPage - 1) / kPage;
+}
+// The sequence whose entries (numbered over all sequences, first[] its running sum) hold entry i.
+__device__ __forceinline__ int owner_of(const int* first, int batch, int i) {
+    int lo = 0, hi = batch - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// ---- fork ---------------------------------------------------------------------------------
+struct Fork {
+    int src, ctx, flags;
+    bool want, page;             // to be forked; needs a page of its own
+};
+__device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* src, int batch, int b) {
+    Fork f = {src[b], 0, 0, false, false};
+    if (f.src < 0) return f;
+    if (f.src >= batch || src[f.src] >= 0) {
+        f.flags = SE_DEV_BAD_INDEX;
+        return f;
+    }
+    f.ctx = p.ctx_len[f.src];
+    if (p.n_pages[b] != 0 || !consistent(p, f.ctx, p.n_pages[f.src])) {
+        f.flags = SE_DEV_BAD_LENGTH;
+        return f;
+    }
+    f.want = true;
+    f.page = f.ctx % kPage != 0;
+    return f;
+}
+
+// Every block scans all sequences (a thread a run of them) and writes its share of the table entries;
+// the last block to finish, which has read what the others have, commits counts and lengths.
+// Latency bound but for many long forks (a table entry and an atomic count for each page).
+__global__ void __launch_bounds__(1024, 1)
+    pages_fork_kernel(se_page_pool pool, int32_t* refs, const int32_t* src, int batch,
+                      se_page_carry carry, int* ws) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) int smem[];
+    int* s_first = smem;                     // [batch] first of the sequence's entries
+    int* s_fresh = smem + batch;             // [batch] its own page; -1: needs none; -2: not served
+    __shared__ long long tmp[66];
+    int flags = 0;
+    const int n_free = clamped_free(pool, flags);
+    const int per = (batch + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, batch), b1 = min(b0 + per, batch);
+    long long asked = 0, asks = 0, entries = 0, all = 0;
+    for (int b = b0; b < b1; ++b) asked += fork_of(pool, src, batch, b).page;
+    {
+        long long none = 0, nones;
+        block_scan2(asked, none, tmp, &asks, &nones);
+    }
+    long long run = asked;
+    for (int b = b0; b < b1; ++b) {
+        const Fork f = fork_of(pool, src, batch, b);
+        flags |= f.flags;
+        int fresh = f.want ? -1 : -2;
+        if (f.page) {
+            ++run;
+            const int64_t last = (int64_t)f.src * pool.max_pages_per_seq + f.ctx / kPage;
+            if (run > n_free) {
+                flags |= SE_DEV_CAPACITY;
+                fresh = -2;
+            } else {
+                fresh = pool.free_pages[n_free - run];
+                if (!in_pool(pool, fresh) || !in_pool(pool, pool.block_table[last])) {
+                    flags |= SE_DEV_BAD_INDEX;
+                    fresh = -2;
+                }
+            }
+        }
+        s_fresh[b] = fresh;
+        s_first[b] = fresh == -2 ? 0 : f.ctx / kPage;
+        entries += s_first[b];
+    }
+    {
+        long long none = 0, nones;
+        block_scan2(entries, none, tmp, &all, &nones);
+    }
+    for (int b = b0; b < b1; ++b) {
+        const int n = s_first[b];
+        s_first[b] = static_cast<int>(min(entries, 0x7fffffffll));
+        entries += n;
+    }
+    __syncthreads();
+    // table entries; more than 2^31 of them do not fit a table of a pool's pages
+    const int total = static_cast<int>(min(all, 0x7fffffffll));
+    for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
+         i += (long long)gridDim.x * blockDim.x) {
+        const int b = owner_of(s_first, batch, static_cast<int>(i));
+        const int64_t p = i - s_first[b];
+        const int page = pool.block_table[(int64_t)src[b] * pool.max_pages_per_seq + p];
+        pool.block_table[(int64_t)b * pool.max_pages_per_seq + p] = page;
+        if (in_pool(pool, page))
+            atomicAdd(refs + page, 1);
+        else
+            flags |= SE_DEV_BAD_INDEX;
+    }
+    if (flags) flag(ws, flags);
+    if (gridDim.x > 1 && !last_block(ws + kCounterWord)) return;
+    __syncthreads();
+    // (each thread its own sequences: sources are no forks, so nothing read here is written)
+    for (int b = threadIdx.x; b < batch; b += blockDim.x) {
+        const int fresh = s_fresh[b];
+        int from_seq = -1, from_page = -1;
+        if (fresh != -2) {
+            from_seq = src[b];
+            const int ctx = pool.ctx_len[from_seq];
+            if (fresh >= 0) {
+                from_page = pool.block_table[(int64_t)from_seq * pool.max_pages_per_seq + ctx / kPage];
+                pool.block_table[(int64_t)b * pool.max_pages_per_seq + ctx / kPage] = fresh;
+            }
+            pool.ctx_len[b] = ctx;
+            pool.n_pages[b] = (ctx + kPage - 1) / kPage;
+        }
+        carry.from_seq[b] = from_seq;
+        carry.from_page[b] = from_page;
+    }
+    if (threadIdx.x == 0) {
+        *pool.n_free = n_free - static_cast<int>(min(asks, (long long)n_free));
+        ws[kCounterWord] = 0;
+    }
+}
+
+// ---- truncation ---------------------------------------------------------------------------
+struct Cut {
+    int n, ctx, held, after;     // tokens and pages it is cut to
+    int last, flags;             // the page that is then its last
+    bool act, copy;              // cut at all; needs a page of its own for the last one's rows
+};
+__device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs, const int32_t* keep,
+                                      int b) {
+    Cut c = {keep[b], 0, 0, 0, -1, 0, false, false};
+    if (c.n < 0) return c;
+    c.ctx = p.ctx_len[b];
+    c.held = p.n_pages[b];
+    if (!consistent(p, c.ctx, c.held)) {
+        c.flags = SE_DEV_BAD_LENGTH;
+        return c;
+    }
+    c.n = min(c.n, c.ctx);
+    c.after = (c.n + kPage - 1) / kPage;
+    if (c.n % kPage != 0) {
+        c.last = p.block_table[(int64_t)b * p.max_pages_per_seq + c.after - 1];
+        if (!in_pool(p, c.last)) {
+            c.flags = SE_DEV_BAD_INDEX;
+            return c;
+        }
+        c.copy = refs != nullptr && refs[c.last] > 0;
+    }
+    c.act = true;
+    return c;
+}
+
+// One cluster of blocks, whose hardware barrier divides the phases; every block scans all
+// sequences itself, then takes a contiguous part of the entries (a page that a sequence lets go,
+// in the order of sequence and logical page).
+//   count down  each entry takes one off its page's count and notes its sequence as the
+//               page's last, if it is that
+//   count       an entry is freed when its page's count fell below zero and it is the last:
+//               which entry that is depends on no timing
+//   push        freed entries to their place by a running sum, counts and notes back to zero
+//   commit      tables, lengths, the stack's top
+// Latency bound: a cut of a decode step lets go of a page here and there.
+__global__ void __launch_bounds__(1024, 1)
+    pages_truncate_kernel(se_page_pool pool, int32_t* refs, const int32_t* keep, int batch,
+                          se_page_carry carry, int* ws) {
+    pdl_wait();
+    pdl_trigger();
+    extern __shared__ __align__(16) int smem[];
+    int* s_first = smem;                     // [batch] first of the sequence's entries
+    int* s_base = smem + batch;              // [batch] logical page of its first entry
+    int* s_fresh = smem + 2 * batch;         // [batch] own page for the last rows; -1: none; -2: not cut
+    __shared__ long long tmp[66];
+    __shared__ int s_count, s_scan[33];
+    int* who = ws + kWhoWord;
+    const int rank = cluster_rank(), ranks = cluster_size(), nt = blockDim.x;
+    int flags = 0;
+    const int n_free = clamped_free(pool, flags);
+    const int per = (batch + nt - 1) / nt;
+    const int b0 = min(static_cast<int>(threadIdx.x) * per, batch), b1 = min(b0 + per, batch);
+    long long asked = 0, asks = 0, entries = 0, all = 0, none = 0, nones = 0;
+    for (int b = b0; b < b1; ++b) asked += cut_of(pool, refs, keep, b).copy;
+    block_scan2(asked, none, tmp, &asks, &nones);
+    for (int b = b0; b < b1; ++b) {
+        const Cut c = cut_of(pool, refs, keep, b);
+        flags |= c.flags;
+        int fresh = c.act ? -1 : -2;
+        if (c.copy) {
+            ++asked;
+            if (asked > n_free) {
+                flags |= SE_DEV_CAPACITY;
+                fresh = -2;
+            } else {
+                fresh = pool.free_pages[n_free - asked];
+                if (!in_pool(pool, fresh)) {
+                    flags |= SE_DEV_BAD_INDEX;
+                    fresh = -2;
+                }
+            }
+        }
+        s_fresh[b] = fresh;
+        s_base[b] = c.after - (fresh >= 0);
+        s_first[b] = fresh == -2 ? 0 : c.held - s_base[b];
+        entries += s_first[b];
+    }
+    none = 0;
+    block_scan2(entries, none, tmp, &all, &nones);
+    for (int b = b0; b < b1; ++b) {
+        const int n = s_first[b];
+        s_first[b] = static_cast<int>(min(entries, 0x7fffffffll));
+        entries += n;
+    }
+    const int taken = static_cast<int>(min(asks, (long long)n_free));
+    const int total = static_cast<int>(min(all, 0x7fffffffll));
+    // this block's entries [e0, e1)
+    const int e0 = static_cast<int>((long long)total * rank / ranks);
+    const int e1 = static_cast<int>((long long)total * (rank + 1) / ranks);
+    auto entry = [&](int i, int& b) {
+        b = owner_of(s_first, batch, i);
+        return pool.block_table[(int64_t)b * pool.max_pages_per_seq + s_base[b] + (i - s_first[b])];
+    };
+    auto freed = [&](int i, int& page) {
+        int b;
+        page = entry(i, b);
+        if (!in_pool(pool, page)) return false;
+        return refs == nullptr || (__ldcg(refs + page) < 0 && __ldcg(who + page) == b + 1);
+    };
+    cluster_sync();                                          // all counts are as before the call
+    if (refs != nullptr && total > 0) {
+        for (int i = e0 + threadIdx.x; i < e1; i += nt) {
+            int b;
+            const int page = entry(i, b);
+            if (!in_pool(pool, page)) continue;
+            atomicSub(refs + page, 1);
+            atomicMax(who + page, b + 1);
+        }
+        __threadfence();
+        cluster_sync();
+    }
+    int mine = 0;
+    for (int i = e0 + threadIdx.x; i < e1; i += nt) {
+        int page;
+        mine += freed(i, page);
+        if (!in_pool(pool, page)) flags |= SE_DEV_BAD_INDEX;
+    }
+    int count;
+    block_exclusive_scan(mine, s_scan, &count);
+    if (threadIdx.x == 0) s_count = count;
+    cluster_sync();
+    int before = 0, all_freed = 0;
+    for (int r = 0; r < ranks; ++r) {
+        const int n = cluster_peek(&s_count, r);
+        before += r < rank ? n : 0;
+        all_freed += n;
+    }
+    cluster_sync();                                          // every block has looked; none leaves early
+    const bool fits = (long long)n_free - taken + all_freed <= pool.num_pages;
+    if (!fits) flags |= SE_DEV_CAPACITY;
+    if (flags) flag(ws, flags);
+    // the stack's entries from here down
+    int top = n_free - taken + all_freed - 1 - before;
+    for (int i0 = e0; i0 < e1; i0 += nt) {
+        const int i = i0 + threadIdx.x;
+        int page = -1, tile;
+        const bool f = i < e1 && freed(i, page);
+        const int place = block_exclusive_scan(f, s_scan, &tile);
+        if (f && fits) pool.free_pages[top - place] = page;
+        top -= tile;
+        if (refs != nullptr && i < e1 && in_pool(pool, page)) {
+            if (!fits) {
+                atomicAdd(refs + page, 1);
+                who[page] = 0;
+            } else if (f) {
+                refs[page] = 0;
+                who[page] = 0;
+            } else if (__ldcg(who + page) == owner_of(s_first, batch, i) + 1) {
+                who[page] = 0;                               // still held by others
+            }
+        }
+    }
+    cluster_sync();                                          // the tables have been read
+    for (int b = rank * nt + threadIdx.x; fits && b < batch; b += ranks * nt) {
+        const int fresh = s_fresh[b];
+        int from_page = -1;
+        if (fresh != -2) {
+            const int n = min(keep[b], pool.ctx_len[b]), after = (n + kPage - 1) / kPage;
+            const int64_t last = (int64_t)b * pool.max_pages_per_seq + after - 1;
+            if (n % kPage != 0 && (n < pool.ctx_len[b] || fresh >= 0))
+                from_page = pool.block_table[last];
+            if (fresh >= 0) pool.block_table[last] = fresh;
+            pool.ctx_len[b] = n;
+            pool.n_pages[b] = after;
+        }
+        carry.from_seq[b] = -1;
+        carry.from_page[b] = from_page;
+    }
+    if (fits && rank == 0 && threadIdx.x == 0) *pool.n_free = n_free - taken + all_freed;
+}
+
+// ---- carry --------------------------------------------------------------------------------
+// Block (x, b) copies its share of sequence b's summaries; block (0, b) also the rows of its last page, a
+// warp for each KV head, whose summary it makes from them.  HBM bound when many summaries are
+// copied, else latency.
+template <int D>
+__global__ void __launch_bounds__(128)
+    pages_carry_kernel(se_paged_kv kv, se_page_carry carry, int batch, int* status) {
+    constexpr int SEGS = D / 8, RP = 32 / SEGS, IT = kPage / RP, U = 8;
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.y, H = kv.num_kv_heads;
+    const int from_seq = carry.from_seq[b], from_page = carry.from_page[b];
+    if (from_seq < 0 && from_page < 0) return;
+    const int n = kv.ctx_len[b], lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (n < 0 || n > (long long)kv.max_pages_per_seq * kPage) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) flag(status, SE_DEV_BAD_LENGTH);
+        return;
+    }
+    uint4* M = static_cast<uint4*>(kv.meta);
+    const int64_t page_vecs = (int64_t)H * 2 * SEGS, seq_vecs = kv.max_pages_per_seq * page_vecs;
+    if (M != nullptr && from_seq >= 0 && from_seq != b) {
+        if (from_seq >= batch) {
+            if (blockIdx.x == 0 && threadIdx.x == 0) flag(status, SE_DEV_BAD_INDEX);
+        } else {
+            const uint4* src = M + from_seq * seq_vecs;
+            uint4* dst = M + b * seq_vecs;
+            const int64_t vecs = (n / kPage) * page_vecs, step = (int64_t)gridDim.x * blockDim.x;
+            for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += U * step) {
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u * step < vecs) x[u] = src[i + u * step];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i + u * step < vecs) dst[i + u * step] = x[u];
+            }
+        }
+    }
+    const int rows = n % kPage;
+    if (blockIdx.x != 0 || from_page < 0 || rows == 0) return;
+    const int to = kv.block_table[(int64_t)b * kv.max_pages_per_seq + n / kPage];
+    if (from_page >= kv.num_pages || to < 0 || to >= kv.num_pages) {
+        if (threadIdx.x == 0) flag(status, SE_DEV_BAD_INDEX);
+        return;
+    }
+    const bool move = from_page != to;
+    uint4* K = static_cast<uint4*>(kv.k);
+    uint4* V = static_cast<uint4*>(kv.v);
+    const int seg = lane % SEGS, rp = lane / SEGS;
+    for (int h = warp; h < H; h += blockDim.x >> 5) {
+        const int64_t from = ((int64_t)from_page * H + h) * kPage * SEGS + seg;
+        const int64_t at = ((int64_t)to * H + h) * kPage * SEGS + seg;
+        uint4 k[IT], v[IT];
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = i * RP + rp;
+            if (r < rows) {
+                k[i] = K[from + r * SEGS];
+                if (move) v[i] = V[from + r * SEGS];
+            }
+        }
+        Bf8 mn, mx;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)              // none yet: min and max pass a NaN over
+            mn.x[e] = mx.x[e] = CUDART_NAN_F;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = i * RP + rp;
+            if (r < rows) {
+                if (move) {
+                    K[at + r * SEGS] = k[i];
+                    V[at + r * SEGS] = v[i];
+                }
+                const Bf8 x = unpack8(k[i]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    mn.x[e] = fminf(mn.x[e], x.x[e]);
+                    mx.x[e] = fmaxf(mx.x[e], x.x[e]);
+                }
+            }
+        }
+        if (M == nullptr) continue;
+#pragma unroll
+        for (int o = SEGS; o < 32; o <<= 1)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                mn.x[e] = fminf(mn.x[e], __shfl_xor_sync(0xffffffffu, mn.x[e], o));
+                mx.x[e] = fmaxf(mx.x[e], __shfl_xor_sync(0xffffffffu, mx.x[e], o));
+            }
+        if (rp == 0) {
+            const int64_t m0 = b * seq_vecs + (n / kPage) * page_vecs + (int64_t)h * 2 * SEGS + seg;
+            M[m0] = pack8(mn);
+            M[m0 + SEGS] = pack8(mx);
+        }
+    }
+}
+
+int table_threads(int batch) { return batch > 512 ? 1024 : batch > 256 ? 512 : 256; }
+
+std::atomic<uint64_t> g_fork_smem, g_truncate_smem;
+
+}  // namespace
+
+int page_share_max_batch() { return kMaxBatch; }
+
+size_t pages_truncate_ws_bytes(int num_pages) {
+    return (kWhoWord * sizeof(int) + (size_t)num_pages * sizeof(int) + 255) & ~(size_t)255;
+}
+
+cudaError_t launch_pages_fork(const se_page_pool& pool, int32_t* refs, const int32_t* src, int batch,
+                              const se_page_carry& carry, int* ws, cudaStream_t s) {
+    const int nt = table_threads(batch);
+    const cudaError_t e = allow_smem(pages_fork_kernel, 2 * kMaxBatch * sizeof(int), g_fork_smem);
+    if (e != cudaSuccess) return e;
+    // a block for every 4096 table entries that could be written
+    const int grid = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>(num_sms(), (int64_t)batch * pool.max_pages_per_seq / 4096)));
+    return launch_pdl(pages_fork_kernel, dim3(grid), dim3(nt), 2 * batch * sizeof(int), s, pool, refs,
+                      src, batch, carry, ws);
+}
+
+cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const int32_t* keep,
+                                  int batch, const se_page_carry& carry, int* ws, cudaStream_t s) {
+    const cudaError_t e = allow_smem(pages_truncate_kernel, 3 * kMaxBatch * sizeof(int), g_truncate_smem);
+    if (e != cudaSuccess) return e;
+    // one block for few table entries, else eight
+    const int64_t most = std::min<int64_t>((int64_t)batch * pool.max_pages_per_seq, pool.num_pages);
+    const unsigned ranks = most > 8192 ? 8 : 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(ranks > 1 ? 1024 : table_threads(batch));
+    cfg.dynamicSmemBytes = 3 * batch * sizeof(int);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, pages_truncate_kernel, pool, refs, keep, batch, carry, ws);
+}
+
+cudaError_t launch_pages_carry(const se_paged_kv& kv, const se_page_carry& carry, int batch, int* status,
+                               cudaStream_t s) {
+    // a block moves 16 KB of summaries at once; as many a sequence as fill the GPU
+    const int64_t vecs = (int64_t)kv.max_pages_per_seq * kv.num_kv_heads * kv.head_dim / 4;
+    const int split = static_cast<int>(std::max<int64_t>(
+        1, std::min<int64_t>((vecs + 1023) / 1024, 16 * num_sms() / batch)));
+    const dim3 grid(kv.meta != nullptr ? split : 1, batch);
+    if (kv.head_dim == 128)
+        return launch_pdl(pages_carry_kernel<128>, grid, dim3(128), 0, s, kv, carry, batch, status);
+    return launch_pdl(pages_carry_kernel<64>, grid, dim3(128), 0, s, kv, carry, batch, status);
+}
+
+}  // namespace se

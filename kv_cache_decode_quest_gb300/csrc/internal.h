@@ -96,6 +96,38 @@ cudaError_t launch_chunk_attn(const se_paged_kv& kv, const se_chunk& ck, int bat
                               const ChunkAttnArgs& a, void* ws, cudaEvent_t ev_begin,
                               cudaEvent_t ev_end, cudaStream_t s);
 
+// ---- rope.cu ----
+struct HeadArgs {
+    const void* in;
+    void* out;
+    int64_t in_stride, out_stride;   // elements between tokens
+    int heads;
+};
+cudaError_t launch_qk_rope(const se_rope& rope, const int32_t* pos, int rows, int head_dim,
+                           const HeadArgs& q, const HeadArgs& k, cudaStream_t s);
+cudaError_t launch_rope_append_chunk(const se_paged_kv& kv, const se_rope& rope, const HeadArgs& q,
+                                     const void* k_new, const void* v_new, int64_t row_stride,
+                                     const se_chunk& ck, int batch, int* status, cudaStream_t s);
+
+// ---- verify.cu ----
+int draft_verify_max_batch();
+size_t draft_verify_ws_bytes(int batch, int vocab);
+cudaError_t launch_draft_verify(const void* probs, const void* draft, int64_t row_stride,
+                                int prob_dtype, int vocab, const int32_t* tokens,
+                                const float* accept_u, const float* sample_u, const se_chunk& ck,
+                                int batch, int32_t* n_accepted, int32_t* next_token, int32_t* keep,
+                                int* ws, cudaStream_t s);
+
+// ---- forks.cu ----
+int page_share_max_batch();
+size_t pages_truncate_ws_bytes(int num_pages);
+cudaError_t launch_pages_fork(const se_page_pool& pool, int32_t* refs, const int32_t* src, int batch,
+                              const se_page_carry& carry, int* ws, cudaStream_t s);
+cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const int32_t* keep,
+                                  int batch, const se_page_carry& carry, int* ws, cudaStream_t s);
+cudaError_t launch_pages_carry(const se_paged_kv& kv, const se_page_carry& carry, int batch, int* status,
+                               cudaStream_t s);
+
 // ---- quest.cu ----
 size_t quest_ws_bytes(int units, int max_pages);
 // k_new / v_new non-null: the decode-step append of the new token is fused in

@@ -1,0 +1,329 @@
+// Drafted tokens against the target's probabilities (se_draft_verify): which of them stay, and the token
+// that is drawn behind them.  Draft d with u q(d) < p(d) stays; behind the first refused one the next
+// token comes from max(0, p - q), which leaves every token distributed as p.
+//
+// One row of the vocabulary per sequence is read (two where a draft was refused): HBM bound, a sum and a
+// search.  The weights are integers in units of 2^-60, so sums are exact in any order: the row is cut
+// into tiles of 1024 that any warp of any block may sum, and the last block of a sequence finds
+// the tile and in it the token.  (Sums in fp32 would move a draw over a border in about one of 30
+// draws over 128K tokens; sums in fp64 are as good as these but 30 times slower on this chip.)
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "page_tables.cuh"
+
+namespace se {
+namespace {
+
+constexpr int kTile = 1024;                  // weights of a tile
+constexpr int kMaxBatch = 8192;
+constexpr size_t kSumsAt = 256 + kMaxBatch * sizeof(int);   // counters of the sequences before it
+constexpr float kBelowOne = 0x1.fffffep-1f;
+
+using u64 = unsigned long long;
+
+// x in [0, 1] in units of 2^-60, rounded down (NaN and negative values: 0).
+__device__ __forceinline__ u64 units(float x) {
+    return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p60f);
+}
+__device__ __forceinline__ u64 weight(float p, float q) {
+    const u64 a = units(p), b = units(q);
+    return a > b ? a - b : 0;
+}
+
+template <typename T>
+__device__ __forceinline__ float value(const T* p);
+template <>
+__device__ __forceinline__ float value<float>(const float* p) { return *p; }
+template <>
+__device__ __forceinline__ float value<uint16_t>(const uint16_t* p) {
+    return __uint_as_float(static_cast<uint32_t>(*p) << 16);
+}
+template <typename T>
+__device__ __forceinline__ void widen(uint4 w, float* x) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+    if (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __uint_as_float(a[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = bf_lo(a[i]);
+            x[2 * i + 1] = bf_hi(a[i]);
+        }
+    }
+}
+
+// A row of the vocabulary: of p, of q (NULL: none is taken off), and the token without weight (-1: none).
+template <typename T>
+struct Row {
+    const T* p;
+    const T* q;
+    int vocab, without;
+    int lead;                    // elements between the 16-byte boundary below p and p
+};
+
+// The weights of vector c (16 bytes, on the boundaries) of the row; places outside it get 0.
+template <typename T>
+__device__ __forceinline__ void load_vector(const Row<T>& r, int c, uint4& p, uint4& q) {
+    constexpr int N = 16 / sizeof(T);
+    const int v0 = c * N - r.lead;
+    p = q = make_uint4(0, 0, 0, 0);
+    if (v0 >= 0 && v0 + N <= r.vocab) {
+        p = __ldcs(reinterpret_cast<const uint4*>(r.p + v0));
+        if (r.q != nullptr) q = __ldcs(reinterpret_cast<const uint4*>(r.q + v0));
+    } else {
+        uint32_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (v0 + e >= 0 && v0 + e < r.vocab) {
+                const float x = value<T>(r.p + v0 + e), y = r.q ? value<T>(r.q + v0 + e) : 0.f;
+                if (sizeof(T) == 4) {
+                    a[e & 3] = __float_as_uint(x);
+                    b[e & 3] = __float_as_uint(y);
+                } else {
+                    a[e / 2] |= (__float_as_uint(x) >> 16) << (16 * (e & 1));
+                    b[e / 2] |= (__float_as_uint(y) >> 16) << (16 * (e & 1));
+                }
+            }
+        p = make_uint4(a[0], a[1], a[2], a[3]);
+        q = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void vector_weights(const Row<T>& r, int c, uint4 p, uint4 q, u64* w) {
+    constexpr int N = 16 / sizeof(T);
+    float x[N], y[N];
+    widen<T>(p, x);
+    widen<T>(q, y);
+#pragma unroll
+    for (int e = 0; e < N; ++e) w[e] = r.q != nullptr ? weight(x[e], y[e]) : units(x[e]);
+    const int at = r.without + r.lead - c * N;
+    if (r.without >= 0 && at >= 0 && at < N) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e == at) w[e] = 0;
+    }
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// The sum of tile k of the row, in every lane.
+template <typename T>
+__device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
+    constexpr int N = 16 / sizeof(T), C = kTile / N / 32;
+    uint4 p[C], q[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) load_vector(r, k * (kTile / N) + i * 32 + lane, p[i], q[i]);
+    u64 sum = 0;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        u64 w[N];
+        vector_weights(r, k * (kTile / N) + i * 32 + lane, p[i], q[i], w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum += w[e];
+    }
+    return warp_sum(sum);
+}
+
+// Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads call it.
+__device__ __forceinline__ u64 block_sum_before(u64 x, long long* tmp, u64* total) {
+    long long a = static_cast<long long>(x), none = 0, ta, tb;
+    block_scan2(a, none, tmp, &ta, &tb);
+    *total = static_cast<u64>(ta);
+    return static_cast<u64>(a);
+}
+
+// floor(u * total) for u in [0, 1): u is a whole number m < 2^24 times 2^-s.
+__device__ __forceinline__ u64 part_of(float u, u64 total) {
+    u = fminf(fmaxf(u, 0.f), kBelowOne);
+    const uint32_t bits = __float_as_uint(u);
+    const int e = bits >> 23;
+    const u64 m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
+    const int s = e ? 150 - e : 149;                      // at least 24
+    const u64 lo = m * total, hi = __umul64hi(m, total);
+    return s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? hi >> (s - 64) : 0;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    draft_verify_kernel(const T* probs, const T* draft, int64_t row_stride, int vocab, int tiles,
+                        const int32_t* tokens, const float* accept_u, const float* sample_u,
+                        const int32_t* start, const int32_t* pos, int max_tokens,
+                        int32_t* n_accepted, int32_t* next_token, int32_t* keep, int* ws) {
+    constexpr int N = 16 / sizeof(T);
+    __shared__ int s_stay, s_bad, s_last, s_tile;
+    __shared__ u64 s_rest;
+    __shared__ long long tmp[66];
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int r0 = start[b], r1 = start[b + 1];
+    const bool bad = r0 < 0 || r1 < r0 || r1 > max_tokens;
+    const int first_pos = !bad && r0 < r1 ? pos[r0] : -1;
+    if (first_pos < 0) {                                     // the same in every block of the sequence
+        if (blockIdx.x == 0 && threadIdx.x == 0) {
+            if (bad) flag(ws, SE_DEV_BAD_LENGTH);
+            n_accepted[b] = 0;
+            next_token[b] = keep[b] = -1;
+        }
+        return;
+    }
+    // which drafts stay: every block finds out for itself
+    const int drafts = r1 - r0 - 1;
+    if (warp == 0) {
+        int stay = drafts, bad_token = 0;
+        for (int i0 = 0; i0 < drafts; i0 += 32) {
+            const int t = r0 + i0 + lane;
+            bool out = false;
+            if (i0 + lane < drafts) {
+                const int d = tokens[t + 1];
+                out = true;
+                if (d >= 0 && d < vocab) {
+                    const double u = fminf(fmaxf(accept_u[t + 1], 0.f), kBelowOne);
+                    const double p = value<T>(probs + t * row_stride + d);
+                    const double q = draft ? value<T>(draft + t * row_stride + d) : 1.0;
+                    out = !(u * q < p);
+                }
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, out);
+            if (m != 0) {
+                stay = i0 + __ffs(m) - 1;
+                break;
+            }
+        }
+        if (lane == 0) {
+            if (stay < drafts) {
+                const int d = tokens[r0 + stay + 1];
+                bad_token = d < 0 || d >= vocab;
+            }
+            s_stay = stay;
+            s_bad = bad_token;
+        }
+    }
+    __syncthreads();
+    const int stay = s_stay;
+    const int64_t at = (r0 + stay) * row_stride;
+    Row<T> row;
+    row.p = probs + at;
+    row.q = stay < drafts && draft != nullptr ? draft + at : nullptr;
+    row.vocab = vocab;
+    row.without = stay < drafts && draft == nullptr && !s_bad ? tokens[r0 + stay + 1] : -1;
+    row.lead = static_cast<int>(reinterpret_cast<uintptr_t>(row.p) % 16 / sizeof(T));
+    u64* sums = reinterpret_cast<u64*>(reinterpret_cast<char*>(ws) + kSumsAt) + (int64_t)b * tiles;
+    const int nw = blockDim.x >> 5;
+    for (int k = blockIdx.x * nw + warp; k < tiles; k += gridDim.x * nw) {
+        const u64 sum = tile_sum(row, k, lane);
+        if (lane == 0) sums[k] = sum;
+    }
+    // the sequence's last block goes on
+    int* arrived = ws + 64 + b;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    u64 total = 0;
+    for (int round = 0; round < 2; ++round) {
+        total = 0;
+        for (int k0 = 0; k0 < tiles; k0 += blockDim.x) {
+            const int k = k0 + threadIdx.x;
+            u64 part;
+            block_sum_before(k < tiles ? __ldcg(sums + k) : 0, tmp, &part);
+            total += part;
+        }
+        if (total > 0 || (row.q == nullptr && row.without < 0)) break;
+        // nothing is left of p beside q: drawn from p
+        row.q = nullptr;
+        row.without = -1;
+        for (int k = warp; k < tiles; k += nw) {
+            const u64 sum = tile_sum(row, k, lane);
+            if (lane == 0) __stcg(sums + k, sum);
+        }
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        *arrived = 0;
+        if (s_bad) flag(ws, SE_DEV_BAD_INDEX);
+        if (total == 0) flag(ws, SE_DEV_BAD_VALUE);
+        n_accepted[b] = stay;
+        keep[b] = first_pos + 1 + stay;
+        next_token[b] = total == 0 ? -1 : vocab - 1;
+        s_tile = tiles;
+    }
+    __syncthreads();
+    if (total == 0) return;
+    const u64 want = part_of(sample_u[b], total);             // the first token whose sum passes it
+    u64 before = 0;
+    for (int k0 = 0; k0 < tiles && s_tile == tiles; k0 += blockDim.x) {
+        const int k = k0 + threadIdx.x;
+        const u64 w = k < tiles ? __ldcg(sums + k) : 0;
+        u64 part;
+        const u64 ahead = before + block_sum_before(w, tmp, &part);
+        if (w > 0 && ahead <= want && want < ahead + w) {
+            s_tile = k;
+            s_rest = want - ahead;
+        }
+        before += part;
+        __syncthreads();
+    }
+    if (s_tile == tiles) return;
+    // in the tile: a vector a thread
+    u64 w[N], sum = 0;
+    const int c = s_tile * (kTile / N) + threadIdx.x;
+    if (threadIdx.x < kTile / N) {
+        uint4 p, q;
+        load_vector(row, c, p, q);
+        vector_weights(row, c, p, q, w);
+#pragma unroll
+        for (int e = 0; e < N; ++e) sum += w[e];
+    }
+    u64 part;
+    u64 ahead = block_sum_before(sum, tmp, &part);
+    if (sum > 0 && ahead <= s_rest && s_rest < ahead + sum) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            if (ahead <= s_rest && s_rest < ahead + w[e]) next_token[b] = c * N - row.lead + e;
+            ahead += w[e];
+        }
+    }
+}
+
+}  // namespace
+
+int draft_verify_max_batch() { return kMaxBatch; }
+
+static int verify_tiles(int vocab) { return (vocab + 7 + kTile - 1) / kTile; }   // rows may begin off a boundary
+
+size_t draft_verify_ws_bytes(int batch, int vocab) {
+    return (kSumsAt + (size_t)batch * verify_tiles(vocab) * sizeof(u64) + 255) & ~(size_t)255;
+}
+
+cudaError_t launch_draft_verify(const void* probs, const void* draft, int64_t row_stride,
+                                int prob_dtype, int vocab, const int32_t* tokens,
+                                const float* accept_u, const float* sample_u, const se_chunk& ck,
+                                int batch, int32_t* n_accepted, int32_t* next_token, int32_t* keep,
+                                int* ws, cudaStream_t s) {
+    const int tiles = verify_tiles(vocab);
+    // a block's eight warps have a tile each at least; up to eight blocks an SM
+    const int split = std::max(1, std::min((tiles + 7) / 8, 8 * num_sms() / batch));
+    const dim3 grid(split, batch);
+    if (prob_dtype == 1)
+        return launch_pdl(draft_verify_kernel<float>, grid, dim3(256), 0, s,
+                          static_cast<const float*>(probs), static_cast<const float*>(draft),
+                          row_stride, vocab, tiles, tokens, accept_u, sample_u,
+                          (const int32_t*)ck.start, (const int32_t*)ck.pos, ck.max_tokens, n_accepted,
+                          next_token, keep, ws);
+    return launch_pdl(draft_verify_kernel<uint16_t>, grid, dim3(256), 0, s,
+                      static_cast<const uint16_t*>(probs), static_cast<const uint16_t*>(draft),
+                      row_stride, vocab, tiles, tokens, accept_u, sample_u, (const int32_t*)ck.start,
+                      (const int32_t*)ck.pos, ck.max_tokens, n_accepted, next_token, keep, ws);
+}
+
+}  // namespace se

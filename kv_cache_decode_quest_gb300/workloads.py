@@ -283,6 +283,75 @@ class PromptRun:
         return st
 
 
+class DraftRun:
+    """Layers over one page pool whose sequences decode with drafted tokens, fork and are cut back.
+
+    feed(): the next rows of every sequence (a prompt's, or its last token and the drafts behind
+    it) get pages and positions (se_chunk_plan), and in each layer are rotated, appended
+    (se_rope_append_chunk) and attended (se_chunk_attn).  check(): the target's probabilities decide which
+    drafts stay (se_draft_verify); the others are taken back in every layer (se_pages_truncate,
+    se_pages_carry).  fork() and cut(): sequences copied, and cut to a length."""
+
+    def __init__(self, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, num_pages: int,
+                 max_pages: int, max_rows: int, vocab: int, ropes: list, device="cuda",
+                 out_dtype: int = 0):
+        B, Hq, H, D = batch, num_q_heads, num_kv_heads, head_dim
+        self.B, self.Hq, self.H, self.D, self.ropes, self.out_dtype = B, Hq, H, D, ropes, out_dtype
+        self.scale = 1.0 / math.sqrt(D)
+        self.pool = se.PagePool.empty(B, num_pages, max_pages, device)
+        self.refs = torch.zeros(num_pages, dtype=torch.int32, device=device)
+        self.carry = se.Carry.empty(B, device)
+        self.chunk = se.Chunk.empty(B, max_rows, device)
+
+        def zeros(*shape, dtype=torch.bfloat16):
+            return torch.zeros(*shape, dtype=dtype, device=device)
+        self.kv = [se.PagedKV(zeros(num_pages, H, PAGE, D), zeros(num_pages, H, PAGE, D),
+                              zeros(B, max_pages, H, 2, D), self.pool.block_table, self.pool.ctx_len)
+                   for _ in ropes]
+        self.q = zeros(max_rows, Hq, D)
+        odt = torch.float32 if out_dtype else torch.bfloat16
+        self.out = [zeros(max_rows, Hq, D, dtype=odt) for _ in ropes]
+        self.lse = zeros(max_rows, Hq, dtype=torch.float32)
+        self.n_accepted, self.next_token, self.keep = (zeros(B, dtype=torch.int32) for _ in range(3))
+        self.ws_pool = se.workspace(se.se_pages_truncate_workspace(B, num_pages), device)
+        self.ws_small = se.workspace(se.se_small_workspace(), device)
+        self.ws_attn = se.workspace(se.se_chunk_attn_workspace(B, max_rows, H, Hq, D), device)
+        self.ws_verify = se.workspace(se.se_draft_verify_workspace(B, vocab), device)
+
+    def feed(self, qkv: list, new_len):
+        """qkv: each layer's packed rows [max_rows][Hq + 2 Hkv][D]; outputs in self.out."""
+        Hq, H = self.Hq, self.H
+        se.se_chunk_plan(self.pool, new_len, self.B, self.chunk, self.ws_pool)
+        for layer, (kv, rope, x) in enumerate(zip(self.kv, self.ropes, qkv)):
+            se.se_rope_append_chunk(kv, rope, x[:, :Hq], x[:, Hq:Hq + H], x[:, Hq + H:], self.q,
+                                    self.chunk, self.B, self.ws_small)
+            se.se_chunk_attn(kv, self.q, self.chunk, self.B, Hq, self.scale, self.out[layer], self.lse,
+                             self.ws_attn, out_dtype=self.out_dtype)
+
+    def check(self, probs, draft_probs, tokens, accept_u, sample_u):
+        se.se_draft_verify(probs, draft_probs, tokens, accept_u, sample_u, self.chunk, self.B,
+                           self.n_accepted, self.next_token, self.keep, self.ws_verify)
+        self.cut(self.keep)
+
+    def cut(self, keep):
+        se.se_pages_truncate(self.pool, self.refs, keep, self.B, self.carry, self.ws_pool)
+        self._follow()
+
+    def fork(self, src):
+        se.se_pages_fork(self.pool, self.refs, src, self.B, self.carry, self.ws_pool)
+        self._follow()
+
+    def _follow(self):
+        for kv in self.kv:
+            se.se_pages_carry(kv, self.carry, self.B, self.ws_small)
+
+    def status(self) -> int:
+        st = 0
+        for ws in (self.ws_pool, self.ws_small, self.ws_attn, self.ws_verify):
+            st |= se.status_word(ws)
+        return st
+
+
 class OmniRun:
     """Cross-layer selection reuse over `layers` attention layers of one model:
     every layer keeps its own paged K/V (one block table for all), the filter

@@ -40,3 +40,5 @@ from .h2o import H2OState, h2o_init, h2o_step  # noqa: F401
 from .omnikv import omnikv_layers, source_layer, filter_pages  # noqa: F401
 from .prune import span_keep_positions, sink_recent_pages  # noqa: F401
 from .chunk import chunk_attend  # noqa: F401
+from .rope import rotate  # noqa: F401
+from .verify import verify as draft_verify  # noqa: F401
