@@ -478,10 +478,10 @@ int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void*
  * Tokens so accepted and drawn are distributed as the target's.  keep[b] = pos[start[b]] + 1 + n_accepted[b]:
  * the length to keep, for se_pages_truncate.  No rows, or pos[start[b]] < 0 (no page was left): n_accepted 0,
  * next_token -1, keep -1.
- * The test of a draft is exact.  Weights are taken in units of 2^-60 (rounded down; values above 1 count as
- * 1, negative ones and NaN as 0) and summed as integers, so the result depends on no order of
- * summation.  Rows whose sum passes 8: the token is unspecified (in [0, vocab)).  Random
- * numbers outside [0, 1) count as the nearest inside.
+ * The test of a draft is exact.  Weights (values above 1 count as 1, negative ones and NaN as 0) and their
+ * sums are fp32 numbers with a second word for what rounding loses, then integers: off by less than 2^-40 in
+ * all (less than 2^-50 in all counts as 0), the same for the same row whatever the batch.  Rows whose sum passes 8: the token is
+ * unspecified (in [0, vocab)).  Random numbers outside [0, 1) count as the nearest inside.
  * A row without any weight: next_token -1, SE_DEV_BAD_VALUE.  A drafted token outside [0, vocab) is refused:
  * SE_DEV_BAD_INDEX.  start outside [0, max_tokens] or descending: SE_DEV_BAD_LENGTH, as no rows.
  * probs and draft_probs bf16 (prob_dtype 0) or fp32 (1), rows row_stride elements apart (0: vocab), 16-byte

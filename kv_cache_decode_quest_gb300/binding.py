@@ -229,7 +229,7 @@ class _Measured:
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
-        self.__dict__["_sequences"] = None
+        self.__dict__["_sequences"] = self.__dict__["_device"] = None
 
 
 def _int32_fields(holder):
@@ -621,17 +621,44 @@ def se_chunk_attn(kv: PagedKV, q, chunk: Chunk, batch: int, num_q_heads: int, sc
                                 _stream(stream)), "se_chunk_attn")
 
 
-def _on_device(what: str, *tensors):
-    """Refuses tensors that the kernels cannot reach: the calls run on the current device."""
-    here = None
+# the current device's number alone (private to torch, as above)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _elsewhere(what: str, device: int):
+    where = "the CPU or several devices" if device < 0 else f"cuda:{device}"
+    raise SparseEngineError(f"{what}: a tensor is on {where}, not on the current CUDA device")
+
+
+def _located(holder: _Measured) -> int:
+    """The one device of a holder's tensors (-1: the CPU, -2: several), looked up as `_holds` does."""
+    at = holder._device
+    if at is None:
+        found = {t.get_device() for f in dataclasses.fields(holder)
+                 if isinstance(t := getattr(holder, f.name), torch.Tensor)}
+        at = holder.__dict__["_device"] = found.pop() if len(found) == 1 else -2 if found else -3
+    return at
+
+
+def _on_device(what: str, holders, *tensors) -> int:
+    """The current device; refuses tensors that its kernels cannot reach."""
+    first = tensors[0].get_device()
+    if first < 0 or first != _current_device():
+        _elsewhere(what, first)
     for t in tensors:
-        if t is None:
-            continue
-        at = t.get_device()
-        if here is None:
-            here = torch.cuda.current_device() if at >= 0 else 0
-        if at != here:
-            raise SparseEngineError(f"{what}: a tensor is on {t.device}, not on the current CUDA device")
+        if t is not None and t.get_device() != first:
+            _elsewhere(what, t.get_device())
+    for h in holders:
+        at = _located(h)
+        if at != first and at != -3:                   # (-3: it holds no tensor)
+            _elsewhere(what, at)
+    return first
+
+
+def _stream_on(device: int, stream):
+    if stream is not None or _raw_stream is None:
+        return _stream(stream)
+    return _raw_stream(device)
 
 
 def se_rope_turns(rot_dim: int, base: float = 10000.0, scaling: int = SE_ROPE_PLAIN,
@@ -649,13 +676,18 @@ def se_rope_turns(rot_dim: int, base: float = 10000.0, scaling: int = SE_ROPE_PL
 def _rotated(x, out, rows: int, what: str):
     """(heads, head_dim, stride, out stride) of rows of heads and the tensor they go to."""
     if x is None or out is None:
-        if x is not None or out is not None:
+        if x is not out:
             raise SparseEngineError(f"{what}: rows without a tensor to go to, or the other way round")
         return 0, 0, 0, 0
     if x.dtype is not _BF16 or out.dtype is not _BF16:
         raise SparseEngineError(f"{what}: bfloat16 needed, got {x.dtype} and {out.dtype}")
-    stride = _token_stride(x, what, rows, x.shape[1] if x.dim() == 3 else 0, x.shape[-1])
-    return x.shape[1], x.shape[2], stride, _token_stride(out, f"{what}_out", rows, *x.shape[1:])
+    shape = x.shape
+    if len(shape) != 3:
+        shape = rows, 0, 0                             # (refused below)
+    stride = _token_stride(x, what, rows, shape[1], shape[2])
+    if out is x:
+        return shape[1], shape[2], stride, stride
+    return shape[1], shape[2], stride, _token_stride(out, what + "_out", rows, shape[1], shape[2])
 
 
 def se_qk_rope(rope: Rope, pos, q, k, q_out, k_out, ws, stream=None):
@@ -670,11 +702,13 @@ def se_qk_rope(rope: Rope, pos, q, k, q_out, k_out, ws, stream=None):
         raise SparseEngineError(f"se_qk_rope: q of {dim} channels a head, k of {dim_k}")
     dim = dim or dim_k
     _holds(rope, dim, "se_qk_rope: head_dim")
-    _on_device("se_qk_rope", pos, q, k, q_out, k_out, ws, rope.turns, rope.q_weight, rope.k_weight)
+    here = _on_device("se_qk_rope", (rope,), pos, ws, q, k, q_out, k_out)
     c = rope.c
-    _check(load().se_qk_rope(ctypes.byref(c), _p(pos), rows, hq, hk, dim, _p(q), sq, _p(k), sk,
-                             _p(q_out), oq, _p(k_out), ok, _p(ws), ws.numel(), _stream(stream)),
-           "se_qk_rope")
+    rc = load().se_qk_rope(ctypes.byref(c), pos.data_ptr(), rows, hq, hk, dim, _p(q), sq, _p(k), sk,
+                           _p(q_out), oq, _p(k_out), ok, ws.data_ptr(), ws.numel(),
+                           _stream_on(here, stream))
+    if rc:
+        _check(rc, "se_qk_rope")
 
 
 def se_rope_append_chunk(kv: PagedKV, rope: Rope, q, k_new, v_new, q_out, chunk: Chunk, batch: int,
@@ -694,12 +728,14 @@ def se_rope_append_chunk(kv: PagedKV, rope: Rope, q, k_new, v_new, q_out, chunk:
     _holds(rope, dim, "se_rope_append_chunk: head_dim")
     _holds(kv, batch, "se_rope_append_chunk")
     _holds(chunk, 0, "se_rope_append_chunk")
-    _on_device("se_rope_append_chunk", kv.k, kv.v, kv.meta, kv.ctx_len, q, k_new, v_new, q_out,
-               chunk.slot, ws, rope.turns, rope.q_weight, rope.k_weight)
+    here = _on_device("se_rope_append_chunk", (kv, rope, chunk), k_new, v_new, ws, q, q_out)
     rc = rope.c
-    _check(load().se_rope_append_chunk(ctypes.byref(c), ctypes.byref(rc), _p(q), sq, hq, _p(k_new),
-                                       _p(v_new), stride, _p(q_out), oq, ctypes.byref(cc), batch,
-                                       _p(ws), ws.numel(), _stream(stream)), "se_rope_append_chunk")
+    rc = load().se_rope_append_chunk(ctypes.byref(c), ctypes.byref(rc), _p(q), sq, hq,
+                                     k_new.data_ptr(), v_new.data_ptr(), stride, _p(q_out), oq,
+                                     ctypes.byref(cc), batch, ws.data_ptr(), ws.numel(),
+                                     _stream_on(here, stream))
+    if rc:
+        _check(rc, "se_rope_append_chunk")
 
 
 def se_draft_verify_workspace(batch: int, vocab: int) -> int:
@@ -730,14 +766,16 @@ def se_draft_verify(probs, draft_probs, tokens, accept_u, sample_u, chunk: Chunk
     for t, name in ((n_accepted, "n_accepted"), (next_token, "next_token"), (keep, "keep")):
         _per_sequence(t, batch, f"{what} {name}")
     _holds(chunk, batch, what)
-    _on_device(what, probs, draft_probs, tokens, accept_u, sample_u, chunk.start, chunk.pos, n_accepted,
-               next_token, keep, ws)
+    here = _on_device(what, (chunk,), probs, draft_probs, tokens, accept_u, sample_u, n_accepted,
+                      next_token, keep, ws)
     cc, vocab = chunk.c, probs.shape[1]
     stride = probs.stride(0) if rows > 1 else vocab
-    _check(load().se_draft_verify(_p(probs), _p(draft_probs), stride, int(probs.dtype is _F32), vocab,
-                                  _p(tokens), _p(accept_u), _p(sample_u), ctypes.byref(cc), batch,
-                                  _p(n_accepted), _p(next_token), _p(keep), _p(ws), ws.numel(),
-                                  _stream(stream)), what)
+    rc = load().se_draft_verify(probs.data_ptr(), _p(draft_probs), stride, int(probs.dtype is _F32),
+                                vocab, tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
+                                ctypes.byref(cc), batch, n_accepted.data_ptr(), next_token.data_ptr(),
+                                keep.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(here, stream))
+    if rc:
+        _check(rc, what)
 
 
 def se_pages_truncate_workspace(batch: int, num_pages: int) -> int:
@@ -749,11 +787,12 @@ def _table_edit(name: str, pool: PagePool, page_refs, words, batch: int, carry: 
     _per_sequence(page_refs, pool.free_pages.numel(), f"{name} page_refs")
     _holds(pool, batch, name)
     _holds(carry, batch, name)
-    _on_device(name, pool.free_pages, pool.block_table, pool.ctx_len, page_refs, words, carry.from_seq,
-               carry.from_page, ws)
+    here = _on_device(name, (pool, carry), words, page_refs, ws)
     c, cc = pool.c, carry.c
-    _check(getattr(load(), name)(ctypes.byref(c), _p(page_refs), _p(words), batch, ctypes.byref(cc),
-                                 _p(ws), ws.numel(), _stream(stream)), name)
+    rc = getattr(load(), name)(ctypes.byref(c), _p(page_refs), words.data_ptr(), batch,
+                               ctypes.byref(cc), ws.data_ptr(), ws.numel(), _stream_on(here, stream))
+    if rc:
+        _check(rc, name)
 
 
 def se_pages_fork(pool: PagePool, page_refs, src, batch: int, carry: Carry, ws, stream=None):
@@ -772,11 +811,12 @@ def se_pages_carry(kv: PagedKV, carry: Carry, batch: int, ws, stream=None):
     """One layer's cache follows a fork or a truncation: last pages' rows and page summaries."""
     _holds(kv, batch, "se_pages_carry")
     _holds(carry, batch, "se_pages_carry")
-    _on_device("se_pages_carry", kv.k, kv.v, kv.meta, kv.block_table, kv.ctx_len, carry.from_seq,
-               carry.from_page, ws)
+    here = _on_device("se_pages_carry", (kv, carry), ws)
     c, cc = kv.c, carry.c
-    _check(load().se_pages_carry(ctypes.byref(c), ctypes.byref(cc), batch, _p(ws), ws.numel(),
-                                 _stream(stream)), "se_pages_carry")
+    rc = load().se_pages_carry(ctypes.byref(c), ctypes.byref(cc), batch, ws.data_ptr(), ws.numel(),
+                               _stream_on(here, stream))
+    if rc:
+        _check(rc, "se_pages_carry")
 
 
 def se_quest_select(kv: PagedKV, q, batch: int, num_q_heads: int, budget_tokens, sel_pages,

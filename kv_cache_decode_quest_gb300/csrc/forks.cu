@@ -104,17 +104,22 @@ __global__ void __launch_bounds__(1024, 1)
     __shared__ long long tmp[66];
     int flags = 0;
     const int n_free = clamped_free(pool, flags);
+    // this thread's sequences [b0, b1)
     const int per = (batch + blockDim.x - 1) / blockDim.x;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, batch), b1 = min(b0 + per, batch);
-    long long asked = 0, asks = 0, entries = 0, all = 0;
-    for (int b = b0; b < b1; ++b) asked += fork_of(pool, src, batch, b).page;
-    {
-        long long none = 0, nones;
-        block_scan2(asked, none, tmp, &asks, &nones);
-    }
-    long long run = asked;
+    Fork mine = {-1, 0, 0, false, false};
+    if (b0 < b1) mine = fork_of(pool, src, batch, b0);
+    long long asked = 0, entries = 0, asks, all;
     for (int b = b0; b < b1; ++b) {
-        const Fork f = fork_of(pool, src, batch, b);
+        const Fork f = b == b0 ? mine : fork_of(pool, src, batch, b);
+        asked += f.page;
+        entries += f.want ? f.ctx / kPage : 0;
+    }
+    block_scan2(asked, entries, tmp, &asks, &all);
+    long long run = asked, at = entries;
+    bool less = false;                       // a sequence is not served: those behind it have fewer before them
+    for (int b = b0; b < b1; ++b) {
+        const Fork f = b == b0 ? mine : fork_of(pool, src, batch, b);
         flags |= f.flags;
         int fresh = f.want ? -1 : -2;
         if (f.page) {
@@ -130,19 +135,20 @@ __global__ void __launch_bounds__(1024, 1)
                     fresh = -2;
                 }
             }
+            less |= fresh == -2;
         }
         s_fresh[b] = fresh;
-        s_first[b] = fresh == -2 ? 0 : f.ctx / kPage;
-        entries += s_first[b];
+        s_first[b] = static_cast<int>(min(at, 0x7fffffffll));
+        at += f.want ? f.ctx / kPage : 0;
     }
-    {
-        long long none = 0, nones;
-        block_scan2(entries, none, tmp, &all, &nones);
-    }
-    for (int b = b0; b < b1; ++b) {
-        const int n = s_first[b];
-        s_first[b] = static_cast<int>(min(entries, 0x7fffffffll));
-        entries += n;
+    if (__syncthreads_or(less)) {
+        long long n = 0, none = 0, nones;
+        for (int b = b0; b < b1; ++b) n += s_fresh[b] == -2 ? 0 : pool.ctx_len[src[b]] / kPage;
+        block_scan2(n, none, tmp, &all, &nones);
+        for (int b = b0; b < b1; ++b) {
+            s_first[b] = static_cast<int>(min(n, 0x7fffffffll));
+            n += s_fresh[b] == -2 ? 0 : pool.ctx_len[src[b]] / kPage;
+        }
     }
     __syncthreads();
     // table entries; more than 2^31 of them do not fit a table of a pool's pages
@@ -223,7 +229,10 @@ __device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs
 //               which entry that is depends on no timing
 //   push        freed entries to their place by a running sum, counts and notes back to zero
 //   commit      tables, lengths, the stack's top
-// Latency bound: a cut of a decode step lets go of a page here and there.
+// Few entries (a decode step's: a page here and there) are the first block's alone; then the
+// others leave after the scan.  Latency bound throughout.
+constexpr int kEntries = 4;                  // of a thread at once
+
 __global__ void __launch_bounds__(1024, 1)
     pages_truncate_kernel(se_page_pool pool, int32_t* refs, const int32_t* keep, int batch,
                           se_page_carry carry, int* ws) {
@@ -236,128 +245,191 @@ __global__ void __launch_bounds__(1024, 1)
     __shared__ long long tmp[66];
     __shared__ int s_count, s_scan[33];
     int* who = ws + kWhoWord;
-    const int rank = cluster_rank(), ranks = cluster_size(), nt = blockDim.x;
-    int flags = 0;
+    const int nt = blockDim.x;
+    int rank = cluster_rank(), ranks = cluster_size(), flags = 0;
     const int n_free = clamped_free(pool, flags);
+    // this thread's sequences [b0, b1)
     const int per = (batch + nt - 1) / nt;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, batch), b1 = min(b0 + per, batch);
-    long long asked = 0, asks = 0, entries = 0, all = 0, none = 0, nones = 0;
-    for (int b = b0; b < b1; ++b) asked += cut_of(pool, refs, keep, b).copy;
-    block_scan2(asked, none, tmp, &asks, &nones);
+    Cut mine = {-1, 0, 0, 0, -1, 0, false, false};
+    if (b0 < b1) mine = cut_of(pool, refs, keep, b0);
+    long long asked = 0, entries = 0, asks, all;
     for (int b = b0; b < b1; ++b) {
-        const Cut c = cut_of(pool, refs, keep, b);
+        const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
+        asked += c.copy;
+        entries += c.act ? c.held - c.after + c.copy : 0;
+    }
+    block_scan2(asked, entries, tmp, &asks, &all);
+    long long run = asked, at = entries;
+    bool less = false;                       // a sequence is not served: those behind it have fewer before them
+    for (int b = b0; b < b1; ++b) {
+        const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
         flags |= c.flags;
         int fresh = c.act ? -1 : -2;
         if (c.copy) {
-            ++asked;
-            if (asked > n_free) {
+            ++run;
+            if (run > n_free) {
                 flags |= SE_DEV_CAPACITY;
                 fresh = -2;
             } else {
-                fresh = pool.free_pages[n_free - asked];
+                fresh = pool.free_pages[n_free - run];
                 if (!in_pool(pool, fresh)) {
                     flags |= SE_DEV_BAD_INDEX;
                     fresh = -2;
                 }
             }
+            less |= fresh == -2;
         }
         s_fresh[b] = fresh;
         s_base[b] = c.after - (fresh >= 0);
-        s_first[b] = fresh == -2 ? 0 : c.held - s_base[b];
-        entries += s_first[b];
+        s_first[b] = static_cast<int>(min(at, 0x7fffffffll));
+        at += c.act ? c.held - c.after + c.copy : 0;
     }
-    none = 0;
-    block_scan2(entries, none, tmp, &all, &nones);
-    for (int b = b0; b < b1; ++b) {
-        const int n = s_first[b];
-        s_first[b] = static_cast<int>(min(entries, 0x7fffffffll));
-        entries += n;
+    if (__syncthreads_or(less)) {
+        auto lets = [&](int b) { return s_fresh[b] == -2 ? 0 : pool.n_pages[b] - s_base[b]; };
+        long long n = 0, none = 0, nones;
+        for (int b = b0; b < b1; ++b) n += lets(b);
+        block_scan2(n, none, tmp, &all, &nones);
+        for (int b = b0; b < b1; ++b) {
+            s_first[b] = static_cast<int>(min(n, 0x7fffffffll));
+            n += lets(b);
+        }
     }
     const int taken = static_cast<int>(min(asks, (long long)n_free));
     const int total = static_cast<int>(min(all, 0x7fffffffll));
-    // this block's entries [e0, e1)
+    if (ranks > 1)
+        cluster_sync();                      // all have read what was there before the call
+    else
+        __syncthreads();
+    const bool wide = ranks > 1 && total > nt * kEntries;
+    if (!wide) {
+        if (rank != 0) return;
+        ranks = 1;
+    }
+    auto all_sync = [&]() {
+        if (wide)
+            cluster_sync();
+        else
+            __syncthreads();
+    };
+    // this block's entries [e0, e1), kEntries of a thread side by side
     const int e0 = static_cast<int>((long long)total * rank / ranks);
     const int e1 = static_cast<int>((long long)total * (rank + 1) / ranks);
-    auto entry = [&](int i, int& b) {
-        b = owner_of(s_first, batch, i);
-        return pool.block_table[(int64_t)b * pool.max_pages_per_seq + s_base[b] + (i - s_first[b])];
-    };
-    auto freed = [&](int i, int& page) {
-        int b;
-        page = entry(i, b);
-        if (!in_pool(pool, page)) return false;
-        return refs == nullptr || (__ldcg(refs + page) < 0 && __ldcg(who + page) == b + 1);
-    };
-    cluster_sync();                                          // all counts are as before the call
-    if (refs != nullptr && total > 0) {
-        for (int i = e0 + threadIdx.x; i < e1; i += nt) {
-            int b;
-            const int page = entry(i, b);
-            if (!in_pool(pool, page)) continue;
-            atomicSub(refs + page, 1);
-            atomicMax(who + page, b + 1);
+    const int step = nt * kEntries;
+    int page[kEntries], seq[kEntries];
+    bool have = false;
+    auto fetch = [&](int base) {
+        if (!have || e1 - e0 > step) {                       // (a single step's stay in registers)
+            have = true;
+#pragma unroll
+            for (int r = 0; r < kEntries; ++r) {
+                const int i = base + threadIdx.x * kEntries + r;
+                page[r] = -1;
+                seq[r] = 0;
+                if (i < e1) {
+                    seq[r] = owner_of(s_first, batch, i);
+                    page[r] = pool.block_table[(int64_t)seq[r] * pool.max_pages_per_seq +
+                                               s_base[seq[r]] + (i - s_first[seq[r]])];
+                    if (!in_pool(pool, page[r])) {
+                        flags |= SE_DEV_BAD_INDEX;
+                        page[r] = -1;
+                    }
+                }
+            }
         }
-        __threadfence();
-        cluster_sync();
-    }
-    int mine = 0;
-    for (int i = e0 + threadIdx.x; i < e1; i += nt) {
-        int page;
-        mine += freed(i, page);
-        if (!in_pool(pool, page)) flags |= SE_DEV_BAD_INDEX;
-    }
-    int count;
-    block_exclusive_scan(mine, s_scan, &count);
-    if (threadIdx.x == 0) s_count = count;
-    cluster_sync();
+    };
+    // bit r: entry r is freed
+    auto freed = [&]() {
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < kEntries; ++r) {
+            if (page[r] < 0) continue;
+            if (refs == nullptr) {
+                m |= 1u << r;
+            } else {
+                const int n = __ldcg(refs + page[r]), last = __ldcg(who + page[r]);
+                if (n < 0 && last == seq[r] + 1) m |= 1u << r;
+            }
+        }
+        return m;
+    };
     int before = 0, all_freed = 0;
-    for (int r = 0; r < ranks; ++r) {
-        const int n = cluster_peek(&s_count, r);
-        before += r < rank ? n : 0;
-        all_freed += n;
-    }
-    cluster_sync();                                          // every block has looked; none leaves early
-    const bool fits = (long long)n_free - taken + all_freed <= pool.num_pages;
-    if (!fits) flags |= SE_DEV_CAPACITY;
-    if (flags) flag(ws, flags);
-    // the stack's entries from here down
-    int top = n_free - taken + all_freed - 1 - before;
-    for (int i0 = e0; i0 < e1; i0 += nt) {
-        const int i = i0 + threadIdx.x;
-        int page = -1, tile;
-        const bool f = i < e1 && freed(i, page);
-        const int place = block_exclusive_scan(f, s_scan, &tile);
-        if (f && fits) pool.free_pages[top - place] = page;
-        top -= tile;
-        if (refs != nullptr && i < e1 && in_pool(pool, page)) {
-            if (!fits) {
-                atomicAdd(refs + page, 1);
-                who[page] = 0;
-            } else if (f) {
-                refs[page] = 0;
-                who[page] = 0;
-            } else if (__ldcg(who + page) == owner_of(s_first, batch, i) + 1) {
-                who[page] = 0;                               // still held by others
+    if (total > 0) {
+        if (refs != nullptr) {
+            for (int base = e0; base < e1; base += step) {
+                fetch(base);
+#pragma unroll
+                for (int r = 0; r < kEntries; ++r) {
+                    if (page[r] < 0) continue;
+                    atomicSub(refs + page[r], 1);
+                    atomicMax(who + page[r], seq[r] + 1);
+                }
+            }
+            __threadfence();
+            all_sync();
+        }
+        int n = 0;
+        for (int base = e0; base < e1; base += step) {
+            fetch(base);
+            n += __popc(freed());
+        }
+        block_exclusive_scan(n, s_scan, &all_freed);
+        if (wide) {
+            if (threadIdx.x == 0) s_count = all_freed;
+            cluster_sync();
+            all_freed = 0;
+            for (int r = 0; r < ranks; ++r) {
+                const int m = cluster_peek(&s_count, r);
+                before += r < rank ? m : 0;
+                all_freed += m;
             }
         }
     }
-    cluster_sync();                                          // the tables have been read
-    for (int b = rank * nt + threadIdx.x; fits && b < batch; b += ranks * nt) {
-        const int fresh = s_fresh[b];
+    const bool fits = (long long)n_free - taken + all_freed <= pool.num_pages;
+    if (!fits) flags |= SE_DEV_CAPACITY;
+    // the stack's entries from here down
+    int top = n_free - taken + all_freed - 1 - before;
+    for (int base = e0; base < e1; base += step) {
+        fetch(base);
+        const uint32_t m = freed();
+        int tile, place = block_exclusive_scan(__popc(m), s_scan, &tile);
+#pragma unroll
+        for (int r = 0; r < kEntries; ++r) {
+            if (page[r] < 0) continue;
+            const bool f = (m >> r) & 1;
+            if (f && fits) pool.free_pages[top - place] = page[r];
+            place += f;
+            if (refs == nullptr) continue;
+            if (!fits) {
+                atomicAdd(refs + page[r], 1);
+                who[page[r]] = 0;
+            } else if (f) {
+                refs[page[r]] = 0;
+                who[page[r]] = 0;
+            } else if (__ldcg(who + page[r]) == seq[r] + 1) {
+                who[page[r]] = 0;                            // still held by others
+            }
+        }
+        top -= tile;
+    }
+    if (flags) flag(ws, flags);
+    if (total > 0) all_sync();                               // the tables have been read
+    if (rank != 0) return;
+    for (int b = b0; b < b1; ++b) {
+        const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
+        const int fresh = fits ? s_fresh[b] : -2;
         int from_page = -1;
         if (fresh != -2) {
-            const int n = min(keep[b], pool.ctx_len[b]), after = (n + kPage - 1) / kPage;
-            const int64_t last = (int64_t)b * pool.max_pages_per_seq + after - 1;
-            if (n % kPage != 0 && (n < pool.ctx_len[b] || fresh >= 0))
-                from_page = pool.block_table[last];
-            if (fresh >= 0) pool.block_table[last] = fresh;
-            pool.ctx_len[b] = n;
-            pool.n_pages[b] = after;
+            if (c.n % kPage != 0 && (c.n < c.ctx || fresh >= 0)) from_page = c.last;
+            if (fresh >= 0)
+                pool.block_table[(int64_t)b * pool.max_pages_per_seq + c.after - 1] = fresh;
+            pool.ctx_len[b] = c.n;
+            pool.n_pages[b] = c.after;
         }
         carry.from_seq[b] = -1;
         carry.from_page[b] = from_page;
     }
-    if (fits && rank == 0 && threadIdx.x == 0) *pool.n_free = n_free - taken + all_freed;
+    if (fits && threadIdx.x == 0) *pool.n_free = n_free - taken + all_freed;
 }
 
 // ---- carry --------------------------------------------------------------------------------
@@ -474,9 +546,9 @@ cudaError_t launch_pages_fork(const se_page_pool& pool, int32_t* refs, const int
     const int nt = table_threads(batch);
     const cudaError_t e = allow_smem(pages_fork_kernel, 2 * kMaxBatch * sizeof(int), g_fork_smem);
     if (e != cudaSuccess) return e;
-    // a block for every 4096 table entries that could be written
+    // a block for every 1024 table entries that could be written
     const int grid = static_cast<int>(std::max<int64_t>(
-        1, std::min<int64_t>(num_sms(), (int64_t)batch * pool.max_pages_per_seq / 4096)));
+        1, std::min<int64_t>(num_sms(), (int64_t)batch * pool.max_pages_per_seq / 1024)));
     return launch_pdl(pages_fork_kernel, dim3(grid), dim3(nt), 2 * batch * sizeof(int), s, pool, refs,
                       src, batch, carry, ws);
 }
@@ -485,9 +557,10 @@ cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const
                                   int batch, const se_page_carry& carry, int* ws, cudaStream_t s) {
     const cudaError_t e = allow_smem(pages_truncate_kernel, 3 * kMaxBatch * sizeof(int), g_truncate_smem);
     if (e != cudaSuccess) return e;
-    // one block for few table entries, else eight
-    const int64_t most = std::min<int64_t>((int64_t)batch * pool.max_pages_per_seq, pool.num_pages);
-    const unsigned ranks = most > 8192 ? 8 : 1;
+    // eight blocks when more pages could be let go than a block takes at once (shared pages count each time)
+    int64_t most = (int64_t)batch * pool.max_pages_per_seq;
+    if (refs == nullptr) most = std::min<int64_t>(most, pool.num_pages);
+    const unsigned ranks = most > 4 * 1024 ? 8 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks);
     cfg.blockDim = dim3(ranks > 1 ? 1024 : table_threads(batch));

@@ -3,10 +3,13 @@
 // token comes from max(0, p - q), which leaves every token distributed as p.
 //
 // One row of the vocabulary per sequence is read (two where a draft was refused): HBM bound, a sum and a
-// search.  The weights are integers in units of 2^-60, so sums are exact in any order: the row is cut
-// into tiles of 1024 that any warp of any block may sum, and the last block of a sequence finds
-// the tile and in it the token.  (Sums in fp32 would move a draw over a border in about one of 30
-// draws over 128K tokens; sums in fp64 are as good as these but 30 times slower on this chip.)
+// search.  A draw compares a running sum of up to millions of weights with a random part of the whole:
+// sums in fp32 would move it over a border in about one of 30 draws over 128K tokens.  So a weight is
+// p - q with its rounding error beside it (exact together), a lane's sum of 32 weights carries its error
+// in a second word, and from there on sums are integers in units of 2^-58, the same in any order:
+// the row is cut into tiles of 1024 that any warp of any block may sum, and the last block of a
+// sequence finds the tile and in it the token.  15 fp32 operations a weight, hidden behind the loads; fp64
+// sums, or every weight made a 64-bit integer, are bound by those units' rates (4 times slower).
 #include <algorithm>
 
 #include "common.cuh"
@@ -23,14 +26,23 @@ constexpr float kBelowOne = 0x1.fffffep-1f;
 
 using u64 = unsigned long long;
 
-// x in [0, 1] in units of 2^-60, rounded down (NaN and negative values: 0).
-__device__ __forceinline__ u64 units(float x) {
-    return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p60f);
-}
-__device__ __forceinline__ u64 weight(float p, float q) {
-    const u64 a = units(p), b = units(q);
-    return a > b ? a - b : 0;
-}
+// A sum in two words: s + lo is exact but for lo's own rounding.
+struct Sum {
+    float s = 0.f, lo = 0.f;
+    // Adds p - q when that is positive (both within [0, 1]).
+    __device__ __forceinline__ void add(float p, float q) {
+        const bool more = p > q;
+        const float d = more ? p - q : 0.f;
+        const float e = more ? (p - d) - q : 0.f;        // what the difference lost
+        const float t = s + d, b = t - s;
+        lo += ((s - (t - b)) + (d - b)) + e;
+        s = t;
+    }
+    // In units of 2^-58 (s up to 32).
+    __device__ __forceinline__ u64 units() const {
+        return __float2ull_rz(s * 0x1p58f) + static_cast<u64>(__float2ll_rz(lo * 0x1p58f));
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ float value(const T* p);
@@ -91,19 +103,19 @@ __device__ __forceinline__ void load_vector(const Row<T>& r, int c, uint4& p, ui
         q = make_uint4(b[0], b[1], b[2], b[3]);
     }
 }
+// The weights' terms of vector c: p and q within [0, 1] (NaN: 0), q 0 where there is none.
 template <typename T>
-__device__ __forceinline__ void vector_weights(const Row<T>& r, int c, uint4 p, uint4 q, u64* w) {
+__device__ __forceinline__ void vector_terms(const Row<T>& r, int c, uint4 p, uint4 q, float* x,
+                                             float* y) {
     constexpr int N = 16 / sizeof(T);
-    float x[N], y[N];
     widen<T>(p, x);
     widen<T>(q, y);
-#pragma unroll
-    for (int e = 0; e < N; ++e) w[e] = r.q != nullptr ? weight(x[e], y[e]) : units(x[e]);
     const int at = r.without + r.lead - c * N;
-    if (r.without >= 0 && at >= 0 && at < N) {
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (e == at) w[e] = 0;
+    for (int e = 0; e < N; ++e) {
+        x[e] = __saturatef(x[e]);
+        y[e] = __saturatef(y[e]);
+        if (r.without >= 0 && e == at) x[e] = 0.f;
     }
 }
 
@@ -120,15 +132,15 @@ __device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
     uint4 p[C], q[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) load_vector(r, k * (kTile / N) + i * 32 + lane, p[i], q[i]);
-    u64 sum = 0;
+    Sum sum;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        u64 w[N];
-        vector_weights(r, k * (kTile / N) + i * 32 + lane, p[i], q[i], w);
+        float x[N], y[N];
+        vector_terms(r, k * (kTile / N) + i * 32 + lane, p[i], q[i], x, y);
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum += w[e];
+        for (int e = 0; e < N; ++e) sum.add(x[e], y[e]);
     }
-    return warp_sum(sum);
+    return warp_sum(sum.units());
 }
 
 // Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads call it.
@@ -279,17 +291,25 @@ __global__ void __launch_bounds__(256)
     const int c = s_tile * (kTile / N) + threadIdx.x;
     if (threadIdx.x < kTile / N) {
         uint4 p, q;
+        float x[N], y[N];
         load_vector(row, c, p, q);
-        vector_weights(row, c, p, q, w);
+        vector_terms(row, c, p, q, x, y);
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum += w[e];
+        for (int e = 0; e < N; ++e) {
+            Sum one;
+            one.add(x[e], y[e]);
+            w[e] = one.units();
+            sum += w[e];
+        }
     }
     u64 part;
     u64 ahead = block_sum_before(sum, tmp, &part);
-    if (sum > 0 && ahead <= s_rest && s_rest < ahead + sum) {
+    // (the weights one by one may end a rounding before the tile's sum: then it is the last)
+    const u64 rest = part == 0 ? 0 : min(s_rest, part - 1);
+    if (sum > 0 && ahead <= rest && rest < ahead + sum) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            if (ahead <= s_rest && s_rest < ahead + w[e]) next_token[b] = c * N - row.lead + e;
+            if (ahead <= rest && rest < ahead + w[e]) next_token[b] = c * N - row.lead + e;
             ahead += w[e];
         }
     }
