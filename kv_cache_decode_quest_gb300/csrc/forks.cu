@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(1024, 1)
     const int step = nt * kEntries;
     int page[kEntries], seq[kEntries];
     bool have = false;
+    uint32_t freed_bits = 0, last_bits = 0;  // of the first eight steps: found once
     auto fetch = [&](int base) {
         if (!have || e1 - e0 > step) {                       // (a single step's stay in registers)
             have = true;
@@ -338,24 +339,36 @@ __global__ void __launch_bounds__(1024, 1)
             }
         }
     };
-    // bit r: entry r is freed
-    auto freed = [&]() {
+    // Bit r: entry r is freed; of `last`: it is its page's last of this call.
+    bool shared = refs != nullptr;
+    auto freed = [&](uint32_t& last) {
         uint32_t m = 0;
+        last = 0;
 #pragma unroll
         for (int r = 0; r < kEntries; ++r) {
             if (page[r] < 0) continue;
-            if (refs == nullptr) {
+            if (!shared) {
                 m |= 1u << r;
             } else {
-                const int n = __ldcg(refs + page[r]), last = __ldcg(who + page[r]);
-                if (n < 0 && last == seq[r] + 1) m |= 1u << r;
+                const int n = __ldcg(refs + page[r]), of = __ldcg(who + page[r]);
+                if (of == seq[r] + 1) last |= 1u << r;
+                if (n < 0 && of == seq[r] + 1) m |= 1u << r;
             }
         }
         return m;
     };
     int before = 0, all_freed = 0;
     if (total > 0) {
-        if (refs != nullptr) {
+        if (shared && !wide && total <= step) {
+            // pages that one sequence holds, as most are, need no counting
+            fetch(e0);
+            bool any = false;
+#pragma unroll
+            for (int r = 0; r < kEntries; ++r)
+                if (page[r] >= 0) any |= refs[page[r]] > 0;
+            shared = __syncthreads_or(any);
+        }
+        if (shared) {
             for (int base = e0; base < e1; base += step) {
                 fetch(base);
 #pragma unroll
@@ -368,10 +381,16 @@ __global__ void __launch_bounds__(1024, 1)
             __threadfence();
             all_sync();
         }
-        int n = 0;
-        for (int base = e0; base < e1; base += step) {
+        int n = 0, k = 0;
+        for (int base = e0; base < e1; base += step, ++k) {
             fetch(base);
-            n += __popc(freed());
+            uint32_t last;
+            const uint32_t m = freed(last);
+            n += __popc(m);
+            if (k < 32 / kEntries) {
+                freed_bits |= m << (k * kEntries);
+                last_bits |= last << (k * kEntries);
+            }
         }
         block_exclusive_scan(n, s_scan, &all_freed);
         if (wide) {
@@ -389,9 +408,15 @@ __global__ void __launch_bounds__(1024, 1)
     if (!fits) flags |= SE_DEV_CAPACITY;
     // the stack's entries from here down
     int top = n_free - taken + all_freed - 1 - before;
-    for (int base = e0; base < e1; base += step) {
+    for (int base = e0, k = 0; base < e1; base += step, ++k) {
         fetch(base);
-        const uint32_t m = freed();
+        uint32_t m, last;
+        if (k < 32 / kEntries) {
+            m = freed_bits >> (k * kEntries) & ((1u << kEntries) - 1);
+            last = last_bits >> (k * kEntries) & ((1u << kEntries) - 1);
+        } else {
+            m = freed(last);
+        }
         int tile, place = block_exclusive_scan(__popc(m), s_scan, &tile);
 #pragma unroll
         for (int r = 0; r < kEntries; ++r) {
@@ -399,14 +424,14 @@ __global__ void __launch_bounds__(1024, 1)
             const bool f = (m >> r) & 1;
             if (f && fits) pool.free_pages[top - place] = page[r];
             place += f;
-            if (refs == nullptr) continue;
+            if (!shared) continue;
             if (!fits) {
                 atomicAdd(refs + page[r], 1);
                 who[page[r]] = 0;
             } else if (f) {
                 refs[page[r]] = 0;
                 who[page[r]] = 0;
-            } else if (__ldcg(who + page[r]) == seq[r] + 1) {
+            } else if ((last >> r) & 1) {
                 who[page[r]] = 0;                            // still held by others
             }
         }
@@ -529,6 +554,12 @@ __global__ void __launch_bounds__(128)
     }
 }
 
+#ifndef RANKS
+#define RANKS 8
+#endif
+#ifndef TTHREADS
+#define TTHREADS 1024
+#endif
 int table_threads(int batch) { return batch > 512 ? 1024 : batch > 256 ? 512 : 256; }
 
 std::atomic<uint64_t> g_fork_smem, g_truncate_smem;
@@ -557,13 +588,14 @@ cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const
                                   int batch, const se_page_carry& carry, int* ws, cudaStream_t s) {
     const cudaError_t e = allow_smem(pages_truncate_kernel, 3 * kMaxBatch * sizeof(int), g_truncate_smem);
     if (e != cudaSuccess) return e;
+    if (RANKS > 8) cudaFuncSetAttribute(pages_truncate_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     // eight blocks when more pages could be let go than a block takes at once (shared pages count each time)
     int64_t most = (int64_t)batch * pool.max_pages_per_seq;
     if (refs == nullptr) most = std::min<int64_t>(most, pool.num_pages);
-    const unsigned ranks = most > 4 * 1024 ? 8 : 1;
+    const unsigned ranks = most > 4 * 1024 ? RANKS : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ranks);
-    cfg.blockDim = dim3(ranks > 1 ? 1024 : table_threads(batch));
+    cfg.blockDim = dim3(ranks > 1 ? TTHREADS : table_threads(batch));
     cfg.dynamicSmemBytes = 3 * batch * sizeof(int);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];

@@ -125,30 +125,49 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
     return x;
 }
 
-// The sum of tile k of the row, in every lane.
+// The sum of tile k of the row, in every lane: `kVectors` vectors of each of p and q in flight.
+constexpr int kVectors = 4;
 template <typename T>
 __device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
     constexpr int N = 16 / sizeof(T), C = kTile / N / 32;
-    uint4 p[C], q[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) load_vector(r, k * (kTile / N) + i * 32 + lane, p[i], q[i]);
     Sum sum;
+#pragma unroll 1
+    for (int i0 = 0; i0 < C; i0 += kVectors) {
+        const int c = k * (kTile / N) + i0 * 32 + lane;
+        uint4 p[kVectors], q[kVectors];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        float x[N], y[N];
-        vector_terms(r, k * (kTile / N) + i * 32 + lane, p[i], q[i], x, y);
+        for (int i = 0; i < kVectors; ++i) load_vector(r, c + i * 32, p[i], q[i]);
 #pragma unroll
-        for (int e = 0; e < N; ++e) sum.add(x[e], y[e]);
+        for (int i = 0; i < kVectors; ++i) {
+            float x[N], y[N];
+            vector_terms(r, c + i * 32, p[i], q[i], x, y);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum.add(x[e], y[e]);
+        }
     }
     return warp_sum(sum.units());
 }
 
-// Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads call it.
-__device__ __forceinline__ u64 block_sum_before(u64 x, long long* tmp, u64* total) {
-    long long a = static_cast<long long>(x), none = 0, ta, tb;
-    block_scan2(a, none, tmp, &ta, &tb);
-    *total = static_cast<u64>(ta);
-    return static_cast<u64>(a);
+// Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads call it, with two
+// buffers in turn (the values read last must not be written by the next call).
+__device__ __forceinline__ u64 block_sum_before(u64 x, u64* tmp, u64* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    u64 y = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 z = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) y += z;
+    }
+    if (lane == 31) tmp[warp] = y;
+    __syncthreads();
+    u64 before = y - x, all = 0;
+    for (int w = 0; w < nw; ++w) {
+        const u64 t = tmp[w];
+        before += w < warp ? t : 0;
+        all += t;
+    }
+    *total = all;
+    return before;
 }
 
 // floor(u * total) for u in [0, 1): u is a whole number m < 2^24 times 2^-s.
@@ -162,8 +181,11 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
     return s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? hi >> (s - 64) : 0;
 }
 
+#ifndef VMIN
+#define VMIN 4
+#endif
 template <typename T>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, VMIN)
     draft_verify_kernel(const T* probs, const T* draft, int64_t row_stride, int vocab, int tiles,
                         const int32_t* tokens, const float* accept_u, const float* sample_u,
                         const int32_t* start, const int32_t* pos, int max_tokens,
@@ -171,7 +193,7 @@ __global__ void __launch_bounds__(256)
     constexpr int N = 16 / sizeof(T);
     __shared__ int s_stay, s_bad, s_last, s_tile;
     __shared__ u64 s_rest;
-    __shared__ long long tmp[66];
+    __shared__ u64 tmp[3][8];
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -241,15 +263,14 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     if (!s_last) return;
     __threadfence();
-    u64 total = 0;
+    // a thread's run of tiles, so that one scan serves any number of them
+    const int per = (tiles + blockDim.x - 1) / blockDim.x;
+    const int k0 = min(static_cast<int>(threadIdx.x) * per, tiles), k1 = min(k0 + per, tiles);
+    u64 total = 0, ahead = 0, held = 0;
     for (int round = 0; round < 2; ++round) {
-        total = 0;
-        for (int k0 = 0; k0 < tiles; k0 += blockDim.x) {
-            const int k = k0 + threadIdx.x;
-            u64 part;
-            block_sum_before(k < tiles ? __ldcg(sums + k) : 0, tmp, &part);
-            total += part;
-        }
+        held = 0;
+        for (int k = k0; k < k1; ++k) held += __ldcg(sums + k);
+        ahead = block_sum_before(held, tmp[round], &total);
         if (total > 0 || (row.q == nullptr && row.without < 0)) break;
         // nothing is left of p beside q: drawn from p
         row.q = nullptr;
@@ -267,24 +288,18 @@ __global__ void __launch_bounds__(256)
         n_accepted[b] = stay;
         keep[b] = first_pos + 1 + stay;
         next_token[b] = total == 0 ? -1 : vocab - 1;
-        s_tile = tiles;
     }
-    __syncthreads();
     if (total == 0) return;
     const u64 want = part_of(sample_u[b], total);             // the first token whose sum passes it
-    u64 before = 0;
-    for (int k0 = 0; k0 < tiles && s_tile == tiles; k0 += blockDim.x) {
-        const int k = k0 + threadIdx.x;
-        const u64 w = k < tiles ? __ldcg(sums + k) : 0;
-        u64 part;
-        const u64 ahead = before + block_sum_before(w, tmp, &part);
-        if (w > 0 && ahead <= want && want < ahead + w) {
-            s_tile = k;
-            s_rest = want - ahead;
-        }
-        before += part;
-        __syncthreads();
+    if (threadIdx.x == 0) s_tile = tiles;
+    __syncthreads();
+    if (ahead <= want && want < ahead + held) {
+        int k = k0;
+        for (u64 w; k < k1 - 1 && ahead + (w = __ldcg(sums + k)) <= want; ++k) ahead += w;
+        s_tile = k;
+        s_rest = want - ahead;
     }
+    __syncthreads();
     if (s_tile == tiles) return;
     // in the tile: a vector a thread
     u64 w[N], sum = 0;
@@ -303,7 +318,7 @@ __global__ void __launch_bounds__(256)
         }
     }
     u64 part;
-    u64 ahead = block_sum_before(sum, tmp, &part);
+    ahead = block_sum_before(sum, tmp[2], &part);
     // (the weights one by one may end a rounding before the tile's sum: then it is the last)
     const u64 rest = part == 0 ? 0 : min(s_rest, part - 1);
     if (sum > 0 && ahead <= rest && rest < ahead + sum) {
@@ -332,7 +347,7 @@ cudaError_t launch_draft_verify(const void* probs, const void* draft, int64_t ro
                                 int* ws, cudaStream_t s) {
     const int tiles = verify_tiles(vocab);
     // a block's eight warps have a tile each at least; up to eight blocks an SM
-    const int split = std::max(1, std::min((tiles + 7) / 8, 8 * num_sms() / batch));
+    const int split = std::max(1, std::min((tiles + 7) / 8, VMIN * num_sms() / batch));
     const dim3 grid(split, batch);
     if (prob_dtype == 1)
         return launch_pdl(draft_verify_kernel<float>, grid, dim3(256), 0, s,
