@@ -9,6 +9,7 @@
 #include <math_constants.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "append.cuh"
 #include "common.cuh"
@@ -317,23 +318,33 @@ __global__ void __launch_bounds__(1024, 1)
     const int e1 = static_cast<int>((long long)total * (rank + 1) / ranks);
     const int step = nt * kEntries;
     int page[kEntries], seq[kEntries];
+    uint32_t open = 0;                       // bit r: entry r may be its page's last of this call
     bool have = false;
     uint32_t freed_bits = 0, last_bits = 0;  // of the first eight steps: found once
     auto fetch = [&](int base) {
         if (!have || e1 - e0 > step) {                       // (a single step's stay in registers)
             have = true;
+            open = 0;
 #pragma unroll
             for (int r = 0; r < kEntries; ++r) {
                 const int i = base + threadIdx.x * kEntries + r;
                 page[r] = -1;
                 seq[r] = 0;
                 if (i < e1) {
-                    seq[r] = owner_of(s_first, batch, i);
-                    page[r] = pool.block_table[(int64_t)seq[r] * pool.max_pages_per_seq +
-                                               s_base[seq[r]] + (i - s_first[seq[r]])];
+                    const int k = owner_of(s_first, batch, i);
+                    const int at = s_base[k] + (i - s_first[k]);
+                    const int32_t* table = pool.block_table + (int64_t)k * pool.max_pages_per_seq + at;
+                    seq[r] = k;
+                    page[r] = table[0];
                     if (!in_pool(pool, page[r])) {
                         flags |= SE_DEV_BAD_INDEX;
                         page[r] = -1;
+                    } else if (refs != nullptr) {
+                        // samples of one prompt lie side by side: where the next sequence lets go of
+                        // the same page, this entry is not the last, and asks no counter
+                        const int j = at - s_base[min(k + 1, batch - 1)];
+                        const int n = k + 1 < batch ? (k + 2 < batch ? s_first[k + 2] : total) - s_first[k + 1] : 0;
+                        if (j < 0 || j >= n || table[pool.max_pages_per_seq] != page[r]) open |= 1u << r;
                     }
                 }
             }
@@ -349,7 +360,7 @@ __global__ void __launch_bounds__(1024, 1)
             if (page[r] < 0) continue;
             if (!shared) {
                 m |= 1u << r;
-            } else {
+            } else if ((open >> r) & 1) {
                 const int n = __ldcg(refs + page[r]), of = __ldcg(who + page[r]);
                 if (of == seq[r] + 1) last |= 1u << r;
                 if (n < 0 && of == seq[r] + 1) m |= 1u << r;
@@ -375,7 +386,7 @@ __global__ void __launch_bounds__(1024, 1)
                 for (int r = 0; r < kEntries; ++r) {
                     if (page[r] < 0) continue;
                     atomicSub(refs + page[r], 1);
-                    atomicMax(who + page[r], seq[r] + 1);
+                    if ((open >> r) & 1) atomicMax(who + page[r], seq[r] + 1);
                 }
             }
             __threadfence();
@@ -554,12 +565,40 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-#ifndef RANKS
-#define RANKS 8
-#endif
 #ifndef TTHREADS
 #define TTHREADS 1024
 #endif
+// Blocks of the truncation's cluster: 16 where the device has room for such a cluster, else the
+// portable 8 (found once per device).
+cudaError_t cluster_blocks(cudaLaunchConfig_t cfg, unsigned* blocks) {
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (n == 0) {
+        e = cudaFuncSetAttribute(pages_truncate_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(16);
+        cfg.dynamicSmemBytes = 3 * kMaxBatch * sizeof(int);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fits = 0;
+        if (cudaOccupancyMaxActiveClusters(&fits, pages_truncate_kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            fits = 0;
+        }
+        n = fits > 0 ? 16 : 8;
+        if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    }
+    *blocks = n;
+    return cudaSuccess;
+}
+
 int table_threads(int batch) { return batch > 512 ? 1024 : batch > 256 ? 512 : 256; }
 
 std::atomic<uint64_t> g_fork_smem, g_truncate_smem;
@@ -586,16 +625,21 @@ cudaError_t launch_pages_fork(const se_page_pool& pool, int32_t* refs, const int
 
 cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const int32_t* keep,
                                   int batch, const se_page_carry& carry, int* ws, cudaStream_t s) {
-    const cudaError_t e = allow_smem(pages_truncate_kernel, 3 * kMaxBatch * sizeof(int), g_truncate_smem);
+    cudaError_t e = allow_smem(pages_truncate_kernel, 3 * kMaxBatch * sizeof(int), g_truncate_smem);
     if (e != cudaSuccess) return e;
-    if (RANKS > 8) cudaFuncSetAttribute(pages_truncate_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    // eight blocks when more pages could be let go than a block takes at once (shared pages count each time)
+
+    // a cluster when more pages could be let go than a block takes at once (shared pages count each time)
     int64_t most = (int64_t)batch * pool.max_pages_per_seq;
     if (refs == nullptr) most = std::min<int64_t>(most, pool.num_pages);
-    const unsigned ranks = most > 4 * 1024 ? RANKS : 1;
+    unsigned ranks = 1;
     cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(table_threads(batch));
+    if (most > 4 * 1024) {
+        cfg.blockDim = dim3(TTHREADS);
+        e = cluster_blocks(cfg, &ranks);
+        if (e != cudaSuccess) return e;
+    }
     cfg.gridDim = dim3(ranks);
-    cfg.blockDim = dim3(ranks > 1 ? TTHREADS : table_threads(batch));
     cfg.dynamicSmemBytes = 3 * batch * sizeof(int);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
