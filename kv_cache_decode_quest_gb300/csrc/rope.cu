@@ -84,47 +84,37 @@ __device__ __forceinline__ void turn_of(unsigned long long turns, float amplitud
     s *= amplitude;
 }
 
-// The norm's weights of this lane's two vectors, as stored.
+// The norm's weights of this lane's pairs.
 struct Weight {
-    uint4 a, b;
+    uint64_t x[4], y[4];
 };
 template <int D, bool PAIRS>
 __device__ __forceinline__ Weight load_weight(const void* w, const HeadLane<D, PAIRS>& l) {
-    Weight r = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    Weight r = {};
     if (w != nullptr) {
-        r.a = static_cast<const uint4*>(w)[l.a];
-        r.b = static_cast<const uint4*>(w)[l.b];
+        const uint4* v = static_cast<const uint4*>(w);
+        to_pairs<PAIRS>(v[l.a], v[l.b], r.x, r.y);
     }
     return r;
 }
 
-// A row's rotation of this lane's pairs: cosines and sines.
+// A row's rotation of this lane's pairs: cosines, sines, and the sines negated.
 struct Turn {
-    float c[8], s[8];
-};
-// Two pairs of it with the norm's weights in it: out = inv (x xx + y xy, y yy + x yx).
-struct Turn2 {
-    uint64_t xx, xy, yy, yx;
-};
-__device__ __forceinline__ Turn2 weighed(const Turn& t, int i, bool norm, const uint64_t* wx,
-                                         const uint64_t* wy) {
-    Turn2 r;
-    r.xx = r.yy = f32x2(t.c[2 * i], t.c[2 * i + 1]);
-    r.xy = f32x2(-t.s[2 * i], -t.s[2 * i + 1]);
-    r.yx = f32x2(t.s[2 * i], t.s[2 * i + 1]);
-    if (norm) {
-        r.xx = mul_f32x2(r.xx, wx[i]);
-        r.xy = mul_f32x2(r.xy, wy[i]);
-        r.yy = mul_f32x2(r.yy, wy[i]);
-        r.yx = mul_f32x2(r.yx, wx[i]);
+    uint64_t c[4], s[4], n[4];
+    __device__ __forceinline__ void set(const float* cos, const float* sin) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            c[i] = f32x2(cos[2 * i], cos[2 * i + 1]);
+            s[i] = f32x2(sin[2 * i], sin[2 * i + 1]);
+            n[i] = f32x2(-sin[2 * i], -sin[2 * i + 1]);
+        }
     }
-    return r;
-}
+};
 
 // One head's two vectors of this lane: normed over the head's D / 16 lanes, weighted, rotated, rounded.
-// turn(i) gives the i-th two pairs' Turn2.
-template <int D, bool PAIRS, typename F>
-__device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, float eps, F turn) {
+template <int D, bool PAIRS>
+__device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, const Weight& w, float eps,
+                                          const Turn& t) {
     uint64_t x[4], y[4], both = 0;
     to_pairs<PAIRS>(u, v, x, y);
     if (norm) {
@@ -140,13 +130,17 @@ __device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, float e
         for (int o = 1; o < D / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
         const float inv = rsqrtf(fmaf(ss, 1.0f / D, eps));
         both = f32x2(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[i] = mul_f32x2(x[i], w.x[i]);
+            y[i] = mul_f32x2(y[i], w.y[i]);
+        }
     }
     uint32_t p[4], q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const Turn2 t = turn(i);
-        uint64_t a = fma_f32x2(x[i], t.xx, mul_f32x2(y[i], t.xy));
-        uint64_t b = fma_f32x2(y[i], t.yy, mul_f32x2(x[i], t.yx));
+        uint64_t a = fma_f32x2(x[i], t.c[i], mul_f32x2(y[i], t.n[i]));
+        uint64_t b = fma_f32x2(y[i], t.c[i], mul_f32x2(x[i], t.s[i]));
         if (norm) {
             a = mul_f32x2(a, both);
             b = mul_f32x2(b, both);
@@ -157,15 +151,6 @@ __device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, float e
     v = make_uint4(q[0], q[1], q[2], q[3]);
 }
 
-#ifndef RMIN
-#define RMIN 8
-#endif
-#ifndef AMIN
-#define AMIN 4
-#endif
-#ifndef RPASS
-#define RPASS 1
-#endif
 struct HeadRows {
     const uint4* in;
     uint4* out;
@@ -173,140 +158,14 @@ struct HeadRows {
     int heads;
 };
 
-constexpr int kRows = kPage;             // rows of a block
-constexpr int kPasses = 4;               // passes of a unit of work
-#ifndef STAGES
-#define STAGES 2
-#endif
-constexpr int kStages = STAGES;
-constexpr int kTable = 2 * kRows - 1;    // rows of the table: a piece may reach 15 rows past the block's
-
-// The cosines and sines of the block's rows: a table in shared memory, or (few rows, many blocks that
-// share them: TABLE false) made by each lane for itself as it needs them.  In the table a lane finds its
-// eight of either as four 16-byte words, the lanes' words side by side (no bank conflicts).
-template <int D, bool PAIRS, bool TABLE>
-struct Turns {
-    static constexpr int kLanes = D / 16;
-    float* table;                        // [rows][4][D / 16][4]
-    // Rows [0, n) behind `first`; pos says which have a place.  Every thread calls it.
-    __device__ __forceinline__ void make(const se_rope& rope, const int32_t* pos, int first, int rows,
-                                         int n) {
-        if (!TABLE) return;
-        const int half = rope.rot_dim / 2;
-        for (int r = threadIdx.x / 16; r < n; r += blockDim.x / 16) {
-            const int at = first + r < rows ? pos[first + r] : -1;
-            for (int i = threadIdx.x % 16; i < half; i += 16) {
-                float c = 1.f, s = 0.f;
-                if (at >= 0) turn_of(rope.turns[i], rope.amplitude, at, c, s);
-                float* t = table + r * D + ((i >> 2 & 1) * kLanes + (i >> 3)) * 4 + (i & 3);
-                t[0] = c;
-                t[2 * kLanes * 4] = s;
-            }
-        }
-        __syncthreads();
-    }
-    // This lane's eight of row r (position at).
-    __device__ __forceinline__ void get(const se_rope& rope, const HeadLane<D, PAIRS>& l, int r, int at,
-                                        float* c, float* s) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = 1.f;
-            s[i] = 0.f;
-        }
-        if (!l.turns) return;
-        if (TABLE) {
-            const float4* t = reinterpret_cast<const float4*>(table + r * D) + l.j;
-            const float4 a = t[0], b = t[kLanes], d = t[2 * kLanes], e = t[3 * kLanes];
-            c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
-            c[4] = b.x; c[5] = b.y; c[6] = b.z; c[7] = b.w;
-            s[0] = d.x; s[1] = d.y; s[2] = d.z; s[3] = d.w;
-            s[4] = e.x; s[5] = e.y; s[6] = e.z; s[7] = e.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) turn_of(rope.turns[8 * l.j + i], rope.amplitude, at, c[i], s[i]);
-        }
-    }
-};
-
-// The heads of the block's rows, 512 / D side by side a pass, as a list of n passes a row.
-struct PassList {
-    HeadRows q;
-    int n;
-    uint32_t inverse;                    // ceil(2^32 / n), 0 for n = 1
-    __device__ __forceinline__ int row_of(int i) const { return inverse ? __umulhi(i, inverse) : i; }
-};
-// A warp's ring of kStages units of work, each of kPasses passes of two 16-byte vectors a lane: copied in by
-// cp.async while the unit before is worked on.  A lane reads what it copied itself: no barriers.
-struct Ring {
-    uint4* mine;                         // this lane's first slot
-    __device__ __forceinline__ uint4* slot(int unit, int pass) const {
-        return mine + ((unit % kStages) * kPasses + pass) * 64;
-    }
-};
-constexpr int kRingWords = kStages * kPasses * 64;   // of a warp, 16 bytes each
-
-// Copies the vectors of passes [p, p1) (kPasses at most) of the list as unit k.
+// ---- rows of heads --------------------------------------------------------------------------
+// A warp takes a row, or one of `parts` parts of its passes (512 / D heads each, queries first, then keys)
+// when there are few rows.  Its lanes make the row's angles together (two each at most) and hand them round.
+// Few registers and one pass at a time, so that many warps hide the latencies that a row is.
 template <int D, bool PAIRS>
-__device__ __forceinline__ void copy_passes(const Ring& ring, int k, const PassList& list, int first,
-                                            int p, int p1, const HeadLane<D, PAIRS>& l, int mine) {
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        if (p + i >= p1) break;
-        const int r = list.row_of(p + i), head = (p + i - r * list.n) * (512 / D) + mine;
-        if (head < list.q.heads) {
-            const uint4* in = list.q.in + (first + r) * list.q.in_stride + head * (D / 8);
-            cp_async16(ring.slot(k, i), in + l.a, 16);
-            cp_async16(ring.slot(k, i) + 32, in + l.b, 16);
-        }
-    }
-}
-// The row that a warp is at, and its rotation: it serves the row's heads one after another.
-struct RowTurn {
-    int row = -1, pos = -1;
-    Turn2 t[4];
-};
-// Turns passes [p, p1) (kPasses at most), which are unit k of the ring.
-template <int D, bool PAIRS, bool TABLE>
-__device__ __forceinline__ void turn_passes(const Ring& ring, int k, const PassList& list,
-                                            const int32_t* pos, int first, int p, int p1,
-                                            const HeadLane<D, PAIRS>& l, int mine, const se_rope& rope,
-                                            const Turns<D, PAIRS, TABLE>& turns, RowTurn& now) {
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-        if (p + i >= p1) break;                              // (these are the same for the whole warp)
-        const int r = list.row_of(p + i), head = (p + i - r * list.n) * (512 / D) + mine;
-        if (r != now.row) {
-            now.row = r;
-            now.pos = pos[first + r];
-            if (now.pos >= 0) {
-                Turn t;
-                turns.get(rope, l, r, now.pos, t.c, t.s);
-                const Weight w = load_weight<D, PAIRS>(rope.q_weight, l);
-                uint64_t wx[4], wy[4];
-                to_pairs<PAIRS>(w.a, w.b, wx, wy);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) now.t[j] = weighed(t, j, rope.q_weight != nullptr, wx, wy);
-            }
-        }
-        if (now.pos < 0) continue;
-        uint4 u = ring.slot(k, i)[0], v = ring.slot(k, i)[32];
-        norm_turn<D, PAIRS>(u, v, rope.q_weight != nullptr, rope.eps, [&](int j) { return now.t[j]; });
-        if (head < list.q.heads) {
-            uint4* out = list.q.out + (first + r) * list.q.out_stride + head * (D / 8);
-            out[l.a] = u;
-            out[l.b] = v;
-        }
-    }
-}
-
-// Rows of heads: a warp takes a row, or one of `parts` parts of its passes (512 / D heads each, queries
-// first, then keys) when there are few rows.  Its lanes make the row's angles together (two each at most)
-// and hand them round.  Few registers, so that many warps hide the two latencies (the position with the
-// first passes, then the stores) that a row is.
-template <int D, bool PAIRS>
-__global__ void __launch_bounds__(128, RMIN)
+__global__ void __launch_bounds__(128, 8)
     qk_rope_kernel(se_rope rope, const int32_t* pos, int rows, int parts, HeadRows q, HeadRows k) {
-    constexpr int HP = 512 / D, A = D / 64, U = RPASS;       // heads a pass, angles a lane, passes at once
+    constexpr int HP = 512 / D, A = D / 64;                  // heads a pass, angles a lane
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, mine = lane / (D / 16);
@@ -316,22 +175,16 @@ __global__ void __launch_bounds__(128, RMIN)
     const HeadLane<D, PAIRS> l(lane, rope.rot_dim);
     const int nq = (q.heads + HP - 1) / HP, n = nq + (k.heads + HP - 1) / HP;
     const int p0 = n * part / parts, p1 = n * (part + 1) / parts;
-    uint4 u[U], v[U];
+    uint4 u = make_uint4(0, 0, 0, 0), v = u;
     auto load = [&](int p) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const bool keys = p + i >= nq;
-            const HeadRows& h = keys ? k : q;
-            const int head = (p + i - (keys ? nq : 0)) * HP + mine;
-            if (p + i < p1 && head < h.heads) {
-                const uint4* in = h.in + row * h.in_stride + head * (D / 8);
-                u[i] = in[l.a];
-                v[i] = in[l.b];
-            }
+        const HeadRows& h = p < nq ? q : k;
+        const int head = (p < nq ? p : p - nq) * HP + mine;
+        if (p < p1 && head < h.heads) {
+            const uint4* in = h.in + row * h.in_stride + head * (D / 8);
+            u = in[l.a];
+            v = in[l.b];
         }
     };
-#pragma unroll
-    for (int i = 0; i < U; ++i) u[i] = v[i] = make_uint4(0, 0, 0, 0);
     load(p0);
     const int at = pos[row];
     unsigned long long step[A];
@@ -339,40 +192,105 @@ __global__ void __launch_bounds__(128, RMIN)
     for (int i = 0; i < A; ++i)
         step[i] = A * lane + i < rope.rot_dim / 2 ? rope.turns[A * lane + i] : 0;
     if (at < 0) return;
-    float ca[A], sa[A];
     Turn t;
+    {
+        float ca[A], sa[A], c[8], s[8];
 #pragma unroll
-    for (int i = 0; i < A; ++i) turn_of(step[i], rope.amplitude, at, ca[i], sa[i]);
+        for (int i = 0; i < A; ++i) turn_of(step[i], rope.amplitude, at, ca[i], sa[i]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float x = __shfl_sync(0xffffffffu, ca[i % A], (8 * l.j + i) / A);
-        const float y = __shfl_sync(0xffffffffu, sa[i % A], (8 * l.j + i) / A);
-        t.c[i] = l.turns ? x : 1.f;
-        t.s[i] = l.turns ? y : 0.f;
+        for (int i = 0; i < 8; ++i) {
+            const float x = __shfl_sync(0xffffffffu, ca[i % A], (8 * l.j + i) / A);
+            const float y = __shfl_sync(0xffffffffu, sa[i % A], (8 * l.j + i) / A);
+            c[i] = l.turns ? x : 1.f;
+            s[i] = l.turns ? y : 0.f;
+        }
+        t.set(c, s);
     }
-    for (int p = p0; p < p1; p += U) {
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            if (p + i >= p1) break;                          // (the same for the whole warp)
-            const bool keys = p + i >= nq;
-            const void* weight = keys ? rope.k_weight : rope.q_weight;
-            const Weight w = load_weight<D, PAIRS>(weight, l);
-            norm_turn<D, PAIRS>(u[i], v[i], weight != nullptr, rope.eps, [&](int j) {
-                uint64_t wx[4], wy[4];
-                to_pairs<PAIRS>(w.a, w.b, wx, wy);           // (only the j-th are made)
-                return weighed(t, j, weight != nullptr, wx, wy);
-            });
-            const HeadRows& h = keys ? k : q;
-            const int head = (p + i - (keys ? nq : 0)) * HP + mine;
+    auto turn = [&](const HeadRows& h, const void* weight, int begin, int end, int skip) {
+        if (begin >= end) return;
+        const Weight wt = load_weight<D, PAIRS>(weight, l);
+        for (int p = begin; p < end; ++p) {
+            norm_turn<D, PAIRS>(u, v, weight != nullptr, wt, rope.eps, t);
+            const int head = (p - skip) * HP + mine;
             if (head < h.heads) {
                 uint4* out = h.out + row * h.out_stride + head * (D / 8);
-                out[l.a] = u[i];
-                out[l.b] = v[i];
+                out[l.a] = u;
+                out[l.b] = v;
+            }
+            load(p + 1);
+        }
+    };
+    turn(q, rope.q_weight, p0, min(p1, nq), 0);
+    turn(k, rope.k_weight, max(p0, nq), p1, nq);
+}
+
+// ---- append ---------------------------------------------------------------------------------
+constexpr int kRows = kPage;             // rows of a block
+constexpr int kPasses = 4;               // passes (512 / D heads of a row, or of several) of a unit of work
+constexpr int kStages = 2;               // units in flight
+constexpr int kAppendBlocks = 4;         // blocks an SM
+constexpr int kTable = 2 * kRows - 1;    // rows of the table: a piece may reach 15 rows past the block's
+
+// The cosines and sines of the block's rows, in shared memory.  A lane finds its eight of either as four
+// 16-byte words, the lanes' words side by side (no bank conflicts).
+template <int D, bool PAIRS>
+struct Turns {
+    static constexpr int kLanes = D / 16;
+    float* table;                        // [rows][4][D / 16][4]
+    // The rows of `mask` behind `first` that have a place (the others' entries mean nothing).
+    __device__ __forceinline__ void make(const se_rope& rope, const int32_t* pos, int first, int rows,
+                                         uint32_t mask) {
+        const int half = rope.rot_dim / 2;
+        for (int r = threadIdx.x / 16; r < kTable; r += blockDim.x / 16) {
+            if (!((mask >> r) & 1)) continue;
+            const int at = first + r < rows ? pos[first + r] : -1;
+            if (at < 0) continue;
+            for (int i = threadIdx.x % 16; i < half; i += 16) {
+                float* t = table + r * D + ((i >> 2 & 1) * kLanes + (i >> 3)) * 4 + (i & 3);
+                turn_of(rope.turns[i], rope.amplitude, at, t[0], t[2 * kLanes * 4]);
             }
         }
-        load(p + U);
     }
-}
+    // This lane's of row r.
+    __device__ __forceinline__ void get(const HeadLane<D, PAIRS>& l, int r, Turn& turn) const {
+        float c[8], s[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            c[i] = 1.f;
+            s[i] = 0.f;
+        }
+        if (l.turns) {
+            const float4* t = reinterpret_cast<const float4*>(table + r * D) + l.j;
+            const float4 a = t[0], b = t[kLanes], d = t[2 * kLanes], e = t[3 * kLanes];
+            c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+            c[4] = b.x; c[5] = b.y; c[6] = b.z; c[7] = b.w;
+            s[0] = d.x; s[1] = d.y; s[2] = d.z; s[3] = d.w;
+            s[4] = e.x; s[5] = e.y; s[6] = e.z; s[7] = e.w;
+        }
+        turn.set(c, s);
+    }
+};
+
+// A warp's ring of kStages units of work, each of kPasses passes of two 16-byte vectors a lane: copied in by
+// cp.async while the unit before is worked on.  A lane reads what it copied itself: no barriers.
+constexpr int kRingWords = kStages * kPasses * 64;   // of a warp, 16 bytes each
+struct Ring {
+    uint4* mine;                         // this lane's first slot
+    int in = 0, out = 0;                 // units copied and taken
+    __device__ __forceinline__ uint4* slot(int unit, int pass) const {
+        return mine + ((unit % kStages) * kPasses + pass) * 64;
+    }
+};
+
+// The passes of the block's rows whose order is free, as a list: n a row, first its queries', then its values'.
+struct PassList {
+    HeadRows q;
+    const uint4* v;
+    int64_t v_stride;
+    int nq, n, kv_heads;
+    uint32_t inverse;                    // ceil(2^32 / n), 0 for n = 1
+    __device__ __forceinline__ int row_of(int i) const { return inverse ? __umulhi(i, inverse) : i; }
+};
 
 // Two channels' smaller (larger) values at once; a NaN gives way to the other value.
 __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
@@ -395,153 +313,206 @@ __device__ __forceinline__ uint4 shfl_xor4(uint4 x, int o) {
 }
 
 // Append of packed rows with the rotation in front.  Pieces as in the plain append: the keys of one sequence's
-// rows in one page are the work of a warp for one KV head (512 / D rows side by side), which rotates
-// them, writes them and folds them, as rounded, into the page's summary, which it owns.  The values of a
-// piece are a unit of their own (32 registers of data either way); then every warp has its part of the
-// rows' queries.
-template <int D, bool PAIRS, bool TABLE>
-__global__ void __launch_bounds__(128, AMIN)
+// rows in one page, for the KV heads that a warp has side by side (fewer heads: rows beside them), are a
+// warp's job; it rotates them, writes them and folds them, as rounded, into the page's summary, which it
+// owns.  Rows follow one another in a lane, so the fold needs no exchange.  The queries and the values of
+// the block's rows, whose order is free, are dealt out so that all warps have about as much to do.
+template <int D, bool PAIRS>
+__global__ void __launch_bounds__(128, kAppendBlocks)
     rope_append_chunk_kernel(se_paged_kv kv, se_rope rope, PassList list, const uint4* k_new,
-                             const uint4* v_new, int64_t row_stride, se_chunk ck, int batch,
-                             int* status) {
-    constexpr int SEGS = D / 8, RP = 512 / D, IT = kPage / RP;
-    static_assert(IT <= kPasses, "a piece is one unit");
-    __shared__ __align__(16) float s_turns[TABLE ? kTable * D : 4];
+                             int64_t k_stride, se_chunk ck, int batch, int side_shift, int* status) {
+    constexpr int SEGS = D / 8, HP = 512 / D;
+    __shared__ __align__(16) float s_turns[kTable * D];
     __shared__ uint4 s_ring[4 * kRingWords];
+    __shared__ uint32_t s_rows[4];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, mine = lane / (D / 16);
     const int H = kv.num_kv_heads;
     const int first = static_cast<int>(blockIdx.x) * kRows;
     const HeadLane<D, PAIRS> l(lane, rope.rot_dim);
-    const Ring ring = {s_ring + warp * kRingWords + lane};
-    // a warp's units: its run of the queries' passes, then every nw-th of the pieces' keys and values
+    Ring ring = {s_ring + warp * kRingWords + lane};
     const int w = warp + (blockDim.x >> 5) * blockIdx.y, nw = (blockDim.x >> 5) * gridDim.y;
-    const int passes = min(kRows, ck.max_tokens - first) * list.n;
-    const int p0 = passes * w / nw, p1 = passes * (w + 1) / nw, n_q = (p1 - p0 + kPasses - 1) / kPasses;
-    auto copy_q = [&](int k) { copy_passes<D, PAIRS>(ring, k, list, first, p0 + k * kPasses, p1, l, mine); };
-#pragma unroll
-    for (int k = 0; k < kStages; ++k) {                      // (what needs no piece is on its way first)
-        if (k < n_q) copy_q(k);
-        if (k < n_q) cp_async_commit();
-    }
     const Pieces pieces = find_pieces(kv, ck, batch, static_cast<int>(blockIdx.x), lane);
     if (pieces.row.bad && lane >= 1 && lane <= kPage && warp == 0 && blockIdx.y == 0)
         flag(status, SE_DEV_BAD_INDEX);
-    if (warp == 0 && blockIdx.y == 0)
-        commit_lengths(kv, ck, batch, pieces.t, lane, pieces.row);
-    const int n_kv = __popc(pieces.lead) * H, back = nw - 1 - w;
-    const int units = n_q + (2 * n_kv > back ? (2 * n_kv - back + nw - 1) / nw : 0);
-    auto piece = [&](int k, bool& values, int& h) {
-        const int u = back + (k - n_q) * nw;                 // keys of all pieces and heads, then values
-        values = u >= n_kv;
-        h = (values ? u - n_kv : u) % H;
-        return piece_at(pieces, (values ? u - n_kv : u) / H, lane);
+    // keys: `side` heads side by side, HP / side rows beside them; job j is of piece j / groups
+    const int side = 1 << side_shift, beside = HP >> side_shift, groups = (H + side - 1) >> side_shift;
+    const int sub_head = mine & (side - 1), sub_row = mine >> side_shift;
+    const int jobs = __popc(pieces.lead) * groups;
+    // the list's passes: every warp the same work, a warp with a job more of keys that much less
+    const int passes = min(kRows, ck.max_tokens - first) * list.n;
+    const int job_cost = jobs > 0 ? (kRows * groups / beside + jobs - 1) / jobs : 0;
+    const int extra = jobs % nw, back = nw - 1 - w;          // warps with back < extra have one job more
+    const int light = nw - extra;                            // (the first warps)
+    int p0, p1;
+    {
+        // x of a light warp, max(0, x - job_cost) of the others
+        const int heavy = max(0, (passes - light * job_cost) / nw);
+        const int left = passes - heavy * extra;             // for the light ones
+        if (w < light) {
+            p0 = left * w / light;
+            p1 = left * (w + 1) / light;
+        } else {
+            p0 = left + heavy * (w - light);
+            p1 = p0 + heavy;
+        }
+    }
+    const int units = (p1 - p0 + kPasses - 1) / kPasses;
+    int copy_job = back, copy_sub = 0;
+    auto piece_of = [&](int job) { return piece_at(pieces, job / groups, lane); };
+    auto subs_of = [&](const Piece& pc) {                    // units of a job
+        return (32 - __clz(pc.rows) + kPasses * beside - 1) / (kPasses * beside);
     };
-    auto copy = [&](int k) {
-        if (k < n_q) {
-            copy_q(k);
-        } else if (k < units) {
-            bool values;
-            int h;
-            const Piece pc = piece(k, values, h);
-            const uint4* in = (values ? v_new : k_new) + (int64_t)(first + pc.f - 1) * row_stride + h * SEGS;
+    auto copy_next = [&]() {
+        if (ring.in < units) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = i * RP + mine;
-                if ((pc.rows >> r) & 1) {
-                    cp_async16(ring.slot(k, i), in + r * row_stride + l.a, 16);
-                    cp_async16(ring.slot(k, i) + 32, in + r * row_stride + l.b, 16);
+            for (int i = 0; i < kPasses; ++i) {
+                const int p = p0 + ring.in * kPasses + i;
+                if (p >= p1) break;
+                const int r = list.row_of(p), at = p - r * list.n;
+                const bool values = at >= list.nq;
+                const int head = (values ? at - list.nq : at) * HP + mine;
+                if (head < (values ? list.kv_heads : list.q.heads)) {
+                    const uint4* in = (values ? list.v + (first + r) * list.v_stride
+                                              : list.q.in + (first + r) * list.q.in_stride) + head * SEGS;
+                    cp_async16(ring.slot(ring.in, i), in + l.a, 16);
+                    cp_async16(ring.slot(ring.in, i) + 32, in + l.b, 16);
                 }
             }
+        } else if (copy_job < jobs) {
+            const Piece pc = piece_of(copy_job);
+            const int head = (copy_job % groups) * side + sub_head;
+            const uint4* in = k_new + (int64_t)(first + pc.f - 1) * k_stride + head * SEGS;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = (copy_sub * kPasses + i) * beside + sub_row;
+                if (r < kPage && ((pc.rows >> r) & 1) && head < H) {
+                    cp_async16(ring.slot(ring.in, i), in + r * k_stride + l.a, 16);
+                    cp_async16(ring.slot(ring.in, i) + 32, in + r * k_stride + l.b, 16);
+                }
+            }
+            if (++copy_sub == subs_of(pc)) {
+                copy_sub = 0;
+                copy_job += nw;
+            }
         }
+        ++ring.in;
         cp_async_commit();
     };
-    for (int k = min(n_q, kStages); k < kStages; ++k) copy(k);
-    Turns<D, PAIRS, TABLE> turns = {s_turns};
-    if (TABLE) {
-        // the block's 16 rows, and up to 15 behind them that its last piece reaches
-        int reach = kRows;
-        if (pieces.lead) {
-            const Piece pc = piece_at(pieces, __popc(pieces.lead) - 1, lane);
-            reach = max(reach, pc.f - 1 + 32 - __clz(pc.rows));
-        }
-        turns.make(rope, ck.pos, first, ck.max_tokens, min(reach, kTable));
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) copy_next();
+    if (warp == 0 && blockIdx.y == 0)
+        commit_lengths(kv, ck, batch, pieces.t, lane, pieces.row);
+    // the rows whose angles the block's warps need (bits 16 and up: a piece may reach past the block's rows)
+    Turns<D, PAIRS> turns = {s_turns};
+    uint32_t need = 0;
+    if (p0 < p1) need = (2u << list.row_of(p1 - 1)) - (1u << list.row_of(p0));
+    for (int job = back; job < jobs; job += nw) {
+        const Piece pc = piece_of(job);
+        need |= pc.rows << (pc.f - 1);
     }
+    if (lane == 0) s_rows[warp] = need;
+    __syncthreads();
+    turns.make(rope, ck.pos, first, ck.max_tokens, s_rows[0] | s_rows[1] | s_rows[2] | s_rows[3]);
+    __syncthreads();
     uint4* K = static_cast<uint4*>(kv.k);
     uint4* V = static_cast<uint4*>(kv.v);
     uint4* M = static_cast<uint4*>(kv.meta);
-    const Weight wk = load_weight<D, PAIRS>(rope.k_weight, l);
-    {
-        RowTurn now;
-        for (int k = 0; k < n_q; ++k) {
+    Turn t;
+    if (units > 0) {
+        const Weight wq = load_weight<D, PAIRS>(rope.q_weight, l);
+        int row = -1, pos = -1, slot = -1;
+        while (ring.out < units) {
             cp_async_wait<kStages - 1>();
-            turn_passes<D, PAIRS, TABLE>(ring, k, list, ck.pos, first, p0 + k * kPasses, p1, l, mine, rope,
-                                         turns, now);
-            copy(k + kStages);
+#pragma unroll 1
+            for (int i = 0; i < kPasses; ++i) {
+                const int p = p0 + ring.out * kPasses + i;
+                if (p >= p1) break;                          // (these are the same for the whole warp)
+                const int r = list.row_of(p), at = p - r * list.n;
+                if (r != row) {
+                    row = r;
+                    pos = __shfl_sync(0xffffffffu, pieces.row.pos, r + 1);
+                    slot = __shfl_sync(0xffffffffu, pieces.row.slot, r + 1);
+                    if (pos >= 0 && at < list.nq) turns.get(l, r, t);
+                }
+                uint4 u = ring.slot(ring.out, i)[0], v = ring.slot(ring.out, i)[32];
+                if (at < list.nq) {
+                    if (pos < 0) continue;
+                    norm_turn<D, PAIRS>(u, v, rope.q_weight != nullptr, wq, rope.eps, t);
+                    const int head = at * HP + mine;
+                    if (head < list.q.heads) {
+                        uint4* out = list.q.out + (first + r) * list.q.out_stride + head * SEGS;
+                        out[l.a] = u;
+                        out[l.b] = v;
+                    }
+                } else {
+                    const int head = (at - list.nq) * HP + mine;
+                    if (slot >= 0 && head < H) {
+                        uint4* out = V + (((int64_t)(slot / kPage) * H + head) * kPage + slot % kPage) * SEGS;
+                        out[l.a] = u;
+                        out[l.b] = v;
+                    }
+                }
+            }
+            ++ring.out;
+            copy_next();
         }
     }
-    for (int k = n_q; k < units; ++k) {
-        bool values;
-        int h;
-        const Piece pc = piece(k, values, h);
-        const int r0 = pc.f - 1, rows = 32 - __clz(pc.rows);  // the piece's first row in the block, its reach
-        const int64_t dst =
-            (((int64_t)(pc.slot0 / kPage) * H + h) * kPage + pc.slot0 % kPage) * SEGS;
-        const int64_t m0 =
-            ((((int64_t)pc.seq0 * kv.max_pages_per_seq + pc.pos0 / kPage) * H + h) * 2) * SEGS;
+    if (back >= jobs) return;
+    const Weight wk = load_weight<D, PAIRS>(rope.k_weight, l);
+    for (int job = back; job < jobs; job += nw) {
+        const Piece pc = piece_of(job);
+        const int head = (job % groups) * side + sub_head, r0 = pc.f - 1;
+        const bool mine_too = head < H;
+        uint4* out = K + (((int64_t)(pc.slot0 / kPage) * H + head) * kPage + pc.slot0 % kPage) * SEGS;
+        uint4* meta = M + ((((int64_t)pc.seq0 * kv.max_pages_per_seq + pc.pos0 / kPage) * H + head) * 2) * SEGS;
         constexpr uint32_t kNone = 0x7fff7fffu;              // NaNs: the other value is taken
-        uint4 mn[2], mx[2], old[4];
+        uint4 mn[2], mx[2];
         mn[0] = mn[1] = mx[0] = mx[1] = make_uint4(kNone, kNone, kNone, kNone);
-        const bool more = pc.pos0 % kPage != 0;              // the page has a summary already
-        if (!values && M != nullptr && more && mine == 0) {
-            old[0] = M[m0 + l.a];
-            old[1] = M[m0 + l.b];
-            old[2] = M[m0 + SEGS + l.a];
-            old[3] = M[m0 + SEGS + l.b];
-        }
-        cp_async_wait<kStages - 1>();
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r = i * RP + mine;
-            if (i * RP >= rows) break;                       // the same for the whole warp
-            uint4 a = ring.slot(k, i)[0], b = ring.slot(k, i)[32];
-            const bool there = (pc.rows >> r) & 1;
-            if (!values) {
-                Turn t;
-                turns.get(rope, l, min(r0 + r, kTable - 1), pc.pos0 + r, t.c, t.s);
-                norm_turn<D, PAIRS>(a, b, rope.k_weight != nullptr, rope.eps, [&](int j) {
-                    uint64_t wx[4], wy[4];
-                    to_pairs<PAIRS>(wk.a, wk.b, wx, wy);     // (only the j-th are made)
-                    return weighed(t, j, rope.k_weight != nullptr, wx, wy);
-                });
+        const int subs = subs_of(pc), rows = 32 - __clz(pc.rows);
+        for (int sub = 0; sub < subs; ++sub) {
+            cp_async_wait<kStages - 1>();
+#pragma unroll 1
+            for (int i = 0; i < kPasses; ++i) {
+                const int r = (sub * kPasses + i) * beside + sub_row;
+                if ((sub * kPasses + i) * beside >= rows) break;   // the same for the whole warp
+                const bool there = r < kPage && ((pc.rows >> r) & 1) && mine_too;
+                uint4 a = ring.slot(ring.out, i)[0], b = ring.slot(ring.out, i)[32];
+                turns.get(l, min(r0 + r, kTable - 1), t);
+                norm_turn<D, PAIRS>(a, b, rope.k_weight != nullptr, wk, rope.eps, t);
                 if (there) {
+                    out[r * SEGS + l.a] = a;
+                    out[r * SEGS + l.b] = b;
                     fold(mn[0], mx[0], a, a);
                     fold(mn[1], mx[1], b, b);
                 }
             }
-            if (there) {
-                uint4* out = (values ? V : K) + dst + r * SEGS;
-                out[l.a] = a;
-                out[l.b] = b;
-            }
+            ++ring.out;
+            copy_next();
         }
-        copy(k + kStages);
-        if (values || M == nullptr) continue;
-#pragma unroll
-        for (int o = D / 16; o < 32; o <<= 1)
+        if (M == nullptr) continue;
+        uint4 old[4];
+        const bool more = pc.pos0 % kPage != 0;              // the page has a summary already
+        if (more && sub_row == 0 && mine_too) {
+            old[0] = meta[l.a];
+            old[1] = meta[l.b];
+            old[2] = meta[SEGS + l.a];
+            old[3] = meta[SEGS + l.b];
+        }
+        for (int o = side * (D / 16); o < 32; o <<= 1)
 #pragma unroll
             for (int g = 0; g < 2; ++g)
                 fold(mn[g], mx[g], shfl_xor4(mn[g], o), shfl_xor4(mx[g], o));
-        if (mine == 0) {
+        if (sub_row == 0 && mine_too) {
             if (more) {
                 fold(mn[0], mx[0], old[0], old[2]);
                 fold(mn[1], mx[1], old[1], old[3]);
             }
-            M[m0 + l.a] = mn[0];
-            M[m0 + l.b] = mn[1];
-            M[m0 + SEGS + l.a] = mx[0];
-            M[m0 + SEGS + l.b] = mx[1];
+            meta[l.a] = mn[0];
+            meta[l.b] = mn[1];
+            meta[SEGS + l.a] = mx[0];
+            meta[SEGS + l.b] = mx[1];
         }
     }
 }
@@ -568,22 +539,22 @@ template <int D, bool PAIRS>
 cudaError_t append_of(const se_paged_kv& kv, const se_rope& rope, const HeadArgs& q, const void* k_new,
                       const void* v_new, int64_t row_stride, const se_chunk& ck, int batch, int* status,
                       cudaStream_t s) {
-    const int groups = (ck.max_tokens + kRows - 1) / kRows;
-    if (groups == 0) return cudaSuccess;
     constexpr int HP = 512 / D;
-    PassList list = {head_rows(q), (q.heads + HP - 1) / HP, 0};
+    const int groups = (ck.max_tokens + kRows - 1) / kRows, H = kv.num_kv_heads;
+    if (groups == 0) return cudaSuccess;
+    PassList list = {head_rows(q), static_cast<const uint4*>(v_new), row_stride / 8,
+                     (q.heads + HP - 1) / HP, 0, H, 0};
+    list.n = list.nq + (H + HP - 1) / HP;
     if (list.n > 1) list.inverse = static_cast<uint32_t>(((1ull << 32) + list.n - 1) / list.n);
     const uint4* k = static_cast<const uint4*>(k_new);
-    const uint4* v = static_cast<const uint4*>(v_new);
-    // few rows: several blocks share 16 of them, down to one unit (a piece's keys of a head, a pass) a warp
-    if (groups < num_sms()) {
-        const int most = kRows * (2 * kv.num_kv_heads + list.n);
-        const int share = std::max(1, std::min(8 * num_sms() / groups, (most + 3) / 4));
-        return launch_pdl(rope_append_chunk_kernel<D, PAIRS, false>, dim3(groups, share), dim3(128), 0, s,
-                          kv, rope, list, k, v, row_stride / 8, ck, batch, status);
-    }
-    return launch_pdl(rope_append_chunk_kernel<D, PAIRS, true>, dim3(groups), dim3(128), 0, s, kv, rope,
-                      list, k, v, row_stride / 8, ck, batch, status);
+    // few rows: several blocks share 16 of them, down to one pass a warp
+    const int share = std::max(1, std::min(kAppendBlocks * num_sms() / groups, (kRows * (list.n + H) + 3) / 4));
+    // KV heads side by side in a job of keys: many rows: as many as there are (a row's rotation serves them
+    // together); few rows: one, so that a piece is several short jobs
+    int side_shift = 0;
+    while (share == 1 && (2 << side_shift) <= std::min(H, HP)) ++side_shift;
+    return launch_pdl(rope_append_chunk_kernel<D, PAIRS>, dim3(groups, share), dim3(128), 0, s, kv, rope, list,
+                      k, row_stride / 8, ck, batch, side_shift, status);
 }
 
 }  // namespace
