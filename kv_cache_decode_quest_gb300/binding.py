@@ -681,13 +681,17 @@ def _rotated(x, out, rows: int, what: str):
         return 0, 0, 0, 0
     if x.dtype is not _BF16 or out.dtype is not _BF16:
         raise SparseEngineError(f"{what}: bfloat16 needed, got {x.dtype} and {out.dtype}")
-    shape = x.shape
+    shape, stride = x.shape, x.stride()
+    to = stride if out is x else out.stride()
+    if len(shape) == 3 == len(to) and rows > 1:            # the usual rows at one look
+        n, h, d = shape
+        if stride[2] == 1 == to[2] and stride[1] == d == to[1] and n >= rows and \
+                stride[0] >= h * d <= to[0] and out.shape == shape:
+            return h, d, stride[0], to[0]
     if len(shape) != 3:
-        shape = rows, 0, 0                             # (refused below)
-    stride = _token_stride(x, what, rows, shape[1], shape[2])
-    if out is x:
-        return shape[1], shape[2], stride, stride
-    return shape[1], shape[2], stride, _token_stride(out, what + "_out", rows, shape[1], shape[2])
+        shape = rows, 0, 0                                 # (refused below)
+    return (shape[1], shape[2], _token_stride(x, what, rows, shape[1], shape[2]),
+            _token_stride(out, what + "_out", rows, shape[1], shape[2]))
 
 
 def se_qk_rope(rope: Rope, pos, q, k, q_out, k_out, ws, stream=None):
@@ -747,17 +751,17 @@ def se_draft_verify(probs, draft_probs, tokens, accept_u, sample_u, chunk: Chunk
     """Which of the chunk's drafted tokens stay and the token behind them; probs and draft_probs (or
     None) [max_tokens][vocab] bf16 or fp32, keep: the lengths for se_pages_truncate."""
     what, rows = "se_draft_verify", chunk.seq.numel()
-    for t in (probs, draft_probs):
-        if t is None:
-            continue
-        if t.dtype is not probs.dtype or t.dtype not in (_BF16, _F32):
+    dtype, shape, stride = probs.dtype, probs.shape, probs.stride()
+    for t in (probs,) if draft_probs is None else (probs, draft_probs):
+        if t.dtype is not dtype or (dtype is not _F32 and dtype is not _BF16):
             raise SparseEngineError(f"{what}: probabilities in bfloat16 or float32 needed, one type for "
                                     f"both, got {t.dtype}")
-        if t.dim() != 2 or t.shape[0] < rows or t.shape[1] != probs.shape[1] or \
-                (rows > 0 and t.shape[1] > 1 and t.stride(1) != 1) or \
-                (rows > 1 and (t.stride(0) != probs.stride(0) or t.stride(0) < t.shape[1])):
+        at, by = t.shape, t.stride()
+        if len(at) != 2 or len(shape) != 2 or at[0] < rows or at[1] != shape[1] or \
+                (rows > 0 and at[1] > 1 and by[1] != 1) or \
+                (rows > 1 and (by[0] != stride[0] or by[0] < at[1])):
             raise SparseEngineError(f"{what}: probabilities of at least [{rows}][vocab] with equal row "
-                                    f"strides needed, got shape {tuple(t.shape)} strides {t.stride()}")
+                                    f"strides needed, got shape {tuple(at)} strides {by}")
     _per_sequence(tokens, rows, f"{what} tokens")
     for t, n, name in ((accept_u, rows, "accept_u"), (sample_u, batch, "sample_u")):
         if t.dtype is not _F32 or t.numel() < n or not t.is_contiguous():
@@ -768,10 +772,9 @@ def se_draft_verify(probs, draft_probs, tokens, accept_u, sample_u, chunk: Chunk
     _holds(chunk, batch, what)
     here = _on_device(what, (chunk,), probs, draft_probs, tokens, accept_u, sample_u, n_accepted,
                       next_token, keep, ws)
-    cc, vocab = chunk.c, probs.shape[1]
-    stride = probs.stride(0) if rows > 1 else vocab
-    rc = load().se_draft_verify(probs.data_ptr(), _p(draft_probs), stride, int(probs.dtype is _F32),
-                                vocab, tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
+    cc, vocab = chunk.c, shape[1]
+    rc = load().se_draft_verify(probs.data_ptr(), _p(draft_probs), stride[0] if rows > 1 else vocab,
+                                int(dtype is _F32), vocab, tokens.data_ptr(), accept_u.data_ptr(), sample_u.data_ptr(),
                                 ctypes.byref(cc), batch, n_accepted.data_ptr(), next_token.data_ptr(),
                                 keep.data_ptr(), ws.data_ptr(), ws.numel(), _stream_on(here, stream))
     if rc:

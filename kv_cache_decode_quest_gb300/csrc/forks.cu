@@ -77,17 +77,20 @@ struct Fork {
 __device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* src, int batch, int b) {
     Fork f = {src[b], 0, 0, false, false};
     if (f.src < 0) return f;
-    if (f.src >= batch || src[f.src] >= 0) {
+    if (f.src >= batch) {
         f.flags = SE_DEV_BAD_INDEX;
         return f;
     }
-    f.ctx = p.ctx_len[f.src];
-    if (p.n_pages[b] != 0 || !consistent(p, f.ctx, p.n_pages[f.src])) {
+    const int its_own = src[f.src], mine = p.n_pages[b], theirs = p.n_pages[f.src];
+    f.ctx = p.ctx_len[f.src];                                // (one latency for the four)
+    if (its_own >= 0) {
+        f.flags = SE_DEV_BAD_INDEX;
+    } else if (mine != 0 || !consistent(p, f.ctx, theirs)) {
         f.flags = SE_DEV_BAD_LENGTH;
-        return f;
+    } else {
+        f.want = true;
+        f.page = f.ctx % kPage != 0;
     }
-    f.want = true;
-    f.page = f.ctx % kPage != 0;
     return f;
 }
 
@@ -199,10 +202,8 @@ struct Cut {
 };
 __device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs, const int32_t* keep,
                                       int b) {
-    Cut c = {keep[b], 0, 0, 0, -1, 0, false, false};
+    Cut c = {keep[b], p.ctx_len[b], p.n_pages[b], 0, -1, 0, false, false};
     if (c.n < 0) return c;
-    c.ctx = p.ctx_len[b];
-    c.held = p.n_pages[b];
     if (!consistent(p, c.ctx, c.held)) {
         c.flags = SE_DEV_BAD_LENGTH;
         return c;
@@ -232,7 +233,7 @@ __device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs
 //   commit      tables, lengths, the stack's top
 // Few entries (a decode step's: a page here and there) are the first block's alone; then the
 // others leave after the scan.  Latency bound throughout.
-constexpr int kEntries = 4;                  // of a thread at once
+constexpr int kEntries = 8;                  // of a thread at once, at most
 
 __global__ void __launch_bounds__(1024, 1)
     pages_truncate_kernel(se_page_pool pool, int32_t* refs, const int32_t* keep, int batch,
@@ -313,10 +314,10 @@ __global__ void __launch_bounds__(1024, 1)
         else
             __syncthreads();
     };
-    // this block's entries [e0, e1), kEntries of a thread side by side
+    // this block's entries [e0, e1), `each` of a thread side by side (few: one)
     const int e0 = static_cast<int>((long long)total * rank / ranks);
     const int e1 = static_cast<int>((long long)total * (rank + 1) / ranks);
-    const int step = nt * kEntries;
+    const int each = min(kEntries, max(1, (e1 - e0 + nt - 1) / nt)), step = nt * each;
     int page[kEntries], seq[kEntries];
     uint32_t open = 0;                       // bit r: entry r may be its page's last of this call
     bool have = false;
@@ -325,28 +326,33 @@ __global__ void __launch_bounds__(1024, 1)
         if (!have || e1 - e0 > step) {                       // (a single step's stay in registers)
             have = true;
             open = 0;
+            const int i0 = base + threadIdx.x * each;
+            int k = owner_of(s_first, batch, min(i0, e1 - 1)), next[kEntries];
 #pragma unroll
             for (int r = 0; r < kEntries; ++r) {
-                const int i = base + threadIdx.x * kEntries + r;
                 page[r] = -1;
+                next[r] = -1;
                 seq[r] = 0;
-                if (i < e1) {
-                    const int k = owner_of(s_first, batch, i);
-                    const int at = s_base[k] + (i - s_first[k]);
+                if (r < each && i0 + r < e1) {
+                    while (k + 1 < batch && s_first[k + 1] <= i0 + r) ++k;
+                    const int at = s_base[k] + (i0 + r - s_first[k]);
                     const int32_t* table = pool.block_table + (int64_t)k * pool.max_pages_per_seq + at;
                     seq[r] = k;
                     page[r] = table[0];
-                    if (!in_pool(pool, page[r])) {
-                        flags |= SE_DEV_BAD_INDEX;
-                        page[r] = -1;
-                    } else if (refs != nullptr) {
-                        // samples of one prompt lie side by side: where the next sequence lets go of
-                        // the same page, this entry is not the last, and asks no counter
-                        const int j = at - s_base[min(k + 1, batch - 1)];
-                        const int n = k + 1 < batch ? (k + 2 < batch ? s_first[k + 2] : total) - s_first[k + 1] : 0;
-                        if (j < 0 || j >= n || table[pool.max_pages_per_seq] != page[r]) open |= 1u << r;
-                    }
+                    // samples of one prompt lie side by side: where the next sequence lets go of
+                    // the same page, this entry is not the last, and asks no counter
+                    const int j = at - s_base[min(k + 1, batch - 1)];
+                    const int n = k + 1 < batch ? (k + 2 < batch ? s_first[k + 2] : total) - s_first[k + 1] : 0;
+                    if (refs != nullptr && j >= 0 && j < n) next[r] = table[pool.max_pages_per_seq];
                 }
+            }
+#pragma unroll
+            for (int r = 0; r < kEntries; ++r) {
+                if (r < each && i0 + r < e1 && !in_pool(pool, page[r])) {
+                    flags |= SE_DEV_BAD_INDEX;
+                    page[r] = -1;
+                }
+                if (page[r] != next[r]) open |= 1u << r;
             }
         }
     };

@@ -181,6 +181,9 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
     return s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? hi >> (s - 64) : 0;
 }
 
+#ifndef VS
+#define VS 4
+#endif
 #ifndef VMIN
 #define VMIN 4
 #endif
@@ -347,7 +350,7 @@ cudaError_t launch_draft_verify(const void* probs, const void* draft, int64_t ro
                                 int* ws, cudaStream_t s) {
     const int tiles = verify_tiles(vocab);
     // a block's eight warps have a tile each at least; up to eight blocks an SM
-    const int split = std::max(1, std::min((tiles + 7) / 8, VMIN * num_sms() / batch));
+    const int split = std::max(1, std::min((tiles + 7) / 8, VS * num_sms() / batch));
     const dim3 grid(split, batch);
     if (prob_dtype == 1)
         return launch_pdl(draft_verify_kernel<float>, grid, dim3(256), 0, s,
