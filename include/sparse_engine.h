@@ -82,7 +82,8 @@ extern "C" {
 #define SE_ROPE_PLAIN  0         /* not at all */
 #define SE_ROPE_LINEAR 1         /* every frequency by 1 / factor */
 #define SE_ROPE_NTK    2         /* by a larger base */
-#define SE_ROPE_YARN   3         /* slow ones by 1 / factor, fast ones not, a ramp over the index between */
+#define SE_ROPE_YARN   3         /* slow ones by 1 / factor, fast ones not, between them a ramp over
+                                    the pair's index */
 #define SE_ROPE_BANDS  4         /* the same with a ramp over the frequency */
 
 typedef void* se_stream_t;       /* cudaStream_t */
@@ -307,7 +308,7 @@ size_t se_h2o_workspace(int batch, int num_kv_heads, int num_q_heads, int head_d
 size_t se_page_pool_workspace(int batch);   /* se_chunk_plan and se_pages_release */
 size_t se_chunk_attn_workspace(int batch, int max_tokens, int num_kv_heads, int num_q_heads,
                                int head_dim);
-size_t se_pages_truncate_workspace(int batch, int num_pages);   /* also what se_page_pool_workspace gives */
+size_t se_pages_truncate_workspace(int batch, int num_pages);   /* serves the pool's other calls too */
 size_t se_draft_verify_workspace(int batch, int vocab);
 
 /* ---- page summaries ----------------------------------------------------- */
@@ -423,38 +424,44 @@ int se_chunk_attn(const se_paged_kv* kv, const void* q, const se_chunk* chunk, i
  *   YARN   f[i] * (1 - r) + f[i] / s * r with r = clamp((i - lo) / max(hi - lo, 0.001), 0, 1),
  *          lo = max(0, floor(d(high))), hi = min(rot_dim - 1, ceil(d(low))),
  *          d(x) = rot_dim * ln(L / (2 pi x)) / (2 ln base); *amplitude = 0.1 ln(s) + 1
- *   BANDS  f[i] * r + f[i] / s * (1 - r) with r = clamp((L f[i] / 2 pi - low) / (high - low), 0, 1)
- * and *amplitude (host; 1 but for YARN; may be NULL).  base > 1, rot_dim a multiple of 16 from 16 to
- * 128, factor >= 1, for YARN and BANDS L > 0 and 0 < low < high: else SE_ERR_INVALID_ARG. */
+ *   BANDS  f[i] * r + f[i] / s * (1 - r),
+ *          r = clamp((L f[i] / 2 pi - low) / (high - low), 0, 1)
+ * and *amplitude (host; 1 but for YARN; may be NULL).  base > 1, rot_dim a multiple of 16 from
+ * 16 to 128, factor >= 1, for YARN and BANDS L > 0 and 0 < low < high: else
+ * SE_ERR_INVALID_ARG. */
 int se_rope_turns(double base, int rot_dim, const se_rope_scaling* scaling, uint64_t* turns,
                   float* amplitude);
 
 /* For each row t with pos[t] >= 0 (int32 [rows]: a chunk's pos, or the lengths before a
  * decode step's append) and each head x of q (with q_weight) and k (with k_weight):
  *   y = x * weight / sqrt(mean(x^2) + eps)            (no weight: y = x)
- *   out[i] = amplitude * (y[i] cos a - y[j] sin a),  out[j] = amplitude * (y[j] cos a + y[i] sin a)
- * over the pairs (i, j) of the layout with a = 2 pi pos[t] turns / 2^64; channels past rot_dim: out = y.
- * All in fp32, rounded once, to bf16.  Rows with pos[t] < 0 are left as they were.
- * q bf16 [rows][num_q_heads][head_dim], k bf16 [rows][num_kv_heads][head_dim], tokens *_stride
- * elements apart (0: dense; a multiple of 8); q_out, k_out the same with their own strides.  q_out
- * may be q (with the same stride) and k_out k; any other overlap gives unspecified results.  Either of q, k
- * may be NULL with 0 heads.  Limits: rows <= 2^24, head_dim 64 or 128, at most 1024 heads.
+ *   out[i] = amplitude * (y[i] cos a - y[j] sin a)
+ *   out[j] = amplitude * (y[j] cos a + y[i] sin a)
+ * over the pairs (i, j) of the layout, a = 2 pi (pos[t] * turns mod 2^64) / 2^64; channels past
+ * rot_dim: out = y.  All in fp32, rounded once, to bf16.  Rows with pos[t] < 0 are left as
+ * they were.
+ * q bf16 [rows][num_q_heads][head_dim], k bf16 [rows][num_kv_heads][head_dim], tokens
+ * *_stride elements apart (0: dense; a multiple of 8); q_out, k_out the same with their own
+ * strides.  q_out may be q (with the same stride) and k_out k; any other overlap gives
+ * unspecified results.  Either of q, k may be NULL with 0 heads.
+ * Limits: rows <= 2^24, head_dim 64 or 128, at most 1024 heads.
  * Workspace: se_small_workspace(). */
 int se_qk_rope(const se_rope* rope, const int32_t* pos, int rows, int num_q_heads, int num_kv_heads,
                int head_dim, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* ws,
                size_t ws_bytes, se_stream_t stream);
 
-/* se_qk_rope of the chunk's queries and keys followed by se_kv_append_chunk of the
- * rotated keys (rounded to bf16, and folded into the summaries as rounded) and of v_new, in one kernel.
- * q_out gets every row with pos[t] >= 0; what is appended, dropped and committed is as in
- * se_kv_append_chunk.  q, q_out may be NULL with num_q_heads 0.  kv_stride: elements between
- * tokens of k_new and of v_new (0: dense).  Limits and other arguments: those of the two calls.
- * Workspace: se_small_workspace(). */
-int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void* q, int64_t q_stride,
-                         int num_q_heads, const void* k_new, const void* v_new, int64_t kv_stride,
-                         void* q_out, int64_t q_out_stride, const se_chunk* chunk, int batch,
-                         void* ws, size_t ws_bytes, se_stream_t stream);
+/* se_qk_rope of the chunk's queries and keys followed by se_kv_append_chunk of the rotated
+ * keys (rounded to bf16, and folded into the summaries as rounded) and of v_new, in one
+ * kernel: the same bits.  q_out gets every row with pos[t] >= 0; what is appended, dropped
+ * and committed is as in se_kv_append_chunk.  q, q_out may be NULL with num_q_heads 0.
+ * kv_stride: elements between tokens of k_new and of v_new (0: dense).  Limits and other
+ * arguments: those of the two calls.  Workspace: se_small_workspace(). */
+int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void* q,
+                         int64_t q_stride, int num_q_heads, const void* k_new, const void* v_new,
+                         int64_t kv_stride, void* q_out, int64_t q_out_stride,
+                         const se_chunk* chunk, int batch, void* ws, size_t ws_bytes,
+                         se_stream_t stream);
 
 /* ---- drafted tokens checked, sequences forked and cut back ---------------------------
  * A step that checks drafts: the chunk's rows of sequence b are its last token that stands and
@@ -469,75 +476,94 @@ int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void*
  * was drawn from; NULL: the drafts were not drawn (looked up, say), each counts as certain.
  * Draft i = 0.. (the token d of row t + 1, t = start[b] + i) stays while
  *   accept_u[t+1] * draft_probs[t][d] < probs[t][d]          (float [max_tokens], in [0, 1))
- * and n_accepted[b] is the number of drafts that stay before the first that does not.  With t =
- * start[b] + n_accepted[b] the next token is drawn from the weights
+ * and n_accepted[b] is the number of drafts that stay before the first that does not.  With
+ * t = start[b] + n_accepted[b] the next token is drawn from the weights
  *   w[v] = max(0, probs[t][v] - draft_probs[t][v])  where a draft was refused (without
  *          draft_probs: probs[t][v], but 0 for the refused token), or
- *   w[v] = probs[t][v]                              where all stayed, or where the first are all 0:
- * next_token[b] is the first v with w[0] + ... + w[v] > sample_u[b] * sum(w)  (float [batch], in [0, 1)).
- * Tokens so accepted and drawn are distributed as the target's.  keep[b] = pos[start[b]] + 1 + n_accepted[b]:
- * the length to keep, for se_pages_truncate.  No rows, or pos[start[b]] < 0 (no page was left): n_accepted 0,
- * next_token -1, keep -1.
- * The test of a draft is exact.  Weights (values above 1 count as 1, negative ones and NaN as 0) and their
- * sums are fp32 numbers with a second word for what rounding loses, then integers: off by less than 2^-40 in
- * all (less than 2^-50 in all counts as 0), the same for the same row whatever the batch.  Rows whose sum passes 8: the token is
- * unspecified (in [0, vocab)).  Random numbers outside [0, 1) count as the nearest inside.
- * A row without any weight: next_token -1, SE_DEV_BAD_VALUE.  A drafted token outside [0, vocab) is refused:
- * SE_DEV_BAD_INDEX.  start outside [0, max_tokens] or descending: SE_DEV_BAD_LENGTH, as no rows.
- * probs and draft_probs bf16 (prob_dtype 0) or fp32 (1), rows row_stride elements apart (0: vocab), 16-byte
- * aligned; the rows themselves need no alignment.  chunk->seq and chunk->slot are not read.
- * Limits: 1 <= vocab <= 2^22, batch <= 8192.  Workspace: se_draft_verify_workspace(batch, vocab),
- * zero-filled before its first use: it holds arrival counters at a fixed offset, which every
- * call leaves at zero, so one workspace serves calls of any shape whose size it covers. */
+ *   w[v] = probs[t][v]  where all stayed, or where the first are all 0:
+ * next_token[b] is the first v with w[0] + ... + w[v] > sample_u[b] * sum(w) (float [batch], in
+ * [0, 1)).  Tokens so accepted and drawn are distributed as the target's.
+ * keep[b] = pos[start[b]] + 1 + n_accepted[b]: the length to keep, for se_pages_truncate.
+ * No rows, or pos[start[b]] < 0 (no page was left): n_accepted 0, next_token -1, keep -1.
+ * The test of a draft is exact.  Weights (values above 1 count as 1, negative ones and NaN as
+ * 0) and their sums are fp32 numbers with a second word for what rounding loses, then
+ * integers: off by less than 2^-40 in all (a sum below 2^-50 may count as 0), the same for
+ * the same row whatever the batch.  Rows whose sum passes 8: the token is unspecified (in
+ * [0, vocab)).  Random numbers outside [0, 1) count as the nearest inside, NaN as 0.
+ * A row without any weight: next_token -1, SE_DEV_BAD_VALUE.  A drafted token outside
+ * [0, vocab) is refused: SE_DEV_BAD_INDEX.  start outside [0, max_tokens] or descending:
+ * SE_DEV_BAD_LENGTH, as no rows.
+ * probs and draft_probs bf16 (prob_dtype 0) or fp32 (1), rows row_stride elements apart (0:
+ * vocab), 16-byte aligned; the rows themselves need no alignment.  chunk->seq and
+ * chunk->slot are not read.
+ * Limits: 1 <= vocab <= 2^22, batch <= 8192.
+ * Workspace: se_draft_verify_workspace(batch, vocab), zero-filled before its first use: it
+ * holds arrival counters at a fixed offset, which every call leaves at zero, so one
+ * workspace serves calls of any shape whose size it covers. */
 int se_draft_verify(const void* probs, const void* draft_probs, int64_t row_stride, int prob_dtype,
                     int vocab, const int32_t* tokens, const float* accept_u, const float* sample_u,
                     const se_chunk* chunk, int batch, int32_t* n_accepted, int32_t* next_token,
                     int32_t* keep, void* ws, size_t ws_bytes, se_stream_t stream);
 
 /* Sequences that share pages.  page_refs int32 [num_pages]: how many sequences hold a page
- * beside the first (0 for a page that one holds or none; zero-filled at the start, kept by these two
- * calls).  A page that two sequences hold is full, and no append writes it: the last, partly filled page of
- * a sequence is always its own.  A pool with shared pages lets them go by se_pages_truncate (to
- * length 0) and not by se_pages_release, which knows no counts.
+ * beside the first (0 for a page that one holds or none; zero-filled at the start, kept by
+ * these two calls).  A page that two sequences hold is full, and no append writes it: the
+ * last, partly filled page of a sequence is always its own.  A pool with shared pages lets
+ * them go by se_pages_truncate (to length 0) and not by se_pages_release, which knows no
+ * counts.
  *
- * se_pages_fork: every sequence b with src[b] >= 0 (int32 [batch]; -1: none) becomes a copy of
- * sequence src[b], which holds its pages on: the full pages are shared, page_refs counts them, and
- * for a partly filled last page b takes one from the stack.  Sequences are served in order: b's page is the
- * one i below the top of the stack where i forks before it take a page; when the stack has
- * no page for it: SE_DEV_CAPACITY, it stays empty (those that need no page are served all the same).
- * A served b gets n_pages = ceil(ctx_len / 16), ctx_len as its source, carry->from_seq[b] = src[b]
- * and from_page[b] = the source's last page if partly filled, else -1; every other sequence -1 and -1.  Pages that the source
- * holds past its length (planned, not appended) are not shared.
- * src[b] outside [0, batch), or a source that is forked in the same call itself: SE_DEV_BAD_INDEX; b that holds
- * pages, or a source whose lengths are inconsistent: SE_DEV_BAD_LENGTH: that b stays as it was.
- * Limits: batch <= 8192; num_pages and max_pages_per_seq < 2^27.  Workspace: as se_chunk_plan. */
+ * se_pages_fork: every sequence b with src[b] >= 0 (int32 [batch]; negative: none) becomes a
+ * copy of sequence src[b], which holds its pages on: the full pages are shared, page_refs
+ * counts them, and for a partly filled last page b takes one from the stack.  Sequences are
+ * served in order: b's page is the one i below the top of the stack where i forks before it
+ * ask for a page; when the stack has none for it: SE_DEV_CAPACITY, it stays empty (those
+ * that need no page are served all the same).
+ * A served b gets n_pages = ceil(ctx_len / 16), ctx_len as its source, carry->from_seq[b] =
+ * src[b] and from_page[b] = the source's last page if partly filled, else -1; every other
+ * sequence -1 and -1.  Pages that the source holds past its length (planned, not appended)
+ * are not shared.
+ * src[b] past the batch, or a source that is forked in the same call itself:
+ * SE_DEV_BAD_INDEX; b that holds pages, or a source whose lengths are inconsistent:
+ * SE_DEV_BAD_LENGTH; that b stays as it was.  A page outside the pool on the stack, or where
+ * the source's last rows are: SE_DEV_BAD_INDEX, b stays empty; among the shared ones:
+ * SE_DEV_BAD_INDEX, b has it as the source has, uncounted.
+ * Limits: batch <= 8192; num_pages and max_pages_per_seq < 2^27.
+ * Workspace: as se_chunk_plan. */
 int se_pages_fork(const se_page_pool* pool, int32_t* page_refs, const int32_t* src, int batch,
                   const se_page_carry* carry, void* ws, size_t ws_bytes, se_stream_t stream);
 
-/* se_pages_truncate: sequence b with keep[b] >= 0 (int32 [batch]; negative: left alone) is cut to n =
- * min(keep[b], ctx_len[b]) tokens and holds ceil(n / 16) pages afterwards: it lets go of the others, planned
- * ones included.  Where the page that is then its last is partly filled and shared, b takes one of its
- * own from the stack (as it is before the call, in order of the sequences; none left: SE_DEV_CAPACITY, b stays as it
- * was) and lets go of the shared one.  A page that nobody holds any more goes back on the stack: the
- * freed pages in the order of (sequence, logical page), a page that several let go at the place of the last of them, the
- * first of all on top (as se_pages_release).
- * carry->from_page[b] = the page that held the last, partly filled page's rows if the length became
- * less or a page was taken, else -1; from_seq[b] = -1.  Entries of the block table past the pages held mean nothing.
- * page_refs may be NULL where no pages are shared.  Inconsistent lengths: SE_DEV_BAD_LENGTH, or a last page outside
- * the pool: SE_DEV_BAD_INDEX, b stays as it was; a page let go that is outside the pool: SE_DEV_BAD_INDEX,
- * it does not reach the stack.  A stack that would pass num_pages entries: SE_DEV_CAPACITY, nothing is changed.
- * Limits: as se_pages_fork.  Workspace: se_pages_truncate_workspace(batch, num_pages), zero-filled before
- * its first use; every call leaves it at zero past the status word. */
+/* se_pages_truncate: sequence b with keep[b] >= 0 (int32 [batch]; negative: left alone) is cut
+ * to n = min(keep[b], ctx_len[b]) tokens and holds ceil(n / 16) pages afterwards: it lets go
+ * of the others, planned ones included (so not between a plan and the append of its rows).
+ * Where the page that is then its last is partly filled and shared, b takes one of its own
+ * from the stack (as it is before the call, in order of the sequences; none left:
+ * SE_DEV_CAPACITY, b stays as it was) and lets go of the shared one.  A page that nobody
+ * holds any more goes back on the stack: the freed pages in the order of (sequence, logical
+ * page), a page that several let go at the place of the last of them, the first of all on
+ * top (as se_pages_release).
+ * carry->from_page[b] = the page that held the last, partly filled page's rows if the length
+ * became less or a page was taken, else -1; from_seq[b] = -1.  Entries of the block table
+ * past the pages held mean nothing.
+ * page_refs may be NULL where no pages are shared.
+ * Inconsistent lengths: SE_DEV_BAD_LENGTH, or a last page outside the pool:
+ * SE_DEV_BAD_INDEX, b stays as it was; a page let go that is outside the pool:
+ * SE_DEV_BAD_INDEX, it does not reach the stack.  A stack that would pass num_pages entries:
+ * SE_DEV_CAPACITY, nothing is changed.
+ * Limits: as se_pages_fork.
+ * Workspace: se_pages_truncate_workspace(batch, num_pages), zero-filled before its first
+ * use; every call leaves it at zero past the status word. */
 int se_pages_truncate(const se_page_pool* pool, int32_t* page_refs, const int32_t* keep, int batch,
                       const se_page_carry* carry, void* ws, size_t ws_bytes, se_stream_t stream);
 
-/* One layer's cache follows a fork or a truncation (before the next append; the tables and
- * lengths as that call left them): for sequence b with n = ctx_len[b] tokens, the summaries of its full
- * pages come from sequence from_seq[b], and with from_page[b] >= 0 the n % 16 rows of its last
- * page from page from_page[b] (not copied when it is that page itself) and its summary from those rows.  The
- * cache is then as if sequence b had been appended token by token.  kv->meta may be NULL (rows
- * alone).  A sequence or page outside the cache: SE_DEV_BAD_INDEX, skipped; ctx_len outside [0, 16 *
- * max_pages_per_seq]: SE_DEV_BAD_LENGTH, skipped.  Limits: batch <= 8192.  Workspace: se_small_workspace(). */
+/* One layer's cache follows a fork or a truncation (before the next append, fork or
+ * truncation; the tables and lengths as that call left them): for sequence b with n =
+ * ctx_len[b] tokens, the summaries of its full pages come from sequence from_seq[b], and
+ * with from_page[b] >= 0 the n % 16 rows of its last page from page from_page[b] (not copied
+ * when it is that page itself) and its summary from those rows.  The cache is then as if
+ * sequence b had been appended token by token.  kv->meta may be NULL (rows alone).
+ * A sequence or page outside the cache: SE_DEV_BAD_INDEX, skipped; ctx_len outside [0, 16 *
+ * max_pages_per_seq]: SE_DEV_BAD_LENGTH, skipped.  Limits: batch <= 8192.
+ * Workspace: se_small_workspace(). */
 int se_pages_carry(const se_paged_kv* kv, const se_page_carry* carry, int batch, void* ws,
                    size_t ws_bytes, se_stream_t stream);
 

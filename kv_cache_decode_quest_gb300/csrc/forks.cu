@@ -94,9 +94,10 @@ __device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* sr
     return f;
 }
 
-// Every block scans all sequences (a thread a run of them) and writes its share of the table entries;
-// the last block to finish, which has read what the others have, commits counts and lengths.
-// Latency bound but for many long forks (a table entry and an atomic count for each page).
+// Every block scans all sequences (a thread a run of them) and writes its share of the
+// table entries; the last block to finish, which has read what the others have, commits
+// counts and lengths. Latency bound but for many long forks (a table entry and an atomic
+// count for each page).
 __global__ void __launch_bounds__(1024, 1)
     pages_fork_kernel(se_page_pool pool, int32_t* refs, const int32_t* src, int batch,
                       se_page_carry carry, int* ws) {
@@ -374,9 +375,10 @@ __global__ void __launch_bounds__(1024, 1)
         }
         return m;
     };
-    int before = 0, all_freed = 0;
+    int before = 0, all_freed = 0, place = 0;
+    const bool once = total <= step && !wide;                // each thread's entries are in its registers
     if (total > 0) {
-        if (shared && !wide && total <= step) {
+        if (shared && once) {
             // pages that one sequence holds, as most are, need no counting
             fetch(e0);
             bool any = false;
@@ -409,7 +411,7 @@ __global__ void __launch_bounds__(1024, 1)
                 last_bits |= last << (k * kEntries);
             }
         }
-        block_exclusive_scan(n, s_scan, &all_freed);
+        place = block_exclusive_scan(n, s_scan, &all_freed);
         if (wide) {
             if (threadIdx.x == 0) s_count = all_freed;
             cluster_sync();
@@ -434,7 +436,8 @@ __global__ void __launch_bounds__(1024, 1)
         } else {
             m = freed(last);
         }
-        int tile, place = block_exclusive_scan(__popc(m), s_scan, &tile);
+        int tile = 0;
+        if (!once) place = block_exclusive_scan(__popc(m), s_scan, &tile);
 #pragma unroll
         for (int r = 0; r < kEntries; ++r) {
             if (page[r] < 0) continue;
@@ -455,7 +458,7 @@ __global__ void __launch_bounds__(1024, 1)
         top -= tile;
     }
     if (flags) flag(ws, flags);
-    if (total > 0) all_sync();                               // the tables have been read
+    if (total > 0 && !once) all_sync();                      // the tables have been read
     if (rank != 0) return;
     for (int b = b0; b < b1; ++b) {
         const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
@@ -475,9 +478,9 @@ __global__ void __launch_bounds__(1024, 1)
 }
 
 // ---- carry --------------------------------------------------------------------------------
-// Block (x, b) copies its share of sequence b's summaries; block (0, b) also the rows of its last page, a
-// warp for each KV head, whose summary it makes from them.  HBM bound when many summaries are
-// copied, else latency.
+// Block (x, b) copies its share of sequence b's summaries; block (0, b) also the rows of
+// its last page, a warp for each KV head, whose summary it makes from them.  HBM bound when
+// many summaries are copied, else latency.
 template <int D>
 __global__ void __launch_bounds__(128)
     pages_carry_kernel(se_paged_kv kv, se_page_carry carry, int batch, int* status) {
@@ -634,7 +637,8 @@ cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const
     cudaError_t e = allow_smem(pages_truncate_kernel, 3 * kMaxBatch * sizeof(int), g_truncate_smem);
     if (e != cudaSuccess) return e;
 
-    // a cluster when more pages could be let go than a block takes at once (shared pages count each time)
+    // a cluster when more pages could be let go than a block takes at once (shared pages
+    // count each time)
     int64_t most = (int64_t)batch * pool.max_pages_per_seq;
     if (refs == nullptr) most = std::min<int64_t>(most, pool.num_pages);
     unsigned ranks = 1;

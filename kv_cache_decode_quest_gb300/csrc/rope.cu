@@ -1,17 +1,19 @@
-// Norms of queries and keys per head with the rotation to the token's position (se_qk_rope), and the
-// same ahead of the append of a chunk (se_rope_append_chunk): what a layer does to its packed q | k | v
-// rows before the attention over the paged cache ("长程 agent 把显存撑爆以后", section
-// "四、为什么进不了 vLLM 一类的引擎": pages and a table from tokens to pages).
+// Norms of queries and keys per head with the rotation to the token's position
+// (se_qk_rope), and the same ahead of the append of a chunk (se_rope_append_chunk): what a
+// layer does to its packed q | k | v rows before the attention over the paged cache ("长程
+// agent 把显存撑爆以后", section "四、为什么进不了 vLLM 一类的引擎": pages and a table from tokens to pages).
 //
-// A head's row is x' = R(pos) diag(w) x / sqrt(mean x^2 + eps), R a rotation of pairs of channels by pos * f_i.
-// The angle is kept in turns as a 64-bit fraction: pos * turns[i] mod 2^64 is exact in integers at
-// any position (two 32-bit multiplies), where pos * f_i in fp32 would be off by 2^-24 of the angle
-// itself, 0.06 rad at position 10^6.  Its upper 32 bits are half a turn's signed fraction for sincospif.
+// A head's row is x' = R(pos) diag(w) x / sqrt(mean x^2 + eps), R a rotation of pairs of
+// channels by pos * f_i. The angle is kept in turns as a 64-bit fraction: pos * turns[i]
+// mod 2^64 is exact in integers at any position (two 32-bit multiplies), where pos * f_i in
+// fp32 would be off by 2^-24 of the angle itself, 0.06 rad at position 10^6.  Its upper 32
+// bits are half a turn's signed fraction for sincospif.
 //
-// Layout: a lane owns 8 whole pairs of a head, two 16-byte vectors: with halves, vector j and vector j
-// + rot_dim / 16; with pairs, vectors 2j and 2j + 1.  Either way its angles are 8j .. 8j + 7, no value
-// crosses lanes in the rotation, and a head takes D / 16 lanes: a warp has 512 / D heads side by
-// side.  Channels past rot_dim lie in lanes of their own (cosine 1, sine 0).
+// Layout: a lane owns 8 whole pairs of a head, two 16-byte vectors: with halves, vector j
+// and vector j + rot_dim / 16; with pairs, vectors 2j and 2j + 1.  Either way its angles
+// are 8j .. 8j + 7, no value crosses lanes in the rotation, and a head takes D / 16 lanes:
+// a warp has 512 / D heads side by side.  Channels past rot_dim lie in lanes of their own
+// (cosine 1, sine 0).
 #include <algorithm>
 
 #include "append.cuh"
@@ -36,8 +38,8 @@ struct HeadLane {
     }
 };
 
-// Eight pairs (x, y) of two vectors, two by two in packed fp32: of halves, channel i of one and of the
-// other; of pairs, channels 2i and 2i + 1 of the two as one run.
+// Eight pairs (x, y) of two vectors, two by two in packed fp32: of halves, channel i of one
+// and of the other; of pairs, channels 2i and 2i + 1 of the two as one run.
 template <bool PAIRS>
 __device__ __forceinline__ void to_pairs(uint4 u, uint4 v, uint64_t* x, uint64_t* y) {
     const uint32_t p[4] = {u.x, u.y, u.z, u.w}, q[4] = {v.x, v.y, v.z, v.w};
@@ -111,7 +113,8 @@ struct Turn {
     }
 };
 
-// One head's two vectors of this lane: normed over the head's D / 16 lanes, weighted, rotated, rounded.
+// One head's two vectors of this lane: normed over the head's D / 16 lanes, weighted,
+// rotated, rounded.
 template <int D, bool PAIRS>
 __device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, const Weight& w, float eps,
                                           const Turn& t) {
@@ -159,9 +162,10 @@ struct HeadRows {
 };
 
 // ---- rows of heads --------------------------------------------------------------------------
-// A warp takes a row, or one of `parts` parts of its passes (512 / D heads each, queries first, then keys)
-// when there are few rows.  Its lanes make the row's angles together (two each at most) and hand them round.
-// Few registers and one pass at a time, so that many warps hide the latencies that a row is.
+// A warp takes a row, or one of `parts` parts of its passes (512 / D heads each, queries
+// first, then keys) when there are few rows.  Its lanes make the row's angles together (two
+// each at most) and hand them round. Few registers and one pass at a time, so that many
+// warps hide the latencies that a row is.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(128, 8)
     qk_rope_kernel(se_rope rope, const int32_t* pos, int rows, int parts, HeadRows q, HeadRows k) {
@@ -231,23 +235,38 @@ constexpr int kStages = 2;               // units in flight
 constexpr int kAppendBlocks = 4;         // blocks an SM
 constexpr int kTable = 2 * kRows - 1;    // rows of the table: a piece may reach 15 rows past the block's
 
-// The cosines and sines of the block's rows, in shared memory.  A lane finds its eight of either as four
-// 16-byte words, the lanes' words side by side (no bank conflicts).
+// The cosines and sines of the block's rows, in shared memory.  A lane finds its eight of
+// either as four 16-byte words, the lanes' words side by side (no bank conflicts).
 template <int D, bool PAIRS>
 struct Turns {
     static constexpr int kLanes = D / 16;
     float* table;                        // [rows][4][D / 16][4]
+    // This thread's angles: the same four of every row that it makes.
+    unsigned long long step[4];
+    __device__ __forceinline__ void load(const se_rope& rope) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int i = threadIdx.x % 16 + 16 * k;
+            step[k] = i < rope.rot_dim / 2 ? rope.turns[i] : 0;
+        }
+    }
     // The rows of `mask` behind `first` that have a place (the others' entries mean nothing).
     __device__ __forceinline__ void make(const se_rope& rope, const int32_t* pos, int first, int rows,
                                          uint32_t mask) {
-        const int half = rope.rot_dim / 2;
         for (int r = threadIdx.x / 16; r < kTable; r += blockDim.x / 16) {
             if (!((mask >> r) & 1)) continue;
             const int at = first + r < rows ? pos[first + r] : -1;
             if (at < 0) continue;
-            for (int i = threadIdx.x % 16; i < half; i += 16) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                const int i = threadIdx.x % 16 + 16 * k;
+                float c, s;
+                turn_of(step[k], rope.amplitude, at, c, s);
                 float* t = table + r * D + ((i >> 2 & 1) * kLanes + (i >> 3)) * 4 + (i & 3);
-                turn_of(rope.turns[i], rope.amplitude, at, t[0], t[2 * kLanes * 4]);
+                if (i < rope.rot_dim / 2) {
+                    t[0] = c;
+                    t[2 * kLanes * 4] = s;
+                }
             }
         }
     }
@@ -271,8 +290,9 @@ struct Turns {
     }
 };
 
-// A warp's ring of kStages units of work, each of kPasses passes of two 16-byte vectors a lane: copied in by
-// cp.async while the unit before is worked on.  A lane reads what it copied itself: no barriers.
+// A warp's ring of kStages units of work, each of kPasses passes of two 16-byte vectors a
+// lane: copied in by cp.async while the unit before is worked on.  A lane reads what it
+// copied itself: no barriers.
 constexpr int kRingWords = kStages * kPasses * 64;   // of a warp, 16 bytes each
 struct Ring {
     uint4* mine;                         // this lane's first slot
@@ -282,7 +302,8 @@ struct Ring {
     }
 };
 
-// The passes of the block's rows whose order is free, as a list: n a row, first its queries', then its values'.
+// The passes of the block's rows whose order is free, as a list: n a row, first its
+// queries', then its values'.
 struct PassList {
     HeadRows q;
     const uint4* v;
@@ -312,11 +333,12 @@ __device__ __forceinline__ uint4 shfl_xor4(uint4 x, int o) {
                       __shfl_xor_sync(0xffffffffu, x.z, o), __shfl_xor_sync(0xffffffffu, x.w, o));
 }
 
-// Append of packed rows with the rotation in front.  Pieces as in the plain append: the keys of one sequence's
-// rows in one page, for the KV heads that a warp has side by side (fewer heads: rows beside them), are a
-// warp's job; it rotates them, writes them and folds them, as rounded, into the page's summary, which it
-// owns.  Rows follow one another in a lane, so the fold needs no exchange.  The queries and the values of
-// the block's rows, whose order is free, are dealt out so that all warps have about as much to do.
+// Append of packed rows with the rotation in front.  Pieces as in the plain append: the
+// keys of one sequence's rows in one page, for the KV heads that a warp has side by side
+// (fewer heads: rows beside them), are a warp's job; it rotates them, writes them and folds
+// them, as rounded, into the page's summary, which it owns.  Rows follow one another in a
+// lane, so the fold needs no exchange.  The queries and the values of the block's rows,
+// whose order is free, are dealt out so that all warps have about as much to do.
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(128, kAppendBlocks)
     rope_append_chunk_kernel(se_paged_kv kv, se_rope rope, PassList list, const uint4* k_new,
@@ -332,6 +354,9 @@ __global__ void __launch_bounds__(128, kAppendBlocks)
     const int first = static_cast<int>(blockIdx.x) * kRows;
     const HeadLane<D, PAIRS> l(lane, rope.rot_dim);
     Ring ring = {s_ring + warp * kRingWords + lane};
+    Turns<D, PAIRS> turns;
+    turns.table = s_turns;
+    turns.load(rope);
     const int w = warp + (blockDim.x >> 5) * blockIdx.y, nw = (blockDim.x >> 5) * gridDim.y;
     const Pieces pieces = find_pieces(kv, ck, batch, static_cast<int>(blockIdx.x), lane);
     if (pieces.row.bad && lane >= 1 && lane <= kPage && warp == 0 && blockIdx.y == 0)
@@ -340,23 +365,31 @@ __global__ void __launch_bounds__(128, kAppendBlocks)
     const int side = 1 << side_shift, beside = HP >> side_shift, groups = (H + side - 1) >> side_shift;
     const int sub_head = mine & (side - 1), sub_row = mine >> side_shift;
     const int jobs = __popc(pieces.lead) * groups;
-    // the list's passes: every warp the same work, a warp with a job more of keys that much less
+    // the list's passes: a warp has that much less of them as its jobs take
     const int passes = min(kRows, ck.max_tokens - first) * list.n;
-    const int job_cost = jobs > 0 ? (kRows * groups / beside + jobs - 1) / jobs : 0;
-    const int extra = jobs % nw, back = nw - 1 - w;          // warps with back < extra have one job more
-    const int light = nw - extra;                            // (the first warps)
-    int p0, p1;
-    {
-        // x of a light warp, max(0, x - job_cost) of the others
-        const int heavy = max(0, (passes - light * job_cost) / nw);
-        const int left = passes - heavy * extra;             // for the light ones
-        if (w < light) {
-            p0 = left * w / light;
-            p1 = left * (w + 1) / light;
-        } else {
-            p0 = left + heavy * (w - light);
-            p1 = p0 + heavy;
+    const int back = nw - 1 - w;                             // its first job
+    int p0 = passes * w / nw, p1 = passes * (w + 1) / nw;
+    if (nw <= 4 && jobs <= 64) {
+        int cost = 0, all = 0;                               // lane i: of warp i's jobs
+        for (int i = 0, job = 0; job < jobs; ++i) {
+            const Piece pc = piece_at(pieces, i, lane);
+            const int span = (32 - __clz(pc.rows) + beside - 1) / beside;
+            for (int g = 0; g < groups; ++g, ++job) {
+                if (job % nw == nw - 1 - lane) cost += span;
+                all += span;
+            }
         }
+        int share = lane < nw ? max(0, (passes + all + nw - 1) / nw - cost) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, share, o);
+            if (lane >= o) share += x;
+        }
+        const int total = max(1, __shfl_sync(0xffffffffu, share, 31));
+        const int upto = __shfl_sync(0xffffffffu, share, w);
+        const int before = __shfl_sync(0xffffffffu, share, max(w - 1, 0));
+        p0 = passes * (w > 0 ? before : 0) / total;
+        p1 = passes * upto / total;
     }
     const int units = (p1 - p0 + kPasses - 1) / kPasses;
     int copy_job = back, copy_sub = 0;
@@ -404,8 +437,8 @@ __global__ void __launch_bounds__(128, kAppendBlocks)
     for (int k = 0; k < kStages; ++k) copy_next();
     if (warp == 0 && blockIdx.y == 0)
         commit_lengths(kv, ck, batch, pieces.t, lane, pieces.row);
-    // the rows whose angles the block's warps need (bits 16 and up: a piece may reach past the block's rows)
-    Turns<D, PAIRS> turns = {s_turns};
+    // the rows whose angles the block's warps need (bits 16 and up: a piece may reach past
+    // the block's rows)
     uint32_t need = 0;
     if (p0 < p1) need = (2u << list.row_of(p1 - 1)) - (1u << list.row_of(p0));
     for (int job = back; job < jobs; job += nw) {
@@ -549,8 +582,8 @@ cudaError_t append_of(const se_paged_kv& kv, const se_rope& rope, const HeadArgs
     const uint4* k = static_cast<const uint4*>(k_new);
     // few rows: several blocks share 16 of them, down to one pass a warp
     const int share = std::max(1, std::min(kAppendBlocks * num_sms() / groups, (kRows * (list.n + H) + 3) / 4));
-    // KV heads side by side in a job of keys: many rows: as many as there are (a row's rotation serves them
-    // together); few rows: one, so that a piece is several short jobs
+    // KV heads side by side in a job of keys: many rows: as many as there are (a row's
+    // rotation serves them together); few rows: one, so that a piece is several short jobs
     int side_shift = 0;
     while (share == 1 && (2 << side_shift) <= std::min(H, HP)) ++side_shift;
     return launch_pdl(rope_append_chunk_kernel<D, PAIRS>, dim3(groups, share), dim3(128), 0, s, kv, rope, list,

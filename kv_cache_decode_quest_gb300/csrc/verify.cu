@@ -1,15 +1,18 @@
-// Drafted tokens against the target's probabilities (se_draft_verify): which of them stay, and the token
-// that is drawn behind them.  Draft d with u q(d) < p(d) stays; behind the first refused one the next
-// token comes from max(0, p - q), which leaves every token distributed as p.
+// Drafted tokens against the target's probabilities (se_draft_verify): which of them stay,
+// and the token that is drawn behind them.  Draft d with u q(d) < p(d) stays; behind the
+// first refused one the next token comes from max(0, p - q), which leaves every token
+// distributed as p.
 //
-// One row of the vocabulary per sequence is read (two where a draft was refused): HBM bound, a sum and a
-// search.  A draw compares a running sum of up to millions of weights with a random part of the whole:
-// sums in fp32 would move it over a border in about one of 30 draws over 128K tokens.  So a weight is
-// p - q with its rounding error beside it (exact together), a lane's sum of 32 weights carries its error
-// in a second word, and from there on sums are integers in units of 2^-58, the same in any order:
-// the row is cut into tiles of 1024 that any warp of any block may sum, and the last block of a
-// sequence finds the tile and in it the token.  15 fp32 operations a weight, hidden behind the loads; fp64
-// sums, or every weight made a 64-bit integer, are bound by those units' rates (4 times slower).
+// One row of the vocabulary per sequence is read (two where a draft was refused): HBM
+// bound, a sum and a search.  A draw compares a running sum of up to millions of weights
+// with a random part of the whole: sums in fp32 would move it over a border in about one of
+// 30 draws over 128K tokens.  So a weight is p - q with its rounding error beside it (exact
+// together), a lane's sum of 32 weights carries its error in a second word, and from there
+// on sums are integers in units of 2^-58, the same in any order: the row is cut into tiles
+// of 1024 that any warp of any block may sum, and the last block of a sequence finds the
+// tile and in it the token.  15 fp32 operations a weight, hidden behind the loads; fp64
+// sums, or every weight made a 64-bit integer, are bound by those units' rates (4 times
+// slower).
 #include <algorithm>
 
 #include "common.cuh"
@@ -67,7 +70,8 @@ __device__ __forceinline__ void widen(uint4 w, float* x) {
     }
 }
 
-// A row of the vocabulary: of p, of q (NULL: none is taken off), and the token without weight (-1: none).
+// A row of the vocabulary: of p, of q (NULL: none is taken off), and the token without
+// weight (-1: none).
 template <typename T>
 struct Row {
     const T* p;
@@ -148,8 +152,9 @@ __device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
     return warp_sum(sum.units());
 }
 
-// Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads call it, with two
-// buffers in turn (the values read last must not be written by the next call).
+// Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads
+// call it, with two buffers in turn (the values read last must not be written by the next
+// call).
 __device__ __forceinline__ u64 block_sum_before(u64 x, u64* tmp, u64* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     u64 y = x;

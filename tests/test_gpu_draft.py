@@ -206,3 +206,38 @@ def test_quest_decodes_from_a_forked_cache():
     # the tokens went to pages of their own
     a, b = run.pool.block_table[:, L // 16].tolist()
     assert a != b and run.pool.block_table[0, :L // 16].equal(run.pool.block_table[1, :L // 16])
+
+
+def test_two_runs_on_two_streams():
+    """Steps of two runs in flight at once, each with workspaces of its own: as one after the other."""
+    B, rows, vocab, D = 6, 48, 4000, 64
+    new, make = i32([8] * B), lambda: DraftRun(B, 4, 2, D, num_pages=200, max_pages=30, max_rows=rows,   # noqa: E731
+                                               vocab=vocab, ropes=[se.Rope.make(D), se.Rope.make(32)])
+    g = np.random.default_rng(44)
+    data = []
+    for _ in range(2):
+        x = g.standard_normal((rows, vocab)) * 2
+        p = torch.softmax(torch.from_numpy(x).float(), 1).cuda()
+        qkv = [torch.from_numpy(g.standard_normal((rows, 8, D))).bfloat16().cuda() for _ in range(2)]
+        data.append((qkv, p, i32(np.roll(x.argmax(1), 1)), torch.from_numpy(g.random(rows)).float().cuda(),
+                     torch.from_numpy(g.random(B)).float().cuda()))
+
+    def step(run, d):
+        run.feed(d[0], new)
+        run.check(d[1], None, d[2], d[3], d[4])
+    alone, both = [make(), make()], [make(), make()]
+    for run, d in zip(alone, data):
+        for _ in range(6):
+            step(run, d)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(6):
+        for run, d, s in zip(both, data, streams):
+            with torch.cuda.stream(s):
+                step(run, d)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert a.status() == b.status() == 0
+        for x, y in ((a.keep, b.keep), (a.next_token, b.next_token), (a.kv[1].k, b.kv[1].k),
+                     (a.kv[0].meta, b.kv[0].meta), (a.pool.free_pages, b.pool.free_pages)):
+            assert x.equal(y)

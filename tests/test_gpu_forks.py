@@ -360,3 +360,59 @@ def test_replayed_from_a_graph():
         of.carry(b.o, x.k, x.v, x.meta, fs, fp)
         x.same(b)
         x.append(b, b.grow([n, 0, 0, 0, 0]))
+
+
+def test_more_entries_than_the_cluster_holds_at_once():
+    """Hundreds of samples of one long prompt let go together, and all but one of them: the pages that
+    come back, their order and the counts."""
+    g = np.random.default_rng(37)
+    pages, batch, maxp = 5000, 420, 2010
+    b = Both(pages, batch, maxp, g)
+    b.grow([2003 * 16 + 5] + [0] * (batch - 1))
+    src = np.full(batch, -1)
+    src[1:] = 0
+    for keep in (0, 1000 * 16 + 3):
+        assert b.fork(src) == 0 and max(b.o_refs) == batch - 1
+        some = np.full(batch, keep)
+        some[[0, 17]] = -1, -1
+        if keep:
+            some[5:200] = 0                                      # others keep a part, in pages of their own
+        assert b.cut(some) == 0
+        assert b.cut(np.where(np.arange(batch) == 0, -1, 0)) == 0 and max(b.o_refs) == 0
+    assert b.cut([0] * batch) == 0 and sorted(b.o.free) == list(range(pages))
+
+
+FIRST_CALL = """
+import torch
+from kv_cache_decode_quest_gb300 import binding as se
+B, pages, maxp = 20, 20000, 900
+pool = se.PagePool.empty(B, pages, maxp)
+refs, carry = torch.zeros(pages, dtype=torch.int32, device="cuda"), se.Carry.empty(B)
+ws = se.workspace(se.se_pages_truncate_workspace(B, pages))
+keep = torch.zeros(B, dtype=torch.int32, device="cuda")
+src = torch.tensor([-1] + [0] * (B - 1), dtype=torch.int32, device="cuda")
+new = torch.tensor([14000] + [0] * (B - 1), dtype=torch.int32, device="cuda")
+chunk = se.Chunk.empty(B, 14000)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    se.se_chunk_plan(pool, new, B, chunk, ws)
+    pool.ctx_len[:1] = 14000
+    se.se_pages_fork(pool, refs, src, B, carry, ws)
+    se.se_pages_truncate(pool, refs, keep, B, carry, ws)
+for _ in range(2):
+    graph.replay()
+    torch.cuda.synchronize()
+    assert se.status_word(ws) == 0 and int(pool.n_free) == pages and not refs.any()
+    assert not ws[4:].any() and pool.free_pages.flip(0).equal(torch.arange(pages, device="cuda").int())
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
+                       timeout=250)
+    assert r.returncode == 0, r.stderr[-2000:]
