@@ -19,8 +19,9 @@
 namespace se {
 namespace {
 
-constexpr int kMaxBatch = 8192;              // first entry and state of every sequence in shared memory
-constexpr int kWhoWord = 128;                // workspace words of the pages (se_pages_truncate), zero between calls
+constexpr int kMaxBatch = 8192;              // sequences whose entries shared memory numbers
+constexpr int kWhoWord = 128;                // a workspace word for each page from here on, zero
+                                             // between calls (se_pages_truncate)
 
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
@@ -74,7 +75,8 @@ struct Fork {
     int src, ctx, flags;
     bool want, page;             // to be forked; needs a page of its own
 };
-__device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* src, int batch, int b) {
+__device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* src, int batch,
+                                        int b) {
     Fork f = {src[b], 0, 0, false, false};
     if (f.src < 0) return f;
     if (f.src >= batch) {
@@ -96,8 +98,8 @@ __device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* sr
 
 // Every block scans all sequences (a thread a run of them) and writes its share of the
 // table entries; the last block to finish, which has read what the others have, commits
-// counts and lengths. Latency bound but for many long forks (a table entry and an atomic
-// count for each page).
+// counts and lengths.  Latency bound: four samples of a 2K prompt about 4 us, 64 of a 32K one
+// (131,008 table entries, each with an atomic count) 9.
 __global__ void __launch_bounds__(1024, 1)
     pages_fork_kernel(se_page_pool pool, int32_t* refs, const int32_t* src, int batch,
                       se_page_carry carry, int* ws) {
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(1024, 1)
     }
     block_scan2(asked, entries, tmp, &asks, &all);
     long long run = asked, at = entries;
-    bool less = false;                       // a sequence is not served: those behind it have fewer before them
+    bool less = false;                       // one is not served: fewer entries before the next
     for (int b = b0; b < b1; ++b) {
         const Fork f = b == b0 ? mine : fork_of(pool, src, batch, b);
         flags |= f.flags;
@@ -180,8 +182,9 @@ __global__ void __launch_bounds__(1024, 1)
             from_seq = src[b];
             const int ctx = pool.ctx_len[from_seq];
             if (fresh >= 0) {
-                from_page = pool.block_table[(int64_t)from_seq * pool.max_pages_per_seq + ctx / kPage];
-                pool.block_table[(int64_t)b * pool.max_pages_per_seq + ctx / kPage] = fresh;
+                const int64_t maxp = pool.max_pages_per_seq;
+                from_page = pool.block_table[from_seq * maxp + ctx / kPage];
+                pool.block_table[b * maxp + ctx / kPage] = fresh;
             }
             pool.ctx_len[b] = ctx;
             pool.n_pages[b] = (ctx + kPage - 1) / kPage;
@@ -201,8 +204,8 @@ struct Cut {
     int last, flags;             // the page that is then its last
     bool act, copy;              // cut at all; needs a page of its own for the last one's rows
 };
-__device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs, const int32_t* keep,
-                                      int b) {
+__device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs,
+                                      const int32_t* keep, int b) {
     Cut c = {keep[b], p.ctx_len[b], p.n_pages[b], 0, -1, 0, false, false};
     if (c.n < 0) return c;
     if (!consistent(p, c.ctx, c.held)) {
@@ -233,7 +236,12 @@ __device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs
 //   push        freed entries to their place by a running sum, counts and notes back to zero
 //   commit      tables, lengths, the stack's top
 // Few entries (a decode step's: a page here and there) are the first block's alone; then the
-// others leave after the scan.  Latency bound throughout.
+// others leave after the scan.
+// Latency bound: nothing let go 4 us, a decode step's pages 7 to 11, 64 samples of a 32K prompt
+// (131,008 entries, all of shared pages) about 24: random counts from 16 SMs.  With cold
+// caches: on one block 1694 us, on eight 82, on sixteen, with the entries that the next
+// sequence follows uncounted, 36, each thread's entries fetched once 28.  A launch over all
+// SMs would need a barrier across them for each phase.
 constexpr int kEntries = 8;                  // of a thread at once, at most
 
 __global__ void __launch_bounds__(1024, 1)
@@ -244,7 +252,7 @@ __global__ void __launch_bounds__(1024, 1)
     extern __shared__ __align__(16) int smem[];
     int* s_first = smem;                     // [batch] first of the sequence's entries
     int* s_base = smem + batch;              // [batch] logical page of its first entry
-    int* s_fresh = smem + 2 * batch;         // [batch] own page for the last rows; -1: none; -2: not cut
+    int* s_fresh = smem + 2 * batch;         // [batch] page for the last rows; -1: none; -2: not cut
     __shared__ long long tmp[66];
     __shared__ int s_count, s_scan[33];
     int* who = ws + kWhoWord;
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(1024, 1)
     }
     block_scan2(asked, entries, tmp, &asks, &all);
     long long run = asked, at = entries;
-    bool less = false;                       // a sequence is not served: those behind it have fewer before them
+    bool less = false;                       // one is not served: fewer entries before the next
     for (int b = b0; b < b1; ++b) {
         const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
         flags |= c.flags;
@@ -323,6 +331,7 @@ __global__ void __launch_bounds__(1024, 1)
     uint32_t open = 0;                       // bit r: entry r may be its page's last of this call
     bool have = false;
     uint32_t freed_bits = 0, last_bits = 0;  // of the first eight steps: found once
+    auto first_of = [&](int b) { return b < batch ? s_first[b] : total; };
     auto fetch = [&](int base) {
         if (!have || e1 - e0 > step) {                       // (a single step's stay in registers)
             have = true;
@@ -337,13 +346,14 @@ __global__ void __launch_bounds__(1024, 1)
                 if (r < each && i0 + r < e1) {
                     while (k + 1 < batch && s_first[k + 1] <= i0 + r) ++k;
                     const int at = s_base[k] + (i0 + r - s_first[k]);
-                    const int32_t* table = pool.block_table + (int64_t)k * pool.max_pages_per_seq + at;
+                    const int32_t* table =
+                        pool.block_table + (int64_t)k * pool.max_pages_per_seq + at;
                     seq[r] = k;
                     page[r] = table[0];
                     // samples of one prompt lie side by side: where the next sequence lets go of
                     // the same page, this entry is not the last, and asks no counter
                     const int j = at - s_base[min(k + 1, batch - 1)];
-                    const int n = k + 1 < batch ? (k + 2 < batch ? s_first[k + 2] : total) - s_first[k + 1] : 0;
+                    const int n = k + 1 < batch ? first_of(k + 2) - s_first[k + 1] : 0;
                     if (refs != nullptr && j >= 0 && j < n) next[r] = table[pool.max_pages_per_seq];
                 }
             }
@@ -376,7 +386,7 @@ __global__ void __launch_bounds__(1024, 1)
         return m;
     };
     int before = 0, all_freed = 0, place = 0;
-    const bool once = total <= step && !wide;                // each thread's entries are in its registers
+    const bool once = total <= step && !wide;                // the entries are all in registers
     if (total > 0) {
         if (shared && once) {
             // pages that one sequence holds, as most are, need no counting
@@ -480,7 +490,9 @@ __global__ void __launch_bounds__(1024, 1)
 // ---- carry --------------------------------------------------------------------------------
 // Block (x, b) copies its share of sequence b's summaries; block (0, b) also the rows of
 // its last page, a warp for each KV head, whose summary it makes from them.  HBM bound when
-// many summaries are copied, else latency.
+// many summaries are copied (64 samples of a 32K prompt: 268 MB written in 43.9 us, 6.1 TB/s,
+// their source read once into L2), else latency (2.6 to 4.3 us).  At 64 registers, twice the
+// warps, 42 to 50 us.
 template <int D>
 __global__ void __launch_bounds__(128)
     pages_carry_kernel(se_paged_kv kv, se_page_carry carry, int batch, int* status) {
@@ -504,7 +516,8 @@ __global__ void __launch_bounds__(128)
             const uint4* src = M + from_seq * seq_vecs;
             uint4* dst = M + b * seq_vecs;
             const int64_t vecs = (n / kPage) * page_vecs, step = (int64_t)gridDim.x * blockDim.x;
-            for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs; i += U * step) {
+            for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < vecs;
+                 i += U * step) {
                 uint4 x[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u)
@@ -574,9 +587,6 @@ __global__ void __launch_bounds__(128)
     }
 }
 
-#ifndef TTHREADS
-#define TTHREADS 1024
-#endif
 // Blocks of the truncation's cluster: 16 where the device has room for such a cluster, else the
 // portable 8 (found once per device).
 cudaError_t cluster_blocks(cudaLaunchConfig_t cfg, unsigned* blocks) {
@@ -586,7 +596,8 @@ cudaError_t cluster_blocks(cudaLaunchConfig_t cfg, unsigned* blocks) {
     if (e != cudaSuccess) return e;
     int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
     if (n == 0) {
-        e = cudaFuncSetAttribute(pages_truncate_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        e = cudaFuncSetAttribute(pages_truncate_kernel,
+                                 cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -628,8 +639,8 @@ cudaError_t launch_pages_fork(const se_page_pool& pool, int32_t* refs, const int
     // a block for every 1024 table entries that could be written
     const int grid = static_cast<int>(std::max<int64_t>(
         1, std::min<int64_t>(num_sms(), (int64_t)batch * pool.max_pages_per_seq / 1024)));
-    return launch_pdl(pages_fork_kernel, dim3(grid), dim3(nt), 2 * batch * sizeof(int), s, pool, refs,
-                      src, batch, carry, ws);
+    return launch_pdl(pages_fork_kernel, dim3(grid), dim3(nt), 2 * batch * sizeof(int), s, pool,
+                      refs, src, batch, carry, ws);
 }
 
 cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const int32_t* keep,
@@ -645,7 +656,7 @@ cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(table_threads(batch));
     if (most > 4 * 1024) {
-        cfg.blockDim = dim3(TTHREADS);
+        cfg.blockDim = dim3(1024);
         e = cluster_blocks(cfg, &ranks);
         if (e != cudaSuccess) return e;
     }
@@ -663,8 +674,8 @@ cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const
     return cudaLaunchKernelEx(&cfg, pages_truncate_kernel, pool, refs, keep, batch, carry, ws);
 }
 
-cudaError_t launch_pages_carry(const se_paged_kv& kv, const se_page_carry& carry, int batch, int* status,
-                               cudaStream_t s) {
+cudaError_t launch_pages_carry(const se_paged_kv& kv, const se_page_carry& carry, int batch,
+                               int* status, cudaStream_t s) {
     // a block moves 16 KB of summaries at once; as many a sequence as fill the GPU
     const int64_t vecs = (int64_t)kv.max_pages_per_seq * kv.num_kv_heads * kv.head_dim / 4;
     const int split = static_cast<int>(std::max<int64_t>(

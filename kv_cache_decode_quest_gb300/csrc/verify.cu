@@ -10,9 +10,10 @@
 // together), a lane's sum of 32 weights carries its error in a second word, and from there
 // on sums are integers in units of 2^-58, the same in any order: the row is cut into tiles
 // of 1024 that any warp of any block may sum, and the last block of a sequence finds the
-// tile and in it the token.  15 fp32 operations a weight, hidden behind the loads; fp64
-// sums, or every weight made a 64-bit integer, are bound by those units' rates (4 times
-// slower).
+// tile and in it the token.  15 fp32 operations a weight, hidden behind the loads.
+// 256 sequences over 131,072 tokens (about 1.6 rows each) take 43.5 us, 4.9 TB/s: 72% of the
+// copy rate; the rest is three latencies before a block knows its row, and the last
+// sequences' search.  Every weight made a 64-bit integer 122 us; two waves of blocks 52.
 #include <algorithm>
 
 #include "common.cuh"
@@ -186,14 +187,10 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
     return s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? hi >> (s - 64) : 0;
 }
 
-#ifndef VS
-#define VS 4
-#endif
-#ifndef VMIN
-#define VMIN 4
-#endif
+constexpr int kBlocks = 4;                   // blocks an SM
+
 template <typename T>
-__global__ void __launch_bounds__(256, VMIN)
+__global__ void __launch_bounds__(256, kBlocks)
     draft_verify_kernel(const T* probs, const T* draft, int64_t row_stride, int vocab, int tiles,
                         const int32_t* tokens, const float* accept_u, const float* sample_u,
                         const int32_t* start, const int32_t* pos, int max_tokens,
@@ -342,7 +339,8 @@ __global__ void __launch_bounds__(256, VMIN)
 
 int draft_verify_max_batch() { return kMaxBatch; }
 
-static int verify_tiles(int vocab) { return (vocab + 7 + kTile - 1) / kTile; }   // rows may begin off a boundary
+// (rows may begin off a 16-byte boundary: up to 7 places more)
+static int verify_tiles(int vocab) { return (vocab + 7 + kTile - 1) / kTile; }
 
 size_t draft_verify_ws_bytes(int batch, int vocab) {
     return (kSumsAt + (size_t)batch * verify_tiles(vocab) * sizeof(u64) + 255) & ~(size_t)255;
@@ -354,8 +352,8 @@ cudaError_t launch_draft_verify(const void* probs, const void* draft, int64_t ro
                                 int batch, int32_t* n_accepted, int32_t* next_token, int32_t* keep,
                                 int* ws, cudaStream_t s) {
     const int tiles = verify_tiles(vocab);
-    // a block's eight warps have a tile each at least; up to eight blocks an SM
-    const int split = std::max(1, std::min((tiles + 7) / 8, VS * num_sms() / batch));
+    // a block's eight warps have a tile each at least; one wave of blocks
+    const int split = std::max(1, std::min((tiles + 7) / 8, kBlocks * num_sms() / batch));
     const dim3 grid(split, batch);
     if (prob_dtype == 1)
         return launch_pdl(draft_verify_kernel<float>, grid, dim3(256), 0, s,
