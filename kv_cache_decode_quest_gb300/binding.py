@@ -426,7 +426,7 @@ class Rope(_Measured):
             raise SparseEngineError(f"Rope.turns: contiguous int64 tensor needed, got {t.dtype}")
         if self.rot_dim and (t is None or 2 * t.numel() < self.rot_dim):
             raise SparseEngineError(f"Rope.turns: {self.rot_dim // 2} entries needed")
-        widths = {1 << 20}
+        widths = set()
         for name in ("q_weight", "k_weight"):
             w = getattr(self, name)
             if w is not None:
@@ -434,7 +434,9 @@ class Rope(_Measured):
                     raise SparseEngineError(f"Rope.{name}: contiguous bfloat16 [head_dim] needed, got "
                                             f"{w.dtype} of shape {tuple(w.shape)}")
                 widths.add(w.numel())
-        return min(widths)
+        if len(widths) > 1:
+            raise SparseEngineError("Rope: norm weights of two lengths")
+        return widths.pop() if widths else 0
 
     @property
     def c(self) -> RopeC:
@@ -673,6 +675,14 @@ def se_rope_turns(rot_dim: int, base: float = 10000.0, scaling: int = SE_ROPE_PL
     return turns, amplitude.value
 
 
+def _rope_fits(rope: Rope, dim: int, what: str):
+    n = rope._sequences
+    if n is None:
+        n = rope.__dict__["_sequences"] = rope._measure()
+    if n and n != dim:
+        raise SparseEngineError(f"{what}: norm weights of {n} channels, heads of {dim}")
+
+
 def _rotated(x, out, rows: int, what: str):
     """(heads, head_dim, stride, out stride) of rows of heads and the tensor they go to."""
     if x is None or out is None:
@@ -705,7 +715,7 @@ def se_qk_rope(rope: Rope, pos, q, k, q_out, k_out, ws, stream=None):
     if hq and hk and dim != dim_k:
         raise SparseEngineError(f"se_qk_rope: q of {dim} channels a head, k of {dim_k}")
     dim = dim or dim_k
-    _holds(rope, dim, "se_qk_rope: head_dim")
+    _rope_fits(rope, dim, "se_qk_rope")
     here = _on_device("se_qk_rope", (rope,), pos, ws, q, k, q_out, k_out)
     c = rope.c
     rc = load().se_qk_rope(ctypes.byref(c), pos.data_ptr(), rows, hq, hk, dim, _p(q), sq, _p(k), sk,
@@ -729,7 +739,7 @@ def se_rope_append_chunk(kv: PagedKV, rope: Rope, q, k_new, v_new, q_out, chunk:
     hq, dim_q, sq, oq = _rotated(q, q_out, rows, "se_rope_append_chunk q")
     if hq and dim_q != dim:
         raise SparseEngineError(f"se_rope_append_chunk: q of {dim_q} channels a head, the cache of {dim}")
-    _holds(rope, dim, "se_rope_append_chunk: head_dim")
+    _rope_fits(rope, dim, "se_rope_append_chunk")
     _holds(kv, batch, "se_rope_append_chunk")
     _holds(chunk, 0, "se_rope_append_chunk")
     here = _on_device("se_rope_append_chunk", (kv, rope, chunk), k_new, v_new, ws, q, q_out)

@@ -243,6 +243,7 @@ __device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs
 // sequence follows uncounted, 36, each thread's entries fetched once 28.  A launch over all
 // SMs would need a barrier across them for each phase.
 constexpr int kEntries = 8;                  // of a thread at once, at most
+constexpr int kAsks = -3;                    // asks for a page of its own
 
 __global__ void __launch_bounds__(1024, 1)
     pages_truncate_kernel(se_page_pool pool, int32_t* refs, const int32_t* keep, int batch,
@@ -262,39 +263,39 @@ __global__ void __launch_bounds__(1024, 1)
     // this thread's sequences [b0, b1)
     const int per = (batch + nt - 1) / nt;
     const int b0 = min(static_cast<int>(threadIdx.x) * per, batch), b1 = min(b0 + per, batch);
-    Cut mine = {-1, 0, 0, 0, -1, 0, false, false};
-    if (b0 < b1) mine = cut_of(pool, refs, keep, b0);
+    Cut mine = {-1, 0, 0, 0, -1, 0, false, false};           // (the first of them)
     long long asked = 0, entries = 0, asks, all;
     for (int b = b0; b < b1; ++b) {
-        const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
+        const Cut c = cut_of(pool, refs, keep, b);
+        if (b == b0) mine = c;
+        flags |= c.flags;
+        s_fresh[b] = !c.act ? -2 : c.copy ? kAsks : -1;
+        s_base[b] = c.after - c.copy;
+        s_first[b] = c.act ? c.held - s_base[b] : 0;         // (their count, so far)
         asked += c.copy;
-        entries += c.act ? c.held - c.after + c.copy : 0;
+        entries += s_first[b];
     }
     block_scan2(asked, entries, tmp, &asks, &all);
-    long long run = asked, at = entries;
     bool less = false;                       // one is not served: fewer entries before the next
     for (int b = b0; b < b1; ++b) {
-        const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
-        flags |= c.flags;
-        int fresh = c.act ? -1 : -2;
-        if (c.copy) {
-            ++run;
-            if (run > n_free) {
+        if (s_fresh[b] == kAsks) {
+            ++asked;
+            int fresh = -2;
+            if (asked > n_free) {
                 flags |= SE_DEV_CAPACITY;
-                fresh = -2;
             } else {
-                fresh = pool.free_pages[n_free - run];
+                fresh = pool.free_pages[n_free - asked];
                 if (!in_pool(pool, fresh)) {
                     flags |= SE_DEV_BAD_INDEX;
                     fresh = -2;
                 }
             }
+            s_fresh[b] = fresh;
             less |= fresh == -2;
         }
-        s_fresh[b] = fresh;
-        s_base[b] = c.after - (fresh >= 0);
-        s_first[b] = static_cast<int>(min(at, 0x7fffffffll));
-        at += c.act ? c.held - c.after + c.copy : 0;
+        const int n = s_first[b];
+        s_first[b] = static_cast<int>(min(entries, 0x7fffffffll));
+        entries += n;
     }
     if (__syncthreads_or(less)) {
         auto lets = [&](int b) { return s_fresh[b] == -2 ? 0 : pool.n_pages[b] - s_base[b]; };
@@ -327,159 +328,143 @@ __global__ void __launch_bounds__(1024, 1)
     const int e0 = static_cast<int>((long long)total * rank / ranks);
     const int e1 = static_cast<int>((long long)total * (rank + 1) / ranks);
     const int each = min(kEntries, max(1, (e1 - e0 + nt - 1) / nt)), step = nt * each;
+    const bool once = e1 - e0 <= step;       // they stay in registers
+    auto first_of = [&](int b) { return b < batch ? s_first[b] : total; };
     int page[kEntries], seq[kEntries];
     uint32_t open = 0;                       // bit r: entry r may be its page's last of this call
-    bool have = false;
-    uint32_t freed_bits = 0, last_bits = 0;  // of the first eight steps: found once
-    auto first_of = [&](int b) { return b < batch ? s_first[b] : total; };
-    auto fetch = [&](int base) {
-        if (!have || e1 - e0 > step) {                       // (a single step's stay in registers)
-            have = true;
-            open = 0;
-            const int i0 = base + threadIdx.x * each;
-            int k = owner_of(s_first, batch, min(i0, e1 - 1)), next[kEntries];
+    uint32_t freed_bits = 0, last_bits = 0;  // of the first steps: found once
+    bool have = false, shared = refs != nullptr, fits = true;
+    int before = 0, all_freed = 0, place = 0, top = 0, count = 0;
+    // probe: does any entry's page have other holders (as most have not: nothing to count)?
+    enum { kProbe, kCountDown, kCount, kPush, kEnd };
+    int phase = total == 0 ? kEnd : !shared ? kCount : once && !wide ? kProbe : kCountDown;
+    while (phase != kEnd) {
+        bool any = false;
+        int k = 0;
+        for (int base = e0; base < e1; base += step, ++k) {
+            if (!have || !once) {
+                have = true;
+                open = 0;
+                const int i0 = base + threadIdx.x * each;
+                int b = owner_of(s_first, batch, min(i0, e1 - 1)), next[kEntries];
 #pragma unroll
-            for (int r = 0; r < kEntries; ++r) {
-                page[r] = -1;
-                next[r] = -1;
-                seq[r] = 0;
-                if (r < each && i0 + r < e1) {
-                    while (k + 1 < batch && s_first[k + 1] <= i0 + r) ++k;
-                    const int at = s_base[k] + (i0 + r - s_first[k]);
-                    const int32_t* table =
-                        pool.block_table + (int64_t)k * pool.max_pages_per_seq + at;
-                    seq[r] = k;
-                    page[r] = table[0];
-                    // samples of one prompt lie side by side: where the next sequence lets go of
-                    // the same page, this entry is not the last, and asks no counter
-                    const int j = at - s_base[min(k + 1, batch - 1)];
-                    const int n = k + 1 < batch ? first_of(k + 2) - s_first[k + 1] : 0;
-                    if (refs != nullptr && j >= 0 && j < n) next[r] = table[pool.max_pages_per_seq];
+                for (int r = 0; r < kEntries; ++r) {
+                    page[r] = next[r] = -1;
+                    seq[r] = 0;
+                    if (r < each && i0 + r < e1) {
+                        while (b + 1 < batch && s_first[b + 1] <= i0 + r) ++b;
+                        const int at = s_base[b] + (i0 + r - s_first[b]);
+                        const int32_t* table =
+                            pool.block_table + (int64_t)b * pool.max_pages_per_seq + at;
+                        seq[r] = b;
+                        page[r] = table[0];
+                        // samples of one prompt lie side by side: where the next sequence lets
+                        // go of the same page, this entry is not the last, and asks no counter
+                        const int j = at - s_base[min(b + 1, batch - 1)];
+                        const int n = b + 1 < batch ? first_of(b + 2) - s_first[b + 1] : 0;
+                        if (shared && j >= 0 && j < n) next[r] = table[pool.max_pages_per_seq];
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < kEntries; ++r) {
+                    if (r < each && i0 + r < e1 && !in_pool(pool, page[r])) {
+                        flags |= SE_DEV_BAD_INDEX;
+                        page[r] = -1;
+                    }
+                    if (page[r] != next[r]) open |= 1u << r;
                 }
             }
-#pragma unroll
-            for (int r = 0; r < kEntries; ++r) {
-                if (r < each && i0 + r < e1 && !in_pool(pool, page[r])) {
-                    flags |= SE_DEV_BAD_INDEX;
-                    page[r] = -1;
-                }
-                if (page[r] != next[r]) open |= 1u << r;
-            }
-        }
-    };
-    // Bit r: entry r is freed; of `last`: it is its page's last of this call.
-    bool shared = refs != nullptr;
-    auto freed = [&](uint32_t& last) {
-        uint32_t m = 0;
-        last = 0;
-#pragma unroll
-        for (int r = 0; r < kEntries; ++r) {
-            if (page[r] < 0) continue;
-            if (!shared) {
-                m |= 1u << r;
-            } else if ((open >> r) & 1) {
-                const int n = __ldcg(refs + page[r]), of = __ldcg(who + page[r]);
-                if (of == seq[r] + 1) last |= 1u << r;
-                if (n < 0 && of == seq[r] + 1) m |= 1u << r;
-            }
-        }
-        return m;
-    };
-    int before = 0, all_freed = 0, place = 0;
-    const bool once = total <= step && !wide;                // the entries are all in registers
-    if (total > 0) {
-        if (shared && once) {
-            // pages that one sequence holds, as most are, need no counting
-            fetch(e0);
-            bool any = false;
-#pragma unroll
-            for (int r = 0; r < kEntries; ++r)
-                if (page[r] >= 0) any |= refs[page[r]] > 0;
-            shared = __syncthreads_or(any);
-        }
-        if (shared) {
-            for (int base = e0; base < e1; base += step) {
-                fetch(base);
+            // bit r of m: entry r is freed; of last: it is its page's last of this call
+            uint32_t m = 0, last = 0;
+            if (phase == kPush && k < 32 / kEntries) {
+                m = freed_bits >> (k * kEntries) & ((1u << kEntries) - 1);
+                last = last_bits >> (k * kEntries) & ((1u << kEntries) - 1);
+            } else if (phase >= kCount) {
 #pragma unroll
                 for (int r = 0; r < kEntries; ++r) {
                     if (page[r] < 0) continue;
-                    atomicSub(refs + page[r], 1);
-                    if ((open >> r) & 1) atomicMax(who + page[r], seq[r] + 1);
+                    if (!shared) {
+                        m |= 1u << r;
+                    } else if ((open >> r) & 1) {
+                        const int n = __ldcg(refs + page[r]), of = __ldcg(who + page[r]);
+                        if (of == seq[r] + 1) last |= 1u << r;
+                        if (n < 0 && of == seq[r] + 1) m |= 1u << r;
+                    }
                 }
             }
+            if (phase == kCount) {
+                count += __popc(m);
+                if (k < 32 / kEntries) {
+                    freed_bits |= m << (k * kEntries);
+                    last_bits |= last << (k * kEntries);
+                }
+                continue;
+            }
+            int tile = 0;
+            if (phase == kPush && !(once && !wide))
+                place = block_exclusive_scan(__popc(m), s_scan, &tile);
+#pragma unroll
+            for (int r = 0; r < kEntries; ++r) {
+                const int p = page[r];
+                if (p < 0) continue;
+                if (phase == kProbe) {
+                    any |= refs[p] > 0;
+                } else if (phase == kCountDown) {
+                    atomicSub(refs + p, 1);
+                    if ((open >> r) & 1) atomicMax(who + p, seq[r] + 1);
+                } else {
+                    const bool f = (m >> r) & 1;
+                    if (f && fits) pool.free_pages[top - place] = p;
+                    place += f;
+                    if (!shared) continue;
+                    if (!fits) atomicAdd(refs + p, 1);
+                    if (fits && f) refs[p] = 0;
+                    if (!fits || ((last >> r) & 1)) who[p] = 0;
+                }
+            }
+            top -= tile;
+        }
+        if (phase == kProbe) {
+            shared = __syncthreads_or(any);
+            phase = shared ? kCountDown : kCount;
+        } else if (phase == kCountDown) {
             __threadfence();
             all_sync();
-        }
-        int n = 0, k = 0;
-        for (int base = e0; base < e1; base += step, ++k) {
-            fetch(base);
-            uint32_t last;
-            const uint32_t m = freed(last);
-            n += __popc(m);
-            if (k < 32 / kEntries) {
-                freed_bits |= m << (k * kEntries);
-                last_bits |= last << (k * kEntries);
+            phase = kCount;
+        } else if (phase == kCount) {
+            place = block_exclusive_scan(count, s_scan, &all_freed);
+            if (wide) {
+                if (threadIdx.x == 0) s_count = all_freed;
+                cluster_sync();
+                all_freed = 0;
+                for (int r = 0; r < ranks; ++r) {
+                    const int n = cluster_peek(&s_count, r);
+                    before += r < rank ? n : 0;
+                    all_freed += n;
+                }
             }
-        }
-        place = block_exclusive_scan(n, s_scan, &all_freed);
-        if (wide) {
-            if (threadIdx.x == 0) s_count = all_freed;
-            cluster_sync();
-            all_freed = 0;
-            for (int r = 0; r < ranks; ++r) {
-                const int m = cluster_peek(&s_count, r);
-                before += r < rank ? m : 0;
-                all_freed += m;
-            }
-        }
-    }
-    const bool fits = (long long)n_free - taken + all_freed <= pool.num_pages;
-    if (!fits) flags |= SE_DEV_CAPACITY;
-    // the stack's entries from here down
-    int top = n_free - taken + all_freed - 1 - before;
-    for (int base = e0, k = 0; base < e1; base += step, ++k) {
-        fetch(base);
-        uint32_t m, last;
-        if (k < 32 / kEntries) {
-            m = freed_bits >> (k * kEntries) & ((1u << kEntries) - 1);
-            last = last_bits >> (k * kEntries) & ((1u << kEntries) - 1);
+            fits = (long long)n_free - taken + all_freed <= pool.num_pages;
+            if (!fits) flags |= SE_DEV_CAPACITY;
+            top = n_free - taken + all_freed - 1 - before;   // the stack's entries from here down
+            phase = kPush;
         } else {
-            m = freed(last);
+            if (wide || !once) all_sync();                   // the tables have been read
+            phase = kEnd;
         }
-        int tile = 0;
-        if (!once) place = block_exclusive_scan(__popc(m), s_scan, &tile);
-#pragma unroll
-        for (int r = 0; r < kEntries; ++r) {
-            if (page[r] < 0) continue;
-            const bool f = (m >> r) & 1;
-            if (f && fits) pool.free_pages[top - place] = page[r];
-            place += f;
-            if (!shared) continue;
-            if (!fits) {
-                atomicAdd(refs + page[r], 1);
-                who[page[r]] = 0;
-            } else if (f) {
-                refs[page[r]] = 0;
-                who[page[r]] = 0;
-            } else if ((last >> r) & 1) {
-                who[page[r]] = 0;                            // still held by others
-            }
-        }
-        top -= tile;
     }
     if (flags) flag(ws, flags);
-    if (total > 0 && !once) all_sync();                      // the tables have been read
     if (rank != 0) return;
     for (int b = b0; b < b1; ++b) {
-        const Cut c = b == b0 ? mine : cut_of(pool, refs, keep, b);
         const int fresh = fits ? s_fresh[b] : -2;
         int from_page = -1;
         if (fresh != -2) {
-            if (c.n % kPage != 0 && (c.n < c.ctx || fresh >= 0)) from_page = c.last;
-            if (fresh >= 0)
-                pool.block_table[(int64_t)b * pool.max_pages_per_seq + c.after - 1] = fresh;
-            pool.ctx_len[b] = c.n;
-            pool.n_pages[b] = c.after;
+            const int ctx = b == b0 ? mine.ctx : pool.ctx_len[b];
+            const int n = b == b0 ? mine.n : min(keep[b], ctx), after = (n + kPage - 1) / kPage;
+            int32_t* last = pool.block_table + (int64_t)b * pool.max_pages_per_seq + after - 1;
+            if (n % kPage != 0 && (n < ctx || fresh >= 0)) from_page = b == b0 ? mine.last : *last;
+            if (fresh >= 0) *last = fresh;
+            pool.ctx_len[b] = n;
+            pool.n_pages[b] = after;
         }
         carry.from_seq[b] = -1;
         carry.from_page[b] = from_page;

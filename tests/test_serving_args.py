@@ -199,10 +199,11 @@ def test_binding_rope_holder(lib):
             call(binding.Rope(None, 0, q_weight=w))
         with refused("k_weight.*bfloat16"):
             call(binding.Rope(None, 0, k_weight=w))
-    with refused("too short"):
-        call(binding.Rope(None, 0, q_weight=z(32)))
+    for n in (32, 128):
+        with refused(f"weights of {n} channels, heads of 64"):
+            call(binding.Rope(None, 0, q_weight=z(n)))
     good.k_weight = z(16)
-    with refused("too short"):
+    with refused("two lengths"):
         call(good)
     with refused("invalid argument"):
         binding.Rope.make(40, device="cpu")
