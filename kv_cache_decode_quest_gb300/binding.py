@@ -266,9 +266,10 @@ class PagedKV(_Measured):
 
     @property
     def c(self) -> PagedKVC:
-        P, H, S, D = self.k.shape
-        return PagedKVC(_p(self.k), _p(self.v), _p(self.meta), _p(self.block_table),
-                        _p(self.ctx_len), P, self.block_table.shape[1], H, D, S)
+        k, meta, table = self.k, self.meta, self.block_table
+        P, H, S, D = k.shape
+        return PagedKVC(k.data_ptr(), self.v.data_ptr(), None if meta is None else meta.data_ptr(),
+                        table.data_ptr(), self.ctx_len.data_ptr(), P, table.shape[1], H, D, S)
 
 
 @dataclasses.dataclass
@@ -440,8 +441,10 @@ class Rope(_Measured):
 
     @property
     def c(self) -> RopeC:
-        return RopeC(_p(self.turns), self.rot_dim, self.layout, self.amplitude, self.eps,
-                     _p(self.q_weight), _p(self.k_weight))
+        t, q, k = self.turns, self.q_weight, self.k_weight
+        return RopeC(None if t is None else t.data_ptr(), self.rot_dim, self.layout, self.amplitude,
+                     self.eps, None if q is None else q.data_ptr(),
+                     None if k is None else k.data_ptr())
 
     @staticmethod
     def make(rot_dim: int, base: float = 10000.0, scaling: int = SE_ROPE_PLAIN, factor: float = 1.0,
@@ -633,28 +636,29 @@ def _elsewhere(what: str, device: int):
 
 
 def _located(holder: _Measured) -> int:
-    """The one device of a holder's tensors (-1: the CPU, -2: several), looked up as `_holds` does."""
-    at = holder._device
-    if at is None:
-        found = {t.get_device() for f in dataclasses.fields(holder)
-                 if isinstance(t := getattr(holder, f.name), torch.Tensor)}
-        at = holder.__dict__["_device"] = found.pop() if len(found) == 1 else -2 if found else -3
+    """The one device of a holder's tensors (-1: the CPU, -2: several), looked up once after each
+    assignment."""
+    found = {t.get_device() for f in dataclasses.fields(holder)
+             if isinstance(t := getattr(holder, f.name), torch.Tensor)}
+    at = holder.__dict__["_device"] = found.pop() if len(found) == 1 else -2 if found else -3
     return at
 
 
 def _on_device(what: str, holders, *tensors) -> int:
     """The current device; refuses tensors that its kernels cannot reach."""
-    first = tensors[0].get_device()
-    if first < 0 or first != _current_device():
-        _elsewhere(what, first)
-    for t in tensors:
-        if t is not None and t.get_device() != first:
+    here = tensors[0].get_device()
+    if here < 0 or here != _current_device():
+        _elsewhere(what, here)
+    for t in tensors[1:]:
+        if t is not None and t.get_device() != here:
             _elsewhere(what, t.get_device())
     for h in holders:
-        at = _located(h)
-        if at != first and at != -3:                   # (-3: it holds no tensor)
+        at = h._device
+        if at is None:
+            at = _located(h)
+        if at != here and at != -3:                    # (-3: it holds no tensor)
             _elsewhere(what, at)
-    return first
+    return here
 
 
 def _stream_on(device: int, stream):
