@@ -169,29 +169,36 @@ struct HeadRows {
 // each at most) and hand them round.
 // A row is two latencies (its position with the first pass, then the stores), so what counts
 // is how many warps wait at once: 64 registers, one pass at a time, 32 warps an SM.  16,384
-// rows of 16 heads of 64 channels: 13.5 us, 5.0 TB/s of rows read and written (73% of the
+// rows of 16 heads of 64 channels: 12.9 us, 5.2 TB/s of rows read and written (77% of the
 // copy rate), issue slots half busy.  With four passes a warp in flight and 100 registers 18.0
 // us; through a ring in shared memory 18.7 to 20.6; a table of angles for 16 rows a block
 // 16.5.  64 rows of 36 heads of 128 (a decode step): 1.9 us.
-template <int D, bool PAIRS>
-__global__ void __launch_bounds__(128, 8)
+// AHEAD: the next pass is loaded before this one is worked on, at 72 registers (16,384 rows of 36
+// heads of 128 channels, nine passes: 50.1 us, 89% of the copy rate, against 52.7 us; rows of two
+// passes 13.7 us against 12.9).
+template <int D, bool PAIRS, bool AHEAD>
+__global__ void __launch_bounds__(128, AHEAD ? 7 : 8)
     qk_rope_kernel(se_rope rope, const int32_t* pos, int rows, int parts, HeadRows q, HeadRows k) {
     constexpr int HP = 512 / D, A = D / 64;                  // heads a pass, angles a lane
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, mine = lane / (D / 16);
-    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-    const int row = static_cast<int>(w / parts), part = static_cast<int>(w - (int64_t)row * parts);
+    const int nq = (q.heads + HP - 1) / HP, n = nq + (k.heads + HP - 1) / HP;
+    int row = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5), p0 = 0, p1 = n;
+    if (parts > 1) {
+        const int part = row % parts;
+        row /= parts;
+        p0 = n * part / parts;
+        p1 = n * (part + 1) / parts;
+    }
     if (row >= rows) return;
     const HeadLane<D, PAIRS> l(lane, rope.rot_dim);
-    const int nq = (q.heads + HP - 1) / HP, n = nq + (k.heads + HP - 1) / HP;
-    const int p0 = n * part / parts, p1 = n * (part + 1) / parts;
     uint4 u = make_uint4(0, 0, 0, 0), v = u;
     auto load = [&](int p) {
         const HeadRows& h = p < nq ? q : k;
         const int head = (p < nq ? p : p - nq) * HP + mine;
         if (p < p1 && head < h.heads) {
-            const uint4* in = h.in + row * h.in_stride + head * (D / 8);
+            const uint4* in = h.in + (int64_t)row * h.in_stride + head * (D / 8);
             u = in[l.a];
             v = in[l.b];
         }
@@ -207,13 +214,17 @@ __global__ void __launch_bounds__(128, 8)
     {
         float ca[A], sa[A], c[8], s[8];
 #pragma unroll
-        for (int i = 0; i < A; ++i) turn_of(step[i], rope.amplitude, at, ca[i], sa[i]);
+        for (int i = 0; i < A; ++i) {
+            turn_of(step[i], rope.amplitude, at, ca[i], sa[i]);
+            if (A * lane + i >= rope.rot_dim / 2) {          // channels that are not rotated
+                ca[i] = 1.f;
+                sa[i] = 0.f;
+            }
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float x = __shfl_sync(0xffffffffu, ca[i % A], (8 * l.j + i) / A);
-            const float y = __shfl_sync(0xffffffffu, sa[i % A], (8 * l.j + i) / A);
-            c[i] = l.turns ? x : 1.f;
-            s[i] = l.turns ? y : 0.f;
+            c[i] = __shfl_sync(0xffffffffu, ca[i % A], (8 * l.j + i) / A);
+            s[i] = __shfl_sync(0xffffffffu, sa[i % A], (8 * l.j + i) / A);
         }
         t.set(c, s);
     }
@@ -221,14 +232,23 @@ __global__ void __launch_bounds__(128, 8)
         if (begin >= end) return;
         const Weight wt = load_weight<D, PAIRS>(weight, l);
         for (int p = begin; p < end; ++p) {
-            norm_turn<D, PAIRS>(u, v, weight != nullptr, wt, rope.eps, t);
-            const int head = (p - skip) * HP + mine;
-            if (head < h.heads) {
-                uint4* out = h.out + row * h.out_stride + head * (D / 8);
-                out[l.a] = u;
-                out[l.b] = v;
+            auto pass = [&](uint4& a, uint4& b) {
+                norm_turn<D, PAIRS>(a, b, weight != nullptr, wt, rope.eps, t);
+                const int head = (p - skip) * HP + mine;
+                if (head < h.heads) {
+                    uint4* out = h.out + (int64_t)row * h.out_stride + head * (D / 8);
+                    out[l.a] = a;
+                    out[l.b] = b;
+                }
+            };
+            if (AHEAD) {
+                uint4 a = u, b = v;
+                load(p + 1);
+                pass(a, b);
+            } else {
+                pass(u, v);
+                load(p + 1);
             }
-            load(p + 1);
         }
     };
     turn(q, rope.q_weight, p0, min(p1, nq), 0);
@@ -586,10 +606,13 @@ cudaError_t rows_of(const se_rope& rope, const int32_t* pos, int rows, const Hea
     if (rows == 0 || passes == 0) return cudaSuccess;
     // few rows: their passes are spread over warps until the GPU has four a scheduler
     const int parts = std::max(1, std::min(passes, 16 * num_sms() / rows));
-    const int64_t warps = (int64_t)rows * parts;
-    const dim3 grid(static_cast<unsigned>((warps + 3) / 4));
-    return launch_pdl(qk_rope_kernel<D, PAIRS>, grid, dim3(128), 0, s, rope, pos, rows, parts,
-                      head_rows(q), head_rows(k));
+    const dim3 grid((rows * parts + 3) / 4);     // (parts is 1 for more than 16 num_sms() rows)
+    auto run = [&](auto kernel) {
+        return launch_pdl(kernel, grid, dim3(128), 0, s, rope, pos, rows, parts, head_rows(q),
+                          head_rows(k));
+    };
+    return passes > 2 * parts ? run(qk_rope_kernel<D, PAIRS, true>)
+                              : run(qk_rope_kernel<D, PAIRS, false>);
 }
 
 template <int D, bool PAIRS>
