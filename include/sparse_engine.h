@@ -488,7 +488,7 @@ int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void*
  * The test of a draft is exact.  Weights (values above 1 count as 1, negative ones and NaN as
  * 0) and their sums are fp32 numbers with a second word for what rounding loses, then
  * integers: off by less than 2^-40 in all (a sum below 2^-50 may count as 0), the same for
- * the same row whatever the batch.  Rows whose sum passes 8: the token is unspecified (in
+ * the same row whatever the batch.  Rows whose sum passes 8: the token is unspecified (-1 or in
  * [0, vocab)).  Random numbers outside [0, 1) count as the nearest inside, NaN as 0.
  * A row without any weight: next_token -1, SE_DEV_BAD_VALUE.  A drafted token outside
  * [0, vocab) is refused: SE_DEV_BAD_INDEX.  start outside [0, max_tokens] or descending:
@@ -527,7 +527,8 @@ int se_draft_verify(const void* probs, const void* draft_probs, int64_t row_stri
  * SE_DEV_BAD_LENGTH; that b stays as it was.  A page outside the pool on the stack, or where
  * the source's last rows are: SE_DEV_BAD_INDEX, b stays empty; among the shared ones:
  * SE_DEV_BAD_INDEX, b has it as the source has, uncounted.
- * Limits: batch <= 8192; num_pages and max_pages_per_seq < 2^27.
+ * Limits: batch <= 8192; num_pages and max_pages_per_seq < 2^27; batch * max_pages_per_seq
+ * <= 2^30.
  * Workspace: as se_chunk_plan. */
 int se_pages_fork(const se_page_pool* pool, int32_t* page_refs, const int32_t* src, int batch,
                   const se_page_carry* carry, void* ws, size_t ws_bytes, se_stream_t stream);

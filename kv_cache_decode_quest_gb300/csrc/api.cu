@@ -142,6 +142,7 @@ int check_pool(const se_page_pool* p) {
 
 constexpr int kMaxChunkTokens = 1 << 24;
 constexpr int kMaxChunkPages = 1 << 26;      // of a sequence: positions stay below 2^30
+constexpr int64_t kMaxTableEntries = 1 << 30;   // of a block table whose pages are counted
 
 int check_chunk(const se_chunk* c) {
     if (!c || !c->start || c->max_tokens < 0) return SE_ERR_INVALID_ARG;
@@ -466,7 +467,8 @@ int se_pages_fork(const se_page_pool* pool, int32_t* page_refs, const int32_t* s
     int rc = check_pool(pool);
     if (rc) return rc;
     if (batch < 0) return SE_ERR_INVALID_ARG;
-    if (batch > page_share_max_batch()) return SE_ERR_UNSUPPORTED;
+    if (batch > page_share_max_batch() || (int64_t)batch * pool->max_pages_per_seq > kMaxTableEntries)
+        return SE_ERR_UNSUPPORTED;
     if (!page_refs || !carry || !carry->from_seq || !carry->from_page) return SE_ERR_INVALID_ARG;
     if (batch > 0 && !src) return SE_ERR_INVALID_ARG;
     if ((rc = check_ws(ws, ws_bytes, se_page_pool_workspace(batch)))) return rc;
@@ -480,7 +482,8 @@ int se_pages_truncate(const se_page_pool* pool, int32_t* page_refs, const int32_
     int rc = check_pool(pool);
     if (rc) return rc;
     if (batch < 0) return SE_ERR_INVALID_ARG;
-    if (batch > page_share_max_batch()) return SE_ERR_UNSUPPORTED;
+    if (batch > page_share_max_batch() || (int64_t)batch * pool->max_pages_per_seq > kMaxTableEntries)
+        return SE_ERR_UNSUPPORTED;
     if (!carry || !carry->from_seq || !carry->from_page) return SE_ERR_INVALID_ARG;
     if (batch > 0 && !keep) return SE_ERR_INVALID_ARG;
     if ((rc = check_ws(ws, ws_bytes, se_pages_truncate_workspace(batch, pool->num_pages)))) return rc;

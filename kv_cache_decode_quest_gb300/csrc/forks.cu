@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(1024, 1)
             less |= fresh == -2;
         }
         s_fresh[b] = fresh;
-        s_first[b] = static_cast<int>(min(at, 0x7fffffffll));
+        s_first[b] = static_cast<int>(at);
         at += f.want ? f.ctx / kPage : 0;
     }
     if (__syncthreads_or(less)) {
@@ -153,13 +153,13 @@ __global__ void __launch_bounds__(1024, 1)
         for (int b = b0; b < b1; ++b) n += s_fresh[b] == -2 ? 0 : pool.ctx_len[src[b]] / kPage;
         block_scan2(n, none, tmp, &all, &nones);
         for (int b = b0; b < b1; ++b) {
-            s_first[b] = static_cast<int>(min(n, 0x7fffffffll));
+            s_first[b] = static_cast<int>(n);
             n += s_fresh[b] == -2 ? 0 : pool.ctx_len[src[b]] / kPage;
         }
     }
     __syncthreads();
-    // table entries; more than 2^31 of them do not fit a table of a pool's pages
-    const int total = static_cast<int>(min(all, 0x7fffffffll));
+    // table entries (a block table of these calls has at most 2^30)
+    const int total = static_cast<int>(all);
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < total;
          i += (long long)gridDim.x * blockDim.x) {
         const int b = owner_of(s_first, batch, static_cast<int>(i));
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(1024, 1)
             less |= fresh == -2;
         }
         const int n = s_first[b];
-        s_first[b] = static_cast<int>(min(entries, 0x7fffffffll));
+        s_first[b] = static_cast<int>(entries);
         entries += n;
     }
     if (__syncthreads_or(less)) {
@@ -303,12 +303,12 @@ __global__ void __launch_bounds__(1024, 1)
         for (int b = b0; b < b1; ++b) n += lets(b);
         block_scan2(n, none, tmp, &all, &nones);
         for (int b = b0; b < b1; ++b) {
-            s_first[b] = static_cast<int>(min(n, 0x7fffffffll));
+            s_first[b] = static_cast<int>(n);
             n += lets(b);
         }
     }
     const int taken = static_cast<int>(min(asks, (long long)n_free));
-    const int total = static_cast<int>(min(all, 0x7fffffffll));
+    const int total = static_cast<int>(all);
     if (ranks > 1)
         cluster_sync();                      // all have read what was there before the call
     else

@@ -145,6 +145,10 @@ def test_fork_and_truncate(lib):
                     dict(c=carry(from_page=None)), dict(p=None)):
             assert call(**bad) == INVALID, bad
         assert call(batch=8193) == UNSUPPORTED and call(p=pool(num_pages=1 << 28)) == UNSUPPORTED
+        # 2^30 entries of the block table are served, more are not
+        assert call(p=pool(max_pages_per_seq=1 << 26), batch=16, ws=None) == WORKSPACE
+        assert call(p=pool(max_pages_per_seq=1 << 26), batch=17) == UNSUPPORTED
+        assert call(p=pool(max_pages_per_seq=(1 << 27) - 1), batch=9) == UNSUPPORTED
         assert call(ws=None) == WORKSPACE and call(n=511) == WORKSPACE and call(ws=ODD) == WORKSPACE
         assert call(batch=0, src=None) == 0
     assert fork(refs=None) == INVALID and cut(n=need - 1) == WORKSPACE
