@@ -11,7 +11,7 @@
 // on sums are integers in units of 2^-58, the same in any order: the row is cut into tiles
 // of 1024 that any warp of any block may sum, and the last block of a sequence finds the
 // tile and in it the token.  15 fp32 operations a weight, hidden behind the loads.
-// 256 sequences over 131,072 tokens (about 1.6 rows each) take 43.5 us, 4.9 TB/s: 72% of the
+// 256 sequences over 131,072 tokens (about 1.6 rows each) take 41.7 us, 5.1 TB/s: 75% of the
 // copy rate; the rest is three latencies before a block knows its row, and the last
 // sequences' search.  Every weight made a 64-bit integer 122 us; two waves of blocks 52.
 #include <algorithm>
@@ -196,15 +196,27 @@ __global__ void __launch_bounds__(256, kBlocks)
                         const int32_t* start, const int32_t* pos, int max_tokens,
                         int32_t* n_accepted, int32_t* next_token, int32_t* keep, int* ws) {
     constexpr int N = 16 / sizeof(T);
-    __shared__ int s_stay, s_bad, s_last, s_tile;
+    __shared__ int s_stay, s_token, s_last, s_tile;
     __shared__ u64 s_rest;
     __shared__ u64 tmp[3][8];
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float draw_u = sample_u[b];
     int r0 = start[b], r1 = start[b + 1];
     const bool bad = r0 < 0 || r1 < r0 || r1 > max_tokens;
+    const int drafts = bad ? 0 : r1 - r0 - 1;
     const int first_pos = !bad && r0 < r1 ? pos[r0] : -1;
+    // (the first 32 drafts come with the position: one latency less)
+    int d = -1;
+    float u = 0.f;
+    auto load_drafts = [&](int i0) {
+        if (warp == 0 && i0 + lane < drafts) {
+            d = tokens[r0 + i0 + lane + 1];
+            u = accept_u[r0 + i0 + lane + 1];
+        }
+    };
+    load_drafts(0);
     if (first_pos < 0) {                                     // the same in every block of the sequence
         if (blockIdx.x == 0 && threadIdx.x == 0) {
             if (bad) flag(ws, SE_DEV_BAD_LENGTH);
@@ -214,45 +226,42 @@ __global__ void __launch_bounds__(256, kBlocks)
         return;
     }
     // which drafts stay: every block finds out for itself
-    const int drafts = r1 - r0 - 1;
     if (warp == 0) {
-        int stay = drafts, bad_token = 0;
+        int stay = drafts, refused = -1;
         for (int i0 = 0; i0 < drafts; i0 += 32) {
-            const int t = r0 + i0 + lane;
+            if (i0 > 0) load_drafts(i0);
             bool out = false;
             if (i0 + lane < drafts) {
-                const int d = tokens[t + 1];
+                const int64_t t = r0 + i0 + lane;
                 out = true;
                 if (d >= 0 && d < vocab) {
-                    const double u = fminf(fmaxf(accept_u[t + 1], 0.f), kBelowOne);
+                    const double x = fminf(fmaxf(u, 0.f), kBelowOne);
                     const double p = value<T>(probs + t * row_stride + d);
                     const double q = draft ? value<T>(draft + t * row_stride + d) : 1.0;
-                    out = !(u * q < p);
+                    out = !(x * q < p);
                 }
             }
             const uint32_t m = __ballot_sync(0xffffffffu, out);
             if (m != 0) {
                 stay = i0 + __ffs(m) - 1;
+                refused = __shfl_sync(0xffffffffu, d, __ffs(m) - 1);
                 break;
             }
         }
         if (lane == 0) {
-            if (stay < drafts) {
-                const int d = tokens[r0 + stay + 1];
-                bad_token = d < 0 || d >= vocab;
-            }
             s_stay = stay;
-            s_bad = bad_token;
+            s_token = refused;
         }
     }
     __syncthreads();
-    const int stay = s_stay;
+    const int stay = s_stay, refused = s_token;              // (the refused draft, if one is)
+    const bool outside = stay < drafts && (refused < 0 || refused >= vocab);
     const int64_t at = (r0 + stay) * row_stride;
     Row<T> row;
     row.p = probs + at;
     row.q = stay < drafts && draft != nullptr ? draft + at : nullptr;
     row.vocab = vocab;
-    row.without = stay < drafts && draft == nullptr && !s_bad ? tokens[r0 + stay + 1] : -1;
+    row.without = stay < drafts && draft == nullptr && !outside ? refused : -1;
     row.lead = static_cast<int>(reinterpret_cast<uintptr_t>(row.p) % 16 / sizeof(T));
     u64* sums = reinterpret_cast<u64*>(reinterpret_cast<char*>(ws) + kSumsAt) + (int64_t)b * tiles;
     const int nw = blockDim.x >> 5;
@@ -288,14 +297,14 @@ __global__ void __launch_bounds__(256, kBlocks)
     }
     if (threadIdx.x == 0) {
         *arrived = 0;
-        if (s_bad) flag(ws, SE_DEV_BAD_INDEX);
+        if (outside) flag(ws, SE_DEV_BAD_INDEX);
         if (total == 0) flag(ws, SE_DEV_BAD_VALUE);
         n_accepted[b] = stay;
         keep[b] = first_pos + 1 + stay;
         next_token[b] = total == 0 ? -1 : vocab - 1;
     }
     if (total == 0) return;
-    const u64 want = part_of(sample_u[b], total);             // the first token whose sum passes it
+    const u64 want = part_of(draw_u, total);             // the first token whose sum passes it
     if (threadIdx.x == 0) s_tile = tiles;
     __syncthreads();
     if (ahead <= want && want < ahead + held) {
