@@ -23,29 +23,6 @@ constexpr int kMaxBatch = 8192;              // sequences whose entries shared m
 constexpr int kWhoWord = 128;                // a workspace word for each page from here on, zero
                                              // between calls (se_pages_truncate)
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-    return r;
-}
-// A word of another block's shared memory, of the same variable as `p` here.
-__device__ __forceinline__ int cluster_peek(const int* p, uint32_t rank) {
-    uint32_t a;
-    int v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ int clamped_free(const se_page_pool& pool, int& flags) {
     const int n = *pool.n_free;
     if (n >= 0 && n <= pool.num_pages) return n;
@@ -645,18 +622,8 @@ cudaError_t launch_pages_truncate(const se_page_pool& pool, int32_t* refs, const
         e = cluster_blocks(cfg, &ranks);
         if (e != cudaSuccess) return e;
     }
-    cfg.gridDim = dim3(ranks);
-    cfg.dynamicSmemBytes = 3 * batch * sizeof(int);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ranks;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, pages_truncate_kernel, pool, refs, keep, batch, carry, ws);
+    return launch_cluster(pages_truncate_kernel, dim3(ranks), cfg.blockDim, 3 * batch * sizeof(int),
+                          ranks, s, pool, refs, keep, batch, carry, ws);
 }
 
 cudaError_t launch_pages_carry(const se_paged_kv& kv, const se_page_carry& carry, int batch,

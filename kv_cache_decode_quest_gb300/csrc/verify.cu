@@ -188,8 +188,9 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
 }
 
 constexpr int kBlocks = 4;                   // blocks an SM
+constexpr int kCluster = 8;                  // blocks of a cluster, at most
 
-template <typename T>
+template <typename T, bool CLUSTER>
 __global__ void __launch_bounds__(256, kBlocks)
     draft_verify_kernel(const T* probs, const T* draft, int64_t row_stride, int vocab, int tiles,
                         const int32_t* tokens, const float* accept_u, const float* sample_u,
@@ -199,6 +200,8 @@ __global__ void __launch_bounds__(256, kBlocks)
     __shared__ int s_stay, s_token, s_last, s_tile;
     __shared__ u64 s_rest;
     __shared__ u64 tmp[3][8];
+    extern __shared__ __align__(16) u64 s_sums[];            // [tiles] (CLUSTER)
+    if (CLUSTER) cluster_arrive();
     pdl_wait();
     pdl_trigger();
     const int b = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -217,6 +220,7 @@ __global__ void __launch_bounds__(256, kBlocks)
         }
     };
     load_drafts(0);
+    if (CLUSTER) cluster_wait();                             // (all blocks have begun)
     if (first_pos < 0) {                                     // the same in every block of the sequence
         if (blockIdx.x == 0 && threadIdx.x == 0) {
             if (bad) flag(ws, SE_DEV_BAD_LENGTH);
@@ -267,23 +271,35 @@ __global__ void __launch_bounds__(256, kBlocks)
     const int nw = blockDim.x >> 5;
     for (int k = blockIdx.x * nw + warp; k < tiles; k += gridDim.x * nw) {
         const u64 sum = tile_sum(row, k, lane);
-        if (lane == 0) sums[k] = sum;
+        if (lane == 0) {
+            if (CLUSTER)
+                cluster_poke(s_sums + k, 0, sum);
+            else
+                sums[k] = sum;
+        }
     }
-    // the sequence's last block goes on
+    // the sequence's last block goes on; of a cluster the first
     int* arrived = ws + 64 + b;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
+    if (CLUSTER) {
+        __syncwarp();
+        cluster_sync();
+        if (blockIdx.x != 0) return;
+    } else {
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0) s_last = atomicAdd(arrived, 1) == static_cast<int>(gridDim.x) - 1;
+        __syncthreads();
+        if (!s_last) return;
+        __threadfence();
+    }
+    auto sum_of = [&](int k) { return CLUSTER ? s_sums[k] : __ldcg(sums + k); };
     // a thread's run of tiles, so that one scan serves any number of them
     const int per = (tiles + blockDim.x - 1) / blockDim.x;
     const int k0 = min(static_cast<int>(threadIdx.x) * per, tiles), k1 = min(k0 + per, tiles);
     u64 total = 0, ahead = 0, held = 0;
     for (int round = 0; round < 2; ++round) {
         held = 0;
-        for (int k = k0; k < k1; ++k) held += __ldcg(sums + k);
+        for (int k = k0; k < k1; ++k) held += sum_of(k);
         ahead = block_sum_before(held, tmp[round], &total);
         if (total > 0 || (row.q == nullptr && row.without < 0)) break;
         // nothing is left of p beside q: drawn from p
@@ -291,12 +307,12 @@ __global__ void __launch_bounds__(256, kBlocks)
         row.without = -1;
         for (int k = warp; k < tiles; k += nw) {
             const u64 sum = tile_sum(row, k, lane);
-            if (lane == 0) __stcg(sums + k, sum);
+            if (lane == 0) *(CLUSTER ? s_sums + k : sums + k) = sum;
         }
         __syncthreads();
     }
     if (threadIdx.x == 0) {
-        *arrived = 0;
+        if (!CLUSTER) *arrived = 0;
         if (outside) flag(ws, SE_DEV_BAD_INDEX);
         if (total == 0) flag(ws, SE_DEV_BAD_VALUE);
         n_accepted[b] = stay;
@@ -309,7 +325,7 @@ __global__ void __launch_bounds__(256, kBlocks)
     __syncthreads();
     if (ahead <= want && want < ahead + held) {
         int k = k0;
-        for (u64 w; k < k1 - 1 && ahead + (w = __ldcg(sums + k)) <= want; ++k) ahead += w;
+        for (u64 w; k < k1 - 1 && ahead + (w = sum_of(k)) <= want; ++k) ahead += w;
         s_tile = k;
         s_rest = want - ahead;
     }
@@ -364,16 +380,18 @@ cudaError_t launch_draft_verify(const void* probs, const void* draft, int64_t ro
     // a block's eight warps have a tile each at least; one wave of blocks
     const int split = std::max(1, std::min((tiles + 7) / 8, kBlocks * num_sms() / batch));
     const dim3 grid(split, batch);
+    auto run = [&](auto kernel, auto type, int cluster) {
+        using T = decltype(type);
+        return launch_cluster(kernel, grid, dim3(256), cluster ? tiles * sizeof(u64) : 0, cluster, s,
+                              static_cast<const T*>(probs), static_cast<const T*>(draft), row_stride,
+                              vocab, tiles, tokens, accept_u, sample_u, (const int32_t*)ck.start,
+                              (const int32_t*)ck.pos, ck.max_tokens, n_accepted, next_token, keep, ws);
+    };
     if (prob_dtype == 1)
-        return launch_pdl(draft_verify_kernel<float>, grid, dim3(256), 0, s,
-                          static_cast<const float*>(probs), static_cast<const float*>(draft),
-                          row_stride, vocab, tiles, tokens, accept_u, sample_u,
-                          (const int32_t*)ck.start, (const int32_t*)ck.pos, ck.max_tokens, n_accepted,
-                          next_token, keep, ws);
-    return launch_pdl(draft_verify_kernel<uint16_t>, grid, dim3(256), 0, s,
-                      static_cast<const uint16_t*>(probs), static_cast<const uint16_t*>(draft),
-                      row_stride, vocab, tiles, tokens, accept_u, sample_u, (const int32_t*)ck.start,
-                      (const int32_t*)ck.pos, ck.max_tokens, n_accepted, next_token, keep, ws);
+        return split <= kCluster ? run(draft_verify_kernel<float, true>, float(), split)
+                                 : run(draft_verify_kernel<float, false>, float(), 0);
+    return split <= kCluster ? run(draft_verify_kernel<uint16_t, true>, uint16_t(), split)
+                             : run(draft_verify_kernel<uint16_t, false>, uint16_t(), 0);
 }
 
 }  // namespace se
