@@ -10,10 +10,15 @@
 // together), a lane's sum of 32 weights carries its error in a second word, and from there
 // on sums are integers in units of 2^-58, the same in any order: the row is cut into tiles
 // of 1024 that any warp of any block may sum, and the last block of a sequence finds the
-// tile and in it the token.  15 fp32 operations a weight, hidden behind the loads.
-// 256 sequences over 131,072 tokens (about 1.6 rows each) take 41.7 us, 5.1 TB/s: 75% of the
-// copy rate; the rest is three latencies before a block knows its row, and the last
-// sequences' search.  Every weight made a 64-bit integer 122 us; two waves of blocks 52.
+// tile and in it the token.  Two weights at once in packed fp32: 5 operations a weight of p
+// alone, 9 with q (one by one 41.4 us for the 39.6 below).
+// Up to eight blocks of a sequence are a cluster, whose first block gets the sums in shared
+// memory; more (a large vocabulary, few sequences) meet over a counter in memory (one
+// sequence of 32,000 tokens: 5.2 us against 6.0).
+// 256 sequences over 131,072 tokens (about 1.6 rows each) take 39.6 us, 5.4 TB/s: 79% of the
+// copy rate; the rest is three latencies before a block knows its row, blocks with two rows
+// beside blocks with one, and the last sequences' search.  Every weight made a 64-bit
+// integer 122 us; two waves of blocks 52; rows through a ring in shared memory 7 us more.
 #include <algorithm>
 
 #include "common.cuh"
@@ -30,21 +35,43 @@ constexpr float kBelowOne = 0x1.fffffep-1f;
 
 using u64 = unsigned long long;
 
-// A sum in two words: s + lo is exact but for lo's own rounding.
+__device__ __forceinline__ uint64_t sub_f32x2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Two sums side by side (packed fp32), each in two words: s + lo is exact but for lo's own
+// rounding.
 struct Sum {
-    float s = 0.f, lo = 0.f;
-    // Adds p - q when that is positive (both within [0, 1]).
-    __device__ __forceinline__ void add(float p, float q) {
-        const bool more = p > q;
-        const float d = more ? p - q : 0.f;
-        const float e = more ? (p - d) - q : 0.f;        // what the difference lost
-        const float t = s + d, b = t - s;
-        lo += ((s - (t - b)) + (d - b)) + e;
-        s = t;
+    uint64_t s = 0, lo = 0;
+    __device__ __forceinline__ void add(uint64_t d) {        // each within [0, 1]
+        lo = add_f32x2(lo, lost(d));
     }
-    // In units of 2^-58 (s up to 32).
+    // Adds p - q, q at most p.
+    __device__ __forceinline__ void add(uint64_t p, uint64_t q) {
+        const uint64_t d = sub_f32x2(p, q);
+        const uint64_t e = sub_f32x2(sub_f32x2(p, d), q);    // what the difference lost
+        lo = add_f32x2(lo, add_f32x2(lost(d), e));
+    }
+    // In units of 2^-58 (each s up to 16).
     __device__ __forceinline__ u64 units() const {
+        float a, b, c, d;
+        f32x2_split(s, a, b);
+        f32x2_split(lo, c, d);
+        return units(a, c) + units(b, d);
+    }
+    static __device__ __forceinline__ u64 units(float s, float lo) {
         return __float2ull_rz(s * 0x1p58f) + static_cast<u64>(__float2ll_rz(lo * 0x1p58f));
+    }
+
+  private:
+    // Adds d to s; what that lost.
+    __device__ __forceinline__ uint64_t lost(uint64_t d) {
+        const uint64_t t = add_f32x2(s, d), b = sub_f32x2(t, s);
+        const uint64_t x = add_f32x2(sub_f32x2(s, sub_f32x2(t, b)), sub_f32x2(d, b));
+        s = t;
+        return x;
     }
 };
 
@@ -81,47 +108,45 @@ struct Row {
     int lead;                    // elements between the 16-byte boundary below p and p
 };
 
-// The weights of vector c (16 bytes, on the boundaries) of the row; places outside it get 0.
+// Vector c (16 bytes, on the boundaries) of `from`, the row's p or q; places outside the row
+// get 0.
 template <typename T>
-__device__ __forceinline__ void load_vector(const Row<T>& r, int c, uint4& p, uint4& q) {
+__device__ __forceinline__ uint4 load_vector(const Row<T>& r, const T* from, int c) {
     constexpr int N = 16 / sizeof(T);
     const int v0 = c * N - r.lead;
-    p = q = make_uint4(0, 0, 0, 0);
-    if (v0 >= 0 && v0 + N <= r.vocab) {
-        p = __ldcs(reinterpret_cast<const uint4*>(r.p + v0));
-        if (r.q != nullptr) q = __ldcs(reinterpret_cast<const uint4*>(r.q + v0));
-    } else {
-        uint32_t a[4] = {0, 0, 0, 0}, b[4] = {0, 0, 0, 0};
+    if (v0 >= 0 && v0 + N <= r.vocab) return __ldcs(reinterpret_cast<const uint4*>(from + v0));
+    uint32_t a[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (v0 + e >= 0 && v0 + e < r.vocab) {
-                const float x = value<T>(r.p + v0 + e), y = r.q ? value<T>(r.q + v0 + e) : 0.f;
-                if (sizeof(T) == 4) {
-                    a[e & 3] = __float_as_uint(x);
-                    b[e & 3] = __float_as_uint(y);
-                } else {
-                    a[e / 2] |= (__float_as_uint(x) >> 16) << (16 * (e & 1));
-                    b[e / 2] |= (__float_as_uint(y) >> 16) << (16 * (e & 1));
-                }
-            }
-        p = make_uint4(a[0], a[1], a[2], a[3]);
-        q = make_uint4(b[0], b[1], b[2], b[3]);
-    }
+    for (int e = 0; e < N; ++e)
+        if (v0 + e >= 0 && v0 + e < r.vocab) {
+            const uint32_t x = __float_as_uint(value<T>(from + v0 + e));
+            if (sizeof(T) == 4)
+                a[e & 3] = x;
+            else
+                a[e / 2] |= (x >> 16) << (16 * (e & 1));
+        }
+    return make_uint4(a[0], a[1], a[2], a[3]);
 }
-// The weights' terms of vector c: p and q within [0, 1] (NaN: 0), q 0 where there is none.
+// Vector c's values of p within [0, 1] (NaN: 0), 0 for the token without weight.
 template <typename T>
-__device__ __forceinline__ void vector_terms(const Row<T>& r, int c, uint4 p, uint4 q, float* x,
-                                             float* y) {
+__device__ __forceinline__ void p_terms(const Row<T>& r, int c, uint4 p, float* x) {
     constexpr int N = 16 / sizeof(T);
     widen<T>(p, x);
-    widen<T>(q, y);
-    const int at = r.without + r.lead - c * N;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-        x[e] = __saturatef(x[e]);
-        y[e] = __saturatef(y[e]);
-        if (r.without >= 0 && e == at) x[e] = 0.f;
-    }
+    for (int e = 0; e < N; ++e) x[e] = __saturatef(x[e]);
+    const int at = r.without < 0 ? -1 : r.without + r.lead - c * N;
+    if (at >= 0 && at < N)
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e == at) x[e] = 0.f;
+}
+// What q takes off each of them: at most all.
+template <typename T>
+__device__ __forceinline__ void q_terms(uint4 q, const float* x, float* y) {
+    constexpr int N = 16 / sizeof(T);
+    widen<T>(q, y);
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = fminf(fmaxf(y[e], 0.f), x[e]);
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 x) {
@@ -130,27 +155,39 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
     return x;
 }
 
-// The sum of tile k of the row, in every lane: `kVectors` vectors of each of p and q in flight.
-constexpr int kVectors = 4;
-template <typename T>
-__device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
-    constexpr int N = 16 / sizeof(T), C = kTile / N / 32;
+// The sum of tile k of the row, in every lane: up to eight vectors a lane in flight.
+template <typename T, bool BOTH>
+__device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
+    constexpr int N = 16 / sizeof(T), C = kTile / N / 32, V = BOTH ? 4 : C;
     Sum sum;
 #pragma unroll 1
-    for (int i0 = 0; i0 < C; i0 += kVectors) {
+    for (int i0 = 0; i0 < C; i0 += V) {
         const int c = k * (kTile / N) + i0 * 32 + lane;
-        uint4 p[kVectors], q[kVectors];
+        uint4 p[V], q[V];
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i) load_vector(r, c + i * 32, p[i], q[i]);
+        for (int i = 0; i < V; ++i) {
+            p[i] = load_vector(r, r.p, c + i * 32);
+            if (BOTH) q[i] = load_vector(r, r.q, c + i * 32);
+        }
 #pragma unroll
-        for (int i = 0; i < kVectors; ++i) {
+        for (int i = 0; i < V; ++i) {
             float x[N], y[N];
-            vector_terms(r, c + i * 32, p[i], q[i], x, y);
+            p_terms(r, c + i * 32, p[i], x);
+            if (BOTH) q_terms<T>(q[i], x, y);
 #pragma unroll
-            for (int e = 0; e < N; ++e) sum.add(x[e], y[e]);
+            for (int e = 0; e < N; e += 2) {
+                if (BOTH)
+                    sum.add(f32x2(x[e], x[e + 1]), f32x2(y[e], y[e + 1]));
+                else
+                    sum.add(f32x2(x[e], x[e + 1]));
+            }
         }
     }
     return warp_sum(sum.units());
+}
+template <typename T>
+__device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
+    return r.q != nullptr ? tile_sum_of<T, true>(r, k, lane) : tile_sum_of<T, false>(r, k, lane);
 }
 
 // Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads
@@ -335,15 +372,13 @@ __global__ void __launch_bounds__(256, kBlocks)
     u64 w[N], sum = 0;
     const int c = s_tile * (kTile / N) + threadIdx.x;
     if (threadIdx.x < kTile / N) {
-        uint4 p, q;
         float x[N], y[N];
-        load_vector(row, c, p, q);
-        vector_terms(row, c, p, q, x, y);
+        p_terms(row, c, load_vector(row, row.p, c), x);
+        if (row.q != nullptr) q_terms<T>(load_vector(row, row.q, c), x, y);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            Sum one;
-            one.add(x[e], y[e]);
-            w[e] = one.units();
+            const float q = row.q != nullptr ? y[e] : 0.f, d = x[e] - q;
+            w[e] = Sum::units(d, (x[e] - d) - q);
             sum += w[e];
         }
     }
