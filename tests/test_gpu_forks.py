@@ -85,10 +85,12 @@ def random_keep(g, b, share):
     return keep
 
 
-# few entries: one block; more than 8192: a cluster of eight; sequences per thread one and several
+# up to 4096 entries: one block; more: a cluster, of 256, 512 or 1024 threads a block; sequences per
+# thread one and several
 @pytest.mark.parametrize("batch,hi,pages,maxp", [
     (1, 40, 6, 5), (4, 50, 20, 9), (16, 100, 120, 20), (300, 60, 1500, 30), (257, 90, 9000, 40),
-    (1025, 40, 20000, 17), (2500, 60, 9001, 12), (3, 40000, 12000, 8200)])
+    (1025, 40, 20000, 17), (2500, 60, 9001, 12), (3, 40000, 12000, 8200),
+    (40, 6000, 30000, 1000), (70, 6000, 60000, 1000)])
 def test_many_steps(batch, hi, pages, maxp):
     g = np.random.default_rng([31, batch, pages])
     b = Both(pages, batch, maxp, g)
