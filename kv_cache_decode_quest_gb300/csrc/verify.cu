@@ -18,7 +18,7 @@
 // 256 sequences over 131,072 tokens (about 1.6 rows each) take 39.6 us, 5.4 TB/s: 79% of the
 // copy rate; the rest is three latencies before a block knows its row, blocks with two rows
 // beside blocks with one, and the last sequences' search.  Every weight made a 64-bit
-// integer 122 us; two waves of blocks 52; rows through a ring in shared memory 7 us more.
+// integer 122 us; two waves of blocks 52; rows through a ring in shared memory 4 us more.
 #include <algorithm>
 
 #include "common.cuh"
