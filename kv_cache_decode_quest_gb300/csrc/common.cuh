@@ -83,12 +83,15 @@ __device__ __forceinline__ unsigned long long globaltimer() {
 }
 
 // ---- clusters ---------------------------------------------------------------
-// The cluster's barrier, whole warps at a time: what was written before arriving is seen
-// after waiting.
+// The cluster's barrier: what was written before arriving is seen after waiting.  The
+// instructions take whole warps (.aligned), so each first brings its warp together: behind a
+// loop of unequal length or a branch of some lanes nothing else promises that.
 __device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_sync() {

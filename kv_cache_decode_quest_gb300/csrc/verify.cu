@@ -317,7 +317,6 @@ __global__ void __launch_bounds__(256, kBlocks)
     // the sequence's last block goes on; of a cluster the first
     int* arrived = ws + 64 + b;
     if (CLUSTER) {
-        __syncwarp();
         cluster_sync();
         if (blockIdx.x != 0) return;
     } else {
