@@ -13,11 +13,10 @@
 // Layout: a lane owns 8 whole pairs of a head, two 16-byte vectors: with halves, vector j
 // and vector j + rot_dim / 16; with pairs, vectors 2j and 2j + 1.  Either way its angles
 // are 8j .. 8j + 7, no value crosses lanes in the rotation, and a head takes D / 16 lanes:
-// a warp has 512 / D heads side by side.  Channels past rot_dim lie in lanes of their own
-// (cosine 1, sine 0).
+// a warp has 512 / D heads side by side.  Channels past rot_dim lie in lanes of their own,
+// which leave the rotation out.
 #include <algorithm>
 
-#include "append.cuh"
 #include "chunk_rows.cuh"
 #include "common.cuh"
 #include "internal.h"
@@ -116,10 +115,13 @@ struct Turn {
 };
 
 // One head's two vectors of this lane: normed over the head's D / 16 lanes, weighted,
-// rotated, rounded.
-template <int D, bool PAIRS>
+// rotated, rounded.  ALL: every channel is rotated; else only the lanes of which `turns` holds
+// rotate (a cosine of 1 and a sine of 0 would make NaN of a value beside an infinity).  The
+// choice costs two selects a value: 16,384 rows of 16 heads of 64 channels take 14.3 us with it,
+// 13.8 where all rotate and it is left out; the append of 8 x 8192 rows 214 and 210 us.
+template <int D, bool PAIRS, bool ALL>
 __device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, const Weight& w, float eps,
-                                          const Turn& t) {
+                                          bool turns, const Turn& t) {
     uint64_t x[4], y[4], both = 0;
     to_pairs<PAIRS>(u, v, x, y);
     if (norm) {
@@ -144,8 +146,11 @@ __device__ __forceinline__ void norm_turn(uint4& u, uint4& v, bool norm, const W
     uint32_t p[4], q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        uint64_t a = fma_f32x2(x[i], t.c[i], mul_f32x2(y[i], t.n[i]));
-        uint64_t b = fma_f32x2(y[i], t.c[i], mul_f32x2(x[i], t.s[i]));
+        uint64_t a = x[i], b = y[i];
+        if (ALL || turns) {
+            a = fma_f32x2(x[i], t.c[i], mul_f32x2(y[i], t.n[i]));
+            b = fma_f32x2(y[i], t.c[i], mul_f32x2(x[i], t.s[i]));
+        }
         if (norm) {
             a = mul_f32x2(a, both);
             b = mul_f32x2(b, both);
@@ -176,7 +181,7 @@ struct HeadRows {
 // AHEAD: the next pass is loaded before this one is worked on, at 72 registers (16,384 rows of 36
 // heads of 128 channels, nine passes: 50.1 us, 89% of the copy rate, against 52.7 us; rows of two
 // passes 13.7 us against 12.9).
-template <int D, bool PAIRS, bool AHEAD>
+template <int D, bool PAIRS, bool ALL, bool AHEAD>
 __global__ void __launch_bounds__(128, AHEAD ? 7 : 8)
     qk_rope_kernel(se_rope rope, const int32_t* pos, int rows, int parts, HeadRows q, HeadRows k) {
     constexpr int HP = 512 / D, A = D / 64;                  // heads a pass, angles a lane
@@ -214,13 +219,7 @@ __global__ void __launch_bounds__(128, AHEAD ? 7 : 8)
     {
         float ca[A], sa[A], c[8], s[8];
 #pragma unroll
-        for (int i = 0; i < A; ++i) {
-            turn_of(step[i], rope.amplitude, at, ca[i], sa[i]);
-            if (A * lane + i >= rope.rot_dim / 2) {          // channels that are not rotated
-                ca[i] = 1.f;
-                sa[i] = 0.f;
-            }
-        }
+        for (int i = 0; i < A; ++i) turn_of(step[i], rope.amplitude, at, ca[i], sa[i]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             c[i] = __shfl_sync(0xffffffffu, ca[i % A], (8 * l.j + i) / A);
@@ -233,7 +232,7 @@ __global__ void __launch_bounds__(128, AHEAD ? 7 : 8)
         const Weight wt = load_weight<D, PAIRS>(weight, l);
         for (int p = begin; p < end; ++p) {
             auto pass = [&](uint4& a, uint4& b) {
-                norm_turn<D, PAIRS>(a, b, weight != nullptr, wt, rope.eps, t);
+                norm_turn<D, PAIRS, ALL>(a, b, weight != nullptr, wt, rope.eps, l.turns, t);
                 const int head = (p - skip) * HP + mine;
                 if (head < h.heads) {
                     uint4* out = h.out + (int64_t)row * h.out_stride + head * (D / 8);
@@ -297,14 +296,11 @@ struct Turns {
             }
         }
     }
-    // This lane's of row r.
+    // This lane's of row r (nothing for a lane whose channels are not rotated).
     __device__ __forceinline__ void get(const HeadLane<D, PAIRS>& l, int r, Turn& turn) const {
         float c[8], s[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = 1.f;
-            s[i] = 0.f;
-        }
+        for (int i = 0; i < 8; ++i) c[i] = s[i] = 0.f;
         if (l.turns) {
             const float4* t = reinterpret_cast<const float4*>(table + r * D) + l.j;
             const float4 a = t[0], b = t[kLanes], d = t[2 * kLanes], e = t[3 * kLanes];
@@ -378,7 +374,7 @@ __device__ __forceinline__ int64_t place_of(int slot, int heads, int h) {
 // us without), heads side by side instead of a head's rows (223), a short loop instead of four
 // passes unrolled (232).  Latency bound below: 64 single tokens 5.1 us; 256 sequences with up
 // to 65 rows 21.6 us (a third of the copy rate: 12 warps an SM, each a chain of some 17 passes).
-template <int D, bool PAIRS>
+template <int D, bool PAIRS, bool ALL>
 __global__ void __launch_bounds__(128, kAppendBlocks)
     rope_append_chunk_kernel(se_paged_kv kv, se_rope rope, PassList list, const uint4* k_new,
                              int64_t k_stride, se_chunk ck, int batch, int side_shift,
@@ -514,7 +510,7 @@ __global__ void __launch_bounds__(128, kAppendBlocks)
                 uint4 u = ring.slot(ring.out, i)[0], v = ring.slot(ring.out, i)[32];
                 if (at < list.nq) {
                     if (pos < 0) continue;
-                    norm_turn<D, PAIRS>(u, v, rope.q_weight != nullptr, wq, rope.eps, t);
+                    norm_turn<D, PAIRS, ALL>(u, v, rope.q_weight != nullptr, wq, rope.eps, l.turns, t);
                     const int head = at * HP + mine;
                     if (head < list.q.heads) {
                         uint4* out = list.q.out + (first + r) * list.q.out_stride + head * SEGS;
@@ -556,7 +552,7 @@ __global__ void __launch_bounds__(128, kAppendBlocks)
                 const bool there = r < kPage && ((pc.rows >> r) & 1) && mine_too;
                 uint4 a = ring.slot(ring.out, i)[0], b = ring.slot(ring.out, i)[32];
                 turns.get(l, min(r0 + r, kTable - 1), t);
-                norm_turn<D, PAIRS>(a, b, rope.k_weight != nullptr, wk, rope.eps, t);
+                norm_turn<D, PAIRS, ALL>(a, b, rope.k_weight != nullptr, wk, rope.eps, l.turns, t);
                 if (there) {
                     out[r * SEGS + l.a] = a;
                     out[r * SEGS + l.b] = b;
@@ -611,8 +607,11 @@ cudaError_t rows_of(const se_rope& rope, const int32_t* pos, int rows, const Hea
         return launch_pdl(kernel, grid, dim3(128), 0, s, rope, pos, rows, parts, head_rows(q),
                           head_rows(k));
     };
-    return passes > 2 * parts ? run(qk_rope_kernel<D, PAIRS, true>)
-                              : run(qk_rope_kernel<D, PAIRS, false>);
+    if (rope.rot_dim == D)
+        return passes > 2 * parts ? run(qk_rope_kernel<D, PAIRS, true, true>)
+                                  : run(qk_rope_kernel<D, PAIRS, true, false>);
+    return passes > 2 * parts ? run(qk_rope_kernel<D, PAIRS, false, true>)
+                              : run(qk_rope_kernel<D, PAIRS, false, false>);
 }
 
 template <int D, bool PAIRS>
@@ -636,8 +635,12 @@ cudaError_t append_of(const se_paged_kv& kv, const se_rope& rope, const HeadArgs
     // (the ragged chunks 8.4 us against 13.2, the 65,536 rows 213 us against 211)
     int side_shift = 0;
     while (share == 1 && (2 << side_shift) <= std::min(H, HP)) ++side_shift;
-    return launch_pdl(rope_append_chunk_kernel<D, PAIRS>, dim3(groups, share), dim3(128), 0, s, kv,
-                      rope, list, k, row_stride / 8, ck, batch, side_shift, status);
+    auto run = [&](auto kernel) {
+        return launch_pdl(kernel, dim3(groups, share), dim3(128), 0, s, kv, rope, list, k,
+                          row_stride / 8, ck, batch, side_shift, status);
+    };
+    return rope.rot_dim == D ? run(rope_append_chunk_kernel<D, PAIRS, true>)
+                             : run(rope_append_chunk_kernel<D, PAIRS, false>);
 }
 
 }  // namespace
