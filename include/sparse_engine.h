@@ -524,8 +524,9 @@ int se_draft_verify(const void* probs, const void* draft_probs, int64_t row_stri
  * are not shared.
  * src[b] past the batch, or a source that is forked in the same call itself:
  * SE_DEV_BAD_INDEX; b that holds pages, or a source whose lengths are inconsistent:
- * SE_DEV_BAD_LENGTH; that b stays as it was.  A page outside the pool on the stack, or where
- * the source's last rows are: SE_DEV_BAD_INDEX, b stays empty; among the shared ones:
+ * SE_DEV_BAD_LENGTH; that b stays as it was.  A page outside the pool where the source's last
+ * rows are: SE_DEV_BAD_INDEX, b asks for no page and stays empty; on the stack:
+ * SE_DEV_BAD_INDEX, b stays empty (that entry is used up); among the shared ones:
  * SE_DEV_BAD_INDEX, b has it as the source has, uncounted.
  * Limits: batch <= 8192; num_pages and max_pages_per_seq < 2^27; batch * max_pages_per_seq
  * <= 2^30.

@@ -66,6 +66,9 @@ __device__ __forceinline__ Fork fork_of(const se_page_pool& p, const int32_t* sr
         f.flags = SE_DEV_BAD_INDEX;
     } else if (mine != 0 || !consistent(p, f.ctx, theirs)) {
         f.flags = SE_DEV_BAD_LENGTH;
+    } else if (f.ctx % kPage != 0 &&                         // (it asks for no page that it cannot use)
+               !in_pool(p, p.block_table[(int64_t)f.src * p.max_pages_per_seq + f.ctx / kPage])) {
+        f.flags = SE_DEV_BAD_INDEX;
     } else {
         f.want = true;
         f.page = f.ctx % kPage != 0;
@@ -108,13 +111,12 @@ __global__ void __launch_bounds__(1024, 1)
         int fresh = f.want ? -1 : -2;
         if (f.page) {
             ++run;
-            const int64_t last = (int64_t)f.src * pool.max_pages_per_seq + f.ctx / kPage;
             if (run > n_free) {
                 flags |= SE_DEV_CAPACITY;
                 fresh = -2;
             } else {
                 fresh = pool.free_pages[n_free - run];
-                if (!in_pool(pool, fresh) || !in_pool(pool, pool.block_table[last])) {
+                if (!in_pool(pool, fresh)) {
                     flags |= SE_DEV_BAD_INDEX;
                     fresh = -2;
                 }

@@ -32,6 +32,9 @@ def fork(pool, refs, src):
             continue
         full = n // PAGE
         if n % PAGE:
+            if not 0 <= pool.block_table[s, full] < pool.num_pages:
+                flags |= BAD_INDEX
+                continue
             asked += 1
             if asked > free0:
                 flags |= CAPACITY

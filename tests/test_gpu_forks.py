@@ -418,3 +418,25 @@ def test_the_first_call_of_a_process_may_be_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True,
                        timeout=250)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_a_source_whose_last_page_does_not_exist_takes_no_page():
+    """A fork of it asks for none: the stack keeps its pages, the forks behind it get theirs."""
+    for batch, pages, maxp in ((6, 12, 6), (900, 3000, 12)):
+        b = Both(pages, batch, maxp)
+        b.grow([40, 20] + [0] * (batch - 2))
+        src = np.full(batch, -1)
+        src[2:6] = [1, 0, 1, 0]
+        for bad in (pages, -1):
+            b.o.block_table[1, 1] = bad
+            b.p.block_table[1, 1] = bad
+            before = len(b.o.free)
+            assert b.fork(src) == BAD_INDEX
+            assert b.o.n_pages[2:6].tolist() == [0, 3, 0, 3] and len(b.o.free) == before - 2
+            assert b.cut(np.where(np.isin(np.arange(batch), (3, 5)), 0, -1)) == 0
+            assert len(b.o.free) == before
+        # the last page of the stack goes to the fork that can be served
+        b.o.free = b.o.free[:1]
+        b.p.n_free.fill_(1)
+        src[5] = -1
+        assert b.fork(src) == BAD_INDEX and b.o.n_pages[2:6].tolist() == [0, 3, 0, 0]

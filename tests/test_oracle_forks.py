@@ -96,3 +96,13 @@ def test_a_truncation_to_nothing_is_a_release():
     of.truncate(a, None, [0, -1, 0])
     oc.release(b, np.array([1, 0, 1]))
     assert a.free == b.free and a.n_pages.tolist() == b.n_pages.tolist()
+
+
+def test_a_source_whose_last_page_does_not_exist_costs_no_page():
+    pool, refs = oc.Pool(10, 4, 4), [0] * 10
+    oc.plan(pool, [20, 20, 0, 0], 40)
+    pool.ctx[:2] = 20
+    pool.block_table[0, 1] = 10
+    fs, fp, flags = of.fork(pool, refs, [-1, -1, 0, 1])
+    assert flags == of.BAD_INDEX and fs.tolist() == [-1, -1, -1, 1] and pool.n_pages.tolist() == [2, 2, 0, 2]
+    assert len(pool.free) == 5 and sum(refs) == 1
