@@ -487,9 +487,12 @@ int se_rope_append_chunk(const se_paged_kv* kv, const se_rope* rope, const void*
  * No rows, or pos[start[b]] < 0 (no page was left): n_accepted 0, next_token -1, keep -1.
  * The test of a draft is exact.  Weights (values above 1 count as 1, negative ones and NaN as
  * 0) and their sums are fp32 numbers with a second word for what rounding loses, then
- * integers: off by less than 2^-40 in all (a sum below 2^-50 may count as 0), the same for
- * the same row whatever the batch.  Rows whose sum passes 8: the token is unspecified (-1 or in
- * [0, vocab)).  Random numbers outside [0, 1) count as the nearest inside, NaN as 0.
+ * integers.  A row's running sums are off by less than 2^-38 where they come to 1, 2^-35 where
+ * they come to 8, and where they come to less than 2^-16 by less than a part in 2^22 of the
+ * whole; no token without weight is drawn.  They are the same for the same row at the same
+ * offset from a 16-byte boundary, whatever the batch.  Rows whose sum passes 8: the token is
+ * unspecified (-1 or in [0, vocab)).  Random numbers outside [0, 1) count as the nearest
+ * inside, NaN as 0.
  * A row without any weight: next_token -1, SE_DEV_BAD_VALUE.  A drafted token outside
  * [0, vocab) is refused: SE_DEV_BAD_INDEX.  start outside [0, max_tokens] or descending:
  * SE_DEV_BAD_LENGTH, as no rows.

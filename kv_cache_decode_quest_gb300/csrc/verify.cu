@@ -11,7 +11,10 @@
 // on sums are integers in units of 2^-58, the same in any order: the row is cut into tiles
 // of 1024 that any warp of any block may sum, and the last block of a sequence finds the
 // tile and in it the token.  Two weights at once in packed fp32: 5 operations a weight of p
-// alone, 9 with q (one by one 41.4 us for the 39.6 below).
+// alone, 9 with q (one by one 41.4 us for the 39.6 below).  A row whose weights come to little
+// (hardly any is left of p beside q, or the row is no distribution) would lose them below those
+// units: its last block makes the sums again, with the weights scaled by a power of two (up to
+// four times where nothing is left: 256 such sequences 265 us).
 // Up to eight blocks of a sequence are a cluster, whose first block gets the sums in shared
 // memory; more (a large vocabulary, few sequences) meet over a counter in memory (one
 // sequence of 32,000 tokens: 0.8 us more).
@@ -97,14 +100,15 @@ __device__ __forceinline__ void widen(uint4 w, float* x) {
     }
 }
 
-// A row of the vocabulary: of p, of q (NULL: none is taken off), and the token without
-// weight (-1: none).
+// A row of the vocabulary: of p, of q (NULL: none is taken off), the token without weight
+// (-1: none), and the power of two that all weights are multiplied with.
 template <typename T>
 struct Row {
     const T* p;
     const T* q;
     int vocab, without;
     int lead;                    // elements between the 16-byte boundary below p and p
+    float scale;
 };
 
 // Vector c (16 bytes, on the boundaries) of `from`, the row's p or q; places outside the row
@@ -126,13 +130,13 @@ __device__ __forceinline__ uint4 load_vector(const Row<T>& r, const T* from, int
         }
     return make_uint4(a[0], a[1], a[2], a[3]);
 }
-// Vector c's values of p within [0, 1] (NaN: 0), 0 for the token without weight.
-template <typename T>
+// Vector c's values of p within [0, 1] (NaN: 0), scaled, 0 for the token without weight.
+template <typename T, bool SCALED>
 __device__ __forceinline__ void p_terms(const Row<T>& r, int c, uint4 p, float* x) {
     constexpr int N = 16 / sizeof(T);
     widen<T>(p, x);
 #pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = __saturatef(x[e]);
+    for (int e = 0; e < N; ++e) x[e] = SCALED ? __saturatef(x[e]) * r.scale : __saturatef(x[e]);
     const int at = r.without < 0 ? -1 : r.without + r.lead - c * N;
     if (at >= 0 && at < N)
 #pragma unroll
@@ -140,12 +144,13 @@ __device__ __forceinline__ void p_terms(const Row<T>& r, int c, uint4 p, float* 
             if (e == at) x[e] = 0.f;
 }
 // What q takes off each of them: at most all.
-template <typename T>
-__device__ __forceinline__ void q_terms(uint4 q, const float* x, float* y) {
+template <typename T, bool SCALED>
+__device__ __forceinline__ void q_terms(const Row<T>& r, uint4 q, const float* x, float* y) {
     constexpr int N = 16 / sizeof(T);
     widen<T>(q, y);
 #pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = fminf(fmaxf(y[e], 0.f), x[e]);
+    for (int e = 0; e < N; ++e)
+        y[e] = fminf(SCALED ? fmaxf(y[e], 0.f) * r.scale : fmaxf(y[e], 0.f), x[e]);
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 x) {
@@ -155,7 +160,7 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
 }
 
 // The sum of tile k of the row, in every lane: up to eight vectors a lane in flight.
-template <typename T, bool BOTH>
+template <typename T, bool BOTH, bool SCALED>
 __device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
     constexpr int N = 16 / sizeof(T), C = kTile / N / 32, V = BOTH ? 4 : C;
     Sum sum;
@@ -171,8 +176,8 @@ __device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float x[N], y[N];
-            p_terms(r, c + i * 32, p[i], x);
-            if (BOTH) q_terms<T>(q[i], x, y);
+            p_terms<T, SCALED>(r, c + i * 32, p[i], x);
+            if (BOTH) q_terms<T, SCALED>(r, q[i], x, y);
 #pragma unroll
             for (int e = 0; e < N; e += 2) {
                 if (BOTH)
@@ -184,9 +189,10 @@ __device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
     }
     return warp_sum(sum.units());
 }
-template <typename T>
+template <typename T, bool SCALED>
 __device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
-    return r.q != nullptr ? tile_sum_of<T, true>(r, k, lane) : tile_sum_of<T, false>(r, k, lane);
+    return r.q != nullptr ? tile_sum_of<T, true, SCALED>(r, k, lane)
+                          : tile_sum_of<T, false, SCALED>(r, k, lane);
 }
 
 // Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads
@@ -221,6 +227,19 @@ __device__ __forceinline__ u64 part_of(float u, u64 total) {
     const int s = e ? 150 - e : 149;                      // at least 24
     const u64 lo = m * total, hi = __umul64hi(m, total);
     return s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? hi >> (s - 64) : 0;
+}
+
+// How far sums are off: a lane's sum of a tile by less than four units where it is cut to them,
+// those of a row (2^22 tokens, 32 a lane) by 2^19 units, 2^-39; the second words' own rounding is
+// less than 2^-40 of the sum (16 terms of up to 2^-24 of it, or twice that with q's, each
+// added with 2^-24 of their sum).  Together below 2^-38 of a row that sums to 1.  A sum
+// below 2^-16 is made again, scaled so that the true one stays below 2^-2; scaled it passes
+// 2^-16, or the scale is the last: there the smallest fp32 number is 2^17 units, nothing is cut,
+// and a sum of 0 is one of no weights.
+constexpr u64 kSmall = 1ull << 42;
+constexpr int kMaxShift = 108;
+__device__ __forceinline__ int next_shift(int shift, u64 total) {      // (at least 13 more)
+    return min(kMaxShift, shift + 56 - (64 - __clzll(static_cast<long long>(total + (1u << 19)))));
 }
 
 constexpr int kBlocks = 4;                   // blocks an SM
@@ -303,10 +322,11 @@ __global__ void __launch_bounds__(256, kBlocks)
     row.vocab = vocab;
     row.without = stay < drafts && draft == nullptr && !outside ? refused : -1;
     row.lead = static_cast<int>(reinterpret_cast<uintptr_t>(row.p) % 16 / sizeof(T));
+    row.scale = 1.f;
     u64* sums = reinterpret_cast<u64*>(reinterpret_cast<char*>(ws) + kSumsAt) + (int64_t)b * tiles;
     const int nw = blockDim.x >> 5;
     for (int k = blockIdx.x * nw + warp; k < tiles; k += gridDim.x * nw) {
-        const u64 sum = tile_sum(row, k, lane);
+        const u64 sum = tile_sum<T, false>(row, k, lane);
         if (lane == 0) {
             if (CLUSTER)
                 cluster_poke(s_sums + k, 0, sum);
@@ -332,16 +352,25 @@ __global__ void __launch_bounds__(256, kBlocks)
     const int per = (tiles + blockDim.x - 1) / blockDim.x;
     const int k0 = min(static_cast<int>(threadIdx.x) * per, tiles), k1 = min(k0 + per, tiles);
     u64 total = 0, ahead = 0, held = 0;
-    for (int round = 0; round < 2; ++round) {
+    int shift = 0;
+    for (int round = 0;; ++round) {
         held = 0;
         for (int k = k0; k < k1; ++k) held += sum_of(k);
-        ahead = block_sum_before(held, tmp[round], &total);
-        if (total > 0 || (row.q == nullptr && row.without < 0)) break;
-        // nothing is left of p beside q: drawn from p
-        row.q = nullptr;
-        row.without = -1;
+        ahead = block_sum_before(held, tmp[round & 1], &total);
+        if (total >= kSmall) break;
+        if (shift < kMaxShift) {
+            shift = next_shift(shift, total);
+        } else if (total == 0 && (row.q != nullptr || row.without >= 0)) {
+            // nothing is left of p beside q: drawn from p
+            row.q = nullptr;
+            row.without = -1;
+            shift = 0;
+        } else {
+            break;
+        }
+        row.scale = __int_as_float((127 + shift) << 23);
         for (int k = warp; k < tiles; k += nw) {
-            const u64 sum = tile_sum(row, k, lane);
+            const u64 sum = tile_sum<T, true>(row, k, lane);
             if (lane == 0) *(CLUSTER ? s_sums + k : sums + k) = sum;
         }
         __syncthreads();
@@ -371,18 +400,20 @@ __global__ void __launch_bounds__(256, kBlocks)
     const int c = s_tile * (kTile / N) + threadIdx.x;
     if (threadIdx.x < kTile / N) {
         float x[N], y[N];
-        p_terms(row, c, load_vector(row, row.p, c), x);
-        if (row.q != nullptr) q_terms<T>(load_vector(row, row.q, c), x, y);
+        p_terms<T, true>(row, c, load_vector(row, row.p, c), x);
+        if (row.q != nullptr) q_terms<T, true>(row, load_vector(row, row.q, c), x, y);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             const float q = row.q != nullptr ? y[e] : 0.f, d = x[e] - q;
+            // (less than a unit counts as one: a tile that was chosen has a token with weight)
             w[e] = Sum::units(d, (x[e] - d) - q);
+            if (w[e] == 0 && d > 0.f) w[e] = 1;
             sum += w[e];
         }
     }
     u64 part;
     ahead = block_sum_before(sum, tmp[2], &part);
-    // (the weights one by one may end a rounding before the tile's sum: then it is the last)
+    // (the weights one by one may end before the tile's sum, by up to a unit each: then it is the last)
     const u64 rest = part == 0 ? 0 : min(s_rest, part - 1);
     if (sum > 0 && ahead <= rest && rest < ahead + sum) {
 #pragma unroll
