@@ -250,6 +250,14 @@ def _holds(holder: _Measured, batch: int, what: str):
                                 f"{batch} sequences")
 
 
+def _summarises(kv, batch: int, what: str):
+    """_holds, and room for the page summaries of `batch` sequences (or none kept)."""
+    _holds(kv, batch, what)
+    if kv._summarised < batch:
+        raise SparseEngineError(f"{what}: contiguous PagedKV.meta of at least [{batch}][max_pages][heads][2]"
+                                f"[head_dim] needed, got {tuple(kv.meta.shape)}")
+
+
 @dataclasses.dataclass
 class PagedKV(_Measured):
     k: torch.Tensor            # bf16 [num_pages][Hkv][16][D]
@@ -259,10 +267,23 @@ class PagedKV(_Measured):
     ctx_len: torch.Tensor      # int32 [B]
 
     def _measure(self) -> int:
-        for t in (self.k, self.v, self.meta):
+        k, v, meta, table = self.k, self.v, self.meta, self.block_table
+        for t in (k, v, meta):
             if t is not None and t.dtype is not torch.bfloat16:
                 raise SparseEngineError(f"PagedKV: a bfloat16 cache is needed, got {t.dtype}")
-        return min(self.ctx_len.numel(), self.block_table.shape[0])
+        if k.dim() != 4 or k.shape != v.shape or not k.is_contiguous() or not v.is_contiguous():
+            raise SparseEngineError("PagedKV: contiguous k and v of one shape [pages][heads][16][head_dim] "
+                                    f"needed, got {tuple(k.shape)} and {tuple(v.shape)}")
+        for t, dims, name in ((table, 2, "block_table"), (self.ctx_len, 1, "ctx_len")):
+            if t.dtype is not torch.int32 or t.dim() != dims or not t.is_contiguous():
+                raise SparseEngineError(f"PagedKV.{name}: contiguous int32 tensor of {dims} dimension(s) "
+                                        f"needed, got {t.dtype} of shape {tuple(t.shape)}")
+        n = min(self.ctx_len.numel(), table.shape[0])
+        # sequences whose summaries may be written (a call that only reads pages takes any)
+        fits = meta is None or (meta.is_contiguous() and
+                                meta.shape[1:] == (table.shape[1], k.shape[1], 2, k.shape[3]))
+        self.__dict__["_summarised"] = n if meta is None else min(n, meta.shape[0]) if fits else -1
+        return n
 
     @property
     def c(self) -> PagedKVC:
@@ -593,7 +614,7 @@ def se_kv_append_chunk(kv: PagedKV, k_new, v_new, chunk: Chunk, batch: int, ws, 
         raise SparseEngineError("se_kv_append_chunk: k_new and v_new strides differ")
     if k_new.dtype is not _BF16 or v_new.dtype is not _BF16:
         raise SparseEngineError("se_kv_append_chunk: bfloat16 k_new and v_new needed")
-    _holds(kv, batch, "se_kv_append_chunk")
+    _summarises(kv, batch, "se_kv_append_chunk")
     _holds(chunk, 0, "se_kv_append_chunk")
     _check(load().se_kv_append_chunk(ctypes.byref(c), _p(k_new), _p(v_new), stride,
                                      ctypes.byref(cc), batch, _p(ws), ws.numel(),
@@ -744,7 +765,7 @@ def se_rope_append_chunk(kv: PagedKV, rope: Rope, q, k_new, v_new, q_out, chunk:
     if hq and dim_q != dim:
         raise SparseEngineError(f"se_rope_append_chunk: q of {dim_q} channels a head, the cache of {dim}")
     _rope_fits(rope, dim, "se_rope_append_chunk")
-    _holds(kv, batch, "se_rope_append_chunk")
+    _summarises(kv, batch, "se_rope_append_chunk")
     _holds(chunk, 0, "se_rope_append_chunk")
     here = _on_device("se_rope_append_chunk", (kv, rope, chunk), k_new, v_new, ws, q, q_out)
     rc = rope.c
@@ -826,7 +847,7 @@ def se_pages_truncate(pool: PagePool, page_refs, keep, batch: int, carry: Carry,
 
 def se_pages_carry(kv: PagedKV, carry: Carry, batch: int, ws, stream=None):
     """One layer's cache follows a fork or a truncation: last pages' rows and page summaries."""
-    _holds(kv, batch, "se_pages_carry")
+    _summarises(kv, batch, "se_pages_carry")
     _holds(carry, batch, "se_pages_carry")
     here = _on_device("se_pages_carry", (kv, carry), ws)
     c, cc = kv.c, carry.c
