@@ -13,8 +13,7 @@
 // tile and in it the token.  Two weights at once in packed fp32: 5 operations a weight of p
 // alone, 9 with q (one by one 41.4 us for the 39.6 below).  A row whose weights come to little
 // (hardly any is left of p beside q, or the row is no distribution) would lose them below those
-// units: its last block makes the sums again, with the weights scaled by a power of two (up to
-// four times where nothing is left: 256 such sequences 265 us).
+// units: its last block makes the sums again, with the weights scaled by a power of two.
 // Up to eight blocks of a sequence are a cluster, whose first block gets the sums in shared
 // memory; more (a large vocabulary, few sequences) meet over a counter in memory (one
 // sequence of 32,000 tokens: 0.8 us more).
@@ -159,9 +158,10 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
     return x;
 }
 
-// The sum of tile k of the row, in every lane: up to eight vectors a lane in flight.
+// The sum of tile k of the row, in every lane: up to eight vectors a lane in flight.  SCALED:
+// `some` is set where this lane sees a weight, however small.
 template <typename T, bool BOTH, bool SCALED>
-__device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
+__device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane, bool& some) {
     constexpr int N = 16 / sizeof(T), C = kTile / N / 32, V = BOTH ? 4 : C;
     Sum sum;
 #pragma unroll 1
@@ -180,6 +180,8 @@ __device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
             if (BOTH) q_terms<T, SCALED>(r, q[i], x, y);
 #pragma unroll
             for (int e = 0; e < N; e += 2) {
+                if (SCALED)
+                    some |= BOTH ? x[e] > y[e] || x[e + 1] > y[e + 1] : x[e] > 0.f || x[e + 1] > 0.f;
                 if (BOTH)
                     sum.add(f32x2(x[e], x[e + 1]), f32x2(y[e], y[e + 1]));
                 else
@@ -190,9 +192,9 @@ __device__ __forceinline__ u64 tile_sum_of(const Row<T>& r, int k, int lane) {
     return warp_sum(sum.units());
 }
 template <typename T, bool SCALED>
-__device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane) {
-    return r.q != nullptr ? tile_sum_of<T, true, SCALED>(r, k, lane)
-                          : tile_sum_of<T, false, SCALED>(r, k, lane);
+__device__ __forceinline__ u64 tile_sum(const Row<T>& r, int k, int lane, bool& some) {
+    return r.q != nullptr ? tile_sum_of<T, true, SCALED>(r, k, lane, some)
+                          : tile_sum_of<T, false, SCALED>(r, k, lane, some);
 }
 
 // Exclusive block-wide sum of one value per thread; *total receives the sum.  All threads
@@ -325,8 +327,9 @@ __global__ void __launch_bounds__(256, kBlocks)
     row.scale = 1.f;
     u64* sums = reinterpret_cast<u64*>(reinterpret_cast<char*>(ws) + kSumsAt) + (int64_t)b * tiles;
     const int nw = blockDim.x >> 5;
+    bool some = false;
     for (int k = blockIdx.x * nw + warp; k < tiles; k += gridDim.x * nw) {
-        const u64 sum = tile_sum<T, false>(row, k, lane);
+        const u64 sum = tile_sum<T, false>(row, k, lane, some);
         if (lane == 0) {
             if (CLUSTER)
                 cluster_poke(s_sums + k, 0, sum);
@@ -369,11 +372,12 @@ __global__ void __launch_bounds__(256, kBlocks)
             break;
         }
         row.scale = __int_as_float((127 + shift) << 23);
+        some = false;
         for (int k = warp; k < tiles; k += nw) {
-            const u64 sum = tile_sum<T, true>(row, k, lane);
+            const u64 sum = tile_sum<T, true>(row, k, lane, some);
             if (lane == 0) *(CLUSTER ? s_sums + k : sums + k) = sum;
         }
-        __syncthreads();
+        if (!__syncthreads_or(some)) shift = kMaxShift;      // no scale finds a weight
     }
     if (threadIdx.x == 0) {
         if (!CLUSTER) *arrived = 0;
