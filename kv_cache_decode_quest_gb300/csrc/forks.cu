@@ -220,7 +220,8 @@ __device__ __forceinline__ Cut cut_of(const se_page_pool& p, const int32_t* refs
 // (131,008 entries, all of shared pages) about 24: random counts from 16 SMs.  With cold
 // caches: on one block 1694 us, on eight 82, on sixteen, with the entries that the next
 // sequence follows uncounted, 36, each thread's entries fetched once 28.  A launch over all
-// SMs would need a barrier across them for each phase.
+// SMs would need a barrier across them for each phase.  1024 threads have 64 registers each: 28
+// bytes are spilled.
 constexpr int kEntries = 8;                  // of a thread at once, at most
 constexpr int kAsks = -3;                    // asks for a page of its own
 

@@ -173,14 +173,15 @@ struct HeadRows {
 // first, then keys) when there are few rows.  Its lanes make the row's angles together (two
 // each at most) and hand them round.
 // A row is two latencies (its position with the first pass, then the stores), so what counts
-// is how many warps wait at once: 64 registers, one pass at a time, 32 warps an SM.  16,384
-// rows of 16 heads of 64 channels: 12.9 us, 5.2 TB/s of rows read and written (77% of the
-// copy rate), issue slots half busy.  With four passes a warp in flight and 100 registers 18.0
-// us; through a ring in shared memory 18.7 to 20.6; a table of angles for 16 rows a block
-// 16.5.  64 rows of 36 heads of 128 (a decode step): 1.9 us.
-// AHEAD: the next pass is loaded before this one is worked on, at 72 registers (16,384 rows of 36
-// heads of 128 channels, nine passes: 50.1 us, 89% of the copy rate, against 52.7 us; rows of two
-// passes 13.7 us against 12.9).
+// is how many warps wait at once: 64 registers, one pass at a time, 32 warps an SM (up to 32
+// bytes are spilled).  16,384 rows of 16 heads of 64 channels, pairs: 13.4 us where 32 rotate,
+// 5.0 TB/s of rows read and written (74% of the copy rate), issue slots half busy; with norms
+// 14.3, halves 14.6; where all rotate 13.9 and 14.4.  What was 12.9 then took 18.0 us with four
+// passes a warp in flight and 100 registers, 18.7 to 20.6 through a ring in shared memory, 16.5
+// with a table of angles for 16 rows a block.  64 rows of 36 heads of 128 (a decode step): 1.9 us.
+// AHEAD: the next pass is loaded before this one is worked on, at 72 registers and 24 to 64 bytes
+// spilled (16,384 rows of 36 heads of 128 channels, nine passes: 49.6 to 50.6 us, 89% of the copy
+// rate, against 52.7 us; rows of two passes 13.7 us against 12.9).
 template <int D, bool PAIRS, bool ALL, bool AHEAD>
 __global__ void __launch_bounds__(128, AHEAD ? 7 : 8)
     qk_rope_kernel(se_rope rope, const int32_t* pos, int rows, int parts, HeadRows q, HeadRows k) {

@@ -11,16 +11,17 @@
 // on sums are integers in units of 2^-58, the same in any order: the row is cut into tiles
 // of 1024 that any warp of any block may sum, and the last block of a sequence finds the
 // tile and in it the token.  Two weights at once in packed fp32: 5 operations a weight of p
-// alone, 9 with q (one by one 41.4 us for the 39.6 below).  A row whose weights come to little
+// alone, 9 with q (one by one 41.4 us for the 39.9 below).  A row whose weights come to little
 // (hardly any is left of p beside q, or the row is no distribution) would lose them below those
 // units: its last block makes the sums again, with the weights scaled by a power of two.
 // Up to eight blocks of a sequence are a cluster, whose first block gets the sums in shared
 // memory; more (a large vocabulary, few sequences) meet over a counter in memory (one
 // sequence of 32,000 tokens: 0.8 us more).
-// 256 sequences over 131,072 tokens (about 1.6 rows each) take 39.6 us, 5.4 TB/s: 79% of the
+// 256 sequences over 131,072 tokens (about 1.6 rows each) take 39.9 us, 5.3 TB/s: 78% of the
 // copy rate; the rest is three latencies before a block knows its row, blocks with two rows
-// beside blocks with one, and the last sequences' search.  Every weight made a 64-bit
-// integer 122 us; two waves of blocks 52; rows through a ring in shared memory 4 us more.
+// beside blocks with one, and the last sequences' search.  In bf16 1.5 rows each take 34.6 us,
+// one of p alone 25.4: instructions a weight, not bytes.  Every weight made a 64-bit integer 122
+// us; two waves of blocks 52; rows through a ring in shared memory 4 us more.
 #include <algorithm>
 
 #include "common.cuh"
